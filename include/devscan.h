@@ -57,7 +57,10 @@ typedef enum {
     DS_UINT32 = 1,
     DS_FP32 = 2,
     DS_INT64 = 3,
-    DS_UINT64 = 4
+    DS_UINT64 = 4,
+    DS_BF16 = 5,    /* 5-7: the language-model operators only; the scans and */
+    DS_FP16 = 6,    /* compactions return DS_ERR_UNSUPPORTED_DTYPE for them */
+    DS_FP8_E4M3 = 7
 } ds_dtype;
 
 /* Comparison for compact_if: keep x_i when (x_i OP operand). */
@@ -246,6 +249,107 @@ int ds_radix_pass(const uint32_t* d_keys_in, uint32_t* d_keys_out, const uint32_
  */
 int ds_moe_align(const int32_t* d_topk_ids, int64_t n, int num_experts, int block, int32_t* d_counts,
                  int32_t* d_offsets, int32_t* d_sorted_ids, int64_t capacity, hipStream_t stream);
+
+/*
+ * Language-model operators around the counting sort: token embedding and its
+ * gradient, a mixture-of-experts router in front of ds_moe_align and its
+ * gradient, and the experts' products for a few tokens. Their matrices are
+ * rows of contiguous elements, `stride` elements apart (stride >= the row's
+ * length, else DS_ERR_INVALID_VALUE); pointers are aligned to their element's
+ * size, nothing more. Products, sums, scores and norms are held in 32 bits and
+ * rounded once, to nearest even, as they are written. Outputs must not
+ * overlap any other buffer (DS_ERR_OVERLAP). Results are the same on every
+ * run. Scratch is kept per (device, stream) like the other entry points'.
+ */
+
+/*
+ * Token embedding: d_out[i] = scale * d_table[d_ids[i]], a row of zeros where
+ * d_ids[i] lies outside [0, rows) (padding).
+ *   dtype     DS_FP32, DS_BF16 or DS_FP16, of the table and the output
+ *   d_ids     n ids of id_bytes 4 (int32) or 8 (int64)
+ * n == 0 or dim == 0 enqueues nothing. One launch.
+ */
+int ds_embedding(int dtype, const void* d_table, int64_t rows, int64_t dim, int64_t table_stride, const void* d_ids,
+                 int id_bytes, int64_t n, float scale, void* d_out, int64_t out_stride, hipStream_t stream);
+
+/*
+ * Gradient of the table of ds_embedding: d_grad[v] = scale * the sum of
+ * d_dout[i] over the i with d_ids[i] = v; ids outside [0, rows) are left out.
+ * accumulate 0: every row of d_grad is written, rows that no id names with
+ * zeros. accumulate 1: the sums are added to d_grad and other rows are not
+ * touched. The positions are sorted by id (a counting by rank up to 8,192
+ * ids, above that two passes of the counting sort, three from 261,121 rows
+ * on), so a row's terms are added in the order of the sorted positions,
+ * without atomics.
+ *   dtype       of d_dout: DS_FP32, DS_BF16 or DS_FP16
+ *   grad_dtype  of d_grad: dtype or DS_FP32
+ * n < 2^31, rows <= 133,432,830 (else DS_ERR_TOO_LARGE).
+ */
+int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const void* d_ids, int id_bytes, int64_t n,
+                      float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim, int64_t grad_stride,
+                      int accumulate, hipStream_t stream);
+
+/* Score of an expert in ds_moe_route. */
+typedef enum {
+    DS_SCORE_SOFTMAX = 0, /* softmax of the logits over the experts that can be chosen */
+    DS_SCORE_SIGMOID = 1  /* sigmoid of the expert's own logit */
+} ds_score;
+
+#define DS_ROUTE_MAX_TOP_K 64
+
+/*
+ * Mixture-of-experts router. Expert e of token t has the logit
+ * l = d_logits[t * stride + e]; it can be chosen where s = l + d_bias[e] (an
+ * fp32 sum; d_bias NULL: s = l) is neither -infinity nor NaN. Writes, token by
+ * token, the top_k experts that can be chosen, by s from the largest, equal s
+ * by the lower index, to d_ids[t * top_k + j], and scale times their scores
+ * (ds_score, of l without the bias; with renormalize 1 divided by the sum of
+ * the token's chosen scores, or 0 if that sum is 0) to d_weights. Where fewer
+ * than top_k can be chosen the rest is id -1, weight 0, which ds_moe_align and
+ * ds_moe_experts drop.
+ *   dtype  of the logits: DS_FP32, DS_BF16 or DS_FP16
+ * 1 <= top_k <= min(num_experts, DS_ROUTE_MAX_TOP_K), num_experts <= 511.
+ */
+int ds_moe_route(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
+                 const float* d_bias, int top_k, int score, int renormalize, float scale, float* d_weights,
+                 int32_t* d_ids, hipStream_t stream);
+
+/*
+ * Gradient of ds_moe_route's weights with respect to the logits (the choice
+ * itself has none): d_dlogits[t, e] = sum over j of d_dweights[t, j] *
+ * (d weights[t, j] / d logits[t, e]) for the ids given (ids outside
+ * [0, num_experts) have no part). Scores are taken over the logits that are
+ * neither -infinity nor NaN; the others get 0. All num_experts entries of
+ * every row are written, in the logits' type. Other arguments as ds_moe_route.
+ */
+int ds_moe_route_grad(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
+                      const int32_t* d_ids, const float* d_dweights, int top_k, int score, int renormalize,
+                      float scale, void* d_dlogits, int64_t dlogits_stride, hipStream_t stream);
+
+#define DS_EXPERTS_MAX_WIDTH 1048576
+
+/*
+ * The experts of a mixture-of-experts layer for a few tokens (a decoding
+ * step): y[t] = sum over j < top_k of d_weights[t, j] * w_out[e] h, with
+ * e = d_ids[t, j] and h = silu(w_in[e][0 .. hidden) x[t]) * (w_in[e][hidden ..
+ * 2 hidden) x[t]); choices outside [0, num_experts) are left out. Each used
+ * expert's weights are streamed once for up to 64 of its tokens; h is rounded
+ * to `dtype` once, all products are summed in 32 bits.
+ *   dtype         DS_BF16 or DS_FP16, of x [tokens, dim] and y [tokens, dim]
+ *   weight_dtype  dtype, or DS_FP8_E4M3 with scales
+ *   d_w_in        [num_experts, 2 * hidden, dim], contiguous
+ *   d_w_out       [num_experts, dim, hidden], contiguous
+ *   d_w_in_scale, d_w_out_scale  for DS_FP8_E4M3 (else not read): one fp32
+ *                 factor per 128 x 128 block of each expert's matrix,
+ *                 [num_experts, ceil(rows / 128), ceil(columns / 128)]
+ *   d_ids, d_weights  [tokens, top_k], contiguous
+ * tokens * top_k <= 8,192 and dim, hidden <= DS_EXPERTS_MAX_WIDTH
+ * (else DS_ERR_TOO_LARGE); num_experts <= 8,192.
+ */
+int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int64_t x_stride, int weight_dtype,
+                   const void* d_w_in, const float* d_w_in_scale, const void* d_w_out, const float* d_w_out_scale,
+                   int num_experts, int64_t hidden, const int32_t* d_ids, const float* d_weights, int top_k,
+                   void* d_y, int64_t y_stride, hipStream_t stream);
 
 /*
  * Copy of nbytes from d_in to d_out with the same launch shape, 16-byte

@@ -1,6 +1,6 @@
 """ctypes binding of libdevscan.so (include/devscan.h).
 
-Argument marshalling only: every step of a scan or compaction runs in the HIP
+Argument marshalling only: every step of a scan, compaction or language-model operator runs in the HIP
 kernels of the library. torch provides device memory and streams. Importing
 this module fails with ImportError when the library has not been built; there
 is no fallback.
@@ -16,7 +16,7 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdevscan.so")
 
 # ds_dtype, ds_cmp, ds_algo, ds_status (include/devscan.h)
-DS_INT32, DS_UINT32, DS_FP32, DS_INT64, DS_UINT64 = range(5)
+DS_INT32, DS_UINT32, DS_FP32, DS_INT64, DS_UINT64, DS_BF16, DS_FP16, DS_FP8_E4M3 = range(8)
 CMP = {"<": 0, "<=": 1, ">": 2, ">=": 3, "==": 4, "!=": 5}
 ALGO = {"default": 0, "lookback": 1, "three_pass": 2, "lookback_blocked": 3}
 DS_OK = 0
@@ -30,7 +30,7 @@ DS_ERR_TOO_LARGE = 7
 DS_ERR_STREAM_CAPTURING = 8
 
 EXPORTS = ["scan_exclusive", "scan_inclusive", "ds_scan", "ds_scan_seeded", "ds_scan_noalloc", "compact_if", "ds_compact_unordered", "ds_radix_pass",
-           "ds_moe_align", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan", "ds_tile_pipeline",
+           "ds_moe_align", "ds_embedding", "ds_embedding_grad", "ds_moe_route", "ds_moe_route_grad", "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan", "ds_tile_pipeline",
            "ds_tile_elems", "ds_scan_tile_elems", "ds_query_timeout", "ds_fail_next_allocations", "ds_set_spin_limit",
            "ds_status_string", "ds_release_workspace", "ds_version"]
 TILE_OF = {"scan_exclusive": 0, "scan_inclusive": 1, "three_pass": 2, "compact": 3, "lds_tile_scan": 4,
@@ -62,6 +62,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ds_radix_pass.restype = I
     L.ds_moe_align.argtypes = [P, I64, I, I, P, P, P, I64, P]
     L.ds_moe_align.restype = I
+    F = ctypes.c_float
+    L.ds_embedding.argtypes = [I, P, I64, I64, I64, P, I, I64, F, P, I64, P]
+    L.ds_embedding.restype = I
+    L.ds_embedding_grad.argtypes = [I, P, I64, P, I, I64, F, I, P, I64, I64, I64, I, P]
+    L.ds_embedding_grad.restype = I
+    L.ds_moe_route.argtypes = [I, P, I64, I, I64, P, I, I, I, F, P, P, P]
+    L.ds_moe_route.restype = I
+    L.ds_moe_route_grad.argtypes = [I, P, I64, I, I64, P, P, I, I, I, F, P, I64, P]
+    L.ds_moe_route_grad.restype = I
+    L.ds_moe_experts.argtypes = [I, P, I64, I64, I64, I, P, P, P, P, I, I64, P, P, I, P, I64, P]
+    L.ds_moe_experts.restype = I
     L.ds_copy.argtypes = [P, P, I64, P]
     L.ds_copy.restype = I
     L.ds_bandwidth_pattern.argtypes = [I, I, I, P, P, I64, P]
@@ -287,6 +298,230 @@ def moe_align(topk_ids: torch.Tensor, num_experts: int, block: int, *, stream=No
         _check(lib.ds_moe_align(topk_ids.data_ptr(), n, num_experts, block, counts.data_ptr(), offsets.data_ptr(),
                                 sorted_ids.data_ptr(), cap, _stream_handle(topk_ids, stream)), "ds_moe_align")
     return counts, offsets, sorted_ids
+
+
+# Language-model operators. Their matrices are 2-D tensors whose rows are contiguous; rows may be any distance apart.
+_FLOATS = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _float_code(x: torch.Tensor, name: str) -> int:
+    code = _FLOATS.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16, not {x.dtype}")
+    return code
+
+
+def _check_rows(x: torch.Tensor, name: str, rows: int | None = None, cols: int | None = None, like=None) -> int:
+    """x is a 2-D GPU tensor with contiguous rows, of the given shape and on like's device; returns its row stride."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if x.dim() != 2 or (rows is not None and x.shape[0] != rows) or (cols is not None and x.shape[1] != cols):
+        raise ValueError(f"{name} must be a matrix of shape [{'*' if rows is None else rows}, "
+                         f"{'*' if cols is None else cols}], not {list(x.shape)}")
+    if like is not None and x.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    n, m = x.shape
+    if m > 1 and x.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if n <= 1 or m == 0:
+        return m
+    if x.stride(0) < m:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return x.stride(0)
+
+
+def _check_flat(x: torch.Tensor, name: str, dtypes, shape, like: torch.Tensor):
+    _check_tensor(x, name)
+    if x.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {x.dtype}")
+    if shape is not None and tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {list(shape)}, not {list(x.shape)}")
+    if x.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+
+
+class _On:
+    """Device and stream of a call: outputs are allocated on the stream that the call runs on, and tensors that belong
+    to another stream are kept from reuse until the call has run."""
+
+    def __init__(self, like: torch.Tensor, stream):
+        self.stream = stream
+        if stream is not None and not hasattr(stream, "cuda_stream"):
+            self.stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        self.device = like.device
+        self.switch = torch.cuda.current_device() != like.device.index
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.before = torch.cuda.stream(self.stream)  # also makes the stream's device current
+            self.before.__enter__()
+            self.handle = self.stream.cuda_stream
+        else:
+            if self.switch:
+                self.before = torch.cuda.device(self.device)
+                self.before.__enter__()
+            self.handle = torch.cuda.current_stream(self.device).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self.stream is not None or self.switch:
+            self.before.__exit__(*exc)
+
+    def uses(self, *tensors):
+        if self.stream is not None:
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
+
+
+def embedding(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """scale * table[ids] (int32 or int64 ids of any shape); a row of zeros where an id is no row of the table.
+    Returns [*ids.shape, dim]; `out`, if given, is a matrix [ids.numel(), dim] and is returned as it is."""
+    code = _float_code(table, "table")
+    stride = _check_rows(table, "table")
+    rows, dim = table.shape
+    _check_flat(ids, "ids", (torch.int32, torch.int64), None, table)
+    n = ids.numel()
+    with _On(table, stream) as on:
+        made = out is None
+        if made:
+            out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
+        out_stride = _check_rows(out, "out", n, dim, table)
+        if out.dtype != table.dtype:
+            raise TypeError("out must have the table's dtype")
+        _check(lib.ds_embedding(code, table.data_ptr(), rows, dim, stride, ids.data_ptr(), ids.element_size(), n,
+                                scale, out.data_ptr(), out_stride, on.handle), "ds_embedding")
+        on.uses(table, ids, out)
+    return out.view(*ids.shape, dim) if made else out
+
+
+def embedding_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: float = 1.0,
+                   dtype: torch.dtype | None = None, out: torch.Tensor | None = None, accumulate: bool = False,
+                   stream=None) -> torch.Tensor:
+    """The gradient of embedding's table [rows, dim] from the gradient dout of its output ([*ids.shape, dim], or
+    [ids.numel(), dim] with rows any distance apart). `dtype` is dout's (the default) or float32. accumulate: the sums
+    are added to `out`; otherwise every row is written, into `out` if it is given."""
+    if not isinstance(dout, torch.Tensor) or dout.dim() < 1:
+        raise ValueError("dout must be a GPU tensor")
+    if dout.dim() != 2:
+        if dout.shape[:-1] != ids.shape or not dout.is_contiguous():
+            raise ValueError("dout must be a matrix, or contiguous of shape [*ids.shape, dim]")
+        dout = dout.view(ids.numel(), dout.shape[-1])
+    code = _float_code(dout, "dout")
+    stride = _check_rows(dout, "dout", ids.numel())
+    n, dim = dout.shape
+    _check_flat(ids, "ids", (torch.int32, torch.int64), None, dout)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if dtype is None:
+        dtype = dout.dtype if out is None else out.dtype
+    if dtype not in (dout.dtype, torch.float32):
+        raise TypeError("the gradient's dtype must be dout's or float32")
+    with _On(dout, stream) as on:
+        if out is None:
+            out = torch.empty((rows, dim), dtype=dtype, device=dout.device)
+        grad_stride = _check_rows(out, "out", rows, dim, dout)
+        if out.dtype != dtype:
+            raise TypeError(f"out must be {dtype}")
+        _check(lib.ds_embedding_grad(code, dout.data_ptr(), stride, ids.data_ptr(), ids.element_size(), n, scale,
+                                     _FLOATS[dtype], out.data_ptr(), rows, dim, grad_stride, int(bool(accumulate)),
+                                     on.handle), "ds_embedding_grad")
+        on.uses(dout, ids, out)
+    return out
+
+
+def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
+              renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Each token's top_k experts by logit (+ bias, float32 [experts], for the choice alone), ties to the lower index;
+    returns (weights float32, ids int32), both [tokens, top_k], best first. weights = scale * score, where score is
+    "softmax" over the experts that can be chosen or "sigmoid", with renormalize divided by its sum over the chosen.
+    Experts at -inf or NaN cannot be chosen; where fewer than top_k can, the rest is id -1 with weight 0."""
+    code = _float_code(logits, "logits")
+    stride = _check_rows(logits, "logits")
+    tokens, experts = logits.shape
+    if bias is not None:
+        _check_flat(bias, "bias", (torch.float32,), (experts,), logits)
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {list(SCORES)}")
+    if not 1 <= top_k <= experts:
+        raise ValueError("top_k must be between 1 and the number of experts")
+    with _On(logits, stream) as on:
+        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
+        ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
+        _check(lib.ds_moe_route(code, logits.data_ptr(), tokens, experts, stride,
+                                None if bias is None else bias.data_ptr(), top_k, SCORES[score],
+                                int(bool(renormalize)), scale, weights.data_ptr(), ids.data_ptr(), on.handle),
+               "ds_moe_route")
+        on.uses(logits, bias, weights, ids)
+    return weights, ids
+
+
+def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, *, score: str = "softmax",
+                   renormalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+    """The gradient of moe_route's weights with respect to its logits, from the ids it chose and the gradient dweights
+    (float32 [tokens, top_k]) of the weights; in the logits' dtype."""
+    code = _float_code(logits, "logits")
+    stride = _check_rows(logits, "logits")
+    tokens, experts = logits.shape
+    if ids.dim() != 2:
+        raise ValueError("ids must be [tokens, top_k]")
+    top_k = ids.shape[1]
+    _check_flat(ids, "ids", (torch.int32,), (tokens, top_k), logits)
+    _check_flat(dweights, "dweights", (torch.float32,), (tokens, top_k), logits)
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {list(SCORES)}")
+    with _On(logits, stream) as on:
+        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
+        _check(lib.ds_moe_route_grad(code, logits.data_ptr(), tokens, experts, stride, ids.data_ptr(),
+                                     dweights.data_ptr(), top_k, SCORES[score], int(bool(renormalize)), scale,
+                                     dlogits.data_ptr(), experts, on.handle), "ds_moe_route_grad")
+        on.uses(logits, ids, dweights, dlogits)
+    return dlogits
+
+
+def moe_experts(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, *,
+                w_in_scale: torch.Tensor | None = None, w_out_scale: torch.Tensor | None = None,
+                out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The experts of a mixture-of-experts layer for a few tokens (tokens * top_k <= 8192): for each token the sum over
+    its choices e = ids[t, j] of weights[t, j] * w_out[e] @ (silu(gate) * up), where gate and up are the first and
+    second half of w_in[e] @ x[t]. x [tokens, dim] bfloat16 or float16; w_in [experts, 2 * hidden, dim] and w_out
+    [experts, dim, hidden] in x's dtype, or float8_e4m3fn with a float32 scale for every block of 128 x 128
+    ([experts, ceil(rows / 128), ceil(columns / 128)]); ids int32, weights float32 [tokens, top_k]. Choices outside
+    [0, experts) are left out."""
+    if _float_code(x, "x") == DS_FP32:
+        raise TypeError("x must be bfloat16 or float16")
+    x_stride = _check_rows(x, "x")
+    tokens, dim = x.shape
+    if w_in.dim() != 3 or w_in.shape[1] % 2 or ids.dim() != 2:
+        raise ValueError("w_in must be [experts, 2 * hidden, dim] and ids [tokens, top_k]")
+    experts, hidden, top_k = w_in.shape[0], w_in.shape[1] // 2, ids.shape[1]
+    eight = w_in.dtype == torch.float8_e4m3fn
+    kinds = (torch.float8_e4m3fn,) if eight else (x.dtype,)
+    _check_flat(w_in, "w_in", kinds, (experts, 2 * hidden, dim), x)
+    _check_flat(w_out, "w_out", kinds, (experts, dim, hidden), x)
+    if eight != (w_in_scale is not None) or eight != (w_out_scale is not None):
+        raise ValueError("8-bit weights, and only they, need w_in_scale and w_out_scale")
+    if eight:
+        blocks = [-(-v // 128) for v in (2 * hidden, dim, hidden)]
+        _check_flat(w_in_scale, "w_in_scale", (torch.float32,), (experts, blocks[0], blocks[1]), x)
+        _check_flat(w_out_scale, "w_out_scale", (torch.float32,), (experts, blocks[1], blocks[2]), x)
+    _check_flat(ids, "ids", (torch.int32,), (tokens, top_k), x)
+    _check_flat(weights, "weights", (torch.float32,), (tokens, top_k), x)
+    with _On(x, stream) as on:
+        if out is None:
+            out = torch.empty((tokens, dim), dtype=x.dtype, device=x.device)
+        y_stride = _check_rows(out, "out", tokens, dim, x)
+        if out.dtype != x.dtype:
+            raise TypeError("out must have x's dtype")
+        _check(lib.ds_moe_experts(_FLOATS[x.dtype], x.data_ptr(), tokens, dim, x_stride,
+                                  DS_FP8_E4M3 if eight else _FLOATS[x.dtype], w_in.data_ptr(),
+                                  w_in_scale.data_ptr() if eight else None, w_out.data_ptr(),
+                                  w_out_scale.data_ptr() if eight else None, experts, hidden, ids.data_ptr(),
+                                  weights.data_ptr(), top_k, out.data_ptr(), y_stride, on.handle), "ds_moe_experts")
+        on.uses(x, w_in, w_out, w_in_scale, w_out_scale, ids, weights, out)
+    return out
 
 
 def copy(src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> torch.Tensor:

@@ -7,6 +7,7 @@
 #include <map>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "devscan.h"
 #include "launch.hpp"
@@ -35,6 +36,8 @@ struct Workspace {
     uint64_t lookback_launches = 0;  // launches that stamped an epoch since the last clear
     char* aux = nullptr;
     size_t aux_cap = 0;
+    bool aux_captured = false;    // some graph holds the address of aux
+    std::vector<char*> retired;   // earlier aux buffers that graphs hold, freed by ds_release_workspace
 };
 
 std::mutex g_mu;
@@ -137,17 +140,21 @@ int get_aux(hipStream_t stream, size_t bytes, char** out)
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return DS_ERR_HIP;
     Workspace& w = g_ws[{dev, stream}];
+    const bool recording = capturing(stream);
     if (w.aux_cap < bytes) {
-        if (capturing(stream)) return DS_ERR_STREAM_CAPTURING;
+        if (recording) return DS_ERR_STREAM_CAPTURING;
         size_t cap = w.aux_cap * 2 > bytes ? w.aux_cap * 2 : bytes;
         if (cap < ((size_t)1 << 20)) cap = (size_t)1 << 20;
         if (refuse_allocation()) return DS_ERR_OUT_OF_MEMORY;
-        if (w.aux) {
+        if (w.aux && w.aux_captured) {
+            w.retired.push_back(w.aux);  // a replay may still write to it
+        } else if (w.aux) {
             if (hipStreamSynchronize(stream) != hipSuccess) return DS_ERR_HIP;
             (void)hipFree(w.aux);
-            w.aux = nullptr;
-            w.aux_cap = 0;
         }
+        w.aux = nullptr;
+        w.aux_cap = 0;
+        w.aux_captured = false;
         void* p = nullptr;
         if (hipMalloc(&p, cap) != hipSuccess) {
             (void)hipGetLastError();
@@ -156,6 +163,7 @@ int get_aux(hipStream_t stream, size_t bytes, char** out)
         w.aux = static_cast<char*>(p);
         w.aux_cap = cap;
     }
+    w.aux_captured |= recording;
     *out = w.aux;
     return DS_OK;
 }
@@ -610,6 +618,191 @@ int ds_moe_align(const int32_t* d_topk_ids, int64_t n, int num_experts, int bloc
     return e == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
 
+// Language-model operators. Their matrices are rows of contiguous elements,
+// `stride` elements apart.
+static int float_bytes(int dtype) { return dtype == DS_FP32 ? 4 : dtype == DS_BF16 || dtype == DS_FP16 ? 2 : 0; }
+
+static ds::ElemKind float_kind(int dtype)
+{
+    return dtype == DS_FP32 ? ds::kF32 : dtype == DS_BF16 ? ds::kBF16 : ds::kF16;
+}
+
+// Bytes from the first to the last element of a matrix; -1 past what a pointer can address.
+static int64_t span_bytes(int64_t rows, int64_t cols, int64_t stride, int esz)
+{
+    if (rows <= 0 || cols <= 0) return 0;
+    const __int128 b = ((__int128)(rows - 1) * stride + cols) * esz;
+    return b > ((__int128)1 << 56) ? -1 : (int64_t)b;
+}
+
+struct Buf {
+    const void* p;
+    int64_t bytes;  // 0: not used
+    int align;
+    bool written;
+};
+
+// Every buffer in use is there, aligned, and no written one overlaps another.
+static int check_buffers(const Buf* b, int count)
+{
+    for (int i = 0; i < count; ++i) {
+        if (b[i].bytes < 0) return DS_ERR_TOO_LARGE;
+        if (b[i].bytes && !b[i].p) return DS_ERR_INVALID_VALUE;
+    }
+    for (int i = 0; i < count; ++i)
+        if (b[i].bytes && (uintptr_t)b[i].p % b[i].align) return DS_ERR_MISALIGNED;
+    for (int i = 0; i < count; ++i)
+        for (int j = i + 1; j < count; ++j)
+            if ((b[i].written || b[j].written) && overlaps(b[i].p, (size_t)b[i].bytes, b[j].p, (size_t)b[j].bytes))
+                return DS_ERR_OVERLAP;
+    return DS_OK;
+}
+
+int ds_embedding(int dtype, const void* d_table, int64_t rows, int64_t dim, int64_t table_stride, const void* d_ids,
+                 int id_bytes, int64_t n, float scale, void* d_out, int64_t out_stride, hipStream_t stream)
+{
+    const int esz = float_bytes(dtype);
+    if (!esz) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || dim < 0 || n < 0 || table_stride < dim || out_stride < dim || (id_bytes != 4 && id_bytes != 8))
+        return DS_ERR_INVALID_VALUE;
+    if (n == 0 || dim == 0) return DS_OK;
+    if (n >= ((int64_t)1 << 40) || dim >= ((int64_t)1 << 40)) return DS_ERR_TOO_LARGE;
+    const Buf bufs[3] = {{d_table, span_bytes(rows, dim, table_stride, esz), esz, false},
+                         {d_ids, n * id_bytes, id_bytes, false},
+                         {d_out, span_bytes(n, dim, out_stride, esz), esz, true}};
+    const int st = check_buffers(bufs, 3);
+    if (st != DS_OK) return st;
+    if (ds::embedding_blocks(float_kind(dtype), n, dim) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    return ds::launch_embedding(float_kind(dtype), d_table, rows, dim, table_stride, d_ids, id_bytes == 8, n, scale,
+                                d_out, out_stride, stream) == hipSuccess
+               ? DS_OK
+               : DS_ERR_HIP;
+}
+
+int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const void* d_ids, int id_bytes, int64_t n,
+                      float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim, int64_t grad_stride,
+                      int accumulate, hipStream_t stream)
+{
+    const int esz = float_bytes(dtype), gsz = float_bytes(grad_dtype);
+    if (!esz || !gsz || (grad_dtype != dtype && grad_dtype != DS_FP32)) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || dim < 0 || n < 0 || dout_stride < dim || grad_stride < dim || (id_bytes != 4 && id_bytes != 8) ||
+        (accumulate != 0 && accumulate != 1))
+        return DS_ERR_INVALID_VALUE;
+    if (rows == 0 || dim == 0 || (n == 0 && accumulate)) return DS_OK;
+    if (n >= ((int64_t)1 << 31) || dim >= ((int64_t)1 << 31) || rows > ds::embedding_most_rows())
+        return DS_ERR_TOO_LARGE;
+    const Buf bufs[3] = {{d_dout, span_bytes(n, dim, dout_stride, esz), esz, false},
+                         {d_ids, n * id_bytes, id_bytes, false},
+                         {d_grad, span_bytes(rows, dim, grad_stride, gsz), gsz, true}};
+    int st = check_buffers(bufs, 3);
+    if (st != DS_OK) return st;
+    const ds::EmbeddingGradPlan plan = ds::embedding_grad_plan(float_kind(dtype), n, rows, dim);
+    if (plan.chunks * plan.slabs / 4 >= kMaxTiles || n / 256 >= kMaxTiles) return DS_ERR_TOO_LARGE;
+    std::lock_guard<std::mutex> lock(g_mu);
+    char* aux = nullptr;
+    DevWs dws{nullptr, nullptr, nullptr};
+    Workspace* w = nullptr;
+    if (n > 0) {
+        st = get_aux(stream, (size_t)plan.bytes, &aux);
+        if (st != DS_OK) return st;
+        st = scan_workspace_u32(stream, plan.table_words, &dws, &w);
+        if (st != DS_OK) return st;
+    }
+    const hipError_t e = ds::launch_embedding_grad(float_kind(dtype), float_kind(grad_dtype), plan, d_dout,
+                                                   dout_stride, d_ids, id_bytes == 8, n, rows, dim, scale, d_grad,
+                                                   grad_stride, accumulate != 0, aux, dws, g_spin_limit, stream);
+    if (w) w->lookback_launches += (uint64_t)plan.digits;
+    return e == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
+static int check_route(int dtype, int64_t tokens, int num_experts, int64_t stride, int top_k, int score,
+                       int renormalize)
+{
+    if (!float_bytes(dtype)) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (tokens < 0 || num_experts < 1 || num_experts > ds::route_max_experts() || stride < num_experts || top_k < 1 ||
+        top_k > num_experts || top_k > DS_ROUTE_MAX_TOP_K || score < DS_SCORE_SOFTMAX || score > DS_SCORE_SIGMOID ||
+        (renormalize != 0 && renormalize != 1))
+        return DS_ERR_INVALID_VALUE;
+    return ds::route_blocks(tokens) > kMaxTiles ? DS_ERR_TOO_LARGE : DS_OK;
+}
+
+int ds_moe_route(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
+                 const float* d_bias, int top_k, int score, int renormalize, float scale, float* d_weights,
+                 int32_t* d_ids, hipStream_t stream)
+{
+    int st = check_route(dtype, tokens, num_experts, stride, top_k, score, renormalize);
+    if (st != DS_OK || tokens == 0) return st;
+    const int esz = float_bytes(dtype);
+    const Buf bufs[4] = {{d_logits, span_bytes(tokens, num_experts, stride, esz), esz, false},
+                         {d_bias, d_bias ? (int64_t)num_experts * 4 : 0, 4, false},
+                         {d_weights, tokens * top_k * 4, 4, true},
+                         {d_ids, tokens * top_k * 4, 4, true}};
+    st = check_buffers(bufs, 4);
+    if (st != DS_OK) return st;
+    const ds::RouteArgs a{tokens, stride, num_experts, top_k, score == DS_SCORE_SIGMOID, renormalize != 0, scale};
+    return ds::launch_moe_route(float_kind(dtype), a, d_logits, d_bias, d_weights, d_ids, stream) == hipSuccess
+               ? DS_OK
+               : DS_ERR_HIP;
+}
+
+int ds_moe_route_grad(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
+                      const int32_t* d_ids, const float* d_dweights, int top_k, int score, int renormalize,
+                      float scale, void* d_dlogits, int64_t dlogits_stride, hipStream_t stream)
+{
+    int st = check_route(dtype, tokens, num_experts, stride, top_k, score, renormalize);
+    if (st == DS_OK && dlogits_stride < num_experts) st = DS_ERR_INVALID_VALUE;
+    if (st != DS_OK || tokens == 0) return st;
+    const int esz = float_bytes(dtype);
+    const Buf bufs[4] = {{d_logits, span_bytes(tokens, num_experts, stride, esz), esz, false},
+                         {d_ids, tokens * top_k * 4, 4, false},
+                         {d_dweights, tokens * top_k * 4, 4, false},
+                         {d_dlogits, span_bytes(tokens, num_experts, dlogits_stride, esz), esz, true}};
+    st = check_buffers(bufs, 4);
+    if (st != DS_OK) return st;
+    const ds::RouteArgs a{tokens, stride, num_experts, top_k, score == DS_SCORE_SIGMOID, renormalize != 0, scale};
+    return ds::launch_moe_route_grad(float_kind(dtype), a, d_logits, d_ids, d_dweights, d_dlogits, dlogits_stride,
+                                     stream) == hipSuccess
+               ? DS_OK
+               : DS_ERR_HIP;
+}
+
+int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int64_t x_stride, int weight_dtype,
+                   const void* d_w_in, const float* d_w_in_scale, const void* d_w_out, const float* d_w_out_scale,
+                   int num_experts, int64_t hidden, const int32_t* d_ids, const float* d_weights, int top_k,
+                   void* d_y, int64_t y_stride, hipStream_t stream)
+{
+    if (dtype != DS_BF16 && dtype != DS_FP16) return DS_ERR_UNSUPPORTED_DTYPE;
+    const bool eight = weight_dtype == DS_FP8_E4M3;
+    if (weight_dtype != dtype && !eight) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (tokens < 0 || dim < 1 || hidden < 1 || num_experts < 1 || num_experts > ds::experts_max_experts() ||
+        top_k < 1 || x_stride < dim || y_stride < dim)
+        return DS_ERR_INVALID_VALUE;
+    if (tokens == 0) return DS_OK;
+    if (dim > DS_EXPERTS_MAX_WIDTH || hidden > DS_EXPERTS_MAX_WIDTH || tokens > ds::experts_max_assignments() ||
+        tokens * top_k > ds::experts_max_assignments())
+        return DS_ERR_TOO_LARGE;
+    const int64_t n = tokens * top_k, E = num_experts, wsz = eight ? 1 : 2;
+    const auto blocks = [](int64_t v) { return (v + 127) / 128; };
+    const Buf bufs[8] = {
+        {d_x, span_bytes(tokens, dim, x_stride, 2), 2, false},
+        {d_w_in, E * 2 * hidden * dim * wsz, (int)wsz, false},
+        {d_w_out, E * hidden * dim * wsz, (int)wsz, false},
+        {d_w_in_scale, eight ? E * blocks(2 * hidden) * blocks(dim) * 4 : 0, 4, false},
+        {d_w_out_scale, eight ? E * blocks(dim) * blocks(hidden) * 4 : 0, 4, false},
+        {d_ids, n * 4, 4, false},
+        {d_weights, n * 4, 4, false},
+        {d_y, span_bytes(tokens, dim, y_stride, 2), 2, true}};
+    int st = check_buffers(bufs, 8);
+    if (st != DS_OK) return st;
+    std::lock_guard<std::mutex> lock(g_mu);
+    char* aux = nullptr;
+    st = get_aux(stream, (size_t)ds::experts_aux_bytes(n, (int)dim, (int)hidden), &aux);
+    if (st != DS_OK) return st;
+    const ds::ExpertsCall call{tokens, (int)dim, (int)hidden, num_experts, top_k, d_x, x_stride, d_w_in, d_w_out,
+                               d_w_in_scale, d_w_out_scale, d_ids, d_weights, d_y, y_stride};
+    return ds::launch_moe_experts(float_kind(dtype), eight, call, aux, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
 void ds_release_workspace(void)
 {
     std::lock_guard<std::mutex> lock(g_mu);
@@ -617,6 +810,7 @@ void ds_release_workspace(void)
     for (auto& kv : g_ws) {
         if (kv.second.base) (void)hipFree(kv.second.base);
         if (kv.second.aux) (void)hipFree(kv.second.aux);
+        for (char* p : kv.second.retired) (void)hipFree(p);
     }
     g_ws.clear();
 }

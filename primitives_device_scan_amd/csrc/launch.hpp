@@ -16,7 +16,7 @@ struct DevWs {
     void* totals;        // 8 bytes per tile (three-pass tile totals)
 };
 
-enum ElemKind { kU32 = 0, kF32 = 1, kU64 = 2, kI32 = 3, kI64 = 4 };
+enum ElemKind { kU32 = 0, kF32 = 1, kU64 = 2, kI32 = 3, kI64 = 4, kBF16 = 5, kF16 = 6 };
 
 int64_t tile_elems(ElemKind kind, bool inclusive, int64_t n);  // look-back scan tile for n elements
 int64_t three_pass_tile_elems(int elem_bytes);  // three-pass scan tile
@@ -83,6 +83,69 @@ struct MoeOut {
 // hist, slots: experts * tiles 32-bit words each of scratch.
 hipError_t launch_moe_align(const int32_t* ids, int64_t n, int experts, const MoeOut& out, uint32_t* hist,
                             uint32_t* slots, const DevWs& ws, uint32_t spin_limit, hipStream_t stream);
+
+// One stable key-value pass over digits (key >> shift) & 511 that are all below
+// `buckets` (<= sort_max_buckets()), in tiles of moe_tile_elems() keys; table:
+// sort_pass_words() 32-bit words of scratch; ws: look-back workspace for a
+// scan of that many words.
+int64_t sort_pass_words(int64_t n, uint32_t buckets);
+hipError_t launch_sort_pass(const uint32_t* keys, const uint32_t* vals_in, uint32_t* keys_out, uint32_t* vals_out,
+                            int64_t n, int shift, uint32_t buckets, uint32_t* table, const DevWs& ws,
+                            uint32_t spin_limit, hipStream_t stream);
+
+// Token embedding and the gradient of its table (float kinds).
+int64_t embedding_blocks(ElemKind kind, int64_t n, int64_t dim);  // workgroups of a lookup
+hipError_t launch_embedding(ElemKind kind, const void* table, int64_t rows, int64_t dim, int64_t table_stride,
+                            const void* ids, bool wide_ids, int64_t n, float scale, void* out, int64_t out_stride,
+                            hipStream_t stream);
+
+struct EmbeddingGradPlan {
+    uint32_t base;           // counting-sort digits are below this; 0 with digits == 0
+    int digits;              // counting-sort passes; 0: one launch sorts by rank
+    int chunk;               // sorted positions per wave
+    int64_t slabs, chunks;   // units of work: slabs x chunks
+    int64_t partial_stride;  // elements between rows of the crossing runs' parts
+    int64_t table_words;     // the passes' table, 32-bit words at the start of the scratch
+    int64_t partial_at;      // byte offset of the parts
+    int64_t bytes;           // scratch in all
+};
+EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, int64_t dim);
+int64_t embedding_most_rows();  // rows that the passes' digits can tell apart
+hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& plan, const void* dout,
+                                 int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
+                                 int64_t dim, float scale, void* grad, int64_t grad_stride, bool add, char* aux,
+                                 const DevWs& ws, uint32_t spin_limit, hipStream_t stream);
+
+// Mixture-of-experts router (float kinds) and experts (16-bit kinds).
+struct RouteArgs {
+    int64_t tokens, stride;  // stride: elements between rows of the logits
+    int experts, top_k;
+    bool use_sigmoid, renorm;
+    float scale;
+};
+int route_max_experts();
+int64_t route_blocks(int64_t tokens);
+hipError_t launch_moe_route(ElemKind kind, const RouteArgs& a, const void* logits, const float* bias, float* weights,
+                            int32_t* ids, hipStream_t stream);
+hipError_t launch_moe_route_grad(ElemKind kind, const RouteArgs& a, const void* logits, const int32_t* ids,
+                                 const float* dweights, void* dlogits, int64_t dstride, hipStream_t stream);
+
+struct ExpertsCall {
+    int64_t tokens;
+    int dim, hidden, experts, top_k;
+    const void* x;
+    int64_t x_stride;
+    const void *w_in, *w_out;
+    const float *w_in_scale, *w_out_scale;
+    const int32_t* ids;
+    const float* weights;
+    void* y;
+    int64_t y_stride;
+};
+int64_t experts_max_assignments();
+int experts_max_experts();
+int64_t experts_aux_bytes(int64_t n, int dim, int hidden);  // scratch for n assignments
+hipError_t launch_moe_experts(ElemKind kind, bool eight_bit, const ExpertsCall& call, char* aux, hipStream_t stream);
 
 // Exclusive scan of `count` tile totals in place (one workgroup, carried sum).
 hipError_t launch_scan_totals(ElemKind kind, void* totals, int64_t count, hipStream_t stream);
