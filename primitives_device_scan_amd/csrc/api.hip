@@ -794,12 +794,13 @@ int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int6
         {d_y, span_bytes(tokens, dim, y_stride, 2), 2, true}};
     int st = check_buffers(bufs, 8);
     if (st != DS_OK) return st;
-    std::lock_guard<std::mutex> lock(g_mu);
-    char* aux = nullptr;
-    st = get_aux(stream, (size_t)ds::experts_aux_bytes(n, (int)dim, (int)hidden), &aux);
-    if (st != DS_OK) return st;
     const ds::ExpertsCall call{tokens, (int)dim, (int)hidden, num_experts, top_k, d_x, x_stride, d_w_in, d_w_out,
                                d_w_in_scale, d_w_out_scale, d_ids, d_weights, d_y, y_stride};
+    if (ds::experts_workgroups(eight, call) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    std::lock_guard<std::mutex> lock(g_mu);
+    char* aux = nullptr;
+    st = get_aux(stream, (size_t)ds::experts_aux_bytes(n, num_experts, (int)dim, (int)hidden, eight), &aux);
+    if (st != DS_OK) return st;
     return ds::launch_moe_experts(float_kind(dtype), eight, call, aux, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
 

@@ -67,231 +67,484 @@ __device__ __forceinline__ typename Frag<X>::type widen8(uint32_t lo, uint32_t h
     return r.v;
 }
 
-// A step covers 64 of the depth: lane l of a wave holds row (A) or token (B)
-// l % 16, depth (l / 16) * 16 .. + 15 of the step, as two fragments of 8. Both
-// operands use this order, so the products pair up; a row's 128 bytes (64 in
-// 8 bits) are then read by four lanes side by side.
-constexpr int kStep = 64;
-constexpr int kLaneDepth = 16;
+// ---------------------------------------------------------------------------
+// One wave multiplies RT row tiles of 16 rows by TT blocks of 16 tokens. It
+// takes the weights in stages of 8 KiB: 16 * RT rows by kSegs segments of 16
+// bytes (RT 4: 128 bytes of each of 64 rows; RT 2: 256 bytes of each of 32).
+//
+// In both operands lane l holds row (A) or token (B) l % 16. With s = 4 j +
+// l / 16 the segment that lane l reads at its j-th read of a stage, the lane's
+// values are those at depths s * kSegVals .. + kSegVals - 1 of the stage, one
+// fragment of 8 (16-bit weights) or two (8-bit). Both operands use this order,
+// so the products pair up.
+// ---------------------------------------------------------------------------
+constexpr int kStageBytes = 8192;
+constexpr int kRing = 2;  // stages of a wave in LDS
+constexpr int kDmaOps = kStageBytes / (kWave * kVecBytes);
 
-// One lane's 16 values of a step, as loaded (16-bit types: two 16-byte
-// vectors; 8-bit: one).
-template <typename W> struct StepRegs {
-    u32x4 v[kLaneDepth * sizeof(W) / 16];
+template <typename W, int RT> struct Stage {
+    static constexpr int kRows = 16 * RT;
+    static constexpr int kSegs = kStageBytes / (kRows * kVecBytes);  // per row: 8 or 16
+    static constexpr int kSegVals = kVecBytes / (int)sizeof(W);
+    static constexpr int kDepth = kSegs * kSegVals;
+    static constexpr int kReads = kSegs / 4;        // per tile and lane
+    static constexpr int kFrags = kSegVals / 8;     // per read
 };
 
-template <typename W>
-__device__ __forceinline__ StepRegs<W> load_step(const W* __restrict__ p)
-{
-    StepRegs<W> r;
-    constexpr int kN = kLaneDepth * sizeof(W) / 16;
-    const typename Vec16<W>::type* q = reinterpret_cast<const typename Vec16<W>::type*>(p);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) r.v[i] = q[i];
-    return r;
-}
-
-// The same for the step at the end of the depth: values past `valid` are 0.
-template <typename W>
-__device__ __forceinline__ StepRegs<W> load_step_tail(const W* __restrict__ p, int valid)
-{
-    union {
-        StepRegs<W> r;
-        W w[kLaneDepth];
-    } u;
-    __builtin_memset(&u, 0, sizeof(u));
-#pragma unroll
-    for (int i = 0; i < kLaneDepth; ++i)
-        if (i < valid) u.w[i] = p[i];
-    return u.r;
-}
+template <typename W, int RT> struct ARegs {
+    u32x4 v[RT][Stage<W, RT>::kReads];
+};
+template <typename W, int RT, int TT> struct BRegs {
+    u32x4 v[TT][Stage<W, RT>::kReads][Stage<W, RT>::kFrags];
+};
 
 template <typename X, typename W>
-__device__ __forceinline__ typename Frag<X>::type fragment(const StepRegs<W>& r, int half)
+__device__ __forceinline__ typename Frag<X>::type a_fragment(const u32x4& v, int f)
 {
     if constexpr (sizeof(W) == 1)
-        return widen8<X>(r.v[0][half * 2], r.v[0][half * 2 + 1]);
+        return widen8<X>(v[f * 2], v[f * 2 + 1]);
     else
-        return __builtin_bit_cast(typename Frag<X>::type, r.v[half]);
+        return __builtin_bit_cast(typename Frag<X>::type, v);
 }
 
-// Products of two 16-row tiles with TT blocks of 16 tokens, over the depth
-// [k0, k1): acc[tile][block]. `rows`: this lane's row of each tile; `tok`:
-// this lane's token row of each block. k0 is a multiple of 128; `scale`:
-// null, or this lane's scales, for its four output rows of each tile, of the
-// first block of 128 of the depth; the next block's are one element on.
-template <typename X, typename W, int TT>
-__device__ __forceinline__ void product(const W* const (&rows)[2], const X* const (&tok)[TT],
-                                        const float* const (&scale)[2][4], int k0, int k1, int lane,
-                                        f32x4 (&acc)[2][TT])
+// This lane's values of the token blocks; `valid`: segments of the stage that
+// lie below the end of the depth (the others are 0).
+template <typename X, typename W, int RT, int TT>
+__device__ __forceinline__ void load_b(const X* const (&tok)[TT], int64_t depth0, int lane, BRegs<W, RT, TT>& b)
 {
-    const int off = lane / 16 * kLaneDepth;
+    using S = Stage<W, RT>;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-        for (int b = 0; b < TT; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kBlock = 2 * kStep;  // 128 deep
-    for (int k = k0; k < k1; k += kBlock) {
-        f32x4 sum[2][TT];
+        for (int j = 0; j < S::kReads; ++j)
+#pragma unroll
+            for (int f = 0; f < S::kFrags; ++f)
+                b.v[t][j][f] = *reinterpret_cast<const typename Vec16<X>::type*>(
+                    tok[t] + depth0 + (4 * j + lane / 16) * S::kSegVals + f * 8);
+}
+
+// The same at the end of the depth: of the stage's values the first `valid` are there, the others are 0.
+template <typename X, typename W, int RT, int TT>
+__device__ __forceinline__ void load_b_tail(const X* const (&tok)[TT], int64_t depth0, int valid, int lane,
+                                            BRegs<W, RT, TT>& b)
+{
+    using S = Stage<W, RT>;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < S::kReads; ++j)
+#pragma unroll
+            for (int f = 0; f < S::kFrags; ++f) {
+                const int at = (4 * j + lane / 16) * S::kSegVals + f * 8;
+                X x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = at + i < valid ? tok[t][depth0 + at + i] : (X)0.0f;
+                __builtin_memcpy(&b.v[t][j][f], x, sizeof(x));
+            }
+}
+
+// Scales of a wave's tiles for 8-bit weights, by block of 128 of the depth.
+// Tiles that begin at multiples of 16 rows lie inside one block of 128 rows
+// and have one factor (UNIFORM); else each of a lane's four rows has its own.
+template <int RT, bool UNIFORM> struct Scales {
+    const float* base;                  // of the expert
+    int64_t row[RT][UNIFORM ? 1 : 4];   // of the depth's first block
+    __device__ __forceinline__ float at(int r, int i, int blk) const { return base[row[r][UNIFORM ? 0 : i] + blk]; }
+};
+
+// acc += the products of one stage. blk0: block of 128 of the depth that the
+// stage begins in, last_blk: the depth's last one (8-bit weights, whose stages
+// are one or two whole blocks; the last stage may have only its first).
+template <typename X, typename W, int RT, int TT, bool UNIFORM>
+__device__ __forceinline__ void multiply(const ARegs<W, RT>& a, const BRegs<W, RT, TT>& b,
+                                         const Scales<RT, UNIFORM>& sc, int blk0, int last_blk,
+                                         f32x4 (&acc)[RT][TT])
+{
+    using S = Stage<W, RT>;
+    constexpr int kPerBlock = sizeof(W) == 1 ? 2 : S::kReads;  // reads per block of 128 (8-bit)
+#pragma unroll
+    for (int j0 = 0; j0 < S::kReads; j0 += kPerBlock) {
+        f32x4 sum[RT][TT];
         if constexpr (sizeof(W) == 1) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int b = 0; b < TT; ++b) sum[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        StepRegs<W> a[2][2];
-        StepRegs<X> x[2][TT];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int at = k + s * kStep + off, valid = k1 - at;
-            if (k + (s + 1) * kStep <= k1) {  // uniform
-#pragma unroll
-                for (int r = 0; r < 2; ++r) a[s][r] = load_step<W>(rows[r] + at);
-#pragma unroll
-                for (int b = 0; b < TT; ++b) x[s][b] = load_step<X>(tok[b] + at);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 2; ++r) a[s][r] = load_step_tail<W>(rows[r] + at, valid);
-#pragma unroll
-                for (int b = 0; b < TT; ++b) x[s][b] = load_step_tail<X>(tok[b] + at, valid);
-            }
+                for (int t = 0; t < TT; ++t) sum[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int j = j0; j < j0 + kPerBlock; ++j)
 #pragma unroll
-            for (int half = 0; half < 2; ++half)
+            for (int f = 0; f < S::kFrags; ++f)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const typename Frag<X>::type af = fragment<X, W>(a[s][r], half);
+                for (int r = 0; r < RT; ++r) {
+                    const typename Frag<X>::type af = a_fragment<X, W>(a.v[r][j], f);
 #pragma unroll
-                    for (int b = 0; b < TT; ++b) {
-                        const typename Frag<X>::type bf = fragment<X, X>(x[s][b], half);
+                    for (int t = 0; t < TT; ++t) {
+                        const typename Frag<X>::type bf = __builtin_bit_cast(typename Frag<X>::type, b.v[t][j][f]);
                         if constexpr (sizeof(W) == 1)
-                            sum[r][b] = Frag<X>::mma(af, bf, sum[r][b]);
+                            sum[r][t] = Frag<X>::mma(af, bf, sum[r][t]);
                         else
-                            acc[r][b] = Frag<X>::mma(af, bf, acc[r][b]);
+                            acc[r][t] = Frag<X>::mma(af, bf, acc[r][t]);
                     }
                 }
         if constexpr (sizeof(W) == 1) {
+            const int blk = blk0 + j0 / kPerBlock < last_blk ? blk0 + j0 / kPerBlock : last_blk;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                f32x4 sc;
+            for (int r = 0; r < RT; ++r) {
+                f32x4 s;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[i] = scale[r][i][(k - k0) / kBlock];
+                for (int i = 0; i < 4; ++i) s[i] = sc.at(r, i, blk);
 #pragma unroll
-                for (int b = 0; b < TT; ++b) acc[r][b] += sc * sum[r][b];
+                for (int t = 0; t < TT; ++t) acc[r][t] += s * sum[r][t];
             }
         }
     }
 }
 
-// Which expert a workgroup serves, and that expert's assignments, found in
-// the ids by the workgroup itself. With at least as many slots as experts,
-// slot s is expert s; with fewer (few assignments), slot s is the s-th expert
-// that any assignment names.
+// ---------------------------------------------------------------------------
+// Weights through LDS, for rows that start on 16-byte boundaries. Each wave
+// owns a ring of two stages, filled by loads that write LDS directly: no
+// registers are held by data in flight (16 KiB a wave, 128 KiB a CU), and the
+// lanes of a load take whole 128-byte lines, eight lanes to a line, which the
+// operand layout (16 rows side by side) does not give. Non-temporal: a weight
+// is read once. Row r keeps its segments in the order c ^ (r % 8), so that
+// eight rows' equal segments, which are read together, lie in different banks.
+//
+// Waves begin at different stages of their rows (`turn`) and wrap round: rows
+// that are 2^k bytes apart would otherwise all be read at the same offset, in
+// the same memory channels. Streaming 1.6 GB of 4 KiB rows on MI355X: 5.0 TB/s
+// from a common start, 6.25 with the turn, 6.9 with whole lines and
+// non-temporal loads (register loads in operand order stay at 5.9-6.25).
+// ---------------------------------------------------------------------------
+typedef __attribute__((address_space(3))) char lds_char;
+
+__device__ __forceinline__ void wait_dma(int newer_ops_8)
+{
+    if (newer_ops_8)
+        asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Reads this lane's segments of a stage. The reads and the wait for them are
+// one block, so the compiler, which does not know when the stage was filled,
+// neither adds waits of its own for the ring nor moves a use before the data.
+template <typename W>
+__device__ __forceinline__ void read_stage(uint32_t at, ARegs<W, 4>& a)
+{
+    const uint32_t at1 = at ^ 64u;  // segment s + 4 of the same row
+    asm volatile(
+        "ds_read_b128 %0, %8\n\t"
+        "ds_read_b128 %1, %9\n\t"
+        "ds_read_b128 %2, %8 offset:2048\n\t"
+        "ds_read_b128 %3, %9 offset:2048\n\t"
+        "ds_read_b128 %4, %8 offset:4096\n\t"
+        "ds_read_b128 %5, %9 offset:4096\n\t"
+        "ds_read_b128 %6, %8 offset:6144\n\t"
+        "ds_read_b128 %7, %9 offset:6144\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a.v[0][0]), "=&v"(a.v[0][1]), "=&v"(a.v[1][0]), "=&v"(a.v[1][1]), "=&v"(a.v[2][0]),
+          "=&v"(a.v[2][1]), "=&v"(a.v[3][0]), "=&v"(a.v[3][1])
+        : "v"(at), "v"(at1)
+        : "memory");
+}
+template <typename W>
+__device__ __forceinline__ void read_stage(uint32_t at, ARegs<W, 2>& a)
+{
+    const uint32_t at1 = at ^ 64u;
+    asm volatile(
+        "ds_read_b128 %0, %8\n\t"
+        "ds_read_b128 %1, %9\n\t"
+        "ds_read_b128 %2, %8 offset:128\n\t"
+        "ds_read_b128 %3, %9 offset:128\n\t"
+        "ds_read_b128 %4, %8 offset:4096\n\t"
+        "ds_read_b128 %5, %9 offset:4096\n\t"
+        "ds_read_b128 %6, %8 offset:4224\n\t"
+        "ds_read_b128 %7, %9 offset:4224\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(a.v[0][0]), "=&v"(a.v[0][1]), "=&v"(a.v[0][2]), "=&v"(a.v[0][3]), "=&v"(a.v[1][0]),
+          "=&v"(a.v[1][1]), "=&v"(a.v[1][2]), "=&v"(a.v[1][3])
+        : "v"(at), "v"(at1)
+        : "memory");
+}
+
+template <typename X, typename W, int RT, int TT>
+struct LdsProduct {
+    using S = Stage<W, RT>;
+    const char* src[kDmaOps];  // this lane's 16 bytes of each load, at the start of the depth
+    const X* const (&tok)[TT];
+    const Scales<RT, true>& sc;
+    lds_char* ring;
+    uint32_t read_at;
+    int lane, last_blk;
+    int seg[kDmaOps];  // segment of its row that this lane loads (each load: 64 / kSegs rows)
+
+    __device__ __forceinline__ LdsProduct(const W* const (&tile)[RT], const int (&last)[RT], int64_t depth,
+                                          const X* const (&tok_)[TT], const Scales<RT, true>& sc_, lds_char* ring_, int lane_)
+        : tok(tok_), sc(sc_), ring(ring_), lane(lane_), last_blk((int)((depth - 1) / 128))
+    {
+        const int c = lane % S::kSegs;
+#pragma unroll
+        for (int i = 0; i < kDmaOps; ++i) {
+            const int row = i * (kWave / S::kSegs) + lane / S::kSegs;  // of the stage's kRows
+            const int r = row % 16 < last[i * (kWave / S::kSegs) / 16] ? row % 16 : last[i * (kWave / S::kSegs) / 16];
+            seg[i] = c ^ (row % 8);
+            src[i] = reinterpret_cast<const char*>(tile[i * (kWave / S::kSegs) / 16] + r * depth) + seg[i] * kVecBytes;
+        }
+        const int r = lane % 16, s = lane / 16;
+        read_at = (uint32_t)(uintptr_t)ring + (uint32_t)(r * S::kSegs + (s ^ (r % 8))) * kVecBytes;
+    }
+
+    __device__ __forceinline__ void issue(int slot, int64_t stage, BRegs<W, RT, TT>& b)
+    {
+        load_b<X, W, RT, TT>(tok, stage * S::kDepth, lane, b);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kDmaOps; ++i)
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) uint32_t*)(src[i] + stage * (S::kSegs * kVecBytes)),
+                (__attribute__((address_space(3))) uint32_t*)(ring + slot * kStageBytes + i * (kWave * kVecBytes)), 16,
+                0, 2);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // At the end of the depth only `segs` segments of a row are there: the lanes of the others load the first.
+    __device__ __forceinline__ void issue_tail(int64_t stage, int segs, BRegs<W, RT, TT>& b)
+    {
+        load_b_tail<X, W, RT, TT>(tok, stage * S::kDepth, segs * S::kSegVals, lane, b);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kDmaOps; ++i) {
+            const char* p = src[i] + stage * (S::kSegs * kVecBytes);
+            if (seg[i] >= segs) p -= seg[i] * kVecBytes;
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) uint32_t*)p,
+                (__attribute__((address_space(3))) uint32_t*)(ring + i * (kWave * kVecBytes)), 16, 0, 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // newer: whether one more stage has been issued after this one. At most
+    // the loads of that stage may be outstanding; loads of token values are
+    // older than it, or make the wait stricter than it has to be.
+    __device__ __forceinline__ void use(int slot, int newer, int64_t stage, const BRegs<W, RT, TT>& b,
+                                        f32x4 (&acc)[RT][TT], int segs = S::kSegs)
+    {
+        ARegs<W, RT> a;
+        wait_dma(newer);
+        read_stage<W>(read_at + (uint32_t)slot * kStageBytes, a);
+        __builtin_amdgcn_sched_barrier(0);
+        if (segs < S::kSegs) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < S::kReads; ++j)
+                    if (4 * j + lane / 16 >= segs) a.v[r][j] = u32x4{0u, 0u, 0u, 0u};
+        }
+        multiply<X, W, RT, TT>(a, b, sc, (int)(stage * S::kDepth / 128), last_blk, acc);
+    }
+
+    // Stages [s0, s1) whole, and `segs` segments of stage s1 (0: none).
+    __device__ __forceinline__ void run(int s0, int s1, int segs, uint32_t turn, f32x4 (&acc)[RT][TT])
+    {
+        BRegs<W, RT, TT> b0, b1;
+        const int count = s1 - s0;
+        if (count > 0) {
+            int at = s0 + (int)(turn % (uint32_t)count);
+            const auto next = [&](int s) { return s + 1 < s1 ? s + 1 : s0; };
+            issue(0, at, b0);
+            int j = 0;
+            for (; j + 2 < count; j += 2) {
+                const int a1 = next(at), a2 = next(a1);
+                issue(1, a1, b1);
+                use(0, 1, at, b0, acc);
+                issue(0, a2, b0);
+                use(1, 1, a1, b1, acc);
+                at = a2;
+            }
+            if (j + 1 < count) {
+                const int a1 = next(at);
+                issue(1, a1, b1);
+                use(0, 1, at, b0, acc);
+                use(1, 0, a1, b1, acc);
+            } else {
+                use(0, 0, at, b0, acc);
+            }
+        }
+        if (segs > 0) {
+            issue_tail(s1, segs, b0);
+            use(0, 0, s1, b0, acc, segs);
+        }
+    }
+};
+
+// Weights straight into registers, for rows at any alignment: one stage at a time.
+template <typename X, typename W, int RT, int TT>
+__device__ __forceinline__ void direct_product(const W* const (&tile)[RT], const int (&last)[RT], int64_t depth,
+                                               const X* const (&tok)[TT], const Scales<RT, false>& sc, int64_t k0, int64_t k1,
+                                               int lane, f32x4 (&acc)[RT][TT])
+{
+    using S = Stage<W, RT>;
+    const W* row[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) row[r] = tile[r] + (lane % 16 < last[r] ? lane % 16 : last[r]) * depth;
+    for (int64_t k = k0; k < k1; k += S::kDepth) {
+        ARegs<W, RT> a;
+        BRegs<W, RT, TT> b;
+        if (k + S::kDepth <= k1) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < S::kReads; ++j)
+                    a.v[r][j] = *reinterpret_cast<const typename Vec16<W>::type*>(row[r] + k +
+                                                                                 (4 * j + lane / 16) * S::kSegVals);
+            load_b<X, W, RT, TT>(tok, k, lane, b);
+        } else {
+            const int valid = (int)(k1 - k);
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int j = 0; j < S::kReads; ++j) {
+                    const int at = (4 * j + lane / 16) * S::kSegVals;
+                    W w[S::kSegVals];
+                    __builtin_memset(w, 0, sizeof(w));
+#pragma unroll
+                    for (int i = 0; i < S::kSegVals; ++i)
+                        if (at + i < valid) w[i] = row[r][k + at + i];
+                    __builtin_memcpy(&a.v[r][j], w, sizeof(w));
+                }
+            load_b_tail<X, W, RT, TT>(tok, k, valid, lane, b);
+        }
+        multiply<X, W, RT, TT>(a, b, sc, (int)(k / 128), (int)((depth - 1) / 128), acc);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Which tokens a workgroup serves. Up to 64 assignments, workgroup slot s looks
+// for itself: it serves the expert that assignment s names, unless an earlier
+// one names it too. Above, expert_plan_kernel groups the assignments into
+// blocks of one expert and at most `chunk` assignments, and slot s is block s.
+// ---------------------------------------------------------------------------
+constexpr int kFindMax = kWave;
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxAssignments = 8192;
+constexpr int kMaxExperts = 8192;
+
+// plan[s]: expert of block s (-1: none), plan[blocks + s]: its assignments;
+// list[s * chunk ..]: their indices. One workgroup.
+__global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t* __restrict__ ids, int n, int experts,
+                                                                   int chunk, int blocks, int32_t* __restrict__ plan,
+                                                                   uint16_t* __restrict__ list)
+{
+    constexpr int kPer = kMaxAssignments / kPlanThreads, kEach = kMaxExperts / kPlanThreads;
+    __shared__ uint32_t s_count[kMaxExperts];  // assignments, then the first block
+    __shared__ uint32_t s_wave[kPlanThreads / kWave];
+    int e[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int i = threadIdx.x + j * kPlanThreads;
+        e[j] = i < n ? ids[i] : -1;
+        if (e[j] >= experts) e[j] = -1;
+    }
+    for (int i = threadIdx.x; i < experts; i += kPlanThreads) s_count[i] = 0;
+    __syncthreads();
+    uint32_t rank[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (e[j] >= 0) rank[j] = atomicAdd(&s_count[e[j]], 1u);
+    __syncthreads();
+    // thread t holds experts t * each .. + each - 1
+    const int each = (experts + kPlanThreads - 1) / kPlanThreads;
+    uint32_t c[kEach], own = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int x = threadIdx.x * each + j;
+        c[j] = j < each && x < experts ? s_count[x] : 0u;
+        own += (c[j] + chunk - 1) / chunk;
+    }
+    const uint32_t incl = wave_inclusive_scan(own);
+    if (lane_id() == kWave - 1) s_wave[threadIdx.x / kWave] = incl;
+    __syncthreads();
+    uint32_t first = incl - own, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / kWave; ++w) {
+        if (w < (int)(threadIdx.x / kWave)) first += s_wave[w];
+        total += s_wave[w];
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int x = threadIdx.x * each + j;
+        if (j < each && x < experts) s_count[x] = first;
+        for (uint32_t left = c[j]; left > 0; ++first) {
+            const uint32_t here = left < (uint32_t)chunk ? left : (uint32_t)chunk;
+            plan[first] = x;
+            plan[blocks + first] = (int32_t)here;
+            left -= here;
+        }
+    }
+    for (int b = (int)total + threadIdx.x; b < blocks; b += kPlanThreads) plan[b] = -1;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+        if (e[j] >= 0) list[s_count[e[j]] * chunk + rank[j]] = (uint16_t)(threadIdx.x + j * kPlanThreads);
+}
+
 struct Found {
     int expert, count;  // count 0: nothing to do
 };
 
-__device__ __forceinline__ Found find_assignments(const int32_t* __restrict__ ids, int n, int experts, int slots,
-                                                  int slot, uint16_t* list)
+// Every wave finds the same and writes the same list.
+__device__ __forceinline__ Found find_assignments(const int32_t* __restrict__ ids, int n, int experts, int slot,
+                                                  uint16_t* s_list)
 {
-    __shared__ uint32_t s_used[kThreads];  // bit e: expert e is named (8,192 experts at most)
-    __shared__ int s_expert, s_count;
-    if (threadIdx.x == 0) {
-        s_expert = slots >= experts ? slot : -1;
-        s_count = 0;
-    }
-    if (slots < experts) {
-        s_used[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kThreads) {
-            const int e = ids[i];
-            if (e >= 0 && e < experts) atomicOr(&s_used[e / 32], 1u << (e % 32));
-        }
-        __syncthreads();
-        if (threadIdx.x < kWave) {
-            // lane l counts words 4 l .. 4 l + 3; the lane that holds the slot-th set bit walks its words
-            uint32_t w[4], own = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[j] = s_used[threadIdx.x * 4 + j];
-                own += (uint32_t)__builtin_popcount(w[j]);
-            }
-            const uint32_t before = wave_inclusive_scan(own) - own;
-            if ((uint32_t)slot >= before && (uint32_t)slot < before + own) {
-                int left = slot - (int)before;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t bits = w[j];
-                    while (bits) {
-                        if (left-- == 0) s_expert = ((int)threadIdx.x * 4 + j) * 32 + __builtin_ctz(bits);
-                        bits &= bits - 1;
-                    }
-                }
-            }
-        }
-    }
-    __syncthreads();
-    const int expert = s_expert;
-    if (expert >= 0) {
-        for (int i = threadIdx.x; i < n; i += kThreads)
-            if (ids[i] == expert) list[atomicAdd(&s_count, 1)] = (uint16_t)i;
-    }
-    __syncthreads();
-    return Found{expert, expert >= 0 ? s_count : 0};
+    const int lane = lane_id();
+    const int32_t mine = lane < n ? ids[lane] : -1;
+    const int32_t e = readlane(mine, slot);
+    if (e < 0 || e >= experts) return Found{-1, 0};
+    const uint64_t same = ballot(mine == e);
+    if (__builtin_ctzll(same) < slot) return Found{-1, 0};
+    if (mine == e)
+        s_list[__builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u))] =
+            (uint16_t)lane;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return Found{e, __builtin_popcountll(same)};
 }
 
 struct ExpertArgs {
     const int32_t* ids;
     const void *x, *w, *scale;  // scale: [experts][ceil(rows / 128)][ceil(depth / 128)], or null
     void* out;
-    int64_t x_stride;  // elements between rows of x
-    int n, top_k, experts, slots, slices;
+    int64_t x_stride, out_stride;  // elements between rows of x and of out
+    const int32_t* plan;           // null: the workgroups look for themselves
+    const uint16_t* list;
+    int n, top_k, experts, blocks, slices, chunk;
     int rows, depth;   // of one expert's matrix; gate/up: rows = F (of 2 F), depth = D; down: rows = D, depth = F
 };
 
-// GATED: tiles are gate rows and the up rows that go with them, x rows are the
-// tokens', the output is silu(gate) * up, in X. Otherwise: two tiles of
-// neighbouring rows, x rows are the assignments', the output is 32-bit sums.
-// PARTS waves share a pair of tiles, each with a part of the depth; a
-// workgroup has 4 / PARTS pairs.
-template <typename X, typename W, int TT, bool GATED, int PARTS>
+// GATED: half of the tiles are gate rows, the others the up rows that go with
+// them, x rows are the tokens', the output is silu(gate) * up, in X.
+// Otherwise the tiles are neighbouring rows, x rows are the assignments', the
+// output is 32-bit sums. PARTS waves share the tiles, each with a part of the
+// depth (PARTS 1: every wave has its own tiles).
+template <typename X, typename W, int RT, int TT, bool GATED, int PARTS, bool LDS>
 __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, const uint16_t* list, int first,
-                                             int count, int slice, f32x4* s_part)
+                                             int count, int slice, char* s_mem)
 {
-    constexpr int kPairs = kWaves / PARTS;
+    using S = Stage<W, RT>;
+    constexpr int kHalf = GATED ? RT / 2 : RT;  // tiles of neighbouring rows
     const int lane = lane_id(), wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int part = wave % PARTS, pair = slice * kPairs + wave / PARTS;
-    const int row0 = pair * (GATED ? 16 : 32);
+    const int part = PARTS > 1 ? wave : 0, group = PARTS > 1 ? slice : slice * kWaves + wave;
+    const int row0 = group * (16 * kHalf);
     const int64_t all_rows = GATED ? 2 * (int64_t)a.rows : a.rows;
     const W* w = (const W*)a.w + (int64_t)expert * all_rows * a.depth;
     const int grid_cols = (a.depth + 127) / 128, grid_rows = (int)((all_rows + 127) / 128);
-    // the part of the depth, in whole blocks of 128
-    const int blocks = grid_cols, each = (blocks + PARTS - 1) / PARTS;
-    const int k0 = part * each * 128, k1 = min((part + 1) * each * 128, a.depth);
-    const W* rows[2];
-    const float* scale[2][4];
-    int64_t tile_row[2];  // first row of each tile in the expert's matrix
+    f32x4 acc[RT][TT];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        tile_row[r] = GATED ? (int64_t)r * a.rows + row0 : row0 + 16 * r;
-        const int64_t end = GATED ? (int64_t)(r + 1) * a.rows : a.rows;
-        const int64_t mine = tile_row[r] + lane % 16;
-        rows[r] = w + (mine < end ? mine : end - 1) * a.depth;  // rows past the end repeat the last one
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            scale[r][i] = nullptr;
-            if constexpr (sizeof(W) == 1) {
-                const int64_t out_row = tile_row[r] + lane / 16 * 4 + i;
-                scale[r][i] = (const float*)a.scale +
-                              ((int64_t)expert * grid_rows + (out_row < end ? out_row : end - 1) / 128) * grid_cols +
-                              k0 / 128;
-            }
-        }
-    }
-    const X* tok[TT];
+        for (int b = 0; b < TT; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     int assign[TT];
+    const X* tok[TT];
 #pragma unroll
     for (int b = 0; b < TT; ++b) {
         const int at = first + b * 16 + lane % 16;
@@ -299,140 +552,276 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
         tok[b] = (const X*)a.x + (int64_t)(GATED ? assign[b] / a.top_k : assign[b]) * a.x_stride;
         if (at >= count) assign[b] = -1;
     }
-    f32x4 acc[2][TT];
-    if (row0 < a.rows && k0 < k1) {
-        product<X, W, TT>(rows, tok, scale, k0, k1, lane, acc);
-    } else {
+    // the part of the depth, in whole stages
+    const int stages = (a.depth + S::kDepth - 1) / S::kDepth, each = (stages + PARTS - 1) / PARTS;
+    const int s0 = part * each, s1 = s0 + each < stages ? s0 + each : stages;
+    if (row0 < a.rows && s0 < s1) {
+        const W* tile[RT];
+        int last[RT];  // row of each tile that stands for the rows past the end
+        Scales<RT, LDS> sc;
+        sc.base = (const float*)a.scale + (int64_t)expert * grid_rows * grid_cols;
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < RT; ++r) {
+            const int64_t begin = GATED ? (int64_t)(r / kHalf) * a.rows : 0;
+            int64_t from = row0 + 16 * (r % kHalf);
+            if (from > a.rows - 1) from = a.rows - 1;  // a whole tile past the end
+            last[r] = (int)(a.rows - 1 - from < 15 ? a.rows - 1 - from : 15);
+            tile[r] = w + (begin + from) * a.depth;
+            if constexpr (sizeof(W) == 1) {
 #pragma unroll
-            for (int b = 0; b < TT; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < (LDS ? 1 : 4); ++i) {
+                    int64_t o = begin + from;
+                    if (!LDS) o += lane / 16 * 4 + i < last[r] ? lane / 16 * 4 + i : last[r];
+                    sc.row[r][i] = o / 128 * grid_cols;
+                }
+            }
+        }
+        if constexpr (LDS) {
+            const int segs = a.depth / S::kSegVals - s0 * S::kSegs;  // of the rest of the row
+            const int whole = s1 < stages ? s1 : a.depth / S::kDepth;
+            const uint32_t turn = (blockIdx.x * kWaves + wave) * 5u;
+            LdsProduct<X, W, RT, TT> p(tile, last, a.depth, tok, sc,
+                                       (lds_char*)(s_mem + wave * (kRing * kStageBytes)), lane);
+            p.run(s0, whole, s1 < stages ? 0 : segs - (whole - s0) * S::kSegs, turn, acc);
+        } else {
+            const int64_t k1 = (int64_t)s1 * S::kDepth;
+            direct_product<X, W, RT, TT>(tile, last, a.depth, tok, sc, (int64_t)s0 * S::kDepth,
+                                         k1 < a.depth ? k1 : a.depth, lane, acc);
+        }
     }
-    if constexpr (PARTS > 1) {  // PARTS == kWaves: one pair per workgroup
-        static_assert(PARTS == kWaves, "the parts of one pair are the workgroup's waves");
-        __syncthreads();  // the previous block's sums have been read
+    if constexpr (PARTS > 1) {
+        f32x4* s_part = reinterpret_cast<f32x4*>(s_mem);  // over the rings: every wave is past them
+        __syncthreads();
         if (wave > 0) {
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+            for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int b = 0; b < TT; ++b) s_part[((wave - 1) * 2 * TT + r * TT + b) * kWave + lane] = acc[r][b];
+                for (int b = 0; b < TT; ++b) s_part[((wave - 1) * RT * TT + r * TT + b) * kWave + lane] = acc[r][b];
+        }
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int p = 0; p < PARTS - 1; ++p)
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int b = 0; b < TT; ++b) acc[r][b] += s_part[(p * RT * TT + r * TT + b) * kWave + lane];
         }
         __syncthreads();
         if (wave > 0) return;
-#pragma unroll
-        for (int p = 0; p < PARTS - 1; ++p)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int b = 0; b < TT; ++b) acc[r][b] += s_part[(p * 2 * TT + r * TT + b) * kWave + lane];
     }
     if (row0 >= a.rows) return;
     // lane l holds output rows (l / 16) * 4 .. + 3 of each tile for token l % 16 of each block
-    const int r0 = lane / 16 * 4;
+    const int r0 = row0 + lane / 16 * 4;
 #pragma unroll
     for (int b = 0; b < TT; ++b) {
         if (assign[b] < 0) continue;
         if constexpr (GATED) {
-            X* out = (X*)a.out + (int64_t)assign[b] * a.rows + row0 + r0;
+            X* out = (X*)a.out + (int64_t)assign[b] * a.out_stride;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float g = acc[0][b][i], u = acc[1][b][i];
-                if (row0 + r0 + i < a.rows) out[i] = (X)(g / (1.0f + expf(-g)) * u);
+            for (int t = 0; t < kHalf; ++t) {
+                X h[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float g = acc[t][b][i], u = acc[kHalf + t][b][i];
+                    h[i] = (X)(g / (1.0f + expf(-g)) * u);
+                }
+                const int o = r0 + 16 * t;  // a multiple of 4; rows of `out` are whole vectors, past a.rows unused
+                if (o < a.out_stride) *reinterpret_cast<uint64_t*>(out + o) = __builtin_bit_cast(uint64_t, *(uint64_t*)h);
             }
         } else {
+            float* out = (float*)a.out + (int64_t)assign[b] * a.out_stride;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float* out = (float*)a.out + (int64_t)assign[b] * a.rows + row0 + 16 * r + r0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (row0 + 16 * r + r0 + i < a.rows) out[i] = acc[r][b][i];
+            for (int r = 0; r < RT; ++r) {
+                const int o = r0 + 16 * r;
+                if (o < a.out_stride) *reinterpret_cast<f32x4*>(out + o) = acc[r][b];
             }
         }
     }
 }
 
-constexpr int kMostBlocks = 4;  // blocks of 16 tokens that a wave holds at once
+// Blocks of 16 tokens that a wave holds at once, as registers allow (256 at two
+// waves per SIMD): 8-bit weights have a second set of sums (one per block of
+// 128 of the depth) and twice the depth to a stage, RT 2 twice the depth too.
+template <typename W, int RT = 4> struct MostBlocks {
+    static constexpr int value = (sizeof(W) == 1 ? 2 : 4) * RT / 4;
+};
 
-template <typename X, typename W, bool GATED, int PARTS>
-__global__ __launch_bounds__(kThreads) void expert_kernel(ExpertArgs a)
+template <typename X, typename W, int RT, bool GATED, int PARTS, bool LDS>
+__global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
 {
-    extern __shared__ __align__(16) char s_mem[];
-    f32x4* s_part = reinterpret_cast<f32x4*>(s_mem);
-    uint16_t* list = reinterpret_cast<uint16_t*>(
-        s_mem + (PARTS > 1 ? (PARTS - 1) * 2 * kMostBlocks * kWave * sizeof(f32x4) : 0));
+    static_assert(PARTS == 1 || PARTS == kWaves, "a workgroup's waves share one set of tiles, or none");
+    constexpr int kMost = MostBlocks<W, RT>::value;
+    constexpr int kPart = (PARTS - 1) * RT * kMost * kWave * 16;
+    constexpr int kRings = LDS ? kWaves * kRing * kStageBytes : 0;
+    __shared__ __align__(1024) char s_mem[kRings > kPart ? kRings : kPart > 0 ? kPart : 16];
+    __shared__ uint16_t s_list[kFindMax];
     const int slot = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
-    const Found f = find_assignments(a.ids, a.n, a.experts, a.slots, slot, list);
-    int first = 0;
-    while (f.count - first > 32) {
-        expert_block<X, W, 4, GATED, PARTS>(a, f.expert, list, first, f.count, slice, s_part);
-        first += 64;
+    Found f;
+    const uint16_t* list;
+    if (a.plan) {
+        f = Found{a.plan[slot], a.plan[a.blocks + slot]};
+        if (f.expert < 0) return;
+        list = a.list + (int64_t)slot * a.chunk;
+    } else {
+        f = find_assignments(a.ids, a.n, a.experts, slot, s_list);
+        if (f.count == 0) return;
+        list = s_list;
     }
-    if (f.count - first > 16)
-        expert_block<X, W, 2, GATED, PARTS>(a, f.expert, list, first, f.count, slice, s_part);
-    else if (f.count - first > 0)
-        expert_block<X, W, 1, GATED, PARTS>(a, f.expert, list, first, f.count, slice, s_part);
+    int first = 0;
+    for (; f.count - first > (kMost > 1 ? 8 * kMost : 0); first += 16 * kMost)
+        expert_block<X, W, RT, kMost, GATED, PARTS, LDS>(a, f.expert, list, first, f.count, slice, s_mem);
+    if constexpr (kMost > 2) {
+        if (f.count - first > 16) {
+            expert_block<X, W, RT, 2, GATED, PARTS, LDS>(a, f.expert, list, first, f.count, slice, s_mem);
+            return;
+        }
+    }
+    if (kMost > 1 && f.count - first > 0)
+        expert_block<X, W, RT, 1, GATED, PARTS, LDS>(a, f.expert, list, first, f.count, slice, s_mem);
 }
 
-// y_t = sum over j of weights[t, j] * part[t, j], choices outside the experts left out.
+// y_t = sum over j of weights[t, j] * part[t, j], choices outside the experts
+// left out. A thread sums four columns; rows of `part` are whole vectors.
 template <typename X>
-__global__ __launch_bounds__(kThreads) void expert_sum_kernel(const float* __restrict__ part,
+__global__ __launch_bounds__(kThreads) void expert_sum_kernel(const float* __restrict__ part, int64_t part_stride,
                                                               const int32_t* __restrict__ ids,
                                                               const float* __restrict__ weights, int tokens, int top_k,
                                                               int experts, int dim, X* __restrict__ y,
                                                               int64_t y_stride)
 {
+    const int quads = (dim + 3) / 4;
     const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int t = (int)(at / dim), d = (int)(at % dim);
+    const int t = (int)(at / quads), d = (int)(at % quads) * 4;
     if (t >= tokens) return;
-    float sum = 0.0f;
-    for (int j = 0; j < top_k; ++j) {
-        const int e = ids[t * top_k + j];
-        if (e >= 0 && e < experts) sum += weights[t * top_k + j] * part[((int64_t)t * top_k + j) * dim + d];
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < top_k; j0 += 8) {
+        f32x4 p[8];
+        float w[8];
+        bool live[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t i = (int64_t)t * top_k + (j0 + j < top_k ? j0 + j : top_k - 1);
+            const int e = ids[i];
+            live[j] = j0 + j < top_k && e >= 0 && e < experts;
+            w[j] = weights[i];
+            p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (live[j]) p[j] = *reinterpret_cast<const f32x4*>(part + i * part_stride + d);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (live[j]) sum += w[j] * p[j];
     }
-    y[t * y_stride + d] = (X)sum;
+    X* out = y + t * y_stride + d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (d + i < dim) out[i] = (X)sum[i];
 }
 
-int64_t experts_max_assignments() { return 8192; }
-int experts_max_experts() { return kThreads * 32; }
+int64_t experts_max_assignments() { return kMaxAssignments; }
+int experts_max_experts() { return kMaxExperts; }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int64_t experts_h_bytes(int64_t n, int hidden) { return ceil_div(n * hidden * 2, 256) * 256; }
-int64_t experts_aux_bytes(int64_t n, int dim, int hidden) { return experts_h_bytes(n, hidden) + n * dim * 4; }
+// Scratch: rows of h (16-byte multiples), rows of parts, the plan and its list.
+struct ExpertsScratch {
+    int64_t h_stride, part_stride, blocks, part_at, plan_at, list_at, bytes;
+    ExpertsScratch(int64_t n, int experts, int dim, int hidden, int chunk)
+    {
+        h_stride = ceil_div(hidden, 8) * 8;
+        part_stride = ceil_div(dim, 4) * 4;
+        blocks = (experts < n ? experts : n) + n / chunk;
+        part_at = ceil_div(n * h_stride * 2, 256) * 256;
+        plan_at = part_at + n * part_stride * 4;
+        list_at = plan_at + blocks * 2 * 4;
+        bytes = list_at + blocks * chunk * 2;
+    }
+};
+
+static int experts_chunk(bool eight_bit) { return 16 * (eight_bit ? MostBlocks<fp8>::value : MostBlocks<bf16>::value); }
+
+int64_t experts_aux_bytes(int64_t n, int experts, int dim, int hidden, bool eight_bit)
+{
+    return ExpertsScratch(n, experts, dim, hidden, experts_chunk(eight_bit)).bytes;
+}
+
+// How one launch streams the weights of `blocks` blocks.
+struct ExpertsVariant {
+    bool lds;    // through LDS: every row of every expert starts on a 16-byte boundary
+    bool whole;  // a wave has four tiles of its own and the whole depth
+    int64_t slices;
+};
+
+static ExpertsVariant experts_variant(const void* w, int wbytes, bool gated, int rows, int depth, int64_t blocks)
+{
+    ExpertsVariant v;
+    v.lds = (uintptr_t)w % kVecBytes == 0 && (int64_t)depth * wbytes % kVecBytes == 0 &&
+            (wbytes == 2 || !gated || rows % 16 == 0);
+    // With few experts the four waves of a workgroup share two tiles, so that
+    // there is work for every CU.
+    v.slices = ceil_div(rows, (gated ? 32 : 64) * kWaves);
+    v.whole = v.lds && blocks * v.slices >= 512;
+    if (!v.whole) v.slices = ceil_div(rows, gated ? 16 : 32);
+    return v;
+}
+
+static int64_t experts_blocks(int64_t n, int experts, int dim, int hidden, bool eight_bit)
+{
+    return n > kFindMax ? ExpertsScratch(n, experts, dim, hidden, experts_chunk(eight_bit)).blocks : n;
+}
+
+int64_t experts_workgroups(bool eight_bit, const ExpertsCall& c)
+{
+    const int64_t blocks = experts_blocks(c.tokens * c.top_k, c.experts, c.dim, c.hidden, eight_bit);
+    const int wbytes = eight_bit ? 1 : 2;
+    const int64_t a = experts_variant(c.w_in, wbytes, true, c.hidden, c.dim, blocks).slices;
+    const int64_t b = experts_variant(c.w_out, wbytes, false, c.dim, c.hidden, blocks).slices;
+    return blocks * (a > b ? a : b);
+}
 
 template <typename X, typename W, bool GATED>
 static hipError_t launch_expert_kernel(ExpertArgs a, hipStream_t stream)
 {
-    // A wave streams a whole pair of tiles where that gives every CU work;
-    // with few experts the four waves of a workgroup share one pair.
-    const int64_t pairs = ceil_div(a.rows, GATED ? 16 : 32);
-    const bool whole = a.slots * ceil_div(pairs, kWaves) >= 1024;
-    a.slices = (int)(whole ? ceil_div(pairs, kWaves) : pairs);
-    const dim3 grid((unsigned)((int64_t)a.slots * a.slices)), block(kThreads);
-    const size_t list = (size_t)((a.n + 7) / 8 * 8) * sizeof(uint16_t);
-    if (whole)
-        expert_kernel<X, W, GATED, 1><<<grid, block, list, stream>>>(a);
+    const ExpertsVariant v = experts_variant(a.w, sizeof(W), GATED, a.rows, a.depth, a.blocks);
+    a.slices = (int)v.slices;
+    const dim3 grid((unsigned)(a.blocks * v.slices)), block(kThreads);
+    if (v.whole)
+        expert_kernel<X, W, 4, GATED, 1, true><<<grid, block, 0, stream>>>(a);
+    else if (v.lds)
+        expert_kernel<X, W, 2, GATED, kWaves, true><<<grid, block, 0, stream>>>(a);
     else
-        expert_kernel<X, W, GATED, kWaves>
-            <<<grid, block, list + (kWaves - 1) * 2 * kMostBlocks * kWave * sizeof(f32x4), stream>>>(a);
+        expert_kernel<X, W, 2, GATED, kWaves, false><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename X, typename W>
 static hipError_t experts_typed(const ExpertsCall& c, char* aux, hipStream_t stream)
 {
-    const int n = (int)(c.tokens * c.top_k);
-    char *h = aux, *part = aux + experts_h_bytes(n, c.hidden);
-    const int slots = c.experts < n ? c.experts : n;
-    ExpertArgs a{c.ids, c.x, c.w_in, c.w_in_scale, h, c.x_stride, n, c.top_k, c.experts, slots, 0, c.hidden, c.dim};
+    const int n = (int)(c.tokens * c.top_k), chunk = 16 * MostBlocks<W>::value;
+    const ExpertsScratch s(n, c.experts, c.dim, c.hidden, chunk);
+    char *h = aux, *part = aux + s.part_at;
+    int32_t* plan = nullptr;
+    uint16_t* list = nullptr;
+    const int blocks = (int)experts_blocks(n, c.experts, c.dim, c.hidden, sizeof(W) == 1);
+    if (n > kFindMax) {
+        plan = reinterpret_cast<int32_t*>(aux + s.plan_at);
+        list = reinterpret_cast<uint16_t*>(aux + s.list_at);
+        expert_plan_kernel<<<dim3(1), dim3(kPlanThreads), 0, stream>>>(c.ids, n, c.experts, chunk, blocks, plan, list);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    ExpertArgs a{c.ids, c.x, c.w_in, c.w_in_scale, h, c.x_stride, s.h_stride, plan, list, n, c.top_k, c.experts,
+                 blocks, 0, chunk, c.hidden, c.dim};
     hipError_t e = launch_expert_kernel<X, W, true>(a, stream);
     if (e != hipSuccess) return e;
-    ExpertArgs b{c.ids, h, c.w_out, c.w_out_scale, part, c.hidden, n, c.top_k, c.experts, slots, 0, c.dim, c.hidden};
+    ExpertArgs b{c.ids, h, c.w_out, c.w_out_scale, part, s.h_stride, s.part_stride, plan, list, n, c.top_k, c.experts,
+                 blocks, 0, chunk, c.dim, c.hidden};
     e = launch_expert_kernel<X, W, false>(b, stream);
     if (e != hipSuccess) return e;
-    const int64_t items = (int64_t)c.tokens * c.dim;
+    const int64_t items = c.tokens * ceil_div(c.dim, 4);
     expert_sum_kernel<X><<<dim3((unsigned)ceil_div(items, kThreads)), dim3(kThreads), 0, stream>>>(
-        (const float*)part, c.ids, c.weights, (int)c.tokens, c.top_k, c.experts, c.dim, (X*)c.y, c.y_stride);
+        (const float*)part, s.part_stride, c.ids, c.weights, (int)c.tokens, c.top_k, c.experts, c.dim, (X*)c.y,
+        c.y_stride);
     return hipGetLastError();
 }
 
