@@ -149,16 +149,32 @@ __device__ __forceinline__ void load_b_tail(const X* const (&tok)[TT], int64_t d
 template <int RT, bool UNIFORM> struct Scales {
     const float* base;                  // of the expert
     int64_t row[RT][UNIFORM ? 1 : 4];   // of the depth's first block
-    __device__ __forceinline__ float at(int r, int i, int blk) const { return base[row[r][UNIFORM ? 0 : i] + blk]; }
+};
+template <typename W, int RT, bool UNIFORM> struct ScaleRegs {
+    static constexpr int kBlocks = sizeof(W) == 1 ? Stage<W, RT>::kReads / 2 : 0;  // blocks of 128 in a stage
+    float v[kBlocks ? kBlocks : 1][RT][UNIFORM ? 1 : 4];
 };
 
-// acc += the products of one stage. blk0: block of 128 of the depth that the
-// stage begins in, last_blk: the depth's last one (8-bit weights, whose stages
-// are one or two whole blocks; the last stage may have only its first).
+// The factors of the stage whose first block of 128 is blk0. last_blk: the
+// depth's last block (the last stage may lack its second).
+template <typename W, int RT, bool UNIFORM>
+__device__ __forceinline__ void load_scales(const Scales<RT, UNIFORM>& sc, int blk0, int last_blk,
+                                            ScaleRegs<W, RT, UNIFORM>& s)
+{
+#pragma unroll
+    for (int k = 0; k < ScaleRegs<W, RT, UNIFORM>::kBlocks; ++k) {
+        const int blk = blk0 + k < last_blk ? blk0 + k : last_blk;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < (UNIFORM ? 1 : 4); ++i) s.v[k][r][i] = sc.base[sc.row[r][i] + blk];
+    }
+}
+
+// acc += the products of one stage.
 template <typename X, typename W, int RT, int TT, bool UNIFORM>
 __device__ __forceinline__ void multiply(const ARegs<W, RT>& a, const BRegs<W, RT, TT>& b,
-                                         const Scales<RT, UNIFORM>& sc, int blk0, int last_blk,
-                                         f32x4 (&acc)[RT][TT])
+                                         const ScaleRegs<W, RT, UNIFORM>& sc, f32x4 (&acc)[RT][TT])
 {
     using S = Stage<W, RT>;
     constexpr int kPerBlock = sizeof(W) == 1 ? 2 : S::kReads;  // reads per block of 128 (8-bit)
@@ -188,12 +204,11 @@ __device__ __forceinline__ void multiply(const ARegs<W, RT>& a, const BRegs<W, R
                     }
                 }
         if constexpr (sizeof(W) == 1) {
-            const int blk = blk0 + j0 / kPerBlock < last_blk ? blk0 + j0 / kPerBlock : last_blk;
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
                 f32x4 s;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = sc.at(r, i, blk);
+                for (int i = 0; i < 4; ++i) s[i] = sc.v[j0 / kPerBlock][r][UNIFORM ? 0 : i];
 #pragma unroll
                 for (int t = 0; t < TT; ++t) acc[r][t] += s * sum[r][t];
             }
@@ -295,27 +310,31 @@ struct LdsProduct {
         read_at = (uint32_t)(uintptr_t)ring + (uint32_t)(r * S::kSegs + (s ^ (r % 8))) * kVecBytes;
     }
 
-    __device__ __forceinline__ void issue(int slot, int64_t stage, BRegs<W, RT, TT>& b)
+    // Factors and token values come a stage ahead too: a wait for them where
+    // they are used made the 8-bit products a fifth slower.
+    __device__ __forceinline__ void issue(int slot, int stage, BRegs<W, RT, TT>& b, ScaleRegs<W, RT, true>& s)
     {
-        load_b<X, W, RT, TT>(tok, stage * S::kDepth, lane, b);
+        load_scales<W, RT, true>(sc, stage * (S::kDepth / 64) / 2, last_blk, s);
+        load_b<X, W, RT, TT>(tok, (int64_t)stage * S::kDepth, lane, b);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < kDmaOps; ++i)
             __builtin_amdgcn_global_load_lds(
-                (const __attribute__((address_space(1))) uint32_t*)(src[i] + stage * (S::kSegs * kVecBytes)),
+                (const __attribute__((address_space(1))) uint32_t*)(src[i] + (int64_t)stage * (S::kSegs * kVecBytes)),
                 (__attribute__((address_space(3))) uint32_t*)(ring + slot * kStageBytes + i * (kWave * kVecBytes)), 16,
                 0, 2);
         __builtin_amdgcn_sched_barrier(0);
     }
 
     // At the end of the depth only `segs` segments of a row are there: the lanes of the others load the first.
-    __device__ __forceinline__ void issue_tail(int64_t stage, int segs, BRegs<W, RT, TT>& b)
+    __device__ __forceinline__ void issue_tail(int stage, int segs, BRegs<W, RT, TT>& b, ScaleRegs<W, RT, true>& s)
     {
-        load_b_tail<X, W, RT, TT>(tok, stage * S::kDepth, segs * S::kSegVals, lane, b);
+        load_scales<W, RT, true>(sc, stage * (S::kDepth / 64) / 2, last_blk, s);
+        load_b_tail<X, W, RT, TT>(tok, (int64_t)stage * S::kDepth, segs * S::kSegVals, lane, b);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < kDmaOps; ++i) {
-            const char* p = src[i] + stage * (S::kSegs * kVecBytes);
+            const char* p = src[i] + (int64_t)stage * (S::kSegs * kVecBytes);
             if (seg[i] >= segs) p -= seg[i] * kVecBytes;
             __builtin_amdgcn_global_load_lds(
                 (const __attribute__((address_space(1))) uint32_t*)p,
@@ -327,8 +346,8 @@ struct LdsProduct {
     // newer: whether one more stage has been issued after this one. At most
     // the loads of that stage may be outstanding; loads of token values are
     // older than it, or make the wait stricter than it has to be.
-    __device__ __forceinline__ void use(int slot, int newer, int64_t stage, const BRegs<W, RT, TT>& b,
-                                        f32x4 (&acc)[RT][TT], int segs = S::kSegs)
+    __device__ __forceinline__ void use(int slot, int newer, const BRegs<W, RT, TT>& b,
+                                        const ScaleRegs<W, RT, true>& s, f32x4 (&acc)[RT][TT], int segs = S::kSegs)
     {
         ARegs<W, RT> a;
         wait_dma(newer);
@@ -341,39 +360,40 @@ struct LdsProduct {
                 for (int j = 0; j < S::kReads; ++j)
                     if (4 * j + lane / 16 >= segs) a.v[r][j] = u32x4{0u, 0u, 0u, 0u};
         }
-        multiply<X, W, RT, TT>(a, b, sc, (int)(stage * S::kDepth / 128), last_blk, acc);
+        multiply<X, W, RT, TT>(a, b, s, acc);
     }
 
     // Stages [s0, s1) whole, and `segs` segments of stage s1 (0: none).
     __device__ __forceinline__ void run(int s0, int s1, int segs, uint32_t turn, f32x4 (&acc)[RT][TT])
     {
         BRegs<W, RT, TT> b0, b1;
+        ScaleRegs<W, RT, true> c0, c1;
         const int count = s1 - s0;
         if (count > 0) {
             int at = s0 + (int)(turn % (uint32_t)count);
             const auto next = [&](int s) { return s + 1 < s1 ? s + 1 : s0; };
-            issue(0, at, b0);
+            issue(0, at, b0, c0);
             int j = 0;
             for (; j + 2 < count; j += 2) {
                 const int a1 = next(at), a2 = next(a1);
-                issue(1, a1, b1);
-                use(0, 1, at, b0, acc);
-                issue(0, a2, b0);
-                use(1, 1, a1, b1, acc);
+                issue(1, a1, b1, c1);
+                use(0, 1, b0, c0, acc);
+                issue(0, a2, b0, c0);
+                use(1, 1, b1, c1, acc);
                 at = a2;
             }
             if (j + 1 < count) {
                 const int a1 = next(at);
-                issue(1, a1, b1);
-                use(0, 1, at, b0, acc);
-                use(1, 0, a1, b1, acc);
+                issue(1, a1, b1, c1);
+                use(0, 1, b0, c0, acc);
+                use(1, 0, b1, c1, acc);
             } else {
-                use(0, 0, at, b0, acc);
+                use(0, 0, b0, c0, acc);
             }
         }
         if (segs > 0) {
-            issue_tail(s1, segs, b0);
-            use(0, 0, s1, b0, acc, segs);
+            issue_tail(s1, segs, b0, c0);
+            use(0, 0, b0, c0, acc, segs);
         }
     }
 };
@@ -391,6 +411,8 @@ __device__ __forceinline__ void direct_product(const W* const (&tile)[RT], const
     for (int64_t k = k0; k < k1; k += S::kDepth) {
         ARegs<W, RT> a;
         BRegs<W, RT, TT> b;
+        ScaleRegs<W, RT, false> s;
+        load_scales<W, RT, false>(sc, (int)(k / 128), (int)((depth - 1) / 128), s);
         if (k + S::kDepth <= k1) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -415,7 +437,7 @@ __device__ __forceinline__ void direct_product(const W* const (&tile)[RT], const
                 }
             load_b_tail<X, W, RT, TT>(tok, k, valid, lane, b);
         }
-        multiply<X, W, RT, TT>(a, b, sc, (int)(k / 128), (int)((depth - 1) / 128), acc);
+        multiply<X, W, RT, TT>(a, b, s, acc);
     }
 }
 
