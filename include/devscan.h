@@ -277,13 +277,13 @@ int ds_embedding(int dtype, const void* d_table, int64_t rows, int64_t dim, int6
  * d_dout[i] over the i with d_ids[i] = v; ids outside [0, rows) are left out.
  * accumulate 0: every row of d_grad is written, rows that no id names with
  * zeros. accumulate 1: the sums are added to d_grad and other rows are not
- * touched. The positions are sorted by id (a counting by rank up to 8,192
- * ids, above that two passes of the counting sort, three from 261,121 rows
- * on), so a row's terms are added in the order of the sorted positions,
- * without atomics.
+ * touched. The positions are sorted by id (by rank up to 8,192 ids, by small
+ * counting passes over 9 bits up to 262,144, by ds_radix_pass's passes above),
+ * so a row's terms are added in the order of the sorted positions, without
+ * atomics.
  *   dtype       of d_dout: DS_FP32, DS_BF16 or DS_FP16
  *   grad_dtype  of d_grad: dtype or DS_FP32
- * n < 2^31, rows <= 133,432,830 (else DS_ERR_TOO_LARGE).
+ * n < 2^31, rows < 2^27 (else DS_ERR_TOO_LARGE).
  */
 int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const void* d_ids, int id_bytes, int64_t n,
                       float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim, int64_t grad_stride,

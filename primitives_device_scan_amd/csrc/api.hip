@@ -34,10 +34,11 @@ struct Workspace {
     char* base = nullptr;
     int64_t tile_cap = 0;
     uint64_t lookback_launches = 0;  // launches that stamped an epoch since the last clear
+    bool base_captured = false;   // a graph of ds_embedding_grad holds the address of base
     char* aux = nullptr;
     size_t aux_cap = 0;
     bool aux_captured = false;    // some graph holds the address of aux
-    std::vector<char*> retired;   // earlier aux buffers that graphs hold, freed by ds_release_workspace
+    std::vector<char*> retired;   // earlier buffers that graphs hold, freed by ds_release_workspace
 };
 
 std::mutex g_mu;
@@ -104,13 +105,16 @@ int get_workspace(hipStream_t stream, int64_t tiles, Workspace** out)
         int64_t cap = w.tile_cap * 2 > tiles ? w.tile_cap * 2 : tiles;
         if (cap < 1024) cap = 1024;
         if (refuse_allocation()) return DS_ERR_OUT_OF_MEMORY;
-        if (w.base) {
+        if (w.base && w.base_captured) {
+            w.retired.push_back(w.base);  // a replay may still use it
+        } else if (w.base) {
             // The old buffer may still be in use by work queued on the stream.
             if (hipStreamSynchronize(stream) != hipSuccess) return DS_ERR_HIP;
             (void)hipFree(w.base);
-            w.base = nullptr;
-            w.tile_cap = 0;
         }
+        w.base = nullptr;
+        w.tile_cap = 0;
+        w.base_captured = false;
         void* p = nullptr;
         if (hipMalloc(&p, ws_bytes(cap)) != hipSuccess) {
             (void)hipGetLastError();
@@ -697,7 +701,7 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
     int st = check_buffers(bufs, 3);
     if (st != DS_OK) return st;
     const ds::EmbeddingGradPlan plan = ds::embedding_grad_plan(float_kind(dtype), n, rows, dim);
-    if (plan.chunks * plan.slabs / 4 >= kMaxTiles || n / 256 >= kMaxTiles) return DS_ERR_TOO_LARGE;
+    if (ds::embedding_grad_blocks(plan, n, dim) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
     std::lock_guard<std::mutex> lock(g_mu);
     char* aux = nullptr;
     DevWs dws{nullptr, nullptr, nullptr};
@@ -705,8 +709,12 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
     if (n > 0) {
         st = get_aux(stream, (size_t)plan.bytes, &aux);
         if (st != DS_OK) return st;
-        st = scan_workspace_u32(stream, plan.table_words, &dws, &w);
+    }
+    if (plan.radix_bits) {
+        const int64_t words = ((int64_t)1 << plan.radix_bits) * ds::sort_table_columns(true, n);
+        st = scan_workspace_u32(stream, words, &dws, &w);
         if (st != DS_OK) return st;
+        if (w) w->base_captured |= capturing(stream);
     }
     const hipError_t e = ds::launch_embedding_grad(float_kind(dtype), float_kind(grad_dtype), plan, d_dout,
                                                    dout_stride, d_ids, id_bytes == 8, n, rows, dim, scale, d_grad,

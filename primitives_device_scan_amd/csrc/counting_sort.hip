@@ -632,29 +632,6 @@ hipError_t launch_radix_pass(const uint32_t* keys, const uint32_t* vals_in, uint
                                                                       table, pre, none, n, ws, spin_limit, stream);
 }
 
-// A pass over the digits of packed keys (embedding.hip): `buckets` need not be
-// a power of two, since a real digit never reaches it, and the digit field is
-// always kPackedBits wide. Small tiles: token counts are small next to a radix
-// sort's, and more tiles use more CUs.
-constexpr int kPackedBits = 9;
-
-int64_t sort_pass_words(int64_t n, uint32_t buckets)
-{
-    return (int64_t)buckets * ((n + moe_tile_elems() - 1) / moe_tile_elems());
-}
-
-hipError_t launch_sort_pass(const uint32_t* keys, const uint32_t* vals_in, uint32_t* keys_out, uint32_t* vals_out,
-                            int64_t n, int shift, uint32_t buckets, uint32_t* table, const DevWs& ws,
-                            uint32_t spin_limit, hipStream_t stream)
-{
-    if (n <= 0) return hipSuccess;
-    if (!table || !vals_in || buckets < 2 || buckets > (uint32_t)sort_max_buckets()) return hipErrorInvalidValue;
-    const RadixDigit dig{(uint32_t)shift, (1u << kPackedBits) - 1u, buckets};
-    const MoeSlots none{nullptr, 0, nullptr, nullptr, nullptr};
-    return counting_sort_typed<RadixDigit, 1, kMoeItems, 1>(keys, vals_in, keys_out, vals_out, n, dig, table, table,
-                                                            nullptr, none, n, ws, spin_limit, stream);
-}
-
 hipError_t launch_moe_align(const int32_t* ids, int64_t n, int experts, const MoeOut& out, uint32_t* hist,
                             uint32_t* slots, const DevWs& ws, uint32_t spin_limit, hipStream_t stream)
 {

@@ -7,9 +7,9 @@
 // The gradient goes by sorted tokens: the positions i are put in order of
 // their token (equal tokens in input order), so that each row's terms are
 // consecutive, and are then summed in that order: no atomics on the sums, and
-// the same bits on every run. Up to kRankSortMax tokens one launch sorts
-// (every token's place is the number of tokens that sort before it, counted
-// directly); above, two or three passes of the stable counting sort do.
+// the same bits on every run. A whole new gradient is cleared by workgroups
+// that ride along in the sort's launches: the sort waits on latency and needs
+// few CUs, the clearing needs the memory.
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -18,8 +18,12 @@ namespace ds {
 
 // ---------------------------------------------------------------------------
 // Lookup. A wave takes whole rows: `lanes` lanes (a power of two) side by side
-// on one row, 64 / lanes rows at once, 16 bytes per lane and step.
+// on one row, 64 / lanes rows at once, 16 bytes per lane and step, kLookAhead
+// steps in flight. Outputs are written past the cache: nothing here reads them
+// again, and rows of frequent tokens stay in it.
 // ---------------------------------------------------------------------------
+constexpr int kLookAhead = 4;
+
 template <typename T, typename ID>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(const T* __restrict__ table, int64_t rows, int64_t dim,
                                                              int64_t table_stride, const ID* __restrict__ ids,
@@ -35,17 +39,67 @@ __global__ __launch_bounds__(kThreads) void embedding_kernel(const T* __restrict
     const bool live = id >= 0 && id < rows;
     const T* src = table + (live ? id : 0) * table_stride;
     T* dst = out + i * out_stride;
-    for (int64_t c = (int64_t)(lane_id() % lanes) * N; c < dim; c += (int64_t)lanes * N) {
-        float x[N];
-        if (live) {
-            load_floats<T, N>(src + c, dim - c, x);
+    const int64_t step = (int64_t)lanes * N, vecs = dim / N * N;
+    int64_t c = (int64_t)(lane_id() % lanes) * N;
+    if (!live) {
+        const float zero[N] = {};
+        for (; c < dim; c += step) store_floats<T, N>(dst + c, dim - c, zero);
+        return;
+    }
+    for (; c < vecs; c += step * kLookAhead) {
+        u32x4 v[kLookAhead];
 #pragma unroll
-            for (int j = 0; j < N; ++j) x[j] *= scale;
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) x[j] = 0.0f;
+        for (int k = 0; k < kLookAhead; ++k) {
+            const int64_t at = c + k * step;
+            v[k] = *reinterpret_cast<const typename Vec16<T>::type*>(src + (at < vecs ? at : c));
         }
-        store_floats<T, N>(dst + c, dim - c, x);
+#pragma unroll
+        for (int k = 0; k < kLookAhead; ++k) {
+            const int64_t at = c + k * step;
+            T t[N];
+            __builtin_memcpy(t, &v[k], sizeof(t));
+#pragma unroll
+            for (int j = 0; j < N; ++j) t[j] = (T)((float)t[j] * scale);
+            u32x4 w;
+            __builtin_memcpy(&w, t, sizeof(w));
+            if (at < vecs)
+                __builtin_nontemporal_store(w, reinterpret_cast<typename Vec16<T>::type*>(dst + at));
+        }
+    }
+    // the last, partial vector of the row
+    const int64_t rest = vecs + lane_id() % lanes;
+    if (rest < dim && lane_id() % lanes < N)
+        for (int64_t e = rest; e < dim; e += lanes) dst[e] = (T)((float)src[e] * scale);
+}
+
+// ---------------------------------------------------------------------------
+// Clearing: rows of row_bytes, stride_bytes apart, in units of one 16-byte
+// store per lane of a wave. A launch takes the units [first, last).
+// ---------------------------------------------------------------------------
+struct ClearArgs {
+    char* grad;
+    int64_t row_bytes, stride_bytes, slabs;  // slabs: units per row
+    int64_t first, last;
+    int skip;  // workgroups before the clearing ones
+};
+
+template <int THREADS>
+__device__ __forceinline__ void clear_rows(const ClearArgs& a)
+{
+    constexpr int kPerBlock = THREADS / kWave;
+    const int64_t waves = (int64_t)(gridDim.x - a.skip) * kPerBlock;
+    int64_t u = a.first + (int64_t)(blockIdx.x - a.skip) * kPerBlock +
+                __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const bool one_row = a.last <= a.slabs;
+    for (; u < a.last; u += waves) {
+        const int64_t row = one_row ? 0 : u / a.slabs;
+        const int64_t c = ((u - row * a.slabs) * kWave + lane_id()) * kVecBytes;
+        char* p = a.grad + row * a.stride_bytes + c;
+        if (c + kVecBytes <= a.row_bytes) {
+            __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4_a2*>(p));
+        } else {
+            for (int64_t e = c; e < a.row_bytes; e += 2) *reinterpret_cast<uint16_t*>(a.grad + row * a.stride_bytes + e) = 0;
+        }
     }
 }
 
@@ -68,9 +122,10 @@ constexpr int kRankTokens = kThreads / kRankParts; // tokens per workgroup
 template <typename ID>
 __global__ __launch_bounds__(kThreads) void token_rank_sort_kernel(const ID* __restrict__ ids, uint32_t n,
                                                                    int64_t rows, uint32_t* __restrict__ keys,
-                                                                   uint32_t* __restrict__ places)
+                                                                   uint32_t* __restrict__ places, ClearArgs clear)
 {
     extern __shared__ __align__(16) uint32_t s_key[];  // n rounded up to 64 keys
+    if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kThreads>(clear);
     const uint32_t padded = (n + 63u) & ~63u;
     for (uint32_t j = threadIdx.x; j < padded; j += kThreads) s_key[j] = j < n ? token_key(ids[j], rows) : 0xFFFFFFFFu;
     __syncthreads();
@@ -92,34 +147,155 @@ __global__ __launch_bounds__(kThreads) void token_rank_sort_kernel(const ID* __r
     }
 }
 
-// Keys for the counting-sort passes: the key written in base `base` (at most
-// 511, the most buckets a pass has), kDigitBits bits to a digit, so that two
-// passes order up to 511^2 - 1 = 261,120 rows where 8-bit digits would need
-// three. Digits keep the order of the keys.
+// From kRankSortMax to kTileSortMax tokens: stable counting passes over digits
+// of up to 9 bits, two for up to 2^18 - 1 rows, in one launch to count the
+// first digit and one per pass. A table holds the count of every digit in
+// every tile, digit by digit; each workgroup of a pass sums it up for itself
+// (at most 128 tiles, read from the cache) instead of waiting for a scan
+// launched in between, and counts the next digit of what it places with
+// atomics on the next table (whole numbers: any order gives the same counts).
+// Against the library's general passes (a count, a look-back scan and a
+// scatter launch each, and one launch for the keys) this takes 4 launches
+// fewer for two digits.
+constexpr int64_t kTileSortMax = 262144;
+constexpr int kTileThreads = 512;
+constexpr int kTileWaves = kTileThreads / kWave;
 constexpr int kDigitBits = 9;
+static_assert(1 << kDigitBits == kTileThreads, "one digit per thread");
+
+struct TileSort {
+    uint32_t n;
+    int64_t rows;
+    int bits, digits;          // of a digit; digits of a key
+    int items;                 // keys per thread: tiles of kTileThreads * items
+    int tiles, stride;         // stride: entries per digit in a table, tiles rounded up to 4
+    uint32_t* tables;          // [digits][1 << bits][stride]
+};
 
 template <typename ID>
-__global__ __launch_bounds__(kThreads) void token_digits_kernel(const ID* __restrict__ ids, int64_t n, int64_t rows,
-                                                                uint32_t base, int digits,
-                                                                uint32_t* __restrict__ keys,
-                                                                uint32_t* __restrict__ index)
+__global__ __launch_bounds__(kTileThreads) void token_count_kernel(const ID* __restrict__ ids, TileSort a,
+                                                                   uint32_t* __restrict__ keys, ClearArgs clear)
 {
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= n) return;
-    uint32_t key = token_key(ids[i], rows), packed = 0;
-    for (int d = 0; d < digits; ++d) {
-        packed |= (key % base) << (d * kDigitBits);
-        key /= base;
+    __shared__ uint32_t s_count[kTileThreads];
+    if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kTileThreads>(clear);
+    const uint32_t size = 1u << a.bits;
+    s_count[threadIdx.x] = 0;
+    // the tables of the later digits are counted into by the passes
+    const uint32_t words = size * (uint32_t)a.stride;
+    for (uint32_t i = words + blockIdx.x * kTileThreads + threadIdx.x; i < words * a.digits; i += a.tiles * kTileThreads)
+        a.tables[i] = 0;
+    __syncthreads();
+    const uint32_t first = blockIdx.x * (uint32_t)(kTileThreads * a.items);
+    for (int k = 0; k < a.items; ++k) {
+        const uint32_t i = first + k * kTileThreads + threadIdx.x;
+        if (i < a.n) {
+            const uint32_t key = token_key(ids[i], a.rows);
+            keys[i] = key;
+            atomicAdd(&s_count[key & (size - 1)], 1u);
+        }
     }
-    keys[i] = packed;
-    index[i] = (uint32_t)i;
+    __syncthreads();
+    if (threadIdx.x < size) a.tables[threadIdx.x * a.stride + blockIdx.x] = s_count[threadIdx.x];
 }
 
-__device__ __forceinline__ uint32_t digits_key(uint32_t packed, uint32_t base, int digits)
+// Pass `digit`: keys (and their positions; null: keys are in input order) to
+// their places by that digit.
+template <int ITEMS>
+__global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t* __restrict__ keys,
+                                                                  const uint32_t* __restrict__ index, TileSort a,
+                                                                  int digit, uint32_t* __restrict__ keys_out,
+                                                                  uint32_t* __restrict__ index_out, ClearArgs clear)
 {
-    uint32_t key = 0;
-    for (int d = digits - 1; d >= 0; --d) key = key * base + ((packed >> (d * kDigitBits)) & ((1u << kDigitBits) - 1u));
-    return key;
+    __shared__ uint32_t s_count[kTileWaves][kTileThreads];  // of each wave, then of the waves before it
+    __shared__ uint32_t s_base[kTileThreads];
+    __shared__ uint32_t s_wave[kTileWaves];
+    if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kTileThreads>(clear);
+    const int lane = lane_id(), wave = (int)(threadIdx.x / kWave), tile = blockIdx.x;
+    const uint32_t size = 1u << a.bits, shift = (uint32_t)(digit * a.bits);
+    // this thread's keys, in input order along the wave's segment of the tile
+    const uint32_t seg = (uint32_t)tile * (kTileThreads * ITEMS) + wave * (kWave * ITEMS) + lane;
+    uint32_t key[ITEMS], pos[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const uint32_t i = seg + k * kWave;
+        key[k] = i < a.n ? keys[i] : 0u;
+        pos[k] = i < a.n && index ? index[i] : i;
+    }
+    // digit d = this thread: keys of smaller digits and, of its own, those of the tiles before
+    const uint32_t* table = a.tables + (size_t)digit * size * a.stride;
+    uint32_t total = 0, before = 0;
+    if (threadIdx.x < size) {
+        const u32x4* row = reinterpret_cast<const u32x4*>(table + threadIdx.x * a.stride);
+#pragma unroll 8
+        for (int t = 0; t < a.stride; t += 4) {
+            const u32x4 c = row[t / 4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t v = t + q < a.tiles ? c[q] : 0u;
+                total += v;
+                before += t + q < tile ? v : 0u;
+            }
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) s_count[w][threadIdx.x] = 0;
+    const uint32_t incl = wave_inclusive_scan(total);
+    if (lane == kWave - 1) s_wave[wave] = incl;
+    __syncthreads();
+    uint32_t start = incl - total + before;
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) start += w < wave ? s_wave[w] : 0u;
+    // rank among the wave's keys of the same digit that come before
+    uint32_t rank[ITEMS], d[ITEMS];
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const bool live = seg + k * kWave < a.n;
+        d[k] = (key[k] >> shift) & (size - 1);
+        uint64_t same = ballot(live);
+        for (int b = 0; b < a.bits; ++b) {
+            const bool bit = (d[k] >> b) & 1u;
+            const uint64_t set = ballot(bit);
+            same &= bit ? set : ~set;
+        }
+        const uint32_t below = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
+        const uint32_t run = s_count[wave][d[k]];
+        if (live && below == 0) s_count[wave][d[k]] = run + (uint32_t)__builtin_popcountll(same);
+        rank[k] = run + below;
+    }
+    __syncthreads();
+    uint32_t sum = start;
+#pragma unroll
+    for (int w = 0; w < kTileWaves; ++w) {
+        const uint32_t c = s_count[w][threadIdx.x];
+        s_count[w][threadIdx.x] = sum;
+        sum += c;
+    }
+    __syncthreads();
+    const bool more = digit + 1 < a.digits;
+    uint32_t* next = a.tables + (size_t)(digit + 1) * size * a.stride;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        if (seg + k * kWave < a.n) {
+            const uint32_t to = s_count[wave][d[k]] + rank[k];
+            keys_out[to] = key[k];
+            index_out[to] = pos[k];
+            if (more)
+                atomicAdd(&next[((key[k] >> (shift + a.bits)) & (size - 1)) * a.stride + to / (kTileThreads * ITEMS)], 1u);
+        }
+    }
+}
+
+// Above kTileSortMax tokens: keys and positions for the radix passes.
+template <typename ID>
+__global__ __launch_bounds__(kThreads) void token_keys_kernel(const ID* __restrict__ ids, int64_t n, int64_t rows,
+                                                              uint32_t* __restrict__ keys, uint32_t* __restrict__ index,
+                                                              ClearArgs clear)
+{
+    if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kThreads>(clear);
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= n) return;
+    keys[i] = token_key(ids[i], rows);
+    index[i] = (uint32_t)i;
 }
 
 // ---------------------------------------------------------------------------
@@ -132,11 +308,10 @@ __device__ __forceinline__ uint32_t digits_key(uint32_t packed, uint32_t base, i
 // adds the parts up in order.
 // ---------------------------------------------------------------------------
 struct GradArgs {
-    const uint32_t* keys;   // sorted; packed digits where digits > 0
+    const uint32_t* keys;   // sorted
     const uint32_t* index;  // position of each sorted token in the input
     int64_t n, rows, dim, dout_stride, grad_stride;
-    uint32_t base;
-    int digits, chunk, add;
+    int chunk;
     float scale;
     float* partial;  // [chunks][2][dim rounded up to whole slabs]
     int64_t partial_stride;
@@ -144,134 +319,184 @@ struct GradArgs {
 
 __device__ __forceinline__ uint32_t key_at(const GradArgs& a, int64_t p)
 {
-    if (p < 0 || p >= a.n) return 0xFFFFFFFFu;
-    const uint32_t k = a.keys[p];
-    return a.digits ? digits_key(k, a.base, a.digits) : k;
+    return p >= 0 && p < a.n ? a.keys[p] : 0xFFFFFFFFu;
 }
 
-template <typename O, int N>
-__device__ __forceinline__ void write_row(const GradArgs& a, O* grad, uint32_t key, int64_t c, const float (&acc)[N])
+// One 16-byte load of elements at .. at + N - 1 from `base`, moved down where
+// it would pass `limit` elements (the buffer's end): element j is then at
+// place j + shift. limit >= N.
+template <typename T>
+__device__ __forceinline__ u32x4 load_window(const T* __restrict__ base, int64_t at, int64_t limit)
 {
-    O* p = grad + (int64_t)key * a.grad_stride + c;
-    const int64_t valid = a.dim - c;
-    float x[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) x[j] = acc[j] * a.scale;
-    if (a.add) {
-        constexpr int kPer = Vec16<O>::kN;
-#pragma unroll
-        for (int v = 0; v < N / kPer; ++v) {
-            float old[kPer];
-            load_floats<O, kPer>(p + v * kPer, valid - v * kPer, old);
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) x[v * kPer + j] += old[j];
-        }
+    constexpr int N = Vec16<T>::kN;
+    return *reinterpret_cast<const typename Vec16<T>::type*>(base + (at + N <= limit ? at : limit - N));
+}
+
+template <typename T>
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int elems)
+{
+    const int bytes = elems * (int)sizeof(T);
+    if (bytes & 8) v = u32x4{v[2], v[3], 0u, 0u};
+    if (bytes & 4) v = u32x4{v[1], v[2], v[3], 0u};
+    if constexpr (sizeof(T) == 2) {
+        if (bytes & 2)
+            v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
     }
-    store_floats<O, N>(p, valid, x);
+    return v;
 }
 
-template <int N>
-__device__ __forceinline__ void write_partial(const GradArgs& a, int64_t chunk, int which, int64_t c,
-                                              const float (&acc)[N])
-{
-    store_floats<float, N>(a.partial + (chunk * 2 + which) * a.partial_stride + c, N, acc);
-}
-
-template <typename T, typename O>
+// ADD: the rows that end in the chunk are loaded with the terms, not when the
+// run's sum is ready: a load behind every run is what bounded this otherwise.
+template <typename T, typename O, bool ADD>
 __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __restrict__ dout, O* __restrict__ grad,
                                                                  GradArgs a, int64_t slabs, int64_t units)
 {
-    constexpr int N = Vec16<T>::kN;
-    constexpr int kAhead = 8;  // rows in flight
+    constexpr int N = Vec16<T>::kN, kPer = Vec16<O>::kN;
+    constexpr int kAhead = ADD ? 4 : 8;  // rows in flight
     const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (unit >= units) return;
-    const int64_t chunk = unit / slabs, c = ((unit % slabs) * kWave + lane_id()) * N;
-    const int64_t p0 = chunk * a.chunk;
     const int lane = lane_id();
-    const uint32_t key = lane < a.chunk ? key_at(a, p0 + lane) : 0xFFFFFFFFu;
-    const uint32_t before = key_at(a, p0 - 1), after = key_at(a, p0 + a.chunk);
-    const uint32_t index = lane < a.chunk && p0 + lane < a.n ? a.index[p0 + lane] : 0u;
+    const int64_t chunk = unit / slabs, c = ((unit % slabs) * kWave + lane) * N;
+    const int64_t p0 = chunk * a.chunk;
+    const bool mine = lane < a.chunk;
+    const uint32_t key = mine ? key_at(a, p0 + lane) : 0xFFFFFFFFu;
+    const uint32_t next = mine ? key_at(a, p0 + lane + 1) : 0xFFFFFFFFu;
+    const uint32_t before = key_at(a, p0 - 1);
+    const uint32_t index = mine && p0 + lane < a.n ? a.index[p0 + lane] : 0u;
     const int count = __builtin_popcountll(ballot(key < (uint32_t)a.rows));
     if (count == 0) return;
+    const uint64_t ends = ballot(key != next);  // the run ends at this position
+    bool opened = readlane(key, 0) == before;   // the current run began in an earlier chunk
+    const bool live = c < a.dim;
+    const int64_t col = live ? c : 0, valid = a.dim - col;
+    const int64_t limit = (a.n - 1) * a.dout_stride + a.dim;
     float acc[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
-    uint32_t run = readlane(key, 0);
-    bool opened = run == before;  // the current run began in an earlier chunk
-    const bool live = c < a.dim;
     for (int i0 = 0; i0 < count; i0 += kAhead) {
-        float x[kAhead][N];
+        u32x4 x[kAhead];
+        float old[ADD ? kAhead : 1][N];
+        if (limit >= N) {
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-            if (i0 + i < count && live)
-                load_floats<T, N>(dout + (int64_t)readlane(index, i0 + i) * a.dout_stride + c, a.dim - c, x[i]);
+            for (int i = 0; i < kAhead; ++i)
+                x[i] = load_window(dout, (int64_t)readlane(index, i0 + i < count ? i0 + i : count - 1) * a.dout_stride + col,
+                                   limit);
+        } else {  // fewer than N elements in all
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const T* row = dout + (int64_t)readlane(index, i0 + i < count ? i0 + i : count - 1) * a.dout_stride + col;
+                T t[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) t[j] = j < valid ? row[j] : (T)0.0f;
+                __builtin_memcpy(&x[i], t, sizeof(t));
+            }
+        }
+        if constexpr (ADD) {
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (i0 + i < count && ((ends >> (i0 + i)) & 1u)) {
+                    const O* p = grad + (int64_t)readlane(key, i0 + i) * a.grad_stride + col;
+#pragma unroll
+                    for (int v = 0; v < N / kPer; ++v) {
+                        float o[kPer];
+                        load_floats<O, kPer>(p + v * kPer, valid - v * kPer, o);
+#pragma unroll
+                        for (int j = 0; j < kPer; ++j) old[i][v * kPer + j] = o[j];
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
-            if (i0 + i < count) {
-                const uint32_t k = readlane(key, i0 + i);
-                if (k != run) {
-                    if (live) {
-                        if (opened)
-                            write_partial<N>(a, chunk, 0, c, acc);
-                        else
-                            write_row<O, N>(a, grad, run, c, acc);
+            if (i0 + i < count) {  // uniform
+                const int64_t over =
+                    limit < N ? 0 : (int64_t)readlane(index, i0 + i) * a.dout_stride + col + N - limit;
+                u32x4 v = x[i];
+                if (ballot(over > 0)) v = shift_down<T>(v, over > 0 ? (int)over : 0);
+                T t[N];
+                __builtin_memcpy(t, &v, sizeof(t));
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] += (float)t[j];
+                if ((ends >> (i0 + i)) & 1u) {
+                    if (opened) {
+                        store_floats<float, N>(a.partial + chunk * 2 * a.partial_stride + c, N, acc);
+                    } else if (live) {
+                        float y[N];
+#pragma unroll
+                        for (int j = 0; j < N; ++j) {
+                            y[j] = acc[j] * a.scale;
+                            if constexpr (ADD) y[j] += old[i][j];
+                        }
+                        store_floats<O, N>(grad + (int64_t)readlane(key, i0 + i) * a.grad_stride + c, valid, y);
                     }
                     opened = false;
-                    run = k;
 #pragma unroll
                     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
                 }
-#pragma unroll
-                for (int j = 0; j < N; ++j) acc[j] += x[i][j];
             }
         }
     }
-    if (!live) return;
-    if (opened)
-        write_partial<N>(a, chunk, 0, c, acc);
-    else if (run == after)
-        write_partial<N>(a, chunk, 1, c, acc);
-    else
-        write_row<O, N>(a, grad, run, c, acc);
+    if (!((ends >> (count - 1)) & 1u))  // the last run goes on
+        store_floats<float, N>(a.partial + (chunk * 2 + (opened ? 0 : 1)) * a.partial_stride + c, N, acc);
 }
 
-// The rows whose runs cross chunks: the wave of the chunk in which such a run
-// begins adds its part and the first parts of the chunks that it reaches.
-template <typename O, int N>
-__global__ __launch_bounds__(kThreads) void embedding_join_kernel(O* __restrict__ grad, GradArgs a, int64_t slabs,
+// The rows whose runs cross chunks: the waves of the chunk in which such a run
+// begins, two columns per lane, add its part and the first parts of the chunks
+// that it reaches. kJoinAhead parts are in flight: a token that fills hundreds
+// of chunks is a chain of that many additions for one wave.
+constexpr int kJoinCols = 2;
+constexpr int kJoinAhead = 16;
+
+template <typename O, bool ADD>
+__global__ __launch_bounds__(kThreads) void embedding_join_kernel(O* __restrict__ grad, GradArgs a, int64_t groups,
                                                                   int64_t units)
 {
     const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     if (unit >= units) return;
-    const int64_t chunk = unit / slabs, c = ((unit % slabs) * kWave + lane_id()) * N;
+    const int lane = lane_id();
+    const int64_t chunk = unit / groups, c = ((unit % groups) * kWave + lane) * kJoinCols;
     const int64_t p0 = chunk * a.chunk, end = p0 + a.chunk;
     const uint32_t run = key_at(a, end - 1);
-    if (run >= (uint32_t)a.rows || run != key_at(a, end)) return;      // no run goes on from here
-    if (run == key_at(a, p0) && run == key_at(a, p0 - 1)) return;      // it began earlier
-    if (c >= a.dim) return;
-    float acc[N];
-    const float* p = a.partial + (chunk * 2 + 1) * a.partial_stride + c;
-#pragma unroll
-    for (int j = 0; j < N; ++j) acc[j] = p[j];
-    for (int64_t q = chunk + 1; key_at(a, q * a.chunk) == run; ++q) {
-        p = a.partial + q * 2 * a.partial_stride + c;
-#pragma unroll
-        for (int j = 0; j < N; ++j) acc[j] += p[j];
+    // one look at this chunk's edges (lane 0 the key before it, 1 its first) and at where the next 61 chunks begin
+    const uint32_t edge = key_at(a, lane == 0 ? p0 - 1 : lane == 1 ? p0 : end + (int64_t)(lane - 2) * a.chunk);
+    if (run >= (uint32_t)a.rows || run != readlane(edge, 2)) return;            // no run goes on from here
+    if (run == readlane(edge, 1) && run == readlane(edge, 0)) return;           // it began earlier
+    int64_t reached = __builtin_ctzll(~(ballot(edge == run) >> 2) | 1ull << 62);  // chunks that it reaches
+    for (bool more = reached == 62; more;) {
+        const uint64_t same = ballot(key_at(a, end + (reached + lane) * a.chunk) == run);
+        reached += ~same ? __builtin_ctzll(~same) : kWave;
+        more = !~same;
     }
-    write_row<O, N>(a, grad, run, c, acc);
-}
-
-// Zeros for a whole gradient (rows of `dim` elements, `stride` apart).
-template <typename O>
-__global__ __launch_bounds__(kThreads) void embedding_clear_kernel(O* __restrict__ grad, int64_t rows, int64_t dim,
-                                                                   int64_t stride, int64_t slabs)
-{
-    constexpr int N = Vec16<O>::kN;
-    const int64_t units = rows * slabs, waves = (int64_t)gridDim.x * kWaves;
-    for (int64_t u = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; u < units; u += waves) {
-        const int64_t c = ((u % slabs) * kWave + lane_id()) * N;
-        const float x[N] = {};
-        if (c < dim) store_floats<O, N>(grad + (u / slabs) * stride + c, dim - c, x);
+    const bool live = c < a.dim;
+    if (!live) return;
+    const float* p = a.partial + (chunk * 2 + 1) * a.partial_stride + c;
+    float acc[kJoinCols];
+#pragma unroll
+    for (int j = 0; j < kJoinCols; ++j) acc[j] = p[j];
+    p += a.partial_stride;  // the first parts of the chunks after it
+    for (int64_t q0 = 0; q0 < reached; q0 += kJoinAhead) {
+        float x[kJoinAhead][kJoinCols];
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k) {
+            const int64_t q = q0 + k < reached ? q0 + k : reached - 1;
+#pragma unroll
+            for (int j = 0; j < kJoinCols; ++j) x[k][j] = p[q * 2 * a.partial_stride + j];
+        }
+#pragma unroll
+        for (int k = 0; k < kJoinAhead; ++k)
+            if (q0 + k < reached) {
+#pragma unroll
+                for (int j = 0; j < kJoinCols; ++j) acc[j] += x[k][j];
+            }
+    }
+    O* out = grad + (int64_t)run * a.grad_stride + c;
+#pragma unroll
+    for (int j = 0; j < kJoinCols; ++j) {
+        if (c + j < a.dim) {
+            float y = acc[j] * a.scale;
+            if constexpr (ADD) y += (float)out[j];
+            out[j] = (O)y;
+        }
     }
 }
 
@@ -279,6 +504,7 @@ __global__ __launch_bounds__(kThreads) void embedding_clear_kernel(O* __restrict
 // Launchers
 // ---------------------------------------------------------------------------
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+constexpr int64_t kClearBlocks = 2048;  // at most, per launch
 
 static int lookup_lanes(ElemKind kind, int64_t dim)
 {
@@ -323,28 +549,7 @@ hipError_t launch_embedding(ElemKind kind, const void* table, int64_t rows, int6
     }
 }
 
-int64_t embedding_most_rows()
-{
-    const int64_t most = sort_max_buckets();  // three digits of kDigitBits bits fit a 32-bit key
-    return most * most * most - 1;
-}
-
-// Digits of the counting-sort passes: the fewest, and the smallest base that
-// still holds the keys 0 .. rows.
-static void sort_digits(int64_t rows, uint32_t* base, int* digits)
-{
-    const int64_t most = sort_max_buckets();
-    int d = 1;
-    for (int64_t reach = most; reach < rows + 1; reach *= most) ++d;
-    int64_t b = 2;
-    for (;; ++b) {
-        int64_t reach = 1;
-        for (int i = 0; i < d; ++i) reach *= b;
-        if (reach >= rows + 1) break;
-    }
-    *base = (uint32_t)b;
-    *digits = d;
-}
+int64_t embedding_most_rows() { return ((int64_t)1 << 27) - 1; }
 
 // Positions per chunk: 64 where that leaves work for every CU, fewer for few
 // tokens, so that more waves share the rows.
@@ -363,8 +568,20 @@ EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, in
     p.chunk = sum_chunk(n, p.slabs);
     p.chunks = ceil_div(n, p.chunk);
     p.partial_stride = p.slabs * kWave * per;
-    if (n > kRankSortMax) sort_digits(rows, &p.base, &p.digits);
-    p.table_words = p.digits ? sort_pass_words(n, p.base) : 0;
+    int bits = 1;
+    while (((int64_t)1 << bits) < rows + 1) ++bits;
+    if (n > kTileSortMax) {
+        p.radix_bits = 8;
+        p.digits = (bits + 7) / 8;
+        p.table_words = sort_aux_words(true, n, p.radix_bits);
+    } else if (n > kRankSortMax) {
+        p.digits = (bits + kDigitBits - 1) / kDigitBits;
+        p.bits = (bits + p.digits - 1) / p.digits;
+        p.items = n > kTileSortMax / 2 ? 4 : 2;
+        p.tiles = (int)ceil_div(n, kTileThreads * p.items);
+        p.table_words = (int64_t)p.digits * ((int64_t)ceil_div(p.tiles, 4) * 4 << p.bits);
+    }
+    p.table_words = ceil_div(p.table_words, 4) * 4;
     // keys and index, twice where passes go back and forth; then the parts of rows, 16-byte aligned
     const int64_t words = p.table_words + n * (p.digits ? 4 : 2);
     p.partial_at = ceil_div(words, 4) * 16;
@@ -372,33 +589,56 @@ EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, in
     return p;
 }
 
-template <typename T, typename O>
-static hipError_t embedding_grad_typed(const EmbeddingGradPlan& p, const void* dout, int64_t dout_stride, int64_t n,
-                                       int64_t rows, int64_t dim, float scale, void* grad, int64_t grad_stride,
-                                       bool add, const uint32_t* keys, const uint32_t* index, char* aux,
+template <typename T, typename O, bool ADD>
+static hipError_t embedding_grad_typed(const EmbeddingGradPlan& p, const void* dout, void* grad, const GradArgs& a,
                                        hipStream_t stream)
 {
-    constexpr int N = Vec16<T>::kN;
-    const GradArgs a{keys, index, n, rows, dim, dout_stride, grad_stride, p.base, p.digits, p.chunk, add ? 1 : 0,
-                     scale, reinterpret_cast<float*>(aux + p.partial_at), p.partial_stride};
     const int64_t units = p.chunks * p.slabs;
-    const dim3 grid((unsigned)ceil_div(units, kWaves)), block(kThreads);
-    embedding_sum_kernel<T, O><<<grid, block, 0, stream>>>((const T*)dout, (O*)grad, a, p.slabs, units);
+    embedding_sum_kernel<T, O, ADD><<<dim3((unsigned)ceil_div(units, kWaves)), dim3(kThreads), 0, stream>>>(
+        (const T*)dout, (O*)grad, a, p.slabs, units);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    embedding_join_kernel<O, N><<<grid, block, 0, stream>>>((O*)grad, a, p.slabs, units);
+    const int64_t groups = ceil_div(a.dim, kWave * kJoinCols), joins = p.chunks * groups;
+    embedding_join_kernel<O, ADD><<<dim3((unsigned)ceil_div(joins, kWaves)), dim3(kThreads), 0, stream>>>((O*)grad, a,
+                                                                                                       groups, joins);
     return hipGetLastError();
 }
 
-template <typename O>
-static hipError_t clear_typed(void* grad, int64_t rows, int64_t dim, int64_t stride, hipStream_t stream)
+int64_t embedding_grad_blocks(const EmbeddingGradPlan& p, int64_t n, int64_t dim)
 {
-    const int64_t slabs = ceil_div(dim, kWave * Vec16<O>::kN);
-    const int64_t blocks = ceil_div(rows * slabs, kWaves);
-    embedding_clear_kernel<O><<<dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(kThreads), 0, stream>>>(
-        (O*)grad, rows, dim, stride, slabs);
-    return hipGetLastError();
+    const int64_t join = ceil_div(p.chunks * ceil_div(dim, kWave * kJoinCols), kWaves), keys = ceil_div(n, kThreads);
+    const int64_t sum = ceil_div(p.chunks * p.slabs, kWaves), most = join > sum ? join : sum;
+    return (most > keys ? most : keys) + kClearBlocks;
 }
+
+// The launches of a sort take equal shares of the clearing.
+struct Clearing {
+    ClearArgs a;
+    int64_t units, share;
+    Clearing(bool add, void* grad, int64_t rows, int64_t dim, int64_t stride, int esz, int launches)
+    {
+        a.grad = static_cast<char*>(grad);
+        a.row_bytes = dim * esz;
+        a.stride_bytes = stride * esz;
+        if (stride == dim) {  // one long row
+            a.row_bytes *= rows;
+            rows = 1;
+        }
+        a.slabs = ceil_div(a.row_bytes, kWave * kVecBytes);
+        units = add ? 0 : rows * a.slabs;
+        share = ceil_div(units, launches);
+        a.first = a.last = 0;
+    }
+    // The next launch's part, behind `before` workgroups of `threads`; returns the workgroups in all.
+    unsigned next(int64_t before, int threads)
+    {
+        a.first = a.last;
+        a.last = a.first + share < units ? a.first + share : units;
+        a.skip = (int)before;
+        const int64_t blocks = ceil_div(a.last - a.first, threads / kWave);
+        return (unsigned)(before + (blocks < kClearBlocks ? blocks : kClearBlocks));
+    }
+};
 
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& p, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
@@ -406,42 +646,60 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
                                  const DevWs& ws, uint32_t spin_limit, hipStream_t stream)
 {
     hipError_t e = hipSuccess;
-    if (!add) {
-        if (grad_kind == kF32) e = clear_typed<float>(grad, rows, dim, grad_stride, stream);
-        else e = clear_typed<bf16>(grad, rows, dim, grad_stride, stream);  // any 16-bit type: zero bits
-        if (e != hipSuccess) return e;
-    }
-    if (n == 0) return hipSuccess;
     uint32_t* table = reinterpret_cast<uint32_t*>(aux);
     uint32_t* keys = table + p.table_words;
-    uint32_t* index = keys + n;
-    if (!p.digits) {
-        const dim3 grid((unsigned)ceil_div(n, kRankTokens)), block(kThreads);
-        const size_t lds = (size_t)((n + 63) / 64 * 64) * 4;
+    uint32_t *index = keys + n, *keys2 = index + n, *index2 = keys2 + n;
+    const bool tiled = p.tiles > 0;
+    Clearing clear(add, grad, rows, dim, grad_stride, grad_kind == kF32 ? 4 : 2, tiled ? 1 + p.digits : 1);
+    if (p.radix_bits || n == 0) {
+        const unsigned grid = clear.next(ceil_div(n, kThreads), kThreads);
         if (wide_ids)
-            token_rank_sort_kernel<int64_t><<<grid, block, lds, stream>>>((const int64_t*)ids, (uint32_t)n, rows, keys, index);
+            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int64_t*)ids, n, rows, keys, index, clear.a);
         else
-            token_rank_sort_kernel<int32_t><<<grid, block, lds, stream>>>((const int32_t*)ids, (uint32_t)n, rows, keys, index);
+            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int32_t*)ids, n, rows, keys, index, clear.a);
         e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    } else {
-        const dim3 grid((unsigned)ceil_div(n, kThreads)), block(kThreads);
-        if (wide_ids)
-            token_digits_kernel<int64_t><<<grid, block, 0, stream>>>((const int64_t*)ids, n, rows, p.base, p.digits, keys, index);
-        else
-            token_digits_kernel<int32_t><<<grid, block, 0, stream>>>((const int32_t*)ids, n, rows, p.base, p.digits, keys, index);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        uint32_t *keys2 = index + n, *index2 = keys2 + n;
+        if (e != hipSuccess || n == 0) return e;
         for (int d = 0; d < p.digits; ++d) {
-            e = launch_sort_pass(keys, index, keys2, index2, n, d * kDigitBits, p.base, table, ws, spin_limit, stream);
+            e = launch_radix_pass(keys, index, keys2, index2, n, d * p.radix_bits, p.radix_bits, table, ws, spin_limit, stream);
             if (e != hipSuccess) return e;
             uint32_t* t = keys; keys = keys2; keys2 = t;
             t = index; index = index2; index2 = t;
         }
+    } else if (tiled) {
+        const TileSort a{(uint32_t)n, rows, p.bits, p.digits, p.items, p.tiles, (int)(ceil_div(p.tiles, 4) * 4), table};
+        unsigned grid = clear.next(p.tiles, kTileThreads);
+        if (wide_ids)
+            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)ids, a, keys, clear.a);
+        else
+            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)ids, a, keys, clear.a);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        for (int d = 0; d < p.digits; ++d) {
+            grid = clear.next(p.tiles, kTileThreads);
+            const auto kernel = p.items == 2 ? token_pass_kernel<2> : token_pass_kernel<4>;
+            kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>(keys, d ? index : nullptr, a, d, keys2, index2, clear.a);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            uint32_t* t = keys; keys = keys2; keys2 = t;
+            t = index; index = index2; index2 = t;
+        }
+    } else {
+        const unsigned grid = clear.next(ceil_div(n, kRankTokens), kThreads);
+        const size_t lds = (size_t)((n + 63) / 64 * 64) * 4;
+        if (wide_ids)
+            token_rank_sort_kernel<<<dim3(grid), dim3(kThreads), lds, stream>>>((const int64_t*)ids, (uint32_t)n, rows,
+                                                                               keys, index, clear.a);
+        else
+            token_rank_sort_kernel<<<dim3(grid), dim3(kThreads), lds, stream>>>((const int32_t*)ids, (uint32_t)n, rows,
+                                                                               keys, index, clear.a);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
-#define DS_GRAD(T, O) \
-    return embedding_grad_typed<T, O>(p, dout, dout_stride, n, rows, dim, scale, grad, grad_stride, add, keys, index, aux, stream)
+    const GradArgs a{keys, index, n, rows, dim, dout_stride, grad_stride, p.chunk, scale,
+                     reinterpret_cast<float*>(aux + p.partial_at), p.partial_stride};
+#define DS_GRAD(T, O)                                                              \
+    return add ? embedding_grad_typed<T, O, true>(p, dout, grad, a, stream) \
+               : embedding_grad_typed<T, O, false>(p, dout, grad, a, stream)
     if (kind == kF32 && grad_kind == kF32) DS_GRAD(float, float);
     if (kind == kBF16 && grad_kind == kBF16) DS_GRAD(bf16, bf16);
     if (kind == kBF16 && grad_kind == kF32) DS_GRAD(bf16, float);

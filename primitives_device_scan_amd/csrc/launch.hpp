@@ -84,15 +84,6 @@ struct MoeOut {
 hipError_t launch_moe_align(const int32_t* ids, int64_t n, int experts, const MoeOut& out, uint32_t* hist,
                             uint32_t* slots, const DevWs& ws, uint32_t spin_limit, hipStream_t stream);
 
-// One stable key-value pass over digits (key >> shift) & 511 that are all below
-// `buckets` (<= sort_max_buckets()), in tiles of moe_tile_elems() keys; table:
-// sort_pass_words() 32-bit words of scratch; ws: look-back workspace for a
-// scan of that many words.
-int64_t sort_pass_words(int64_t n, uint32_t buckets);
-hipError_t launch_sort_pass(const uint32_t* keys, const uint32_t* vals_in, uint32_t* keys_out, uint32_t* vals_out,
-                            int64_t n, int shift, uint32_t buckets, uint32_t* table, const DevWs& ws,
-                            uint32_t spin_limit, hipStream_t stream);
-
 // Token embedding and the gradient of its table (float kinds).
 int64_t embedding_blocks(ElemKind kind, int64_t n, int64_t dim);  // workgroups of a lookup
 hipError_t launch_embedding(ElemKind kind, const void* table, int64_t rows, int64_t dim, int64_t table_stride,
@@ -100,8 +91,9 @@ hipError_t launch_embedding(ElemKind kind, const void* table, int64_t rows, int6
                             hipStream_t stream);
 
 struct EmbeddingGradPlan {
-    uint32_t base;           // counting-sort digits are below this; 0 with digits == 0
-    int digits;              // counting-sort passes; 0: one launch sorts by rank
+    int digits;              // sorting passes; 0: one launch sorts by rank
+    int radix_bits;          // of a digit of the radix passes, or 0
+    int bits, items, tiles;  // of a digit, keys per thread and tiles of the small passes, or 0
     int chunk;               // sorted positions per wave
     int64_t slabs, chunks;   // units of work: slabs x chunks
     int64_t partial_stride;  // elements between rows of the crossing runs' parts
@@ -110,7 +102,8 @@ struct EmbeddingGradPlan {
     int64_t bytes;           // scratch in all
 };
 EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, int64_t dim);
-int64_t embedding_most_rows();  // rows that the passes' digits can tell apart
+int64_t embedding_most_rows();
+int64_t embedding_grad_blocks(const EmbeddingGradPlan& plan, int64_t n, int64_t dim);  // workgroups of the largest launch, or more
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& plan, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
                                  int64_t dim, float scale, void* grad, int64_t grad_stride, bool add, char* aux,

@@ -119,9 +119,30 @@ def test_grad(dtype, idt, n, dim, rows):
 @pytest.mark.parametrize("n", [RANK_MAX - 1, RANK_MAX, RANK_MAX + 1, 20_000])
 @pytest.mark.parametrize("rows", [2, 600, 262_000])
 def test_grad_both_sorts(n, rows):
-    # up to 8,192 ids are sorted by rank, more by counting-sort passes: one for 2 rows, two for 600, three for 262,000
+    # up to 8,192 ids are sorted by rank, more by counting passes over 9 bits: one for 2 rows, two for the others
     dout, ids = normal(n, (n, 12), torch.bfloat16), token_ids(n + 7, n, rows)
     check_grad(dout, ids, rows, 1.0, torch.float32, what=f"{n} ids, {rows} rows")
+
+
+@pytest.mark.parametrize("n,rows", [(9_000, 600_000), (131_072, 5000), (131_073, 262_143), (150_001, 262_144),
+                                    (262_144, 70), (262_145, 70), (300_001, 70_000)])
+def test_grad_long_sorts(n, rows):
+    # three passes, tiles of 1,024 and of 2,048 ids, and above 262,144 ids the radix passes
+    dout, ids = normal(n, (n, 3), torch.bfloat16), token_ids(n + 9, n, rows)
+    check_grad(dout, ids, rows, 1.0, torch.float32, what=f"{n} ids, {rows} rows")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,dim", [(1, 1), (1, 7), (2, 1), (2, 3), (3, 2), (5, 9), (40, 15), (33, 531)])
+def test_grad_reads_stay_inside(dtype, n, dim):
+    # the gradient of the last rows of a buffer that ends with them; what lies behind is NaN and must not be seen
+    room = torch.full((n * dim + 64,), float("nan"), dtype=dtype, device="cuda")
+    dout = room[:n * dim].view(n, dim)
+    dout.copy_(normal(n + dim, (n, dim), dtype))
+    ids = token_ids(dim, n, 4, bad=0.0)
+    got = ds.embedding_grad(dout, ids.cuda(), 4)
+    ref, c, s = mo.embedding_grad(mo.f64(dout), ids.numpy(), 4, 1.0)
+    mo.within(got, ref, mo.embedding_grad_bound(ref, c, s, dtype), f"{n} x {dim}")
 
 
 @pytest.mark.parametrize("n", [64, 3000, 12_001])
@@ -193,7 +214,7 @@ def test_two_streams_and_raw_handles():
         mo.within(got[k], ref, mo.embedding_grad_bound(ref, c, a, torch.bfloat16), f"stream {k}")
 
 
-@pytest.mark.parametrize("n", [900, 9001])
+@pytest.mark.parametrize("n", [900, 9001, 270_000])
 def test_graph_replays(n):
     rows, dim = 500, 72
     ids, dout, table = token_ids(1, n, rows).cuda(), normal(2, (n, dim), torch.bfloat16).cuda(), \
