@@ -701,7 +701,7 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
     int st = check_buffers(bufs, 3);
     if (st != DS_OK) return st;
     const ds::EmbeddingGradPlan plan = ds::embedding_grad_plan(float_kind(dtype), n, rows, dim);
-    if (ds::embedding_grad_blocks(plan, n, dim) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
+    if (ds::embedding_grad_blocks(plan, n, rows) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
     std::lock_guard<std::mutex> lock(g_mu);
     char* aux = nullptr;
     DevWs dws{nullptr, nullptr, nullptr};

@@ -7,9 +7,7 @@
 // The gradient goes by sorted tokens: the positions i are put in order of
 // their token (equal tokens in input order), so that each row's terms are
 // consecutive, and are then summed in that order: no atomics on the sums, and
-// the same bits on every run. A whole new gradient is cleared by workgroups
-// that ride along in the sort's launches: the sort waits on latency and needs
-// few CUs, the clearing needs the memory.
+// the same bits on every run.
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -17,90 +15,118 @@
 namespace ds {
 
 // ---------------------------------------------------------------------------
-// Lookup. A wave takes whole rows: `lanes` lanes (a power of two) side by side
-// on one row, 64 / lanes rows at once, 16 bytes per lane and step, kLookAhead
-// steps in flight. Outputs are written past the cache: nothing here reads them
-// again, and rows of frequent tokens stay in it.
+// Lookup. `lanes` lanes (a power of two) stand side by side on one row, 64 /
+// lanes rows at once, 16 bytes per lane and step; a wave takes ROWS such groups
+// of rows and holds STEPS steps of each in flight. Outputs are written past the
+// cache: nothing here reads them again, and rows of frequent tokens stay in it.
 // ---------------------------------------------------------------------------
-constexpr int kLookAhead = 4;
-
-template <typename T, typename ID>
+template <typename T, typename ID, int STEPS, int ROWS>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(const T* __restrict__ table, int64_t rows, int64_t dim,
                                                              int64_t table_stride, const ID* __restrict__ ids,
                                                              int64_t n, float scale, T* __restrict__ out,
                                                              int64_t out_stride, int lanes)
 {
     constexpr int N = Vec16<T>::kN;
-    const int per_wave = kWave / lanes;
+    const int per_wave = kWave / lanes, mine = lane_id() % lanes;
     const int64_t wave = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    const int64_t i = wave * per_wave + lane_id() / lanes;
-    if (i >= n) return;
-    const int64_t id = (int64_t)ids[i];
-    const bool live = id >= 0 && id < rows;
-    const T* src = table + (live ? id : 0) * table_stride;
-    T* dst = out + i * out_stride;
+    const int64_t first = wave * (per_wave * ROWS) + lane_id() / lanes;
+    const T* src[ROWS];
+    bool there[ROWS], live[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int64_t i = first + r * per_wave;
+        there[r] = i < n;
+        const int64_t id = there[r] ? (int64_t)ids[i] : -1;
+        live[r] = id >= 0 && id < rows;
+        src[r] = table + (live[r] ? id : 0) * table_stride;
+    }
     const int64_t step = (int64_t)lanes * N, vecs = dim / N * N;
-    int64_t c = (int64_t)(lane_id() % lanes) * N;
-    if (!live) {
-        const float zero[N] = {};
-        for (; c < dim; c += step) store_floats<T, N>(dst + c, dim - c, zero);
-        return;
-    }
-    for (; c < vecs; c += step * kLookAhead) {
-        u32x4 v[kLookAhead];
+    for (int64_t c = (int64_t)mine * N; c < vecs; c += step * STEPS) {
+        u32x4 v[ROWS][STEPS];
 #pragma unroll
-        for (int k = 0; k < kLookAhead; ++k) {
-            const int64_t at = c + k * step;
-            v[k] = *reinterpret_cast<const typename Vec16<T>::type*>(src + (at < vecs ? at : c));
+        for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                v[r][k] = u32x4{0u, 0u, 0u, 0u};
+                if (live[r] && c + k * step < vecs)
+                    v[r][k] = *reinterpret_cast<const typename Vec16<T>::type*>(src[r] + c + k * step);
+            }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            T* dst = out + (first + r * per_wave) * out_stride + c;
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                T t[N];
+                __builtin_memcpy(t, &v[r][k], sizeof(t));
+#pragma unroll
+                for (int j = 0; j < N; ++j) t[j] = live[r] ? (T)((float)t[j] * scale) : (T)0.0f;
+                u32x4 w;
+                __builtin_memcpy(&w, t, sizeof(w));
+                if (there[r] && c + k * step < vecs)
+                    __builtin_nontemporal_store(w, reinterpret_cast<typename Vec16<T>::type*>(dst + k * step));
+            }
         }
-#pragma unroll
-        for (int k = 0; k < kLookAhead; ++k) {
-            const int64_t at = c + k * step;
-            T t[N];
-            __builtin_memcpy(t, &v[k], sizeof(t));
-#pragma unroll
-            for (int j = 0; j < N; ++j) t[j] = (T)((float)t[j] * scale);
-            u32x4 w;
-            __builtin_memcpy(&w, t, sizeof(w));
-            if (at < vecs)
-                __builtin_nontemporal_store(w, reinterpret_cast<typename Vec16<T>::type*>(dst + at));
-        }
     }
-    // the last, partial vector of the row
-    const int64_t rest = vecs + lane_id() % lanes;
-    if (rest < dim && lane_id() % lanes < N)
-        for (int64_t e = rest; e < dim; e += lanes) dst[e] = (T)((float)src[e] * scale);
+    // the last, partial vector of the rows
+    for (int64_t e = vecs + mine; e < dim; e += lanes)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r)
+            if (there[r])
+                out[(first + r * per_wave) * out_stride + e] = live[r] ? (T)((float)src[r][e] * scale) : (T)0.0f;
 }
 
 // ---------------------------------------------------------------------------
-// Clearing: rows of row_bytes, stride_bytes apart, in units of one 16-byte
-// store per lane of a wave. A launch takes the units [first, last).
+// Clearing of a whole new gradient, by workgroups that ride along in the
+// launches. A sort's launches wait on latency and leave the memory idle, so
+// each clears its first rows whatever their tokens; the launch of the sums
+// clears the rest but for the rows that have tokens.
 // ---------------------------------------------------------------------------
 struct ClearArgs {
     char* grad;
-    int64_t row_bytes, stride_bytes, slabs;  // slabs: units per row
-    int64_t first, last;
-    int skip;  // workgroups before the clearing ones
+    int64_t row_bytes, stride_bytes;
+    int64_t first, last;  // rows
+    int skip;             // workgroups before the clearing ones
+    int per_wave;         // rows of a wave
 };
+
+__device__ __forceinline__ void clear_row(const ClearArgs& a, int64_t row)
+{
+    char* p = a.grad + row * a.stride_bytes;
+    int64_t c = (int64_t)lane_id() * kVecBytes;
+    for (; c + kVecBytes <= a.row_bytes; c += kWave * kVecBytes)
+        __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4_a2*>(p + c));
+    for (; c < a.row_bytes && c + kVecBytes > a.row_bytes; c += 2) *reinterpret_cast<uint16_t*>(p + c) = 0;
+}
+
+template <int THREADS>
+__device__ __forceinline__ int64_t clear_first_row(const ClearArgs& a)
+{
+    constexpr int kPerBlock = THREADS / kWave;
+    return a.first + ((int64_t)(blockIdx.x - a.skip) * kPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) *
+                         a.per_wave;
+}
 
 template <int THREADS>
 __device__ __forceinline__ void clear_rows(const ClearArgs& a)
 {
-    constexpr int kPerBlock = THREADS / kWave;
-    const int64_t waves = (int64_t)(gridDim.x - a.skip) * kPerBlock;
-    int64_t u = a.first + (int64_t)(blockIdx.x - a.skip) * kPerBlock +
-                __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const bool one_row = a.last <= a.slabs;
-    for (; u < a.last; u += waves) {
-        const int64_t row = one_row ? 0 : u / a.slabs;
-        const int64_t c = ((u - row * a.slabs) * kWave + lane_id()) * kVecBytes;
-        char* p = a.grad + row * a.stride_bytes + c;
-        if (c + kVecBytes <= a.row_bytes) {
-            __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4_a2*>(p));
-        } else {
-            for (int64_t e = c; e < a.row_bytes; e += 2) *reinterpret_cast<uint16_t*>(a.grad + row * a.stride_bytes + e) = 0;
-        }
+    const int64_t r0 = clear_first_row<THREADS>(a);
+    for (int64_t r = r0; r < r0 + a.per_wave && r < a.last; ++r) clear_row(a, r);
+}
+
+// The same but for rows among the sorted keys; lane l looks for row r0 + l.
+template <int THREADS>
+__device__ __forceinline__ void clear_other_rows(const ClearArgs& a, const uint32_t* __restrict__ keys, int64_t n)
+{
+    const int64_t r0 = clear_first_row<THREADS>(a), mine = r0 + lane_id();
+    int64_t low = 0, high = n;  // the first key that is not below `mine`
+    while (low < high) {
+        const int64_t mid = (low + high) / 2;
+        if ((int64_t)keys[mid] < mine) low = mid + 1;
+        else high = mid;
     }
+    const uint64_t has = ballot(low < n && (int64_t)keys[low < n ? low : 0] == mine);
+    for (int i = 0; i < a.per_wave && r0 + i < a.last; ++i)
+        if (!((has >> i) & 1u)) clear_row(a, r0 + i);
 }
 
 // ---------------------------------------------------------------------------
@@ -122,10 +148,12 @@ constexpr int kRankTokens = kThreads / kRankParts; // tokens per workgroup
 template <typename ID>
 __global__ __launch_bounds__(kThreads) void token_rank_sort_kernel(const ID* __restrict__ ids, uint32_t n,
                                                                    int64_t rows, uint32_t* __restrict__ keys,
-                                                                   uint32_t* __restrict__ places, ClearArgs clear)
+                                                                   uint32_t* __restrict__ places,
+                                                                   uint32_t* __restrict__ crossing, ClearArgs clear)
 {
     extern __shared__ __align__(16) uint32_t s_key[];  // n rounded up to 64 keys
     if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kThreads>(clear);
+    if (blockIdx.x == 0 && threadIdx.x == 0) crossing[0] = 0;
     const uint32_t padded = (n + 63u) & ~63u;
     for (uint32_t j = threadIdx.x; j < padded; j += kThreads) s_key[j] = j < n ? token_key(ids[j], rows) : 0xFFFFFFFFu;
     __syncthreads();
@@ -174,10 +202,12 @@ struct TileSort {
 
 template <typename ID>
 __global__ __launch_bounds__(kTileThreads) void token_count_kernel(const ID* __restrict__ ids, TileSort a,
-                                                                   uint32_t* __restrict__ keys, ClearArgs clear)
+                                                                   uint32_t* __restrict__ keys,
+                                                                   uint32_t* __restrict__ crossing, ClearArgs clear)
 {
     __shared__ uint32_t s_count[kTileThreads];
     if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kTileThreads>(clear);
+    if (blockIdx.x == 0 && threadIdx.x == 0) crossing[0] = 0;
     const uint32_t size = 1u << a.bits;
     s_count[threadIdx.x] = 0;
     // the tables of the later digits are counted into by the passes
@@ -279,9 +309,31 @@ __global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t
             const uint32_t to = s_count[wave][d[k]] + rank[k];
             keys_out[to] = key[k];
             index_out[to] = pos[k];
-            if (more)
-                atomicAdd(&next[((key[k] >> (shift + a.bits)) & (size - 1)) * a.stride + to / (kTileThreads * ITEMS)], 1u);
         }
+    }
+    if (!more) return;
+    // Counts of the next digit by destination tile, one atomic for the lanes of
+    // a wave that agree on both: a frequent token's keys go to the same words
+    // (65,536 tokens of text-like skew: this launch took 15 us with an atomic
+    // per key).
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+        const bool live = seg + k * kWave < a.n;
+        const uint32_t to = s_count[wave][d[k]] + rank[k], into = to / (kTileThreads * ITEMS);
+        const uint32_t e = (key[k] >> (shift + a.bits)) & (size - 1);
+        uint64_t same = ballot(live);
+        for (int b = 0; b < a.bits; ++b) {
+            const bool bit = (e >> b) & 1u;
+            const uint64_t set = ballot(bit);
+            same &= bit ? set : ~set;
+        }
+        for (int b = 0; b < 8; ++b) {  // at most 128 tiles
+            const bool bit = (into >> b) & 1u;
+            const uint64_t set = ballot(bit);
+            same &= bit ? set : ~set;
+        }
+        const uint32_t below = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
+        if (live && below == 0) atomicAdd(&next[e * a.stride + into], (uint32_t)__builtin_popcountll(same));
     }
 }
 
@@ -289,9 +341,10 @@ __global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t
 template <typename ID>
 __global__ __launch_bounds__(kThreads) void token_keys_kernel(const ID* __restrict__ ids, int64_t n, int64_t rows,
                                                               uint32_t* __restrict__ keys, uint32_t* __restrict__ index,
-                                                              ClearArgs clear)
+                                                              uint32_t* __restrict__ crossing, ClearArgs clear)
 {
     if (blockIdx.x >= (uint32_t)clear.skip) return clear_rows<kThreads>(clear);
+    if (blockIdx.x == 0 && threadIdx.x == 0) crossing[0] = 0;
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i >= n) return;
     keys[i] = token_key(ids[i], rows);
@@ -304,8 +357,9 @@ __global__ __launch_bounds__(kThreads) void token_keys_kernel(const ID* __restri
 // of one slab, run by run. A run that lies inside its chunk is a whole row of
 // the gradient. The part of a run that crosses a chunk's edge goes to
 // `partial` (two 32-bit rows per chunk: 0 for a run that began in an earlier
-// chunk, 1 for one that begins here and goes on), and embedding_join_kernel
-// adds the parts up in order.
+// chunk, 1 for one that begins here and goes on), the chunk in which such a
+// run begins to the list `crossing`, and embedding_join_kernel adds the parts
+// up in order.
 // ---------------------------------------------------------------------------
 struct GradArgs {
     const uint32_t* keys;   // sorted
@@ -315,6 +369,7 @@ struct GradArgs {
     float scale;
     float* partial;  // [chunks][2][dim rounded up to whole slabs]
     int64_t partial_stride;
+    uint32_t* crossing;  // count, then chunks in any order
 };
 
 __device__ __forceinline__ uint32_t key_at(const GradArgs& a, int64_t p)
@@ -349,8 +404,12 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int elems)
 // run's sum is ready: a load behind every run is what bounded this otherwise.
 template <typename T, typename O, bool ADD>
 __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __restrict__ dout, O* __restrict__ grad,
-                                                                 GradArgs a, int64_t slabs, int64_t units)
+                                                                 GradArgs a, int64_t slabs, int64_t units,
+                                                                 ClearArgs clear)
 {
+    if constexpr (!ADD) {
+        if (blockIdx.x >= (uint32_t)clear.skip) return clear_other_rows<kThreads>(clear, a.keys, a.n);
+    }
     constexpr int N = Vec16<T>::kN, kPer = Vec16<O>::kN;
     constexpr int kAhead = ADD ? 4 : 8;  // rows in flight
     const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -436,39 +495,32 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __rest
             }
         }
     }
-    if (!((ends >> (count - 1)) & 1u))  // the last run goes on
+    if (!((ends >> (count - 1)) & 1u)) {  // the last run goes on
         store_floats<float, N>(a.partial + (chunk * 2 + (opened ? 0 : 1)) * a.partial_stride + c, N, acc);
+        if (!opened && unit % slabs == 0 && lane == 0) a.crossing[1 + atomicAdd(a.crossing, 1u)] = (uint32_t)chunk;
+    }
 }
 
-// The rows whose runs cross chunks: the waves of the chunk in which such a run
-// begins, two columns per lane, add its part and the first parts of the chunks
-// that it reaches. kJoinAhead parts are in flight: a token that fills hundreds
-// of chunks is a chain of that many additions for one wave.
+// The rows whose runs cross chunks: for each chunk in the list and 128 columns
+// (two per lane), a wave adds the run's part there and the first parts of the
+// chunks that it reaches. kJoinAhead parts are in flight: a token that fills
+// hundreds of chunks is a chain of that many additions for one wave.
 constexpr int kJoinCols = 2;
 constexpr int kJoinAhead = 16;
 
 template <typename O, bool ADD>
-__global__ __launch_bounds__(kThreads) void embedding_join_kernel(O* __restrict__ grad, GradArgs a, int64_t groups,
-                                                                  int64_t units)
+__device__ __forceinline__ void join_run(O* __restrict__ grad, const GradArgs& a, int64_t chunk, int64_t c)
 {
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (unit >= units) return;
+    const int64_t end = (chunk + 1) * a.chunk;
     const int lane = lane_id();
-    const int64_t chunk = unit / groups, c = ((unit % groups) * kWave + lane) * kJoinCols;
-    const int64_t p0 = chunk * a.chunk, end = p0 + a.chunk;
-    const uint32_t run = key_at(a, end - 1);
-    // one look at this chunk's edges (lane 0 the key before it, 1 its first) and at where the next 61 chunks begin
-    const uint32_t edge = key_at(a, lane == 0 ? p0 - 1 : lane == 1 ? p0 : end + (int64_t)(lane - 2) * a.chunk);
-    if (run >= (uint32_t)a.rows || run != readlane(edge, 2)) return;            // no run goes on from here
-    if (run == readlane(edge, 1) && run == readlane(edge, 0)) return;           // it began earlier
-    int64_t reached = __builtin_ctzll(~(ballot(edge == run) >> 2) | 1ull << 62);  // chunks that it reaches
-    for (bool more = reached == 62; more;) {
-        const uint64_t same = ballot(key_at(a, end + (reached + lane) * a.chunk) == run);
-        reached += ~same ? __builtin_ctzll(~same) : kWave;
-        more = !~same;
+    const uint32_t run = a.keys[end];
+    int64_t reached = 0;  // chunks after this one that begin with the run
+    for (bool more = true; more;) {
+        const uint64_t other = ~ballot(key_at(a, end + (reached + lane) * a.chunk) == run);
+        reached += other ? __builtin_ctzll(other) : kWave;
+        more = !other;
     }
-    const bool live = c < a.dim;
-    if (!live) return;
+    if (c >= a.dim) return;
     const float* p = a.partial + (chunk * 2 + 1) * a.partial_stride + c;
     float acc[kJoinCols];
 #pragma unroll
@@ -500,40 +552,49 @@ __global__ __launch_bounds__(kThreads) void embedding_join_kernel(O* __restrict_
     }
 }
 
+template <typename O, bool ADD>
+__global__ __launch_bounds__(kThreads) void embedding_join_kernel(O* __restrict__ grad, GradArgs a, int64_t groups)
+{
+    const int64_t units = (int64_t)a.crossing[0] * groups;
+    int64_t u = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    for (; u < units; u += (int64_t)gridDim.x * kWaves)
+        join_run<O, ADD>(grad, a, a.crossing[1 + u / groups], ((u % groups) * kWave + lane_id()) * kJoinCols);
+}
+
 // ---------------------------------------------------------------------------
 // Launchers
 // ---------------------------------------------------------------------------
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-constexpr int64_t kClearBlocks = 2048;  // at most, per launch
 
-static int lookup_lanes(ElemKind kind, int64_t dim)
-{
-    const int64_t vecs = ceil_div(dim, kind == kF32 ? 4 : 8);
-    int lanes = 1;
-    while (lanes < kWave && lanes < vecs) lanes *= 2;
-    return lanes;
-}
+// Lanes on a row, steps of a row and groups of rows in flight: the whole row or
+// four steps of it, and eight steps in all where that leaves enough waves.
+struct LookupShape {
+    int lanes, steps, rows;
+    int64_t blocks;
+    LookupShape(ElemKind kind, int64_t n, int64_t dim)
+    {
+        const int64_t vecs = ceil_div(dim, kind == kF32 ? 4 : 8);
+        lanes = 1;
+        while (lanes < kWave && lanes < vecs) lanes *= 2;
+        steps = vecs <= kWave ? 1 : 4;
+        rows = ceil_div(n, kWave / lanes) >= 16384 ? 8 / steps : 1;
+        blocks = ceil_div(n, (int64_t)(kWave / lanes) * rows * kWaves);
+    }
+};
 
-int64_t embedding_blocks(ElemKind kind, int64_t n, int64_t dim)
-{
-    return ceil_div(ceil_div(n, kWave / lookup_lanes(kind, dim)), kWaves);
-}
+int64_t embedding_blocks(ElemKind kind, int64_t n, int64_t dim) { return LookupShape(kind, n, dim).blocks; }
 
-template <typename T>
+template <typename T, typename ID>
 static hipError_t embedding_typed(ElemKind kind, const void* table, int64_t rows, int64_t dim, int64_t table_stride,
-                                  const void* ids, bool wide_ids, int64_t n, float scale, void* out,
-                                  int64_t out_stride, hipStream_t stream)
+                                  const void* ids, int64_t n, float scale, void* out, int64_t out_stride,
+                                  hipStream_t stream)
 {
-    const dim3 grid((unsigned)embedding_blocks(kind, n, dim)), block(kThreads);
-    const int lanes = lookup_lanes(kind, dim);
-    if (wide_ids)
-        embedding_kernel<T, int64_t><<<grid, block, 0, stream>>>((const T*)table, rows, dim, table_stride,
-                                                                 (const int64_t*)ids, n, scale, (T*)out, out_stride,
-                                                                 lanes);
-    else
-        embedding_kernel<T, int32_t><<<grid, block, 0, stream>>>((const T*)table, rows, dim, table_stride,
-                                                                 (const int32_t*)ids, n, scale, (T*)out, out_stride,
-                                                                 lanes);
+    const LookupShape s(kind, n, dim);
+    const auto kernel = s.steps == 1 ? s.rows == 1 ? embedding_kernel<T, ID, 1, 1> : embedding_kernel<T, ID, 1, 8>
+                        : s.rows == 1 ? embedding_kernel<T, ID, 4, 1> : embedding_kernel<T, ID, 4, 2>;
+    kernel<<<dim3((unsigned)s.blocks), dim3(kThreads), 0, stream>>>((const T*)table, rows, dim, table_stride,
+                                                                    (const ID*)ids, n, scale, (T*)out, out_stride,
+                                                                    s.lanes);
     return hipGetLastError();
 }
 
@@ -541,12 +602,18 @@ hipError_t launch_embedding(ElemKind kind, const void* table, int64_t rows, int6
                             const void* ids, bool wide_ids, int64_t n, float scale, void* out, int64_t out_stride,
                             hipStream_t stream)
 {
+#define DS_LOOKUP(T)                                                                                              \
+    return wide_ids ? embedding_typed<T, int64_t>(kind, table, rows, dim, table_stride, ids, n, scale, out,       \
+                                                  out_stride, stream)                                             \
+                    : embedding_typed<T, int32_t>(kind, table, rows, dim, table_stride, ids, n, scale, out,       \
+                                                  out_stride, stream)
     switch (kind) {
-    case kF32: return embedding_typed<float>(kind, table, rows, dim, table_stride, ids, wide_ids, n, scale, out, out_stride, stream);
-    case kBF16: return embedding_typed<bf16>(kind, table, rows, dim, table_stride, ids, wide_ids, n, scale, out, out_stride, stream);
-    case kF16: return embedding_typed<fp16>(kind, table, rows, dim, table_stride, ids, wide_ids, n, scale, out, out_stride, stream);
+    case kF32: DS_LOOKUP(float);
+    case kBF16: DS_LOOKUP(bf16);
+    case kF16: DS_LOOKUP(fp16);
     default: return hipErrorInvalidValue;
     }
+#undef DS_LOOKUP
 }
 
 int64_t embedding_most_rows() { return ((int64_t)1 << 27) - 1; }
@@ -583,62 +650,59 @@ EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, in
     }
     p.table_words = ceil_div(p.table_words, 4) * 4;
     // keys and index, twice where passes go back and forth; then the parts of rows, 16-byte aligned
-    const int64_t words = p.table_words + n * (p.digits ? 4 : 2);
+    p.crossing_at = p.table_words + n * (p.digits ? 4 : 2);
+    const int64_t words = p.crossing_at + 1 + p.chunks;
     p.partial_at = ceil_div(words, 4) * 16;
     p.bytes = p.partial_at + p.chunks * 2 * p.partial_stride * 4;
     return p;
 }
 
+// What each launch of a call clears.
+struct Clearing {
+    ClearArgs a;
+    int64_t rows, share;
+    // A sort's launch takes about 5 us, in which this much can be cleared.
+    static constexpr int64_t kShareBytes = 24 << 20;
+    Clearing(bool add, void* grad, int64_t rows_, int64_t dim, int64_t stride, int esz)
+    {
+        a = ClearArgs{static_cast<char*>(grad), dim * esz, stride * esz, 0, 0, 0, 1};
+        rows = add ? 0 : rows_;
+        share = ceil_div(kShareBytes, a.row_bytes);
+    }
+    // The part of a launch that has `before` workgroups of `threads` of its own; returns the workgroups in all.
+    unsigned next(int64_t before, int threads, bool all = false)
+    {
+        a.first = a.last;
+        a.last = all || rows - a.first < share ? rows : a.first + share;
+        a.skip = (int)before;
+        // as many rows to a wave as leave 8,192 waves (the lanes of a wave look for one row each)
+        const int64_t each = (a.last - a.first) / 8192;
+        a.per_wave = (int)(each < 1 ? 1 : each < kWave ? each : kWave);
+        return (unsigned)(before + ceil_div(a.last - a.first, (int64_t)a.per_wave * (threads / kWave)));
+    }
+};
+
 template <typename T, typename O, bool ADD>
 static hipError_t embedding_grad_typed(const EmbeddingGradPlan& p, const void* dout, void* grad, const GradArgs& a,
-                                       hipStream_t stream)
+                                       Clearing& clear, hipStream_t stream)
 {
     const int64_t units = p.chunks * p.slabs;
-    embedding_sum_kernel<T, O, ADD><<<dim3((unsigned)ceil_div(units, kWaves)), dim3(kThreads), 0, stream>>>(
-        (const T*)dout, (O*)grad, a, p.slabs, units);
+    const unsigned blocks = clear.next(ceil_div(units, kWaves), kThreads, true);
+    embedding_sum_kernel<T, O, ADD><<<dim3(blocks), dim3(kThreads), 0, stream>>>((const T*)dout, (O*)grad, a, p.slabs,
+                                                                                 units, clear.a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t groups = ceil_div(a.dim, kWave * kJoinCols), joins = p.chunks * groups;
-    embedding_join_kernel<O, ADD><<<dim3((unsigned)ceil_div(joins, kWaves)), dim3(kThreads), 0, stream>>>((O*)grad, a,
-                                                                                                       groups, joins);
+    const int64_t groups = ceil_div(a.dim, kWave * kJoinCols), joins = ceil_div(p.chunks * groups, kWaves);
+    embedding_join_kernel<O, ADD><<<dim3((unsigned)(joins < 1024 ? joins : 1024)), dim3(kThreads), 0, stream>>>(
+        (O*)grad, a, groups);
     return hipGetLastError();
 }
 
-int64_t embedding_grad_blocks(const EmbeddingGradPlan& p, int64_t n, int64_t dim)
+int64_t embedding_grad_blocks(const EmbeddingGradPlan& p, int64_t n, int64_t rows)
 {
-    const int64_t join = ceil_div(p.chunks * ceil_div(dim, kWave * kJoinCols), kWaves), keys = ceil_div(n, kThreads);
-    const int64_t sum = ceil_div(p.chunks * p.slabs, kWaves), most = join > sum ? join : sum;
-    return (most > keys ? most : keys) + kClearBlocks;
+    const int64_t sum = ceil_div(p.chunks * p.slabs, kWaves), keys = ceil_div(n, kThreads);
+    return (sum > keys ? sum : keys) + ceil_div(rows, kWaves * kWave) + 8192;
 }
-
-// The launches of a sort take equal shares of the clearing.
-struct Clearing {
-    ClearArgs a;
-    int64_t units, share;
-    Clearing(bool add, void* grad, int64_t rows, int64_t dim, int64_t stride, int esz, int launches)
-    {
-        a.grad = static_cast<char*>(grad);
-        a.row_bytes = dim * esz;
-        a.stride_bytes = stride * esz;
-        if (stride == dim) {  // one long row
-            a.row_bytes *= rows;
-            rows = 1;
-        }
-        a.slabs = ceil_div(a.row_bytes, kWave * kVecBytes);
-        units = add ? 0 : rows * a.slabs;
-        share = ceil_div(units, launches);
-        a.first = a.last = 0;
-    }
-    // The next launch's part, behind `before` workgroups of `threads`; returns the workgroups in all.
-    unsigned next(int64_t before, int threads)
-    {
-        a.first = a.last;
-        a.last = a.first + share < units ? a.first + share : units;
-        a.skip = (int)before;
-        const int64_t blocks = ceil_div(a.last - a.first, threads / kWave);
-        return (unsigned)(before + (blocks < kClearBlocks ? blocks : kClearBlocks));
-    }
-};
 
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& p, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
@@ -650,13 +714,14 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
     uint32_t* keys = table + p.table_words;
     uint32_t *index = keys + n, *keys2 = index + n, *index2 = keys2 + n;
     const bool tiled = p.tiles > 0;
-    Clearing clear(add, grad, rows, dim, grad_stride, grad_kind == kF32 ? 4 : 2, tiled ? 1 + p.digits : 1);
+    uint32_t* crossing = table + p.crossing_at;
+    Clearing clear(add, grad, rows, dim, grad_stride, grad_kind == kF32 ? 4 : 2);
     if (p.radix_bits || n == 0) {
-        const unsigned grid = clear.next(ceil_div(n, kThreads), kThreads);
+        const unsigned grid = clear.next(ceil_div(n, kThreads), kThreads, n == 0);
         if (wide_ids)
-            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int64_t*)ids, n, rows, keys, index, clear.a);
+            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int64_t*)ids, n, rows, keys, index, crossing, clear.a);
         else
-            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int32_t*)ids, n, rows, keys, index, clear.a);
+            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int32_t*)ids, n, rows, keys, index, crossing, clear.a);
         e = hipGetLastError();
         if (e != hipSuccess || n == 0) return e;
         for (int d = 0; d < p.digits; ++d) {
@@ -669,9 +734,9 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
         const TileSort a{(uint32_t)n, rows, p.bits, p.digits, p.items, p.tiles, (int)(ceil_div(p.tiles, 4) * 4), table};
         unsigned grid = clear.next(p.tiles, kTileThreads);
         if (wide_ids)
-            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)ids, a, keys, clear.a);
+            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)ids, a, keys, crossing, clear.a);
         else
-            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)ids, a, keys, clear.a);
+            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)ids, a, keys, crossing, clear.a);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         for (int d = 0; d < p.digits; ++d) {
@@ -688,18 +753,18 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
         const size_t lds = (size_t)((n + 63) / 64 * 64) * 4;
         if (wide_ids)
             token_rank_sort_kernel<<<dim3(grid), dim3(kThreads), lds, stream>>>((const int64_t*)ids, (uint32_t)n, rows,
-                                                                               keys, index, clear.a);
+                                                                               keys, index, crossing, clear.a);
         else
             token_rank_sort_kernel<<<dim3(grid), dim3(kThreads), lds, stream>>>((const int32_t*)ids, (uint32_t)n, rows,
-                                                                               keys, index, clear.a);
+                                                                               keys, index, crossing, clear.a);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const GradArgs a{keys, index, n, rows, dim, dout_stride, grad_stride, p.chunk, scale,
-                     reinterpret_cast<float*>(aux + p.partial_at), p.partial_stride};
+                     reinterpret_cast<float*>(aux + p.partial_at), p.partial_stride, crossing};
 #define DS_GRAD(T, O)                                                              \
-    return add ? embedding_grad_typed<T, O, true>(p, dout, grad, a, stream) \
-               : embedding_grad_typed<T, O, false>(p, dout, grad, a, stream)
+    return add ? embedding_grad_typed<T, O, true>(p, dout, grad, a, clear, stream) \
+               : embedding_grad_typed<T, O, false>(p, dout, grad, a, clear, stream)
     if (kind == kF32 && grad_kind == kF32) DS_GRAD(float, float);
     if (kind == kBF16 && grad_kind == kBF16) DS_GRAD(bf16, bf16);
     if (kind == kBF16 && grad_kind == kF32) DS_GRAD(bf16, float);

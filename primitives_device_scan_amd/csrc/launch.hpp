@@ -98,12 +98,13 @@ struct EmbeddingGradPlan {
     int64_t slabs, chunks;   // units of work: slabs x chunks
     int64_t partial_stride;  // elements between rows of the crossing runs' parts
     int64_t table_words;     // the passes' table, 32-bit words at the start of the scratch
+    int64_t crossing_at;     // word offset of the list of crossing runs
     int64_t partial_at;      // byte offset of the parts
     int64_t bytes;           // scratch in all
 };
 EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, int64_t dim);
 int64_t embedding_most_rows();
-int64_t embedding_grad_blocks(const EmbeddingGradPlan& plan, int64_t n, int64_t dim);  // workgroups of the largest launch, or more
+int64_t embedding_grad_blocks(const EmbeddingGradPlan& plan, int64_t n, int64_t rows);  // workgroups of the largest launch, or more
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& plan, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
                                  int64_t dim, float scale, void* grad, int64_t grad_stride, bool add, char* aux,
