@@ -700,8 +700,8 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
                          {d_grad, span_bytes(rows, dim, grad_stride, gsz), gsz, true}};
     int st = check_buffers(bufs, 3);
     if (st != DS_OK) return st;
-    const ds::EmbeddingGradPlan plan = ds::embedding_grad_plan(float_kind(dtype), n, rows, dim);
-    if (ds::embedding_grad_blocks(plan, n, rows) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
+    const ds::EmbeddingGradPlan plan = ds::embedding_grad_plan(float_kind(grad_dtype), n, rows, dim);
+    if (ds::embedding_grad_blocks(plan, n, rows, dim * gsz) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
     std::lock_guard<std::mutex> lock(g_mu);
     char* aux = nullptr;
     DevWs dws{nullptr, nullptr, nullptr};

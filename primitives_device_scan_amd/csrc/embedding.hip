@@ -89,44 +89,71 @@ struct ClearArgs {
     int per_wave;         // rows of a wave
 };
 
-__device__ __forceinline__ void clear_row(const ClearArgs& a, int64_t row)
+__device__ __forceinline__ void clear_span(char* p, int64_t bytes)
 {
-    char* p = a.grad + row * a.stride_bytes;
     int64_t c = (int64_t)lane_id() * kVecBytes;
-    for (; c + kVecBytes <= a.row_bytes; c += kWave * kVecBytes)
+    for (; c + kVecBytes <= bytes; c += kWave * kVecBytes)
         __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, reinterpret_cast<u32x4_a2*>(p + c));
-    for (; c < a.row_bytes && c + kVecBytes > a.row_bytes; c += 2) *reinterpret_cast<uint16_t*>(p + c) = 0;
+    for (; c < bytes && c + kVecBytes > bytes; c += 2) *reinterpret_cast<uint16_t*>(p + c) = 0;
 }
 
 template <int THREADS>
-__device__ __forceinline__ int64_t clear_first_row(const ClearArgs& a)
+__device__ __forceinline__ int64_t clear_wave(const ClearArgs& a)
 {
-    constexpr int kPerBlock = THREADS / kWave;
-    return a.first + ((int64_t)(blockIdx.x - a.skip) * kPerBlock + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) *
-                         a.per_wave;
+    return (int64_t)(blockIdx.x - a.skip) * (THREADS / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 }
+
+// Rows without gaps are cleared in pieces of kPiece bytes that begin at
+// multiples of it, so that no cache line is written by two waves.
+constexpr int64_t kPiece = 4096;
 
 template <int THREADS>
 __device__ __forceinline__ void clear_rows(const ClearArgs& a)
 {
-    const int64_t r0 = clear_first_row<THREADS>(a);
-    for (int64_t r = r0; r < r0 + a.per_wave && r < a.last; ++r) clear_row(a, r);
+    const int64_t wave = clear_wave<THREADS>(a);
+    if (a.stride_bytes == a.row_bytes) {
+        const int64_t first = a.first * a.row_bytes, last = a.last * a.row_bytes, at = (first / kPiece + wave) * kPiece;
+        const int64_t from = at > first ? at : first, to = at + kPiece < last ? at + kPiece : last;
+        if (from < to) clear_span(a.grad + from, to - from);
+        return;
+    }
+    const int64_t r0 = a.first + wave * a.per_wave, r1 = r0 + a.per_wave < a.last ? r0 + a.per_wave : a.last;
+    for (int64_t r = r0; r < r1; ++r) clear_span(a.grad + r * a.stride_bytes, a.row_bytes);
 }
 
-// The same but for rows among the sorted keys; lane l looks for row r0 + l.
+// The same but for rows among the sorted keys: each half of the wave looks,
+// with 32 probes at a time, for one end of the keys of the wave's rows, then
+// lane l looks for row r0 + l among them. (Seventeen dependent reads for 65,536
+// keys become four and a few.)
 template <int THREADS>
 __device__ __forceinline__ void clear_other_rows(const ClearArgs& a, const uint32_t* __restrict__ keys, int64_t n)
 {
-    const int64_t r0 = clear_first_row<THREADS>(a), mine = r0 + lane_id();
-    int64_t low = 0, high = n;  // the first key that is not below `mine`
-    while (low < high) {
+    const int64_t r0 = a.first + clear_wave<THREADS>(a) * a.per_wave, mine = r0 + lane_id();
+    const int64_t end = r0 + lane_id() / 32 * a.per_wave;
+    int64_t low = 0, size = n;  // the first key that is not below `end` is among low .. low + size
+    while (readlane((int)(size > 0), 0) | readlane((int)(size > 0), 32)) {
+        const int64_t step = size / 32 + 1, at = low + (lane_id() % 32) * step;
+        const bool below = at < low + size && (int64_t)keys[at] < end;
+        const uint32_t which = (uint32_t)(ballot(below) >> (lane_id() / 32 * 32));
+        const int count = __builtin_popcount(which);  // probes below `end`: the first ones
+        if (count == 0) {
+            size = 0;
+        } else {
+            const int64_t from = low + (count - 1) * step + 1, to = low + count * step;
+            size = (to < low + size ? to : low + size) - from;
+            low = from;
+        }
+    }
+    const int64_t last = readlane(low, 32);
+    low = readlane(low, 0);
+    for (int64_t high = last; low < high;) {
         const int64_t mid = (low + high) / 2;
         if ((int64_t)keys[mid] < mine) low = mid + 1;
         else high = mid;
     }
-    const uint64_t has = ballot(low < n && (int64_t)keys[low < n ? low : 0] == mine);
+    const uint64_t has = ballot(low < last && (int64_t)keys[low < last ? low : 0] == mine);
     for (int i = 0; i < a.per_wave && r0 + i < a.last; ++i)
-        if (!((has >> i) & 1u)) clear_row(a, r0 + i);
+        if (!((has >> i) & 1u)) clear_span(a.grad + (r0 + i) * a.stride_bytes, a.row_bytes);
 }
 
 // ---------------------------------------------------------------------------
@@ -176,15 +203,14 @@ __global__ __launch_bounds__(kThreads) void token_rank_sort_kernel(const ID* __r
 }
 
 // From kRankSortMax to kTileSortMax tokens: stable counting passes over digits
-// of up to 9 bits, two for up to 2^18 - 1 rows, in one launch to count the
-// first digit and one per pass. A table holds the count of every digit in
-// every tile, digit by digit; each workgroup of a pass sums it up for itself
-// (at most 128 tiles, read from the cache) instead of waiting for a scan
-// launched in between, and counts the next digit of what it places with
-// atomics on the next table (whole numbers: any order gives the same counts).
-// Against the library's general passes (a count, a look-back scan and a
-// scatter launch each, and one launch for the keys) this takes 4 launches
-// fewer for two digits.
+// of up to 9 bits, two for up to 2^18 - 1 rows, each a launch that counts the
+// digit in every tile and one that places the keys. There is no scan in
+// between: each workgroup of a pass sums the table up for itself (at most 128
+// tiles to a digit, read from the cache, tile by tile so that a wave reads
+// whole lines). For 65,536 tokens the four launches
+// take 5 us each, where the library's general passes with a scan launch each
+// took 36 us in all; one launch less, with the second digit counted by atomics
+// in the first pass, took 11 us more (its words are shared by all XCDs).
 constexpr int64_t kTileSortMax = 262144;
 constexpr int kTileThreads = 512;
 constexpr int kTileWaves = kTileThreads / kWave;
@@ -196,12 +222,14 @@ struct TileSort {
     int64_t rows;
     int bits, digits;          // of a digit; digits of a key
     int items;                 // keys per thread: tiles of kTileThreads * items
-    int tiles, stride;         // stride: entries per digit in a table, tiles rounded up to 4
-    uint32_t* tables;          // [digits][1 << bits][stride]
+    int tiles;
+    uint32_t* table;           // [tiles][1 << bits]
 };
 
+// Counts digit `digit` of every tile. The first launch has the ids and writes
+// the keys; the others (ids null) have the keys.
 template <typename ID>
-__global__ __launch_bounds__(kTileThreads) void token_count_kernel(const ID* __restrict__ ids, TileSort a,
+__global__ __launch_bounds__(kTileThreads) void token_count_kernel(const ID* __restrict__ ids, TileSort a, int digit,
                                                                    uint32_t* __restrict__ keys,
                                                                    uint32_t* __restrict__ crossing, ClearArgs clear)
 {
@@ -210,22 +238,18 @@ __global__ __launch_bounds__(kTileThreads) void token_count_kernel(const ID* __r
     if (blockIdx.x == 0 && threadIdx.x == 0) crossing[0] = 0;
     const uint32_t size = 1u << a.bits;
     s_count[threadIdx.x] = 0;
-    // the tables of the later digits are counted into by the passes
-    const uint32_t words = size * (uint32_t)a.stride;
-    for (uint32_t i = words + blockIdx.x * kTileThreads + threadIdx.x; i < words * a.digits; i += a.tiles * kTileThreads)
-        a.tables[i] = 0;
     __syncthreads();
     const uint32_t first = blockIdx.x * (uint32_t)(kTileThreads * a.items);
     for (int k = 0; k < a.items; ++k) {
         const uint32_t i = first + k * kTileThreads + threadIdx.x;
         if (i < a.n) {
-            const uint32_t key = token_key(ids[i], a.rows);
-            keys[i] = key;
-            atomicAdd(&s_count[key & (size - 1)], 1u);
+            const uint32_t key = ids ? token_key(ids[i], a.rows) : keys[i];
+            if (ids) keys[i] = key;
+            atomicAdd(&s_count[(key >> (digit * a.bits)) & (size - 1)], 1u);
         }
     }
     __syncthreads();
-    if (threadIdx.x < size) a.tables[threadIdx.x * a.stride + blockIdx.x] = s_count[threadIdx.x];
+    if (threadIdx.x < size) a.table[(blockIdx.x << a.bits) + threadIdx.x] = s_count[threadIdx.x];
 }
 
 // Pass `digit`: keys (and their positions; null: keys are in input order) to
@@ -252,18 +276,17 @@ __global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t
         pos[k] = i < a.n && index ? index[i] : i;
     }
     // digit d = this thread: keys of smaller digits and, of its own, those of the tiles before
-    const uint32_t* table = a.tables + (size_t)digit * size * a.stride;
     uint32_t total = 0, before = 0;
     if (threadIdx.x < size) {
-        const u32x4* row = reinterpret_cast<const u32x4*>(table + threadIdx.x * a.stride);
-#pragma unroll 8
-        for (int t = 0; t < a.stride; t += 4) {
-            const u32x4 c = row[t / 4];
+        for (int t0 = 0; t0 < a.tiles; t0 += 16) {
+            uint32_t c[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t v = t + q < a.tiles ? c[q] : 0u;
+            for (int q = 0; q < 16; ++q) c[q] = a.table[((t0 + q < a.tiles ? t0 + q : 0) << a.bits) + threadIdx.x];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                const uint32_t v = t0 + q < a.tiles ? c[q] : 0u;
                 total += v;
-                before += t + q < tile ? v : 0u;
+                before += t0 + q < tile ? v : 0u;
             }
         }
     }
@@ -301,8 +324,6 @@ __global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t
         sum += c;
     }
     __syncthreads();
-    const bool more = digit + 1 < a.digits;
-    uint32_t* next = a.tables + (size_t)(digit + 1) * size * a.stride;
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
         if (seg + k * kWave < a.n) {
@@ -310,30 +331,6 @@ __global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t
             keys_out[to] = key[k];
             index_out[to] = pos[k];
         }
-    }
-    if (!more) return;
-    // Counts of the next digit by destination tile, one atomic for the lanes of
-    // a wave that agree on both: a frequent token's keys go to the same words
-    // (65,536 tokens of text-like skew: this launch took 15 us with an atomic
-    // per key).
-#pragma unroll
-    for (int k = 0; k < ITEMS; ++k) {
-        const bool live = seg + k * kWave < a.n;
-        const uint32_t to = s_count[wave][d[k]] + rank[k], into = to / (kTileThreads * ITEMS);
-        const uint32_t e = (key[k] >> (shift + a.bits)) & (size - 1);
-        uint64_t same = ballot(live);
-        for (int b = 0; b < a.bits; ++b) {
-            const bool bit = (e >> b) & 1u;
-            const uint64_t set = ballot(bit);
-            same &= bit ? set : ~set;
-        }
-        for (int b = 0; b < 8; ++b) {  // at most 128 tiles
-            const bool bit = (into >> b) & 1u;
-            const uint64_t set = ballot(bit);
-            same &= bit ? set : ~set;
-        }
-        const uint32_t below = __builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u));
-        if (live && below == 0) atomicAdd(&next[e * a.stride + into], (uint32_t)__builtin_popcountll(same));
     }
 }
 
@@ -353,7 +350,7 @@ __global__ __launch_bounds__(kThreads) void token_keys_kernel(const ID* __restri
 
 // ---------------------------------------------------------------------------
 // Sums. The sorted positions are cut into chunks of `chunk` (8 to 64), the
-// columns into slabs of one 16-byte access per lane; a wave adds up one chunk
+// columns into slabs of one 16-byte access per lane (of the wider of the two types); a wave adds up one chunk
 // of one slab, run by run. A run that lies inside its chunk is a whole row of
 // the gradient. The part of a run that crosses a chunk's edge goes to
 // `partial` (two 32-bit rows per chunk: 0 for a run that began in an earlier
@@ -377,45 +374,66 @@ __device__ __forceinline__ uint32_t key_at(const GradArgs& a, int64_t p)
     return p >= 0 && p < a.n ? a.keys[p] : 0xFFFFFFFFu;
 }
 
-// One 16-byte load of elements at .. at + N - 1 from `base`, moved down where
-// it would pass `limit` elements (the buffer's end): element j is then at
-// place j + shift. limit >= N.
-template <typename T>
-__device__ __forceinline__ u32x4 load_window(const T* __restrict__ base, int64_t at, int64_t limit)
+// N elements of T, 8 or 16 bytes, as loaded: one access at any alignment.
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+template <typename T, int N> struct Pack {
+    static constexpr int kWords = N * (int)sizeof(T) / 4;
+    uint32_t w[kWords];
+};
+
+// Elements at .. at + N - 1 of `base`, moved down where they would pass `limit`
+// elements (the buffer's end): element j is then at place j + shift. limit >= N.
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load_window(const T* __restrict__ base, int64_t at, int64_t limit)
 {
-    constexpr int N = Vec16<T>::kN;
-    return *reinterpret_cast<const typename Vec16<T>::type*>(base + (at + N <= limit ? at : limit - N));
+    const T* p = base + (at + N <= limit ? at : limit - N);
+    Pack<T, N> r;
+    if constexpr (Pack<T, N>::kWords == 4) {
+        const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const typename Vec16<T>::type*>(p));
+        __builtin_memcpy(&r, &v, sizeof(r));
+    } else {
+        const u32x2_a2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_a2*>(p));
+        __builtin_memcpy(&r, &v, sizeof(r));
+    }
+    return r;
 }
 
-template <typename T>
-__device__ __forceinline__ u32x4 shift_down(u32x4 v, int elems)
+template <typename T, int N>
+__device__ __forceinline__ void shift_down(Pack<T, N>& v, int elems)
 {
+    constexpr int kWords = Pack<T, N>::kWords;
     const int bytes = elems * (int)sizeof(T);
-    if (bytes & 8) v = u32x4{v[2], v[3], 0u, 0u};
-    if (bytes & 4) v = u32x4{v[1], v[2], v[3], 0u};
-    if constexpr (sizeof(T) == 2) {
-        if (bytes & 2)
-            v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+#pragma unroll
+    for (int by = 2; by >= 1; by /= 2)
+        if (bytes & (by * 4)) {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) v.w[i] = i + by < kWords ? v.w[i + by] : 0u;
+        }
+    if (sizeof(T) == 2 && (bytes & 2)) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) v.w[i] = v.w[i] >> 16 | (i + 1 < kWords ? v.w[i + 1] << 16 : 0u);
     }
-    return v;
 }
+
+// Columns per lane: 16 bytes of the wider of the two types.
+template <typename T, typename O> struct GradCols {
+    static constexpr int value = Vec16<O>::kN < Vec16<T>::kN ? Vec16<O>::kN : Vec16<T>::kN;
+};
 
 // ADD: the rows that end in the chunk are loaded with the terms, not when the
 // run's sum is ready: a load behind every run is what bounded this otherwise.
-template <typename T, typename O, bool ADD>
-__global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __restrict__ dout, O* __restrict__ grad,
-                                                                 GradArgs a, int64_t slabs, int64_t units,
-                                                                 ClearArgs clear)
+// Their stores are non-temporal; those of a new gradient are not (65,536
+// tokens of 2,048: 142 us against 127). Terms are read once and loaded
+// non-temporally (127 us against 138). WHOLE: no lane of the wave has a row's
+// last, partial vector.
+template <typename T, typename O, bool ADD, bool WHOLE>
+__device__ __forceinline__ void sum_chunk_of_slab(const T* __restrict__ dout, O* __restrict__ grad, const GradArgs& a,
+                                                  int64_t chunk, int64_t c, bool first_slab)
 {
-    if constexpr (!ADD) {
-        if (blockIdx.x >= (uint32_t)clear.skip) return clear_other_rows<kThreads>(clear, a.keys, a.n);
-    }
-    constexpr int N = Vec16<T>::kN, kPer = Vec16<O>::kN;
-    constexpr int kAhead = ADD ? 4 : 8;  // rows in flight
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (unit >= units) return;
+    constexpr int N = GradCols<T, O>::value;
+    constexpr int kAhead = 8;  // rows in flight
+    using Vec = typename Vec16<O>::type;
     const int lane = lane_id();
-    const int64_t chunk = unit / slabs, c = ((unit % slabs) * kWave + lane) * N;
     const int64_t p0 = chunk * a.chunk;
     const bool mine = lane < a.chunk;
     const uint32_t key = mine ? key_at(a, p0 + lane) : 0xFFFFFFFFu;
@@ -433,20 +451,17 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __rest
 #pragma unroll
     for (int j = 0; j < N; ++j) acc[j] = 0.0f;
     for (int i0 = 0; i0 < count; i0 += kAhead) {
-        u32x4 x[kAhead];
-        float old[ADD ? kAhead : 1][N];
-        if (limit >= N) {
+        Pack<T, N> x[kAhead];
+        u32x4 was[ADD ? kAhead : 1];
 #pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                x[i] = load_window(dout, (int64_t)readlane(index, i0 + i < count ? i0 + i : count - 1) * a.dout_stride + col,
-                                   limit);
-        } else {  // fewer than N elements in all
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i) {
-                const T* row = dout + (int64_t)readlane(index, i0 + i < count ? i0 + i : count - 1) * a.dout_stride + col;
+        for (int i = 0; i < kAhead; ++i) {
+            const int64_t row = (int64_t)readlane(index, i0 + i < count ? i0 + i : count - 1) * a.dout_stride;
+            if (WHOLE || limit >= N) {
+                x[i] = load_window<T, N>(dout, row + col, WHOLE ? INT64_MAX : limit);
+            } else {  // fewer than N elements in all
                 T t[N];
 #pragma unroll
-                for (int j = 0; j < N; ++j) t[j] = j < valid ? row[j] : (T)0.0f;
+                for (int j = 0; j < N; ++j) t[j] = j < valid ? dout[row + col + j] : (T)0.0f;
                 __builtin_memcpy(&x[i], t, sizeof(t));
             }
         }
@@ -455,12 +470,13 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __rest
             for (int i = 0; i < kAhead; ++i) {
                 if (i0 + i < count && ((ends >> (i0 + i)) & 1u)) {
                     const O* p = grad + (int64_t)readlane(key, i0 + i) * a.grad_stride + col;
+                    if (WHOLE || valid >= N) {
+                        was[i] = *reinterpret_cast<const Vec*>(p);
+                    } else {
+                        O t[N];
 #pragma unroll
-                    for (int v = 0; v < N / kPer; ++v) {
-                        float o[kPer];
-                        load_floats<O, kPer>(p + v * kPer, valid - v * kPer, o);
-#pragma unroll
-                        for (int j = 0; j < kPer; ++j) old[i][v * kPer + j] = o[j];
+                        for (int j = 0; j < N; ++j) t[j] = j < valid ? p[j] : (O)0.0f;
+                        __builtin_memcpy(&was[i], t, sizeof(t));
                     }
                 }
             }
@@ -468,25 +484,40 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __rest
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             if (i0 + i < count) {  // uniform
-                const int64_t over =
-                    limit < N ? 0 : (int64_t)readlane(index, i0 + i) * a.dout_stride + col + N - limit;
-                u32x4 v = x[i];
-                if (ballot(over > 0)) v = shift_down<T>(v, over > 0 ? (int)over : 0);
+                if constexpr (!WHOLE) {
+                    const int64_t over =
+                        limit < N ? 0 : (int64_t)readlane(index, i0 + i) * a.dout_stride + col + N - limit;
+                    if (ballot(over > 0)) shift_down<T, N>(x[i], over > 0 ? (int)over : 0);
+                }
                 T t[N];
-                __builtin_memcpy(t, &v, sizeof(t));
+                __builtin_memcpy(t, &x[i], sizeof(t));
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] += (float)t[j];
                 if ((ends >> (i0 + i)) & 1u) {
                     if (opened) {
                         store_floats<float, N>(a.partial + chunk * 2 * a.partial_stride + c, N, acc);
                     } else if (live) {
-                        float y[N];
+                        O o[N];
+                        if constexpr (ADD) __builtin_memcpy(o, &was[i], sizeof(o));
 #pragma unroll
                         for (int j = 0; j < N; ++j) {
-                            y[j] = acc[j] * a.scale;
-                            if constexpr (ADD) y[j] += old[i][j];
+                            float y = acc[j] * a.scale;
+                            if constexpr (ADD) y += (float)o[j];
+                            o[j] = (O)y;
                         }
-                        store_floats<O, N>(grad + (int64_t)readlane(key, i0 + i) * a.grad_stride + c, valid, y);
+                        O* p = grad + (int64_t)readlane(key, i0 + i) * a.grad_stride + c;
+                        if (WHOLE || valid >= N) {
+                            u32x4 u;
+                            __builtin_memcpy(&u, o, sizeof(u));
+                            if constexpr (ADD)
+                                __builtin_nontemporal_store(u, reinterpret_cast<Vec*>(p));
+                            else
+                                *reinterpret_cast<Vec*>(p) = u;
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < N; ++j)
+                                if (j < valid) p[j] = o[j];
+                        }
                     }
                     opened = false;
 #pragma unroll
@@ -497,68 +528,93 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __rest
     }
     if (!((ends >> (count - 1)) & 1u)) {  // the last run goes on
         store_floats<float, N>(a.partial + (chunk * 2 + (opened ? 0 : 1)) * a.partial_stride + c, N, acc);
-        if (!opened && unit % slabs == 0 && lane == 0) a.crossing[1 + atomicAdd(a.crossing, 1u)] = (uint32_t)chunk;
+        if (!opened && first_slab && lane == 0) a.crossing[1 + atomicAdd(a.crossing, 1u)] = (uint32_t)chunk;
     }
+}
+
+template <typename T, typename O, bool ADD>
+__global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __restrict__ dout, O* __restrict__ grad,
+                                                                 GradArgs a, int64_t slabs, int64_t units,
+                                                                 ClearArgs clear)
+{
+    if constexpr (!ADD) {
+        if (blockIdx.x >= (uint32_t)clear.skip) return clear_other_rows<kThreads>(clear, a.keys, a.n);
+    }
+    constexpr int N = GradCols<T, O>::value;
+    static_assert(N == Vec16<O>::kN, "one access per row of the gradient");
+    const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (unit >= units) return;
+    const int64_t chunk = unit / slabs, slab = unit % slabs, c = (slab * kWave + lane_id()) * N;
+    if (a.dim % N == 0 || (slab + 1) * kWave * N <= a.dim)
+        sum_chunk_of_slab<T, O, ADD, true>(dout, grad, a, chunk, c, slab == 0);
+    else
+        sum_chunk_of_slab<T, O, ADD, false>(dout, grad, a, chunk, c, slab == 0);
 }
 
 // The rows whose runs cross chunks: for each chunk in the list and 128 columns
 // (two per lane), a wave adds the run's part there and the first parts of the
-// chunks that it reaches. kJoinAhead parts are in flight: a token that fills
-// hundreds of chunks is a chain of that many additions for one wave.
+// chunks that it reaches. kJoinAhead parts are in flight: a frequent token
+// fills hundreds of chunks, most runs two. (A workgroup per item, the parts
+// split over its waves, took twice as long: most items are short, and it is
+// their number that counts.)
 constexpr int kJoinCols = 2;
 constexpr int kJoinAhead = 16;
 
 template <typename O, bool ADD>
-__device__ __forceinline__ void join_run(O* __restrict__ grad, const GradArgs& a, int64_t chunk, int64_t c)
-{
-    const int64_t end = (chunk + 1) * a.chunk;
-    const int lane = lane_id();
-    const uint32_t run = a.keys[end];
-    int64_t reached = 0;  // chunks after this one that begin with the run
-    for (bool more = true; more;) {
-        const uint64_t other = ~ballot(key_at(a, end + (reached + lane) * a.chunk) == run);
-        reached += other ? __builtin_ctzll(other) : kWave;
-        more = !other;
-    }
-    if (c >= a.dim) return;
-    const float* p = a.partial + (chunk * 2 + 1) * a.partial_stride + c;
-    float acc[kJoinCols];
-#pragma unroll
-    for (int j = 0; j < kJoinCols; ++j) acc[j] = p[j];
-    p += a.partial_stride;  // the first parts of the chunks after it
-    for (int64_t q0 = 0; q0 < reached; q0 += kJoinAhead) {
-        float x[kJoinAhead][kJoinCols];
-#pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k) {
-            const int64_t q = q0 + k < reached ? q0 + k : reached - 1;
-#pragma unroll
-            for (int j = 0; j < kJoinCols; ++j) x[k][j] = p[q * 2 * a.partial_stride + j];
-        }
-#pragma unroll
-        for (int k = 0; k < kJoinAhead; ++k)
-            if (q0 + k < reached) {
-#pragma unroll
-                for (int j = 0; j < kJoinCols; ++j) acc[j] += x[k][j];
-            }
-    }
-    O* out = grad + (int64_t)run * a.grad_stride + c;
-#pragma unroll
-    for (int j = 0; j < kJoinCols; ++j) {
-        if (c + j < a.dim) {
-            float y = acc[j] * a.scale;
-            if constexpr (ADD) y += (float)out[j];
-            out[j] = (O)y;
-        }
-    }
-}
-
-template <typename O, bool ADD>
 __global__ __launch_bounds__(kThreads) void embedding_join_kernel(O* __restrict__ grad, GradArgs a, int64_t groups)
 {
-    const int64_t units = (int64_t)a.crossing[0] * groups;
+    const int lane = lane_id();
+    const int64_t chunks = (a.n + a.chunk - 1) / a.chunk;
     int64_t u = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    for (; u < units; u += (int64_t)gridDim.x * kWaves)
-        join_run<O, ADD>(grad, a, a.crossing[1 + u / groups], ((u % groups) * kWave + lane_id()) * kJoinCols);
+    for (; u < chunks * groups; u += (int64_t)gridDim.x * kWaves) {
+        // loads that depend on each other are what this takes its time for: the item comes with the count
+        const uint32_t count = a.crossing[0], item = a.crossing[1 + u / groups];
+        if (u >= (int64_t)count * groups) return;
+        const int64_t chunk = item, c = ((u % groups) * kWave + lane) * kJoinCols;
+        const int64_t end = (chunk + 1) * a.chunk;
+        // parts 0 (row 1 of this chunk) and 1 .. reached (row 0 of the next ones): rows 2 chunk + 1, + 2, + 4, ...
+        const float* p = a.partial + (chunk * 2 + 1) * a.partial_stride + c;  // c < partial_stride
+        float acc[kJoinCols], second[kJoinCols];
+#pragma unroll
+        for (int j = 0; j < kJoinCols; ++j) {
+            acc[j] = p[j];
+            second[j] = p[a.partial_stride + j];
+        }
+        const uint32_t begins = key_at(a, end + (int64_t)lane * a.chunk);  // keys that the next chunks begin with
+        const uint32_t run = readlane(begins, 0);
+        uint64_t other = ~ballot(begins == run);
+        int64_t reached = other ? __builtin_ctzll(other) : kWave;  // chunks after this one that begin with the run
+        while (!other) {
+            other = ~ballot(key_at(a, end + (reached + lane) * a.chunk) == run);
+            reached += other ? __builtin_ctzll(other) : kWave;
+        }
+#pragma unroll
+        for (int j = 0; j < kJoinCols; ++j) acc[j] += second[j];
+        for (int64_t q0 = 2; q0 <= reached; q0 += kJoinAhead) {
+            float x[kJoinAhead][kJoinCols];
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k) {
+                const int64_t q = q0 + k <= reached ? q0 + k : reached;
+#pragma unroll
+                for (int j = 0; j < kJoinCols; ++j) x[k][j] = p[(2 * q - 1) * a.partial_stride + j];
+            }
+#pragma unroll
+            for (int k = 0; k < kJoinAhead; ++k)
+                if (q0 + k <= reached) {
+#pragma unroll
+                    for (int j = 0; j < kJoinCols; ++j) acc[j] += x[k][j];
+                }
+        }
+        O* out = grad + (int64_t)run * a.grad_stride + c;
+#pragma unroll
+        for (int j = 0; j < kJoinCols; ++j) {
+            if (c + j < a.dim) {
+                float y = acc[j] * a.scale;
+                if constexpr (ADD) y += (float)out[j];
+                out[j] = (O)y;
+            }
+        }
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -627,10 +683,10 @@ static int sum_chunk(int64_t n, int64_t slabs)
     return chunk;
 }
 
-EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, int64_t dim)
+EmbeddingGradPlan embedding_grad_plan(ElemKind grad_kind, int64_t n, int64_t rows, int64_t dim)
 {
     EmbeddingGradPlan p{};
-    const int64_t per = kind == kF32 ? 4 : 8;
+    const int64_t per = grad_kind == kF32 ? 4 : 8;  // columns per lane
     p.slabs = ceil_div(dim, kWave * per);
     p.chunk = sum_chunk(n, p.slabs);
     p.chunks = ceil_div(n, p.chunk);
@@ -646,7 +702,7 @@ EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, in
         p.bits = (bits + p.digits - 1) / p.digits;
         p.items = n > kTileSortMax / 2 ? 4 : 2;
         p.tiles = (int)ceil_div(n, kTileThreads * p.items);
-        p.table_words = (int64_t)p.digits * ((int64_t)ceil_div(p.tiles, 4) * 4 << p.bits);
+        p.table_words = (int64_t)p.tiles << p.bits;
     }
     p.table_words = ceil_div(p.table_words, 4) * 4;
     // keys and index, twice where passes go back and forth; then the parts of rows, 16-byte aligned
@@ -669,8 +725,9 @@ struct Clearing {
         rows = add ? 0 : rows_;
         share = ceil_div(kShareBytes, a.row_bytes);
     }
-    // The part of a launch that has `before` workgroups of `threads` of its own; returns the workgroups in all.
-    unsigned next(int64_t before, int threads, bool all = false)
+    // The part of a launch that has `before` workgroups of `threads` of its own: its share, or all that is left;
+    // others: but for rows that have tokens. Returns the workgroups in all.
+    unsigned next(int64_t before, int threads, bool all = false, bool others = false)
     {
         a.first = a.last;
         a.last = all || rows - a.first < share ? rows : a.first + share;
@@ -678,7 +735,10 @@ struct Clearing {
         // as many rows to a wave as leave 8,192 waves (the lanes of a wave look for one row each)
         const int64_t each = (a.last - a.first) / 8192;
         a.per_wave = (int)(each < 1 ? 1 : each < kWave ? each : kWave);
-        return (unsigned)(before + ceil_div(a.last - a.first, (int64_t)a.per_wave * (threads / kWave)));
+        int64_t waves = ceil_div(a.last - a.first, a.per_wave);
+        if (!others && a.last > a.first && a.stride_bytes == a.row_bytes)
+            waves = ceil_div(a.last * a.row_bytes, kPiece) - a.first * a.row_bytes / kPiece;
+        return (unsigned)(before + ceil_div(waves, threads / kWave));
     }
 };
 
@@ -687,21 +747,22 @@ static hipError_t embedding_grad_typed(const EmbeddingGradPlan& p, const void* d
                                        Clearing& clear, hipStream_t stream)
 {
     const int64_t units = p.chunks * p.slabs;
-    const unsigned blocks = clear.next(ceil_div(units, kWaves), kThreads, true);
+    const unsigned blocks = clear.next(ceil_div(units, kWaves), kThreads, true, true);
     embedding_sum_kernel<T, O, ADD><<<dim3(blocks), dim3(kThreads), 0, stream>>>((const T*)dout, (O*)grad, a, p.slabs,
                                                                                  units, clear.a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t groups = ceil_div(a.dim, kWave * kJoinCols), joins = ceil_div(p.chunks * groups, kWaves);
-    embedding_join_kernel<O, ADD><<<dim3((unsigned)(joins < 1024 ? joins : 1024)), dim3(kThreads), 0, stream>>>(
+    embedding_join_kernel<O, ADD><<<dim3((unsigned)(joins < 2048 ? joins : 2048)), dim3(kThreads), 0, stream>>>(
         (O*)grad, a, groups);
     return hipGetLastError();
 }
 
-int64_t embedding_grad_blocks(const EmbeddingGradPlan& p, int64_t n, int64_t rows)
+int64_t embedding_grad_blocks(const EmbeddingGradPlan& p, int64_t n, int64_t rows, int64_t row_bytes)
 {
     const int64_t sum = ceil_div(p.chunks * p.slabs, kWaves), keys = ceil_div(n, kThreads);
-    return (sum > keys ? sum : keys) + ceil_div(rows, kWaves * kWave) + 8192;
+    const int64_t clear = ceil_div(rows * row_bytes, kPiece * kWaves) + ceil_div(rows, kWaves * kWave) + 8192;
+    return (sum > keys ? sum : keys) + clear;
 }
 
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& p, const void* dout,
@@ -731,15 +792,16 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
             t = index; index = index2; index2 = t;
         }
     } else if (tiled) {
-        const TileSort a{(uint32_t)n, rows, p.bits, p.digits, p.items, p.tiles, (int)(ceil_div(p.tiles, 4) * 4), table};
-        unsigned grid = clear.next(p.tiles, kTileThreads);
-        if (wide_ids)
-            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)ids, a, keys, crossing, clear.a);
-        else
-            token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)ids, a, keys, crossing, clear.a);
-        e = hipGetLastError();
-        if (e != hipSuccess) return e;
+        const TileSort a{(uint32_t)n, rows, p.bits, p.digits, p.items, p.tiles, table};
         for (int d = 0; d < p.digits; ++d) {
+            const void* from = d ? nullptr : ids;
+            unsigned grid = clear.next(p.tiles, kTileThreads);
+            if (wide_ids)
+                token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)from, a, d, keys, crossing, clear.a);
+            else
+                token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)from, a, d, keys, crossing, clear.a);
+            e = hipGetLastError();
+            if (e != hipSuccess) return e;
             grid = clear.next(p.tiles, kTileThreads);
             const auto kernel = p.items == 2 ? token_pass_kernel<2> : token_pass_kernel<4>;
             kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>(keys, d ? index : nullptr, a, d, keys2, index2, clear.a);
@@ -749,7 +811,9 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
             t = index; index = index2; index2 = t;
         }
     } else {
-        const unsigned grid = clear.next(ceil_div(n, kRankTokens), kThreads);
+        // All of it where few rows can have tokens: two launches that clear cost more than some rows cleared in vain
+        // (1,003 tokens, 32,000 rows of 1,000: 17.3 us for both against 19.2).
+        const unsigned grid = clear.next(ceil_div(n, kRankTokens), kThreads, n <= rows / 8);
         const size_t lds = (size_t)((n + 63) / 64 * 64) * 4;
         if (wide_ids)
             token_rank_sort_kernel<<<dim3(grid), dim3(kThreads), lds, stream>>>((const int64_t*)ids, (uint32_t)n, rows,

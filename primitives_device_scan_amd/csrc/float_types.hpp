@@ -48,8 +48,9 @@ __device__ __forceinline__ void load_floats(const T* __restrict__ p, int64_t val
     }
 }
 
-// Rounds N floats to T (nearest even) and writes the first `valid` of them.
-template <typename T, int N>
+// Rounds N floats to T (nearest even) and writes the first `valid` of them
+// (NT: past the cache).
+template <typename T, int N, bool NT = false>
 __device__ __forceinline__ void store_floats(T* __restrict__ p, int64_t valid, const float (&x)[N])
 {
     constexpr int kPer = Vec16<T>::kN;
@@ -62,7 +63,10 @@ __device__ __forceinline__ void store_floats(T* __restrict__ p, int64_t valid, c
         for (int v = 0; v < N / kPer; ++v) {
             u32x4 u;
             __builtin_memcpy(&u, t + v * kPer, sizeof(u));
-            *reinterpret_cast<typename Vec16<T>::type*>(p + v * kPer) = u;
+            if constexpr (NT)
+                __builtin_nontemporal_store(u, reinterpret_cast<typename Vec16<T>::type*>(p + v * kPer));
+            else
+                *reinterpret_cast<typename Vec16<T>::type*>(p + v * kPer) = u;
         }
     } else {
 #pragma unroll

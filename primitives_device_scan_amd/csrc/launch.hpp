@@ -102,9 +102,9 @@ struct EmbeddingGradPlan {
     int64_t partial_at;      // byte offset of the parts
     int64_t bytes;           // scratch in all
 };
-EmbeddingGradPlan embedding_grad_plan(ElemKind kind, int64_t n, int64_t rows, int64_t dim);
+EmbeddingGradPlan embedding_grad_plan(ElemKind grad_kind, int64_t n, int64_t rows, int64_t dim);
 int64_t embedding_most_rows();
-int64_t embedding_grad_blocks(const EmbeddingGradPlan& plan, int64_t n, int64_t rows);  // workgroups of the largest launch, or more
+int64_t embedding_grad_blocks(const EmbeddingGradPlan& plan, int64_t n, int64_t rows, int64_t row_bytes);  // workgroups of the largest launch, or more
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& plan, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
                                  int64_t dim, float scale, void* grad, int64_t grad_stride, bool add, char* aux,
