@@ -7,36 +7,75 @@
 //   p_e = softmax of l over the experts that can be chosen, or sigmoid(l_e)
 //   w_j = scale * p_ids[j], divided by the sum of the chosen p if `renorm`
 //
-// One wave per token; lane l holds experts l, l + 64, ... (at most 8).
+// A token is a group of L lanes, so a wave works on 64 / L tokens at once: with
+// a wave to a token the instructions of the selection were what bounded it.
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
 
 namespace ds {
 
-constexpr int kRouteMaxPerLane = 8;  // 512 experts
+constexpr int kMostExperts = 511;
+constexpr int kMostTopK = 64;
+typedef float f32x4_v __attribute__((ext_vector_type(4)));
+typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Largest value of the wave, in every lane. The operands are never NaN. The
-// lanes that a step does not reach keep their own value.
-__device__ __forceinline__ float wave_max(float x)
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_swap(uint32_t x)
 {
-#define DS_MAX_STEP(CTRL, ROWS)                                                                          \
-    x = fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, x),       \
-                                                                       __builtin_bit_cast(int, x), CTRL, \
-                                                                       ROWS, 0xf, false)))
-    DS_MAX_STEP(0x111, 0xf);
-    DS_MAX_STEP(0x112, 0xf);
-    DS_MAX_STEP(0x114, 0xf);
-    DS_MAX_STEP(0x118, 0xf);
-    DS_MAX_STEP(0x142, 0xa);
-    DS_MAX_STEP(0x143, 0xc);
-#undef DS_MAX_STEP
-    return readlane(x, kWave - 1);
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, CTRL, 0xf, 0xf, true);  // every lane has a source
 }
 
+// x combined over the group's L lanes, in every one of them: neighbours, pairs,
+// then mirrored halves of 8 and of 16 lanes.
+template <int L, typename OP>
+__device__ __forceinline__ uint32_t group_all(uint32_t x, OP op)
+{
+    x = op(x, dpp_swap<0xB1>(x));
+    x = op(x, dpp_swap<0x4E>(x));
+    if constexpr (L >= 8) x = op(x, dpp_swap<0x141>(x));
+    if constexpr (L >= 16) x = op(x, dpp_swap<0x140>(x));
+    return x;
+}
+template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t x)
+{
+    return group_all<L>(x, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+template <int L> __device__ __forceinline__ uint32_t group_min(uint32_t x)
+{
+    return group_all<L>(x, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+template <int L> __device__ __forceinline__ float group_sum(float x)
+{
+    return __builtin_bit_cast(float, group_all<L>(__builtin_bit_cast(uint32_t, x), [](uint32_t a, uint32_t b) {
+                                  return __builtin_bit_cast(
+                                      uint32_t, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
+                              }));
+}
+
+// Floats as whole numbers of the same order, both zeros alike and NaN as -inf;
+// 0 is below every float. (The sum makes -0 a +0 and every NaN a quiet one,
+// which the maximum then drops.)
+constexpr uint32_t kNoKey = 0x007FFFFFu;  // of -inf
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, fmaxf(x + 0.0f, neg_inf()));
+    return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t k)
+{
+    return __builtin_bit_cast(float, k ^ ((uint32_t)((int32_t)~k >> 31) | 0x80000000u));
+}
+template <int L> __device__ __forceinline__ float group_max(float x) { return key_value(group_max<L>(order_key(x))); }
+
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// exp(x) for the sums over all experts: 2^(x log2 e), off by at most 1.5 |x| +
+// 2 steps of 2^-24, relative (the product's two roundings), where the library
+// function takes five times the instructions; 0 below 2^-126.
+__device__ __forceinline__ float exp_sum(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
 
 // sigmoid(x) (1 - sigmoid(x)) without the difference from 1, which loses its
 // digits for large x; 0 at both infinities.
@@ -46,77 +85,180 @@ __device__ __forceinline__ float sigmoid_slope(float x)
     return e / ((1.0f + e) * (1.0f + e));
 }
 
-// Experts per lane is NJ: experts <= 64 * NJ.
-template <typename T, int NJ>
+// This lane's logits of its token: vector v holds experts (v * L + lane) * N ..
+// + N - 1, so that a group's loads are whole lines; -inf past the last expert.
+template <typename T, int L, int NV>
+__device__ __forceinline__ void load_logits(const T* __restrict__ row, int experts, int lane,
+                                            float (&l)[NV][Vec16<T>::kN])
+{
+    constexpr int N = Vec16<T>::kN;
+    if (experts % N == 0) {
+        u32x4 raw[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int e = (v * L + lane) * N;
+            raw[v] = *reinterpret_cast<const typename Vec16<T>::type*>(row + (e < experts ? e : 0));
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            T t[N];
+            __builtin_memcpy(t, &raw[v], sizeof(t));
+#pragma unroll
+            for (int j = 0; j < N; ++j) l[v][j] = (v * L + lane) * N < experts ? (float)t[j] : neg_inf();
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int e = (v * L + lane) * N + j;
+                l[v][j] = e < experts ? (float)row[e] : neg_inf();
+            }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Selection. A token's keys lie in LDS, in strips of S consecutive experts; lane
+// i of the group knows the largest key of strip i. A choice finds the largest
+// of these, the strip that has it (the first, so ties go to the lowest expert),
+// then the group reads that strip, S / L keys to a lane, finds the expert and
+// the strip's next largest key. 65,536 tokens, top-8 of 256, bf16 with a bias:
+// see the launcher.
+// ---------------------------------------------------------------------------
+template <typename T, int L, int S>
 __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict__ logits, int64_t tokens, int experts,
                                                              int64_t stride, const float* __restrict__ bias,
                                                              int top_k, bool use_sigmoid, bool renorm, float scale,
                                                              float* __restrict__ weights, int32_t* __restrict__ ids)
 {
-    const int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    if (t >= tokens) return;
-    const int lane = lane_id();
-    const T* row = logits + t * stride;
-    float sel[NJ], top = neg_inf(), total = 0.0f;
-    float l[NJ];
+    constexpr int N = Vec16<T>::kN, NV = (S + N - 1) / N, P = S / L;
+    constexpr int kStrip = S + 4;  // words; the padding puts the strips' equal places into different banks
+    constexpr int kGroups = kWave / L;
+    static_assert(S % N == 0 && S % L == 0 && S >= 4, "whole vectors to a strip, whole shares to a lane");
+    __shared__ __align__(16) uint32_t s_key[kWaves][kGroups][L * kStrip];
+    __shared__ uint16_t s_id[kWaves][kGroups][kMostTopK];
+    constexpr uint16_t kNone = 0xFFFF;
+    static_assert(L * kStrip >= (L * S < kMostTopK ? L * S : kMostTopK), "the keys' place holds the chosen scores");
+    const int wave = threadIdx.x / kWave, group = lane_id() / L, lane = lane_id() % L;
+    const int64_t t = ((int64_t)blockIdx.x * kWaves + wave) * kGroups + group;
+    const bool there = t < tokens;
+    const T* row = logits + (there ? t : tokens - 1) * stride;
+    uint32_t* keys = s_key[wave][group];
+    uint16_t* choice = s_id[wave][group];
+
+    float l[NV][N];
+    load_logits<T, L, NV>(row, experts, lane, l);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int e = j * kWave + lane;
-        l[j] = e < experts ? (float)row[e] : neg_inf();
-        sel[j] = e < experts && bias ? l[j] + bias[e] : l[j];
-        if (!(sel[j] > neg_inf())) sel[j] = l[j] = neg_inf();  // -inf or NaN: never chosen
-    }
-    if (!use_sigmoid && !renorm) {
+    for (int v = 0; v < NV; ++v) {
+        const int e0 = (v * L + lane) * N;
+        float sel[N];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) top = fmaxf(top, l[j]);
-        top = wave_max(top);
+        for (int j = 0; j < N; ++j) sel[j] = l[v][j];
+        if (bias) {
+            if (experts % N == 0) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) total += sel[j] > neg_inf() ? expf(l[j] - top) : 0.0f;
-        total = wave_sum(total);
-    }
-    int mine = -1;              // lane i: the i-th choice
-    float chosen = neg_inf();   // and its logit
-    for (int i = 0; i < top_k; ++i) {
-        float m = sel[0];
+                for (int j = 0; j < N; j += 4) {
+                    const f32x4_v b = *reinterpret_cast<const f32x4_a4*>(bias + (e0 < experts ? e0 : 0) + j);
 #pragma unroll
-        for (int j = 1; j < NJ; ++j) m = fmaxf(m, sel[j]);
-        m = wave_max(m);
-        if (!(m > neg_inf())) break;  // uniform: nothing left
-        bool found = false;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const uint64_t at = ballot(sel[j] == m);
-            if (!found && at) {
-                found = true;
-                const int src = __builtin_ctzll(at);
-                const float value = readlane(l[j], src);
-                if (lane == i) {
-                    mine = j * kWave + src;
-                    chosen = value;
+                    for (int i = 0; i < 4; ++i) sel[j + i] += b[i];
                 }
-                if (lane == src) sel[j] = neg_inf();
+            } else {
+#pragma unroll
+                for (int j = 0; j < N; ++j) sel[j] += bias[e0 + j < experts ? e0 + j : 0];
             }
         }
+        // -inf past the last expert, but +inf + -inf is NaN: both keys are kNoKey, which is never chosen
+        uint32_t* at = keys + e0 / S * kStrip + e0 % S;
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+            *reinterpret_cast<u32x4*>(at + j) =
+                u32x4{order_key(sel[j]), order_key(sel[j + 1]), order_key(sel[j + 2]), order_key(sel[j + 3])};
     }
-    float w = 0.0f;
-    if (use_sigmoid) {
-        w = mine >= 0 ? sigmoid(chosen) : 0.0f;
-    } else {
-        if (renorm) top = wave_max(chosen);
-        w = mine >= 0 ? expf(chosen - top) : 0.0f;
+    float top = 0.0f, total = 0.0f;
+    if (!use_sigmoid && !renorm) {  // over the experts that can be chosen
+        top = neg_inf();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int e0 = (v * L + lane) * N;
+            const uint32_t* at = keys + e0 / S * kStrip + e0 % S;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (at[j] <= kNoKey) l[v][j] = neg_inf();
+                top = l[v][j] > top ? l[v][j] : top;
+            }
+        }
+        top = group_max<L>(top);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) total += l[v][j] > neg_inf() ? exp_sum(l[v][j] - top) : 0.0f;
+        total = group_sum<L>(total);
     }
-    if (renorm) total = wave_sum(w);
-    if (renorm || !use_sigmoid) w = total > 0.0f || total != total ? w / total : 0.0f;
-    if (lane < top_k) {
-        weights[t * top_k + lane] = w * scale;
-        ids[t * top_k + lane] = mine;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    uint32_t best = 0;  // largest key of this lane's strip
+#pragma unroll
+    for (int j = 0; j < S; j += 4) {
+        const u32x4 k = *reinterpret_cast<const u32x4*>(keys + lane * kStrip + j);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) best = k[q] > best ? k[q] : best;
+    }
+    for (int i = 0; i < top_k; ++i) {
+        const uint32_t m = group_max<L>(best);
+        const uint32_t w = group_min<L>(best == m ? (uint32_t)lane : (uint32_t)L);
+        uint32_t* strip = keys + w * kStrip;
+        uint32_t x[P], at = S;
+#pragma unroll
+        for (int q = 0; q < P; ++q) x[q] = strip[lane * P + q];
+#pragma unroll
+        for (int q = P - 1; q >= 0; --q) at = x[q] == m ? (uint32_t)(lane * P + q) : at;
+        at = group_min<L>(at);
+        uint32_t next = 0;
+#pragma unroll
+        for (int q = 0; q < P; ++q) next = (uint32_t)(lane * P + q) != at && x[q] > next ? x[q] : next;
+        next = group_max<L>(next);
+        if ((uint32_t)lane == w) best = next;
+        if (lane == 0) {
+            strip[at] = 0u;
+            choice[i] = m > kNoKey ? (uint16_t)(w * S + at) : kNone;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    // the chosen logits, their scores, the weights
+    float* chosen = reinterpret_cast<float*>(keys);  // no key is needed any more
+    float most = neg_inf();
+    for (int j = lane; j < top_k; j += L) {
+        const uint16_t id = choice[j];
+        const float x = id != kNone ? (float)row[id] : neg_inf();
+        chosen[j] = x;
+        most = x > most ? x : most;
+    }
+    if (!use_sigmoid && renorm) top = group_max<L>(most);
+    float sum = 0.0f;
+    for (int j = lane; j < top_k; j += L) {
+        const float x = chosen[j];
+        const float p = choice[j] == kNone ? 0.0f : use_sigmoid ? sigmoid(x) : expf(x - top);
+        chosen[j] = p;
+        sum += p;
+    }
+    if (renorm) total = group_sum<L>(sum);
+    for (int j = lane; j < top_k; j += L) {
+        float w = chosen[j];
+        if (renorm || !use_sigmoid) w = total > 0.0f || total != total ? w / total : 0.0f;
+        if (there) {
+            weights[t * top_k + j] = w * scale;
+            ids[t * top_k + j] = choice[j] == kNone ? -1 : choice[j];
+        }
     }
 }
 
+// ---------------------------------------------------------------------------
 // The gradient with respect to the logits, for given ids and d loss / d w:
 // the scores are computed again from the logits, then the chain rule goes
-// through the division by the chosen scores' sum and through the scores.
-template <typename T, int NJ>
+// through the division by the chosen scores' sum and through the scores. The
+// chosen experts' parts are added up in LDS, choice by choice, so an expert
+// that is named twice has its parts added in their order.
+// ---------------------------------------------------------------------------
+template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __restrict__ logits, int64_t tokens,
                                                                   int experts, int64_t stride,
                                                                   const int32_t* __restrict__ ids,
@@ -124,116 +266,145 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
                                                                   bool use_sigmoid, bool renorm, float scale,
                                                                   T* __restrict__ dlogits, int64_t dstride)
 {
-    const int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave;
-    if (t >= tokens) return;
-    const int lane = lane_id();
-    const T* row = logits + t * stride;
-    float l[NJ], p[NJ];
+    constexpr int N = Vec16<T>::kN, kGroups = kWave / L, M = kMostTopK / L;
+    __shared__ __align__(16) float s_dp[kWaves][kGroups][NV * L * N];
+    const int wave = threadIdx.x / kWave, group = lane_id() / L, lane = lane_id() % L;
+    const int64_t t = ((int64_t)blockIdx.x * kWaves + wave) * kGroups + group;
+    const bool there = t < tokens;
+    const int64_t token = there ? t : tokens - 1;
+    const T* row = logits + token * stride;
+    float* dp = s_dp[wave][group];
+    // choice j is held by lane j % L, as its (j / L)-th
+    int id[M];
+    float dw[M], q[M];
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int e = j * kWave + lane;
-        l[j] = e < experts ? (float)row[e] : neg_inf();
-        if (!(l[j] > neg_inf())) l[j] = neg_inf();  // -inf or NaN: no part in the scores
-    }
-    int id = -1;
-    float dw = 0.0f;
-    if (lane < top_k) {
-        id = ids[t * top_k + lane];
-        if (id < 0 || id >= experts) id = -1;
-        if (id >= 0) dw = dweights[t * top_k + lane] * scale;
-    }
-    if (use_sigmoid) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) p[j] = l[j] > neg_inf() ? sigmoid(l[j]) : 0.0f;
-    } else {
-        float top = l[0], total = 0.0f;
-#pragma unroll
-        for (int j = 1; j < NJ; ++j) top = fmaxf(top, l[j]);
-        top = wave_max(top);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            p[j] = l[j] > neg_inf() ? expf(l[j] - top) : 0.0f;
-            total += p[j];
+    for (int m = 0; m < M; ++m) {
+        id[m] = -1;
+        dw[m] = q[m] = 0.0f;
+        if (m * L < top_k) {  // uniform
+            const int j = m * L + lane;
+            if (j < top_k) {
+                id[m] = ids[token * top_k + j];
+                dw[m] = dweights[token * top_k + j] * scale;
+            }
+            if (id[m] < 0 || id[m] >= experts) {
+                id[m] = -1;
+                dw[m] = 0.0f;
+            }
         }
-        total = wave_sum(total);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) p[j] = total > 0.0f || total != total ? p[j] / total : 0.0f;
     }
-    // q: the chosen scores, lane i the i-th
-    float q = 0.0f;
-    for (int i = 0; i < top_k; ++i) {
-        const int e = readlane(id, i);
-        if (e < 0) continue;  // uniform
-        float v = 0.0f;
+    float l[NV][N], top = neg_inf(), total = 0.0f;
+    float chosen[M];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            if (e / kWave == j) v = readlane(p[j], e % kWave);
-        if (lane == i) q = v;
-    }
-    if (renorm) {
-        float total = wave_sum(q);
-        total = total > 0.0f || total != total ? total : 1.0f;
-        const float dot = wave_sum(dw * q) / total;
-        if (id >= 0) dw = (dw - dot) / total;
-    }
-    float dp[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) dp[j] = 0.0f;
-    for (int i = 0; i < top_k; ++i) {
-        const int e = readlane(id, i);
-        const float d = readlane(dw, i);
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-            if (e == j * kWave + lane) dp[j] += d;
-    }
-    float dot = 0.0f;
+    for (int m = 0; m < M; ++m) chosen[m] = m * L < top_k && id[m] >= 0 ? (float)row[id[m]] : neg_inf();
     if (!use_sigmoid) {
+        load_logits<T, L, NV>(row, experts, lane, l);
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) dot += dp[j] * p[j];
-        dot = wave_sum(dot);
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) top = l[v][j] > top ? l[v][j] : top;  // false for NaN
+        top = group_max<L>(top);
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                l[v][j] = l[v][j] > neg_inf() ? exp_sum(l[v][j] - top) : 0.0f;
+                total += l[v][j];
+            }
+        total = group_sum<L>(total);
+        total = total > 0.0f || total != total ? 1.0f / total : 0.0f;
+    }
+    // the chosen scores
+    float sum = 0.0f, dot = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (m * L < top_k) {
+            if (chosen[m] > neg_inf()) q[m] = use_sigmoid ? sigmoid(chosen[m]) : exp_sum(chosen[m] - top) * total;
+            sum += q[m];
+            dot += dw[m] * q[m];
+        }
+    if (renorm) {
+        sum = group_sum<L>(sum);
+        sum = sum > 0.0f || sum != sum ? sum : 1.0f;
+        dot = group_sum<L>(dot) / sum;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            if (id[m] >= 0) dw[m] = (dw[m] - dot) / sum;
     }
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-        const int e = j * kWave + lane;
-        const float d = use_sigmoid ? dp[j] * sigmoid_slope(l[j]) : p[j] * (dp[j] - dot);
-        if (e < experts) dlogits[t * dstride + e] = (T)d;
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < N; j += 4) *reinterpret_cast<f32x4_v*>(dp + (v * L + lane) * N + j) = f32x4_v{0.0f, 0.0f, 0.0f, 0.0f};
+    float all = 0.0f;  // softmax: the part that every expert has, sum of dp p
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+        if (m * L < top_k) {
+            const float d = use_sigmoid ? dw[m] * (chosen[m] > neg_inf() ? sigmoid_slope(chosen[m]) : 0.0f) : dw[m];
+            all += dw[m] * q[m];
+            for (int i = 0; i < L && m * L + i < top_k; ++i)
+                if (lane == i && id[m] >= 0) __hip_atomic_fetch_add(dp + id[m], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
+    if (!use_sigmoid) all = group_sum<L>(all);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    T* out = dlogits + token * dstride;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int e0 = (v * L + lane) * N;
+        float d[N];
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const f32x4_v x = *reinterpret_cast<const f32x4_v*>(dp + e0 + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[j + i] = x[i];
+        }
+        if (!use_sigmoid) {
+#pragma unroll
+            for (int j = 0; j < N; ++j) d[j] = l[v][j] * total * (d[j] - all);
+        }
+        if (there && e0 < experts) store_floats<T, N>(out + e0, experts - e0, d);
     }
 }
 
-int route_max_experts() { return kRouteMaxPerLane * kWave - 1; }
-int64_t route_blocks(int64_t tokens) { return (tokens + kWaves - 1) / kWaves; }
+int route_max_experts() { return kMostExperts; }
+int64_t route_blocks(int64_t tokens) { return (tokens + kWaves - 1) / kWaves; }  // of the largest launch, or more
 
+// Lanes to a token: as few as the keys of a wave's tokens leave LDS for. At
+// 65,536 tokens and top-8 of 256 experts in bf16 with a bias, with sigmoid
+// scores, a wave to a token took 51.6 us.
 template <typename T>
 static hipError_t route_typed(const RouteArgs& a, const void* logits, const float* bias, float* weights, int32_t* ids,
                               hipStream_t stream)
 {
-    const dim3 grid((unsigned)route_blocks(a.tokens)), block(kThreads);
-#define DS_ROUTE(NJ)                                                                                         \
-    moe_route_kernel<T, NJ><<<grid, block, 0, stream>>>((const T*)logits, a.tokens, a.experts, a.stride, bias, \
-                                                        a.top_k, a.use_sigmoid, a.renorm, a.scale, weights, ids)
-    if (a.experts <= kWave) DS_ROUTE(1);
-    else if (a.experts <= 2 * kWave) DS_ROUTE(2);
-    else if (a.experts <= 4 * kWave) DS_ROUTE(4);
-    else DS_ROUTE(8);
-#undef DS_ROUTE
-    return hipGetLastError();
+    const auto launch = [&](auto kernel, int lanes) {
+        const int64_t per_block = kWaves * (kWave / lanes);
+        kernel<<<dim3((unsigned)((a.tokens + per_block - 1) / per_block)), dim3(kThreads), 0, stream>>>(
+            (const T*)logits, a.tokens, a.experts, a.stride, bias, a.top_k, a.use_sigmoid, a.renorm, a.scale, weights,
+            ids);
+        return hipGetLastError();
+    };
+    if (a.experts <= 32) return launch(moe_route_kernel<T, 4, 8>, 4);
+    if (a.experts <= 64) return launch(moe_route_kernel<T, 4, 16>, 4);
+    if (a.experts <= 128) return launch(moe_route_kernel<T, 8, 16>, 8);
+    if (a.experts <= 256) return launch(moe_route_kernel<T, 8, 32>, 8);
+    return launch(moe_route_kernel<T, 16, 32>, 16);
 }
 
 template <typename T>
 static hipError_t route_grad_typed(const RouteArgs& a, const void* logits, const int32_t* ids, const float* dweights,
                                    void* dlogits, int64_t dstride, hipStream_t stream)
 {
-    const dim3 grid((unsigned)route_blocks(a.tokens)), block(kThreads);
-#define DS_ROUTE(NJ)                                                                                           \
-    moe_route_grad_kernel<T, NJ><<<grid, block, 0, stream>>>((const T*)logits, a.tokens, a.experts, a.stride, ids, \
-                                                             dweights, a.top_k, a.use_sigmoid, a.renorm, a.scale, \
-                                                             (T*)dlogits, dstride)
-    if (a.experts <= kWave) DS_ROUTE(1);
-    else if (a.experts <= 2 * kWave) DS_ROUTE(2);
-    else if (a.experts <= 4 * kWave) DS_ROUTE(4);
-    else DS_ROUTE(8);
-#undef DS_ROUTE
-    return hipGetLastError();
+    constexpr int W = 16 / Vec16<T>::kN;  // vectors for 16 experts to a lane
+    const auto launch = [&](auto kernel, int lanes) {
+        const int64_t per_block = kWaves * (kWave / lanes);
+        kernel<<<dim3((unsigned)((a.tokens + per_block - 1) / per_block)), dim3(kThreads), 0, stream>>>(
+            (const T*)logits, a.tokens, a.experts, a.stride, ids, dweights, a.top_k, a.use_sigmoid, a.renorm, a.scale,
+            (T*)dlogits, dstride);
+        return hipGetLastError();
+    };
+    if (a.experts <= 64) return launch(moe_route_grad_kernel<T, 8, W / 2>, 8);
+    if (a.experts <= 128) return launch(moe_route_grad_kernel<T, 8, W>, 8);
+    if (a.experts <= 256) return launch(moe_route_grad_kernel<T, 16, W>, 16);
+    return launch(moe_route_grad_kernel<T, 16, 2 * W>, 16);
 }
 
 hipError_t launch_moe_route(ElemKind kind, const RouteArgs& a, const void* logits, const float* bias, float* weights,
