@@ -301,8 +301,12 @@ def moe_align(topk_ids: torch.Tensor, num_experts: int, block: int, *, stream=No
 
 
 # Language-model operators. Their matrices are 2-D tensors whose rows are contiguous; rows may be any distance apart.
+# Small calls are bound by this code, not by the GPU, so the checks of what is right ask each tensor a few questions and
+# the rest is left to the functions that say what is wrong.
 _FLOATS = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
 SCORES = {"softmax": 0, "sigmoid": 1}
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _float_code(x: torch.Tensor, name: str) -> int:
@@ -312,16 +316,21 @@ def _float_code(x: torch.Tensor, name: str) -> int:
     return code
 
 
-def _check_rows(x: torch.Tensor, name: str, rows: int | None = None, cols: int | None = None, like=None) -> int:
+def _check_rows(x: torch.Tensor, name: str, rows: int | None = None, cols: int | None = None,
+                like: torch.Tensor | None = None) -> int:
     """x is a 2-D GPU tensor with contiguous rows, of the given shape and on like's device; returns its row stride."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
-    if x.dim() != 2 or (rows is not None and x.shape[0] != rows) or (cols is not None and x.shape[1] != cols):
-        raise ValueError(f"{name} must be a matrix of shape [{'*' if rows is None else rows}, "
-                         f"{'*' if cols is None else cols}], not {list(x.shape)}")
-    if like is not None and x.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, not of shape {list(x.shape)}")
     n, m = x.shape
+    if (rows is not None and n != rows) or (cols is not None and m != cols):
+        raise ValueError(f"{name} must be a matrix of shape [{'*' if rows is None else rows}, "
+                         f"{'*' if cols is None else cols}], not {[n, m]}")
+    if like is not None and x.get_device() != like.get_device():
+        raise ValueError(f"{name} must be on {like.device}")
+    if x.is_contiguous():
+        return m
     if m > 1 and x.stride(1) != 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     if n <= 1 or m == 0:
@@ -331,48 +340,48 @@ def _check_rows(x: torch.Tensor, name: str, rows: int | None = None, cols: int |
     return x.stride(0)
 
 
-def _check_flat(x: torch.Tensor, name: str, dtypes, shape, like: torch.Tensor):
+def _check_flat(x: torch.Tensor, name: str, dtype, shape, like: torch.Tensor):
+    """x is contiguous, of the dtype (or a key of the dict of them) and shape given, on like's device."""
     _check_tensor(x, name)
-    if x.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, not {x.dtype}")
-    if shape is not None and tuple(x.shape) != tuple(shape):
+    if x.dtype not in dtype if isinstance(dtype, dict) else x.dtype != dtype:
+        names = " or ".join(str(d) for d in dtype) if isinstance(dtype, dict) else str(dtype)
+        raise TypeError(f"{name} must be {names}, not {x.dtype}")
+    if shape is not None and x.shape != shape:
         raise ValueError(f"{name} must have the shape {list(shape)}, not {list(x.shape)}")
-    if x.device != like.device:
+    if x.get_device() != like.get_device():
         raise ValueError(f"{name} must be on {like.device}")
 
 
-class _On:
-    """Device and stream of a call: outputs are allocated on the stream that the call runs on, and tensors that belong
-    to another stream are kept from reuse until the call has run."""
+def _elsewhere(x: torch.Tensor, stream) -> bool:
+    """Whether a call on x runs on another stream than the current one of the current device."""
+    return stream is not None or x.get_device() != _current_device()
 
-    def __init__(self, like: torch.Tensor, stream):
-        self.stream = stream
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            self.stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-        self.device = like.device
-        self.switch = torch.cuda.current_device() != like.device.index
 
-    def __enter__(self):
-        if self.stream is not None:
-            self.before = torch.cuda.stream(self.stream)  # also makes the stream's device current
-            self.before.__enter__()
-            self.handle = self.stream.cuda_stream
-        else:
-            if self.switch:
-                self.before = torch.cuda.device(self.device)
-                self.before.__enter__()
-            self.handle = torch.cuda.current_stream(self.device).cuda_stream
-        return self
+def _stream_of(x: torch.Tensor) -> int:
+    return torch.cuda.current_stream(x.device).cuda_stream
 
-    def __exit__(self, *exc):
-        if self.stream is not None or self.switch:
-            self.before.__exit__(*exc)
 
-    def uses(self, *tensors):
-        if self.stream is not None:
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(self.stream)
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    def _stream_of(x: torch.Tensor) -> int:  # noqa: F811  the same without a Stream object, 2 us less per call
+        return torch._C._cuda_getCurrentRawStream(x.get_device())
+
+
+def _call_elsewhere(call, x: torch.Tensor, stream, used):
+    """call() with x's device and the stream current: outputs are allocated on the stream that the call runs on, and
+    tensors that belong to another stream are kept from reuse until the call has run."""
+    if stream is None:
+        with torch.cuda.device(x.device):
+            return call()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=x.device)
+    with torch.cuda.stream(stream):  # also makes the stream's device current
+        if _current_device() != x.get_device():
+            raise ValueError(f"the stream must be one of {x.device}")
+        result = call()
+        for t in used:
+            if t is not None:
+                t.record_stream(stream)
+    return result
 
 
 def embedding(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out: torch.Tensor | None = None,
@@ -381,20 +390,27 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out
     Returns [*ids.shape, dim]; `out`, if given, is a matrix [ids.numel(), dim] and is returned as it is."""
     code = _float_code(table, "table")
     stride = _check_rows(table, "table")
+    _check_flat(ids, "ids", _ID_BYTES, None, table)
+    if _elsewhere(table, stream):
+        return _call_elsewhere(lambda: embedding(table, ids, scale=scale, out=out), table, stream, (table, ids, out))
     rows, dim = table.shape
-    _check_flat(ids, "ids", (torch.int32, torch.int64), None, table)
     n = ids.numel()
-    with _On(table, stream) as on:
-        made = out is None
-        if made:
-            out = torch.empty((n, dim), dtype=table.dtype, device=table.device)
+    shaped = None
+    if out is None:
+        shape = ids.shape
+        if len(shape) == 1:
+            out = table.new_empty((n, dim))
+        else:
+            shaped = table.new_empty((*shape, dim))
+            out = shaped.view(n, dim)
+        out_stride = dim
+    else:
         out_stride = _check_rows(out, "out", n, dim, table)
         if out.dtype != table.dtype:
             raise TypeError("out must have the table's dtype")
-        _check(lib.ds_embedding(code, table.data_ptr(), rows, dim, stride, ids.data_ptr(), ids.element_size(), n,
-                                scale, out.data_ptr(), out_stride, on.handle), "ds_embedding")
-        on.uses(table, ids, out)
-    return out.view(*ids.shape, dim) if made else out
+    _check(lib.ds_embedding(code, table.data_ptr(), rows, dim, stride, ids.data_ptr(), _ID_BYTES[ids.dtype], n, scale,
+                            out.data_ptr(), out_stride, _stream_of(table)), "ds_embedding")
+    return out if shaped is None else shaped
 
 
 def embedding_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: float = 1.0,
@@ -410,25 +426,29 @@ def embedding_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: f
             raise ValueError("dout must be a matrix, or contiguous of shape [*ids.shape, dim]")
         dout = dout.view(ids.numel(), dout.shape[-1])
     code = _float_code(dout, "dout")
-    stride = _check_rows(dout, "dout", ids.numel())
-    n, dim = dout.shape
-    _check_flat(ids, "ids", (torch.int32, torch.int64), None, dout)
+    n = ids.numel()
+    stride = _check_rows(dout, "dout", n)
+    _check_flat(ids, "ids", _ID_BYTES, None, dout)
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if dtype is None:
         dtype = dout.dtype if out is None else out.dtype
-    if dtype not in (dout.dtype, torch.float32):
+    if dtype != dout.dtype and dtype != torch.float32:
         raise TypeError("the gradient's dtype must be dout's or float32")
-    with _On(dout, stream) as on:
-        if out is None:
-            out = torch.empty((rows, dim), dtype=dtype, device=dout.device)
+    if _elsewhere(dout, stream):
+        return _call_elsewhere(lambda: embedding_grad(dout, ids, rows, scale=scale, dtype=dtype, out=out,
+                                                      accumulate=accumulate), dout, stream, (dout, ids, out))
+    dim = dout.shape[1]
+    if out is None:
+        out = dout.new_empty((rows, dim), dtype=dtype)
+        grad_stride = dim
+    else:
         grad_stride = _check_rows(out, "out", rows, dim, dout)
         if out.dtype != dtype:
             raise TypeError(f"out must be {dtype}")
-        _check(lib.ds_embedding_grad(code, dout.data_ptr(), stride, ids.data_ptr(), ids.element_size(), n, scale,
-                                     _FLOATS[dtype], out.data_ptr(), rows, dim, grad_stride, int(bool(accumulate)),
-                                     on.handle), "ds_embedding_grad")
-        on.uses(dout, ids, out)
+    _check(lib.ds_embedding_grad(code, dout.data_ptr(), stride, ids.data_ptr(), _ID_BYTES[ids.dtype], n, scale,
+                                 _FLOATS[dtype], out.data_ptr(), rows, dim, grad_stride, 1 if accumulate else 0,
+                                 _stream_of(dout)), "ds_embedding_grad")
     return out
 
 
@@ -442,19 +462,19 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     stride = _check_rows(logits, "logits")
     tokens, experts = logits.shape
     if bias is not None:
-        _check_flat(bias, "bias", (torch.float32,), (experts,), logits)
+        _check_flat(bias, "bias", torch.float32, (experts,), logits)
     if score not in SCORES:
         raise ValueError(f"score must be one of {list(SCORES)}")
     if not 1 <= top_k <= experts:
         raise ValueError("top_k must be between 1 and the number of experts")
-    with _On(logits, stream) as on:
-        weights = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
-        ids = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
-        _check(lib.ds_moe_route(code, logits.data_ptr(), tokens, experts, stride,
-                                None if bias is None else bias.data_ptr(), top_k, SCORES[score],
-                                int(bool(renormalize)), scale, weights.data_ptr(), ids.data_ptr(), on.handle),
-               "ds_moe_route")
-        on.uses(logits, bias, weights, ids)
+    if _elsewhere(logits, stream):
+        return _call_elsewhere(lambda: moe_route(logits, top_k, score=score, bias=bias, renormalize=renormalize,
+                                                 scale=scale), logits, stream, (logits, bias))
+    weights = logits.new_empty((tokens, top_k), dtype=torch.float32)
+    ids = logits.new_empty((tokens, top_k), dtype=torch.int32)
+    _check(lib.ds_moe_route(code, logits.data_ptr(), tokens, experts, stride, None if bias is None else bias.data_ptr(),
+                            top_k, SCORES[score], 1 if renormalize else 0, scale, weights.data_ptr(), ids.data_ptr(),
+                            _stream_of(logits)), "ds_moe_route")
     return weights, ids
 
 
@@ -464,20 +484,21 @@ def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tens
     (float32 [tokens, top_k]) of the weights; in the logits' dtype."""
     code = _float_code(logits, "logits")
     stride = _check_rows(logits, "logits")
-    tokens, experts = logits.shape
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, top_k]")
+    tokens, experts = logits.shape
     top_k = ids.shape[1]
-    _check_flat(ids, "ids", (torch.int32,), (tokens, top_k), logits)
-    _check_flat(dweights, "dweights", (torch.float32,), (tokens, top_k), logits)
+    _check_flat(ids, "ids", torch.int32, (tokens, top_k), logits)
+    _check_flat(dweights, "dweights", torch.float32, (tokens, top_k), logits)
     if score not in SCORES:
         raise ValueError(f"score must be one of {list(SCORES)}")
-    with _On(logits, stream) as on:
-        dlogits = torch.empty((tokens, experts), dtype=logits.dtype, device=logits.device)
-        _check(lib.ds_moe_route_grad(code, logits.data_ptr(), tokens, experts, stride, ids.data_ptr(),
-                                     dweights.data_ptr(), top_k, SCORES[score], int(bool(renormalize)), scale,
-                                     dlogits.data_ptr(), experts, on.handle), "ds_moe_route_grad")
-        on.uses(logits, ids, dweights, dlogits)
+    if _elsewhere(logits, stream):
+        return _call_elsewhere(lambda: moe_route_grad(logits, ids, dweights, score=score, renormalize=renormalize,
+                                                      scale=scale), logits, stream, (logits, ids, dweights))
+    dlogits = logits.new_empty((tokens, experts))
+    _check(lib.ds_moe_route_grad(code, logits.data_ptr(), tokens, experts, stride, ids.data_ptr(), dweights.data_ptr(),
+                                 top_k, SCORES[score], 1 if renormalize else 0, scale, dlogits.data_ptr(), experts,
+                                 _stream_of(logits)), "ds_moe_route_grad")
     return dlogits
 
 
@@ -490,37 +511,42 @@ def moe_experts(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, ids: t
     [experts, dim, hidden] in x's dtype, or float8_e4m3fn with a float32 scale for every block of 128 x 128
     ([experts, ceil(rows / 128), ceil(columns / 128)]); ids int32, weights float32 [tokens, top_k]. Choices outside
     [0, experts) are left out."""
-    if _float_code(x, "x") == DS_FP32:
+    code = _float_code(x, "x")
+    if code == DS_FP32:
         raise TypeError("x must be bfloat16 or float16")
     x_stride = _check_rows(x, "x")
     tokens, dim = x.shape
     if w_in.dim() != 3 or w_in.shape[1] % 2 or ids.dim() != 2:
         raise ValueError("w_in must be [experts, 2 * hidden, dim] and ids [tokens, top_k]")
-    experts, hidden, top_k = w_in.shape[0], w_in.shape[1] // 2, ids.shape[1]
+    experts, both, _ = w_in.shape
+    hidden, top_k = both // 2, ids.shape[1]
     eight = w_in.dtype == torch.float8_e4m3fn
-    kinds = (torch.float8_e4m3fn,) if eight else (x.dtype,)
-    _check_flat(w_in, "w_in", kinds, (experts, 2 * hidden, dim), x)
-    _check_flat(w_out, "w_out", kinds, (experts, dim, hidden), x)
+    kind = torch.float8_e4m3fn if eight else x.dtype
+    _check_flat(w_in, "w_in", kind, (experts, both, dim), x)
+    _check_flat(w_out, "w_out", kind, (experts, dim, hidden), x)
     if eight != (w_in_scale is not None) or eight != (w_out_scale is not None):
         raise ValueError("8-bit weights, and only they, need w_in_scale and w_out_scale")
     if eight:
-        blocks = [-(-v // 128) for v in (2 * hidden, dim, hidden)]
-        _check_flat(w_in_scale, "w_in_scale", (torch.float32,), (experts, blocks[0], blocks[1]), x)
-        _check_flat(w_out_scale, "w_out_scale", (torch.float32,), (experts, blocks[1], blocks[2]), x)
-    _check_flat(ids, "ids", (torch.int32,), (tokens, top_k), x)
-    _check_flat(weights, "weights", (torch.float32,), (tokens, top_k), x)
-    with _On(x, stream) as on:
-        if out is None:
-            out = torch.empty((tokens, dim), dtype=x.dtype, device=x.device)
+        blocks = [-(-v // 128) for v in (both, dim, hidden)]
+        _check_flat(w_in_scale, "w_in_scale", torch.float32, (experts, blocks[0], blocks[1]), x)
+        _check_flat(w_out_scale, "w_out_scale", torch.float32, (experts, blocks[1], blocks[2]), x)
+    _check_flat(ids, "ids", torch.int32, (tokens, top_k), x)
+    _check_flat(weights, "weights", torch.float32, (tokens, top_k), x)
+    if _elsewhere(x, stream):
+        return _call_elsewhere(lambda: moe_experts(x, w_in, w_out, ids, weights, w_in_scale=w_in_scale,
+                                                   w_out_scale=w_out_scale, out=out), x, stream,
+                               (x, w_in, w_out, ids, weights, w_in_scale, w_out_scale, out))
+    if out is None:
+        out = x.new_empty((tokens, dim))
+        y_stride = dim
+    else:
         y_stride = _check_rows(out, "out", tokens, dim, x)
         if out.dtype != x.dtype:
             raise TypeError("out must have x's dtype")
-        _check(lib.ds_moe_experts(_FLOATS[x.dtype], x.data_ptr(), tokens, dim, x_stride,
-                                  DS_FP8_E4M3 if eight else _FLOATS[x.dtype], w_in.data_ptr(),
-                                  w_in_scale.data_ptr() if eight else None, w_out.data_ptr(),
-                                  w_out_scale.data_ptr() if eight else None, experts, hidden, ids.data_ptr(),
-                                  weights.data_ptr(), top_k, out.data_ptr(), y_stride, on.handle), "ds_moe_experts")
-        on.uses(x, w_in, w_out, w_in_scale, w_out_scale, ids, weights, out)
+    _check(lib.ds_moe_experts(code, x.data_ptr(), tokens, dim, x_stride, DS_FP8_E4M3 if eight else code,
+                              w_in.data_ptr(), w_in_scale.data_ptr() if eight else None, w_out.data_ptr(),
+                              w_out_scale.data_ptr() if eight else None, experts, hidden, ids.data_ptr(),
+                              weights.data_ptr(), top_k, out.data_ptr(), y_stride, _stream_of(x)), "ds_moe_experts")
     return out
 
 
