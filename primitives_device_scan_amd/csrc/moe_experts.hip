@@ -5,20 +5,30 @@
 //   y_t = sum over j of weights[t, j] * (w_out[e] h)
 //
 // With a few tokens the weights are what has to be read (3 D F values per
-// expert that any token chose, once), so the kernels are built to stream
-// them: weights go from memory straight into the A operand of the matrix
-// instructions, 16 rows to a tile, and the expert's tokens, at most 16 to a
-// column block, are the B operand, read from the cache.
+// expert that any token chose, once), so the kernels are built to stream them:
+// 16 rows to a tile are the A operand of the matrix instructions, the expert's
+// tokens, 16 to a block, are the B operand, read from the cache.
 //
-// Three launches: gate/up products and activation into `h` (one row per
-// assignment, in x's type), down products into `part` (one 32-bit row per
-// assignment), and the weighted sum over each token's choices, in order of
-// the choices, so that the result is the same on every run. There is no
-// alignment launch before them: each workgroup finds its expert and that
-// expert's assignments in the ids itself.
+// The launches: a plan of which workgroups serve which tokens (above 64
+// assignments), gate/up products and activation into `h` (one row per
+// assignment), down products into `part` (one 32-bit row per assignment) and
+// the weighted sum over each token's choices, in order of the choices, so that
+// the result is the same on every run. (Matrix-vector kernels for one token, with
+// the sum in the down products' launch, took as long: 12 + 11 us against 12 + 7
+// + 4 for top-8 of 128, 2,048 x 768. A launch's 3 us and the bytes are the time.)
+//
+// The matrix instructions take h in x's 16-bit type. Rounding it there would
+// add as much error as the output's own rounding (1.4 times in all), so h is
+// kept as its rounded value and the rounded rest, and a token has two columns
+// in the down products. That costs nothing for an expert of up to eight tokens
+// (blocks are 16 columns wide, and the weights' bytes bound these products); an
+// expert of more takes the rounded values alone (both halves for up to 32
+// tokens made the down products of 256 tokens, top-8 of 256, 5% slower).
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
+
+#include <type_traits>
 
 namespace ds {
 
@@ -123,7 +133,28 @@ __device__ __forceinline__ void load_b(const X* const (&tok)[TT], int64_t depth0
                     tok[t] + depth0 + (4 * j + lane / 16) * S::kSegVals + f * 8);
 }
 
-// The same at the end of the depth: of the stage's values the first `valid` are there, the others are 0.
+// The same at the end of the depth, for depths of whole segments: the first
+// `segs` segments of the stage are there, the others are 0.
+template <typename X, typename W, int RT, int TT>
+__device__ __forceinline__ void load_b_segs(const X* const (&tok)[TT], int64_t depth0, int segs, int lane,
+                                            BRegs<W, RT, TT>& b)
+{
+    using S = Stage<W, RT>;
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int j = 0; j < S::kReads; ++j) {
+            const int s = 4 * j + lane / 16;
+#pragma unroll
+            for (int f = 0; f < S::kFrags; ++f) {
+                const u32x4 v = *reinterpret_cast<const typename Vec16<X>::type*>(
+                    tok[t] + depth0 + (s < segs ? s : 0) * S::kSegVals + f * 8);
+                b.v[t][j][f] = s < segs ? v : u32x4{0u, 0u, 0u, 0u};
+            }
+        }
+}
+
+// The same for any depth: of the stage's values the first `valid` are there.
 template <typename X, typename W, int RT, int TT>
 __device__ __forceinline__ void load_b_tail(const X* const (&tok)[TT], int64_t depth0, int valid, int lane,
                                             BRegs<W, RT, TT>& b)
@@ -330,7 +361,7 @@ struct LdsProduct {
     __device__ __forceinline__ void issue_tail(int stage, int segs, BRegs<W, RT, TT>& b, ScaleRegs<W, RT, true>& s)
     {
         load_scales<W, RT, true>(sc, stage * (S::kDepth / 64) / 2, last_blk, s);
-        load_b_tail<X, W, RT, TT>(tok, (int64_t)stage * S::kDepth, segs * S::kSegVals, lane, b);
+        load_b_segs<X, W, RT, TT>(tok, (int64_t)stage * S::kDepth, segs, lane, b);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < kDmaOps; ++i) {
@@ -452,8 +483,11 @@ constexpr int kPlanThreads = 1024;
 constexpr int kMaxAssignments = 8192;
 constexpr int kMaxExperts = 8192;
 
-// plan[s]: expert of block s (-1: none), plan[blocks + s]: its assignments;
-// list[s * chunk ..]: their indices. One workgroup.
+// plan[s]: expert of block s (-1: none), plan[blocks + s]: its assignments (and
+// kLone where the expert has no other block); list[s * chunk ..]: their indices,
+// in any order: no result depends on it. One workgroup.
+constexpr int kLone = 1 << 16;
+
 __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t* __restrict__ ids, int n, int experts,
                                                                    int chunk, int blocks, int32_t* __restrict__ plan,
                                                                    uint16_t* __restrict__ list)
@@ -500,7 +534,7 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
         for (uint32_t left = c[j]; left > 0; ++first) {
             const uint32_t here = left < (uint32_t)chunk ? left : (uint32_t)chunk;
             plan[first] = x;
-            plan[blocks + first] = (int32_t)here;
+            plan[blocks + first] = (int32_t)here | (here == c[j] ? kLone : 0);
             left -= here;
         }
     }
@@ -513,6 +547,7 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
 
 struct Found {
     int expert, count;  // count 0: nothing to do
+    bool all;           // these are all the assignments of the expert
 };
 
 // Every wave finds the same and writes the same list.
@@ -522,14 +557,14 @@ __device__ __forceinline__ Found find_assignments(const int32_t* __restrict__ id
     const int lane = lane_id();
     const int32_t mine = lane < n ? ids[lane] : -1;
     const int32_t e = readlane(mine, slot);
-    if (e < 0 || e >= experts) return Found{-1, 0};
+    if (e < 0 || e >= experts) return Found{-1, 0, false};
     const uint64_t same = ballot(mine == e);
-    if (__builtin_ctzll(same) < slot) return Found{-1, 0};
+    if (__builtin_ctzll(same) < slot) return Found{-1, 0, false};
     if (mine == e)
         s_list[__builtin_amdgcn_mbcnt_hi((uint32_t)(same >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)same, 0u))] =
             (uint16_t)lane;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    return Found{e, __builtin_popcountll(same)};
+    return Found{e, __builtin_popcountll(same), true};
 }
 
 struct ExpertArgs {
@@ -543,12 +578,30 @@ struct ExpertArgs {
     int rows, depth;   // of one expert's matrix; gate/up: rows = F (of 2 F), depth = D; down: rows = D, depth = F
 };
 
+// The sums of neighbouring columns, in both of them.
+__device__ __forceinline__ f32x4 add_halves(f32x4 v)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] += dpp<0xB1>((float)v[i]);
+    return v;
+}
+
+// A 32-bit h as its value in X and the rest in X (0 where the value is not finite).
+template <typename X>
+__device__ __forceinline__ void split_h(float h, X& high, X& low)
+{
+    high = (X)h;
+    const float rest = h - (float)high;
+    low = (X)(rest - rest == 0.0f ? rest : 0.0f);
+}
+
 // GATED: half of the tiles are gate rows, the others the up rows that go with
-// them, x rows are the tokens', the output is silu(gate) * up, in X.
-// Otherwise the tiles are neighbouring rows, x rows are the assignments', the
-// output is 32-bit sums. PARTS waves share the tiles, each with a part of the
+// them, x rows are the tokens', the output is silu(gate) * up: rows of its high
+// halves, then its low ones. Otherwise the tiles are neighbouring rows, x rows
+// are the assignments' h, the output is 32-bit sums; SPLIT: columns 2 c and
+// 2 c + 1 are the halves of token c. PARTS waves share the tiles, each with a part of the
 // depth (PARTS 1: every wave has its own tiles).
-template <typename X, typename W, int RT, int TT, bool GATED, int PARTS, bool LDS>
+template <typename X, typename W, int RT, int TT, bool GATED, bool SPLIT, int PARTS, bool LDS>
 __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, const uint16_t* list, int first,
                                              int count, int slice, char* s_mem)
 {
@@ -569,10 +622,11 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
     const X* tok[TT];
 #pragma unroll
     for (int b = 0; b < TT; ++b) {
-        const int at = first + b * 16 + lane % 16;
+        const int col = b * 16 + lane % 16, at = first + (SPLIT ? col / 2 : col);
         assign[b] = list[at < count ? at : count - 1];  // columns past the end repeat the last one
         tok[b] = (const X*)a.x + (int64_t)(GATED ? assign[b] / a.top_k : assign[b]) * a.x_stride;
-        if (at >= count) assign[b] = -1;
+        if (SPLIT) tok[b] += col % 2 * (a.x_stride / 2);
+        if (at >= count || (SPLIT && col % 2)) assign[b] = -1;
     }
     // the part of the depth, in whole stages
     const int stages = (a.depth + S::kDepth - 1) / S::kDepth, each = (stages + PARTS - 1) / PARTS;
@@ -633,6 +687,12 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
         if (wave > 0) return;
     }
     if (row0 >= a.rows) return;
+    if constexpr (SPLIT) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int b = 0; b < TT; ++b) acc[r][b] = add_halves(acc[r][b]);
+    }
     // lane l holds output rows (l / 16) * 4 .. + 3 of each tile for token l % 16 of each block
     const int r0 = row0 + lane / 16 * 4;
 #pragma unroll
@@ -642,14 +702,21 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
             X* out = (X*)a.out + (int64_t)assign[b] * a.out_stride;
 #pragma unroll
             for (int t = 0; t < kHalf; ++t) {
-                X h[4];
+                X h[2][4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float g = acc[t][b][i], u = acc[kHalf + t][b][i];
-                    h[i] = (X)(g / (1.0f + expf(-g)) * u);
+                    split_h<X>(g / (1.0f + expf(-g)) * u, h[0][i], h[1][i]);
                 }
-                const int o = r0 + 16 * t;  // a multiple of 4; rows of `out` are whole vectors, past a.rows unused
-                if (o < a.out_stride) *reinterpret_cast<uint64_t*>(out + o) = __builtin_bit_cast(uint64_t, *(uint64_t*)h);
+                const int64_t o = r0 + 16 * t, half = a.out_stride / 2;  // o: a multiple of 4; a half is whole vectors
+                if (o < half) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        uint64_t v;
+                        __builtin_memcpy(&v, h[p], sizeof(v));
+                        *reinterpret_cast<uint64_t*>(out + p * half + o) = v;
+                    }
+                }
             }
         } else {
             float* out = (float*)a.out + (int64_t)assign[b] * a.out_stride;
@@ -682,8 +749,10 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
     Found f;
     const uint16_t* list;
     if (a.plan) {
-        f = Found{a.plan[slot], a.plan[a.blocks + slot]};
-        if (f.expert < 0) return;
+        const int e = a.plan[slot];
+        if (e < 0) return;
+        const int count = a.plan[a.blocks + slot];
+        f = Found{e, count & (kLone - 1), (count & kLone) != 0};
         list = a.list + (int64_t)slot * a.chunk;
     } else {
         f = find_assignments(a.ids, a.n, a.experts, slot, s_list);
@@ -691,16 +760,23 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
         list = s_list;
     }
     int first = 0;
-    for (; f.count - first > (kMost > 1 ? 8 * kMost : 0); first += 16 * kMost)
-        expert_block<X, W, RT, kMost, GATED, PARTS, LDS>(a, f.expert, list, first, f.count, slice, s_mem);
-    if constexpr (kMost > 2) {
-        if (f.count - first > 16) {
-            expert_block<X, W, RT, 2, GATED, PARTS, LDS>(a, f.expert, list, first, f.count, slice, s_mem);
-            return;
-        }
+    const auto pass = [&](auto blocks, auto split) {
+        expert_block<X, W, RT, decltype(blocks)::value, GATED, decltype(split)::value, PARTS, LDS>(
+            a, f.expert, list, first, f.count, slice, s_mem);
+    };
+    constexpr int kMiddle = kMost > 2 ? kMost / 2 : 1;
+    constexpr std::integral_constant<int, kMost> most{};
+    constexpr std::integral_constant<int, kMiddle> middle{};
+    if constexpr (!GATED) {
+        // halves for all tokens of an expert or for none, whatever their order in the list
+        if (f.all && f.count <= 8) return pass(std::integral_constant<int, 1>{}, std::true_type{});
     }
-    if (kMost > 1 && f.count - first > 0)
-        expert_block<X, W, RT, 1, GATED, PARTS, LDS>(a, f.expert, list, first, f.count, slice, s_mem);
+    for (; f.count - first > (kMost > 1 ? 8 * kMost : 0); first += 16 * kMost) pass(most, std::false_type{});
+    if constexpr (kMost > 1) {
+        const int left = f.count - first;
+        if (kMost > 2 && left > 16) pass(middle, std::false_type{});
+        else if (left > 0) pass(std::integral_constant<int, 1>{}, std::false_type{});
+    }
 }
 
 // y_t = sum over j of weights[t, j] * part[t, j], choices outside the experts
@@ -745,12 +821,12 @@ int experts_max_experts() { return kMaxExperts; }
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Scratch: rows of h (16-byte multiples), rows of parts, the plan and its list.
+// Scratch: rows of h (two halves of 16-byte multiples), rows of parts, the plan and its list.
 struct ExpertsScratch {
     int64_t h_stride, part_stride, blocks, part_at, plan_at, list_at, bytes;
     ExpertsScratch(int64_t n, int experts, int dim, int hidden, int chunk)
     {
-        h_stride = ceil_div(hidden, 8) * 8;
+        h_stride = 2 * (ceil_div(hidden, 8) * 8);
         part_stride = ceil_div(dim, 4) * 4;
         blocks = (experts < n ? experts : n) + n / chunk;
         part_at = ceil_div(n * h_stride * 2, 256) * 256;

@@ -187,7 +187,8 @@ def check_experts(args, what):
 @pytest.mark.parametrize("tokens,experts,top_k,dim,hidden", [
     (1, 1, 1, 1, 1), (1, 4, 2, 64, 32), (1, 300, 8, 128, 48), (2, 3, 3, 7, 5), (5, 8, 2, 130, 33), (16, 4, 1, 256, 128),
     (17, 2, 2, 96, 64), (33, 2, 1, 200, 136), (40, 6, 6, 129, 65), (70, 2, 2, 320, 80), (64, 40, 4, 63, 144),
-    (130, 3, 2, 72, 40), (12, 300, 3, 384, 272)])
+    (130, 3, 2, 72, 40), (12, 300, 3, 384, 272), (1, 9, 9, 2048, 768), (3, 40, 5, 320, 208), (4, 64, 16, 144, 1040),
+    (2, 20, 10, 528, 512), (4, 4, 1, 16, 16), (20, 5, 3, 160, 48), (9, 1, 1, 80, 304), (90, 4, 2, 256, 96)])
 def test_experts(dtype, eight, tokens, experts, top_k, dim, hidden):
     say("experts", dtype, eight, tokens, experts, top_k, dim, hidden)
     check_experts(layer(tokens + dim, tokens, experts, top_k, dim, hidden, dtype, eight),
@@ -198,6 +199,33 @@ def test_experts(dtype, eight, tokens, experts, top_k, dim, hidden):
 def test_experts_wide_enough_for_whole_waves(eight):
     # many experts and rows: every wave streams its own rows over the whole depth
     check_experts(layer(3, 24, 64, 8, 544, 1040, torch.bfloat16, eight), "many experts")
+
+
+@pytest.mark.parametrize("dtype,eight", [(torch.bfloat16, False), (torch.float16, False), (torch.bfloat16, True)])
+@pytest.mark.parametrize("tokens,experts,top_k,dim,hidden", [(1, 8, 4, 256, 512), (8, 8, 2, 256, 512),
+                                                            (24, 4, 1, 256, 512)])
+def test_experts_are_as_exact_as_the_output(dtype, eight, tokens, experts, top_k, dim, hidden):
+    # h is held in two halves, so the error is the output's own rounding and that of 32-bit sums, not one more rounding
+    args = layer(tokens + 77, tokens, experts, top_k, dim, hidden, dtype, eight)
+    ref, _ = mo.experts(*args)
+    off = np.linalg.norm(mo.f64(on_gpu(*args)) - ref)
+    own = np.linalg.norm(mo.f64(torch.from_numpy(ref).to(dtype)) - ref)
+    assert off <= 1.1 * own, (off, own)
+
+
+def test_experts_few_tokens_dropped_and_repeated_choices():
+    x, w_in, w_out, ids, weights, _, _ = layer(21, 3, 40, 9, 96, 64, torch.bfloat16)
+    ids[0] = -1
+    ids[1, 4:] = 40
+    ids[1, 1] = ids[1, 0]
+    ids[2, 8] = -(1 << 31)
+    weights[1, 2] = 0.0
+    got = check_experts((x, w_in, w_out, ids, weights, None, None), "few tokens")
+    assert bool((got[0] == 0).all())
+    x[1, 5] = float("inf")
+    x[2] = float("nan")
+    got = on_gpu(x, w_in, w_out, ids, weights, None, None)
+    assert bool((got[0] == 0).all()) and not bool(torch.isfinite(got[1].float()).all()) and bool((got[2] != got[2]).all())
 
 
 def test_experts_dropped_choices_duplicates_and_weights():
