@@ -807,7 +807,7 @@ int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int6
     if (ds::experts_workgroups(eight, call) > kMaxTiles) return DS_ERR_TOO_LARGE;
     std::lock_guard<std::mutex> lock(g_mu);
     char* aux = nullptr;
-    st = get_aux(stream, (size_t)ds::experts_aux_bytes(n, num_experts, (int)dim, (int)hidden, eight), &aux);
+    st = get_aux(stream, (size_t)ds::experts_aux_bytes(eight, call), &aux);
     if (st != DS_OK) return st;
     return ds::launch_moe_experts(float_kind(dtype), eight, call, aux, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }

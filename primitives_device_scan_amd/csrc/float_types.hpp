@@ -48,6 +48,42 @@ __device__ __forceinline__ void load_floats(const T* __restrict__ p, int64_t val
     }
 }
 
+// The 16 bytes of a row from element `at` on, 0 past its end: loaded where they
+// are whole and moved down, so that a row's end costs one access, not one per
+// element (which made rows of odd length several times slower).
+template <typename T>
+__device__ __forceinline__ u32x4 load_end(const T* __restrict__ row, int64_t at, int64_t length)
+{
+    constexpr int N = Vec16<T>::kN;
+    if (length < N) {  // uniform
+        T t[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            t[i] = row[at + i < length ? at + i : 0];
+            if (at + i >= length) __builtin_memset(&t[i], 0, sizeof(T));
+        }
+        u32x4 v;
+        __builtin_memcpy(&v, t, sizeof(v));
+        return v;
+    }
+    const int64_t from = at < length - N ? at : length - N;
+    const u32x4 v = *reinterpret_cast<const typename Vec16<T>::type*>(row + from);
+    const int64_t over = at - from;
+    const int shift = (over < N ? (int)over : N) * (int)sizeof(T) * 8;  // bits
+    uint64_t lo = (uint64_t)v[1] << 32 | v[0], hi = (uint64_t)v[3] << 32 | v[2];
+    if (shift & 64) {
+        lo = hi;
+        hi = 0;
+    }
+    const int rest = shift & 63;
+    if (rest) {
+        lo = lo >> rest | hi << (64 - rest);
+        hi >>= rest;
+    }
+    if (shift >= 128) lo = hi = 0;
+    return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
+}
+
 // Rounds N floats to T (nearest even) and writes the first `valid` of them
 // (NT: past the cache).
 template <typename T, int N, bool NT = false>

@@ -138,7 +138,7 @@ struct ExpertsCall {
 };
 int64_t experts_max_assignments();
 int experts_max_experts();
-int64_t experts_aux_bytes(int64_t n, int experts, int dim, int hidden, bool eight_bit);  // scratch for n assignments
+int64_t experts_aux_bytes(bool eight_bit, const ExpertsCall& call);
 int64_t experts_workgroups(bool eight_bit, const ExpertsCall& call);  // of the largest launch
 hipError_t launch_moe_experts(ElemKind kind, bool eight_bit, const ExpertsCall& call, char* aux, hipStream_t stream);
 

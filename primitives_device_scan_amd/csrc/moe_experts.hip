@@ -22,8 +22,9 @@
 // kept as its rounded value and the rounded rest, and a token has two columns
 // in the down products. That costs nothing for an expert of up to eight tokens
 // (blocks are 16 columns wide, and the weights' bytes bound these products); an
-// expert of more takes the rounded values alone (both halves for up to 32
-// tokens made the down products of 256 tokens, top-8 of 256, 5% slower).
+// expert of more, and all where a workgroup's waves split an expert's tokens,
+// take the rounded values alone (both halves for up to 32 tokens made the down
+// products of 256 tokens, top-8 of 256, 5% slower).
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -154,10 +155,10 @@ __device__ __forceinline__ void load_b_segs(const X* const (&tok)[TT], int64_t d
         }
 }
 
-// The same for any depth: of the stage's values the first `valid` are there.
+// The same for any depth.
 template <typename X, typename W, int RT, int TT>
-__device__ __forceinline__ void load_b_tail(const X* const (&tok)[TT], int64_t depth0, int valid, int lane,
-                                            BRegs<W, RT, TT>& b)
+__device__ __forceinline__ void load_b_end(const X* const (&tok)[TT], int64_t depth0, int64_t depth, int lane,
+                                           BRegs<W, RT, TT>& b)
 {
     using S = Stage<W, RT>;
 #pragma unroll
@@ -165,13 +166,8 @@ __device__ __forceinline__ void load_b_tail(const X* const (&tok)[TT], int64_t d
 #pragma unroll
         for (int j = 0; j < S::kReads; ++j)
 #pragma unroll
-            for (int f = 0; f < S::kFrags; ++f) {
-                const int at = (4 * j + lane / 16) * S::kSegVals + f * 8;
-                X x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = at + i < valid ? tok[t][depth0 + at + i] : (X)0.0f;
-                __builtin_memcpy(&b.v[t][j][f], x, sizeof(x));
-            }
+            for (int f = 0; f < S::kFrags; ++f)
+                b.v[t][j][f] = load_end<X>(tok[t], depth0 + (4 * j + lane / 16) * S::kSegVals + f * 8, depth);
 }
 
 // Scales of a wave's tiles for 8-bit weights, by block of 128 of the depth.
@@ -429,11 +425,12 @@ struct LdsProduct {
     }
 };
 
-// Weights straight into registers, for rows at any alignment: one stage at a time.
+// Weights straight into registers, for rows at any alignment, one stage at a
+// time (a stage ahead in a second set of registers was no faster).
 template <typename X, typename W, int RT, int TT>
 __device__ __forceinline__ void direct_product(const W* const (&tile)[RT], const int (&last)[RT], int64_t depth,
-                                               const X* const (&tok)[TT], const Scales<RT, false>& sc, int64_t k0, int64_t k1,
-                                               int lane, f32x4 (&acc)[RT][TT])
+                                               const X* const (&tok)[TT], const Scales<RT, false>& sc, int64_t k0,
+                                               int64_t k1, int lane, f32x4 (&acc)[RT][TT])
 {
     using S = Stage<W, RT>;
     const W* row[RT];
@@ -443,31 +440,20 @@ __device__ __forceinline__ void direct_product(const W* const (&tile)[RT], const
         ARegs<W, RT> a;
         BRegs<W, RT, TT> b;
         ScaleRegs<W, RT, false> s;
+        const bool whole = k + S::kDepth <= depth;
         load_scales<W, RT, false>(sc, (int)(k / 128), (int)((depth - 1) / 128), s);
-        if (k + S::kDepth <= k1) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-                for (int j = 0; j < S::kReads; ++j)
-                    a.v[r][j] = *reinterpret_cast<const typename Vec16<W>::type*>(row[r] + k +
-                                                                                 (4 * j + lane / 16) * S::kSegVals);
+            for (int j = 0; j < S::kReads; ++j) {
+                const int64_t at = k + (4 * j + lane / 16) * S::kSegVals;
+                a.v[r][j] = whole ? *reinterpret_cast<const typename Vec16<W>::type*>(row[r] + at)
+                                  : load_end<W>(row[r], at, depth);
+            }
+        if (whole)
             load_b<X, W, RT, TT>(tok, k, lane, b);
-        } else {
-            const int valid = (int)(k1 - k);
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int j = 0; j < S::kReads; ++j) {
-                    const int at = (4 * j + lane / 16) * S::kSegVals;
-                    W w[S::kSegVals];
-                    __builtin_memset(w, 0, sizeof(w));
-#pragma unroll
-                    for (int i = 0; i < S::kSegVals; ++i)
-                        if (at + i < valid) w[i] = row[r][k + at + i];
-                    __builtin_memcpy(&a.v[r][j], w, sizeof(w));
-                }
-            load_b_tail<X, W, RT, TT>(tok, k, valid, lane, b);
-        }
+        else
+            load_b_end<X, W, RT, TT>(tok, k, depth, lane, b);
         multiply<X, W, RT, TT>(a, b, s, acc);
     }
 }
@@ -586,55 +572,33 @@ __device__ __forceinline__ f32x4 add_halves(f32x4 v)
     return v;
 }
 
-// A 32-bit h as its value in X and the rest in X (0 where the value is not finite).
+// A 32-bit h as its value in X and the rest in X (0 where the value is not
+// finite). h is pinned to a register: its product would otherwise be rounded
+// straight to 16 bits in some places and to 32 first in others, as the compiler
+// sees fit, and a token's bits would depend on its column.
 template <typename X>
 __device__ __forceinline__ void split_h(float h, X& high, X& low)
 {
+    asm("" : "+v"(h));
     high = (X)h;
     const float rest = h - (float)high;
     low = (X)(rest - rest == 0.0f ? rest : 0.0f);
 }
 
-// GATED: half of the tiles are gate rows, the others the up rows that go with
-// them, x rows are the tokens', the output is silu(gate) * up: rows of its high
-// halves, then its low ones. Otherwise the tiles are neighbouring rows, x rows
-// are the assignments' h, the output is 32-bit sums; SPLIT: columns 2 c and
-// 2 c + 1 are the halves of token c. PARTS waves share the tiles, each with a part of the
-// depth (PARTS 1: every wave has its own tiles).
-template <typename X, typename W, int RT, int TT, bool GATED, bool SPLIT, int PARTS, bool LDS>
-__device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, const uint16_t* list, int first,
-                                             int count, int slice, char* s_mem)
-{
-    using S = Stage<W, RT>;
-    constexpr int kHalf = GATED ? RT / 2 : RT;  // tiles of neighbouring rows
-    const int lane = lane_id(), wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int part = PARTS > 1 ? wave : 0, group = PARTS > 1 ? slice : slice * kWaves + wave;
-    const int row0 = group * (16 * kHalf);
-    const int64_t all_rows = GATED ? 2 * (int64_t)a.rows : a.rows;
-    const W* w = (const W*)a.w + (int64_t)expert * all_rows * a.depth;
-    const int grid_cols = (a.depth + 127) / 128, grid_rows = (int)((all_rows + 127) / 128);
-    f32x4 acc[RT][TT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int b = 0; b < TT; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    int assign[TT];
-    const X* tok[TT];
-#pragma unroll
-    for (int b = 0; b < TT; ++b) {
-        const int col = b * 16 + lane % 16, at = first + (SPLIT ? col / 2 : col);
-        assign[b] = list[at < count ? at : count - 1];  // columns past the end repeat the last one
-        tok[b] = (const X*)a.x + (int64_t)(GATED ? assign[b] / a.top_k : assign[b]) * a.x_stride;
-        if (SPLIT) tok[b] += col % 2 * (a.x_stride / 2);
-        if (at >= count || (SPLIT && col % 2)) assign[b] = -1;
-    }
-    // the part of the depth, in whole stages
-    const int stages = (a.depth + S::kDepth - 1) / S::kDepth, each = (stages + PARTS - 1) / PARTS;
-    const int s0 = part * each, s1 = s0 + each < stages ? s0 + each : stages;
-    if (row0 < a.rows && s0 < s1) {
-        const W* tile[RT];
-        int last[RT];  // row of each tile that stands for the rows past the end
-        Scales<RT, LDS> sc;
+// A wave's tiles from row0 of the output's rows on. GATED: half of the tiles are
+// gate rows, the others the up rows that go with them; otherwise the tiles are
+// neighbouring rows.
+template <typename W, int RT, bool GATED, bool UNIFORM> struct Tiles {
+    static constexpr int kHalf = GATED ? RT / 2 : RT;  // tiles of neighbouring rows
+    const W* tile[RT];
+    int last[RT];  // row of each tile that stands for the rows past the end
+    Scales<RT, UNIFORM> sc;
+
+    __device__ __forceinline__ Tiles(const ExpertArgs& a, int expert, int row0, int lane)
+    {
+        const int64_t all_rows = GATED ? 2 * (int64_t)a.rows : a.rows;
+        const W* w = (const W*)a.w + (int64_t)expert * all_rows * a.depth;
+        const int grid_cols = (a.depth + 127) / 128, grid_rows = (int)((all_rows + 127) / 128);
         sc.base = (const float*)a.scale + (int64_t)expert * grid_rows * grid_cols;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -645,47 +609,42 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
             tile[r] = w + (begin + from) * a.depth;
             if constexpr (sizeof(W) == 1) {
 #pragma unroll
-                for (int i = 0; i < (LDS ? 1 : 4); ++i) {
+                for (int i = 0; i < (UNIFORM ? 1 : 4); ++i) {
                     int64_t o = begin + from;
-                    if (!LDS) o += lane / 16 * 4 + i < last[r] ? lane / 16 * 4 + i : last[r];
+                    if (!UNIFORM) o += lane / 16 * 4 + i < last[r] ? lane / 16 * 4 + i : last[r];
                     sc.row[r][i] = o / 128 * grid_cols;
                 }
             }
         }
-        if constexpr (LDS) {
-            const int segs = a.depth / S::kSegVals - s0 * S::kSegs;  // of the rest of the row
-            const int whole = s1 < stages ? s1 : a.depth / S::kDepth;
-            const uint32_t turn = (blockIdx.x * kWaves + wave) * 5u;
-            LdsProduct<X, W, RT, TT> p(tile, last, a.depth, tok, sc,
-                                       (lds_char*)(s_mem + wave * (kRing * kStageBytes)), lane);
-            p.run(s0, whole, s1 < stages ? 0 : segs - (whole - s0) * S::kSegs, turn, acc);
-        } else {
-            const int64_t k1 = (int64_t)s1 * S::kDepth;
-            direct_product<X, W, RT, TT>(tile, last, a.depth, tok, sc, (int64_t)s0 * S::kDepth,
-                                         k1 < a.depth ? k1 : a.depth, lane, acc);
-        }
     }
-    if constexpr (PARTS > 1) {
-        f32x4* s_part = reinterpret_cast<f32x4*>(s_mem);  // over the rings: every wave is past them
-        __syncthreads();
-        if (wave > 0) {
+};
+
+// A wave's columns: assignments list[first ..], and its lane's row of x for
+// each block of 16 (GATED: the token's; otherwise the assignment's h). SPLIT:
+// columns 2 c and 2 c + 1 are the halves of token c. Columns past the end
+// repeat the last assignment, and have assign -1, as the second halves have.
+template <typename X, int TT, bool GATED, bool SPLIT>
+__device__ __forceinline__ void find_columns(const ExpertArgs& a, const uint16_t* list, int first, int count, int lane,
+                                             int (&assign)[TT], const X* (&tok)[TT])
+{
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int b = 0; b < TT; ++b) s_part[((wave - 1) * RT * TT + r * TT + b) * kWave + lane] = acc[r][b];
-        }
-        __syncthreads();
-        if (wave == 0) {
-#pragma unroll
-            for (int p = 0; p < PARTS - 1; ++p)
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-#pragma unroll
-                    for (int b = 0; b < TT; ++b) acc[r][b] += s_part[(p * RT * TT + r * TT + b) * kWave + lane];
-        }
-        __syncthreads();
-        if (wave > 0) return;
+    for (int b = 0; b < TT; ++b) {
+        const int col = b * 16 + lane % 16, at = first + (SPLIT ? col / 2 : col);
+        assign[b] = list[at < count ? at : count - 1];
+        tok[b] = (const X*)a.x + (int64_t)(GATED ? assign[b] / a.top_k : assign[b]) * a.x_stride;
+        if (SPLIT) tok[b] += col % 2 * (a.x_stride / 2);
+        if (at >= count || (SPLIT && col % 2)) assign[b] = -1;
     }
+}
+
+// GATED: silu(gate) * up, rows of its high halves, then its low ones;
+// otherwise the 32-bit sums. Lane l holds output rows (l / 16) * 4 .. + 3 of
+// each tile for token l % 16 of each block.
+template <typename X, int RT, int TT, bool GATED, bool SPLIT>
+__device__ __forceinline__ void write_results(const ExpertArgs& a, const int (&assign)[TT], int row0, int lane,
+                                              f32x4 (&acc)[RT][TT])
+{
+    constexpr int kHalf = GATED ? RT / 2 : RT;
     if (row0 >= a.rows) return;
     if constexpr (SPLIT) {
 #pragma unroll
@@ -693,7 +652,6 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
 #pragma unroll
             for (int b = 0; b < TT; ++b) acc[r][b] = add_halves(acc[r][b]);
     }
-    // lane l holds output rows (l / 16) * 4 .. + 3 of each tile for token l % 16 of each block
     const int r0 = row0 + lane / 16 * 4;
 #pragma unroll
     for (int b = 0; b < TT; ++b) {
@@ -729,6 +687,221 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
     }
 }
 
+// Where the products of a tile set begin in the depth (taken modulo its
+// stages): not all in the same memory channels, and the same for every token of
+// the expert, whichever workgroup it falls to.
+__device__ __forceinline__ uint32_t first_stage(const ExpertArgs& a, int expert, int group)
+{
+    return ((uint32_t)expert * (uint32_t)(a.slices * kWaves) + (uint32_t)group) * 5u;
+}
+
+template <int RT, int TT>
+__device__ __forceinline__ void clear_sums(f32x4 (&acc)[RT][TT])
+{
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int b = 0; b < TT; ++b) acc[r][b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// The products of a wave. PARTS waves share the tiles, each with a part of the
+// depth (PARTS 1: every wave has its own tiles).
+template <typename X, typename W, int RT, int TT, bool GATED, bool SPLIT, int PARTS, bool LDS>
+__device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, const uint16_t* list, int first,
+                                             int count, int slice, char* s_mem)
+{
+    using S = Stage<W, RT>;
+    const int lane = lane_id(), wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int part = PARTS > 1 ? wave : 0, group = PARTS > 1 ? slice : slice * kWaves + wave;
+    const int row0 = group * (16 * (GATED ? RT / 2 : RT));
+    f32x4 acc[RT][TT];
+    clear_sums(acc);
+    int assign[TT];
+    const X* tok[TT];
+    find_columns<X, TT, GATED, SPLIT>(a, list, first, count, lane, assign, tok);
+    // the part of the depth, in whole stages
+    const int stages = (a.depth + S::kDepth - 1) / S::kDepth, each = (stages + PARTS - 1) / PARTS;
+    const int s0 = part * each, s1 = s0 + each < stages ? s0 + each : stages;
+    if (row0 < a.rows && s0 < s1) {
+        const Tiles<W, RT, GATED, LDS> t(a, expert, row0, lane);
+        if constexpr (LDS) {
+            const int segs = a.depth / S::kSegVals - s0 * S::kSegs;  // of the rest of the row
+            const int whole = s1 < stages ? s1 : a.depth / S::kDepth;
+            const uint32_t turn = first_stage(a, expert, group);
+            LdsProduct<X, W, RT, TT> p(t.tile, t.last, a.depth, tok, t.sc,
+                                       (lds_char*)(s_mem + wave * (kRing * kStageBytes)), lane);
+            p.run(s0, whole, s1 < stages ? 0 : segs - (whole - s0) * S::kSegs, turn, acc);
+        } else {
+            const int64_t k1 = (int64_t)s1 * S::kDepth;
+            direct_product<X, W, RT, TT>(t.tile, t.last, a.depth, tok, t.sc, (int64_t)s0 * S::kDepth,
+                                         k1 < a.depth ? k1 : a.depth, lane, acc);
+        }
+    }
+    if constexpr (PARTS > 1) {
+        f32x4* s_part = reinterpret_cast<f32x4*>(s_mem);  // over the rings: every wave is past them
+        __syncthreads();
+        if (wave > 0) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int b = 0; b < TT; ++b) s_part[((wave - 1) * RT * TT + r * TT + b) * kWave + lane] = acc[r][b];
+        }
+        __syncthreads();
+        if (wave == 0) {
+#pragma unroll
+            for (int p = 0; p < PARTS - 1; ++p)
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int b = 0; b < TT; ++b) acc[r][b] += s_part[(p * RT * TT + r * TT + b) * kWave + lane];
+        }
+        __syncthreads();
+        if (wave > 0) return;
+    }
+    write_results<X, RT, TT, GATED, SPLIT>(a, assign, row0, lane, acc);
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens of one expert: the waves of a workgroup share four tiles and
+// split the tokens, 16 * TT to a wave. The stages of the weights are shared: a
+// wave loads one tile of each, three stages make the ring, and a barrier per
+// stage says that all tiles of it are there and that the stage before the one
+// being overwritten is done with.
+// ---------------------------------------------------------------------------
+constexpr int kWideRing = 3;
+constexpr int kWideOps = kDmaOps / kWaves;  // loads of a wave per stage
+
+template <typename X, typename W, int TT>
+struct WideProduct {
+    using S = Stage<W, 4>;
+    static_assert(kWideOps == 2 && S::kSegs == 8, "a wave loads one tile, eight rows at a time");
+    const char* src[kWideOps];
+    int seg[kWideOps];
+    const X* const (&tok)[TT];
+    const Scales<4, true>& sc;
+    lds_char *ring, *mine;
+    uint32_t read_at;
+    int lane, last_blk;
+
+    __device__ __forceinline__ WideProduct(const W* tile, int last, int64_t depth, const X* const (&tok_)[TT],
+                                           const Scales<4, true>& sc_, lds_char* ring_, int lane_, int wave)
+        : tok(tok_), sc(sc_), ring(ring_), mine(ring_ + wave * (kWideOps * kWave * kVecBytes)), lane(lane_),
+          last_blk((int)((depth - 1) / 128))
+    {
+#pragma unroll
+        for (int i = 0; i < kWideOps; ++i) {
+            const int row = i * 8 + lane / 8, r = row < last ? row : last;
+            seg[i] = lane % 8 ^ row % 8;
+            src[i] = reinterpret_cast<const char*>(tile + r * depth) + seg[i] * kVecBytes;
+        }
+        const int r = lane % 16, s = lane / 16;
+        read_at = (uint32_t)(uintptr_t)ring + (uint32_t)(r * S::kSegs + (s ^ (r % 8))) * kVecBytes;
+    }
+
+    __device__ __forceinline__ void load(int slot, int stage, int segs)
+    {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kWideOps; ++i) {
+            const char* p = src[i] + (int64_t)stage * (S::kSegs * kVecBytes);
+            if (seg[i] >= segs) p -= seg[i] * kVecBytes;
+            __builtin_amdgcn_global_load_lds(
+                (const __attribute__((address_space(1))) uint32_t*)p,
+                (__attribute__((address_space(3))) uint32_t*)(mine + slot * kStageBytes + i * (kWave * kVecBytes)), 16,
+                0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    __device__ __forceinline__ void load_x(int stage, int segs, BRegs<W, 4, TT>& b, ScaleRegs<W, 4, true>& s)
+    {
+        load_scales<W, 4, true>(sc, stage * (S::kDepth / 64) / 2, last_blk, s);
+        if (segs == S::kSegs)
+            load_b<X, W, 4, TT>(tok, (int64_t)stage * S::kDepth, lane, b);
+        else
+            load_b_segs<X, W, 4, TT>(tok, (int64_t)stage * S::kDepth, segs, lane, b);
+    }
+
+    // Of this wave's loads, those of the stage after this one may be outstanding (newer).
+    __device__ __forceinline__ void arrive(bool newer)
+    {
+        __builtin_amdgcn_sched_barrier(0);
+        if (newer)
+            asm volatile("s_waitcnt vmcnt(2)" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    __device__ __forceinline__ void use(int slot, const BRegs<W, 4, TT>& b, const ScaleRegs<W, 4, true>& s,
+                                        f32x4 (&acc)[4][TT], int segs)
+    {
+        ARegs<W, 4> a;
+        read_stage<W>(read_at + (uint32_t)slot * kStageBytes, a);
+        if (segs < S::kSegs) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int j = 0; j < S::kReads; ++j)
+                    if (4 * j + lane / 16 >= segs) a.v[r][j] = u32x4{0u, 0u, 0u, 0u};
+        }
+        multiply<X, W, 4, TT>(a, b, s, acc);
+    }
+
+    // The whole depth, `segs_all` segments. Every wave of the workgroup runs
+    // this with the same stages. (All from the start: tokens' values, read again
+    // by every workgroup, bound this, and are shared in the cache that way.)
+    __device__ __forceinline__ void run(int segs_all, f32x4 (&acc)[4][TT])
+    {
+        const int stages = (segs_all + S::kSegs - 1) / S::kSegs;
+        const auto segs = [&](int s) { return s + 1 < stages ? S::kSegs : segs_all - s * S::kSegs; };
+        BRegs<W, 4, TT> b[2];
+        ScaleRegs<W, 4, true> c[2];
+        load(0, 0, segs(0));
+        load_x(0, segs(0), b[0], c[0]);
+        if (stages > 1) load(1, 1, segs(1));
+        int slot = 0;
+        // two stages at a time, so that the register sets are known to the compiler
+        const auto step = [&](int s, int which) {
+            arrive(s + 1 < stages);
+            if (s + 1 < stages) load_x(s + 1, segs(s + 1), b[which ^ 1], c[which ^ 1]);
+            if (s + 2 < stages) load(slot >= 1 ? slot - 1 : kWideRing - 1, s + 2, segs(s + 2));
+            use(slot, b[which], c[which], acc, segs(s));
+            slot = slot + 1 < kWideRing ? slot + 1 : 0;
+        };
+        int s = 0;
+        for (; s + 1 < stages; s += 2) {
+            step(s, 0);
+            step(s + 1, 1);
+        }
+        if (s < stages) step(s, 0);
+        __builtin_amdgcn_s_barrier();  // the ring is free for the next tiles
+        asm volatile("" ::: "memory");
+    }
+};
+
+template <typename X, typename W, int TT, bool GATED>
+__device__ __forceinline__ void expert_wide(const ExpertArgs& a, int expert, const uint16_t* list, int first, int count,
+                                            int group, char* s_mem)
+{
+    const int lane = lane_id(), wave = (int)__builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int row0 = group * (16 * (GATED ? 2 : 4));
+    if (row0 >= a.rows) return;  // for the whole workgroup
+    f32x4 acc[4][TT];
+    clear_sums(acc);
+    int assign[TT];
+    const X* tok[TT];
+    find_columns<X, TT, GATED, false>(a, list, first + wave * 16 * TT, count, lane, assign, tok);
+    const Tiles<W, 4, GATED, true> t(a, expert, row0, lane);
+    const W* tile = wave == 0 ? t.tile[0] : wave == 1 ? t.tile[1] : wave == 2 ? t.tile[2] : t.tile[3];
+    const int last = wave == 0 ? t.last[0] : wave == 1 ? t.last[1] : wave == 2 ? t.last[2] : t.last[3];
+    WideProduct<X, W, TT> p(tile, last, a.depth, tok, t.sc, (lds_char*)s_mem, lane, wave);
+    p.run(a.depth / Stage<W, 4>::kSegVals, acc);
+    write_results<X, 4, TT, GATED, false>(a, assign, row0, lane, acc);
+}
+
 // Blocks of 16 tokens that a wave holds at once, as registers allow (256 at two
 // waves per SIMD): 8-bit weights have a second set of sums (one per block of
 // 128 of the depth) and twice the depth to a stage, RT 2 twice the depth too.
@@ -736,13 +909,18 @@ template <typename W, int RT = 4> struct MostBlocks {
     static constexpr int value = (sizeof(W) == 1 ? 2 : 4) * RT / 4;
 };
 
-template <typename X, typename W, int RT, bool GATED, int PARTS, bool LDS>
+// How a workgroup takes a block of tokens: every wave with tiles of its own
+// over the whole depth (kStream); all waves on one tile set, each with a part of
+// the depth (kParts) or of the tokens (kWide).
+enum ExpertMode { kStream, kParts, kWide };
+
+template <typename X, typename W, bool GATED, ExpertMode MODE, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
 {
-    static_assert(PARTS == 1 || PARTS == kWaves, "a workgroup's waves share one set of tiles, or none");
+    constexpr int RT = MODE == kParts ? 2 : 4, PARTS = MODE == kParts ? kWaves : 1;
     constexpr int kMost = MostBlocks<W, RT>::value;
     constexpr int kPart = (PARTS - 1) * RT * kMost * kWave * 16;
-    constexpr int kRings = LDS ? kWaves * kRing * kStageBytes : 0;
+    constexpr int kRings = MODE == kWide ? kWideRing * kStageBytes : LDS ? kWaves * kRing * kStageBytes : 0;
     __shared__ __align__(1024) char s_mem[kRings > kPart ? kRings : kPart > 0 ? kPart : 16];
     __shared__ uint16_t s_list[kFindMax];
     const int slot = blockIdx.x / a.slices, slice = blockIdx.x % a.slices;
@@ -759,23 +937,35 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
         if (f.count == 0) return;
         list = s_list;
     }
-    int first = 0;
-    const auto pass = [&](auto blocks, auto split) {
-        expert_block<X, W, RT, decltype(blocks)::value, GATED, decltype(split)::value, PARTS, LDS>(
-            a, f.expert, list, first, f.count, slice, s_mem);
-    };
-    constexpr int kMiddle = kMost > 2 ? kMost / 2 : 1;
-    constexpr std::integral_constant<int, kMost> most{};
-    constexpr std::integral_constant<int, kMiddle> middle{};
-    if constexpr (!GATED) {
-        // halves for all tokens of an expert or for none, whatever their order in the list
-        if (f.all && f.count <= 8) return pass(std::integral_constant<int, 1>{}, std::true_type{});
-    }
-    for (; f.count - first > (kMost > 1 ? 8 * kMost : 0); first += 16 * kMost) pass(most, std::false_type{});
-    if constexpr (kMost > 1) {
-        const int left = f.count - first;
-        if (kMost > 2 && left > 16) pass(middle, std::false_type{});
-        else if (left > 0) pass(std::integral_constant<int, 1>{}, std::false_type{});
+    if constexpr (MODE == kWide) {
+        for (int first = 0; first < f.count; first += 64 * kMost) {
+            const int left = f.count - first;
+            if (left > 32 * kMost)
+                expert_wide<X, W, kMost, GATED>(a, f.expert, list, first, f.count, slice, s_mem);
+            else if (kMost > 2 && left > 64)
+                expert_wide<X, W, kMost / 2, GATED>(a, f.expert, list, first, f.count, slice, s_mem);
+            else
+                expert_wide<X, W, 1, GATED>(a, f.expert, list, first, f.count, slice, s_mem);
+        }
+    } else {
+        int first = 0;
+        const auto pass = [&](auto blocks, auto split) {
+            expert_block<X, W, RT, decltype(blocks)::value, GATED, decltype(split)::value, PARTS, LDS>(
+                a, f.expert, list, first, f.count, slice, s_mem);
+        };
+        constexpr int kMiddle = kMost > 2 ? kMost / 2 : 1;
+        constexpr std::integral_constant<int, kMost> most{};
+        constexpr std::integral_constant<int, kMiddle> middle{};
+        if constexpr (!GATED) {
+            // halves for all tokens of an expert or for none, whatever their order in the list
+            if (f.all && f.count <= 8) return pass(std::integral_constant<int, 1>{}, std::true_type{});
+        }
+        for (; f.count - first > (kMost > 1 ? 8 * kMost : 0); first += 16 * kMost) pass(most, std::false_type{});
+        if constexpr (kMost > 1) {
+            const int left = f.count - first;
+            if (kMost > 2 && left > 16) pass(middle, std::false_type{});
+            else if (left > 0) pass(std::integral_constant<int, 1>{}, std::false_type{});
+        }
     }
 }
 
@@ -836,85 +1026,103 @@ struct ExpertsScratch {
     }
 };
 
-static int experts_chunk(bool eight_bit) { return 16 * (eight_bit ? MostBlocks<fp8>::value : MostBlocks<bf16>::value); }
+// How a call is launched.
+struct ExpertsPlan {
+    bool wide;        // the waves of a workgroup split an expert's tokens
+    int chunk;        // assignments per block of the plan
+    int64_t blocks;   // of tokens
+    struct Launch {
+        ExpertMode mode;
+        bool lds;     // weights through LDS: every row of every expert starts on a 16-byte boundary
+        int64_t slices;
+    } in, out;
 
-int64_t experts_aux_bytes(int64_t n, int experts, int dim, int hidden, bool eight_bit)
-{
-    return ExpertsScratch(n, experts, dim, hidden, experts_chunk(eight_bit)).bytes;
-}
+    ExpertsPlan(bool eight_bit, const ExpertsCall& c)
+    {
+        const int64_t n = c.tokens * c.top_k;
+        const int wbytes = eight_bit ? 1 : 2, most = eight_bit ? MostBlocks<fp8>::value : MostBlocks<bf16>::value;
+        in.lds = whole_vectors(c.w_in, c.dim, wbytes) && (!eight_bit || c.hidden % 16 == 0);
+        out.lds = whole_vectors(c.w_out, c.hidden, wbytes);
+        wide = in.lds && out.lds && n >= kWideTokens * c.experts;
+        chunk = (wide ? 64 : 16) * most;
+        blocks = n > kFindMax ? ExpertsScratch(n, c.experts, c.dim, c.hidden, chunk).blocks : n;
+        const int64_t used = n < c.experts ? n : c.experts;  // experts at most; without a plan, other blocks are idle
+        choose(in, true, c.hidden, used, eight_bit);
+        choose(out, false, c.dim, used, eight_bit);
+    }
 
-// How one launch streams the weights of `blocks` blocks.
-struct ExpertsVariant {
-    bool lds;    // through LDS: every row of every expert starts on a 16-byte boundary
-    bool whole;  // a wave has four tiles of its own and the whole depth
-    int64_t slices;
+private:
+    // On average to an expert: 512 tokens, top-6 of 64, 2,048 x 1,408: 346 us wide, 355 not; top-8 of 256: 583 and 490.
+    static constexpr int64_t kWideTokens = 32;
+
+    static bool whole_vectors(const void* w, int depth, int wbytes)
+    {
+        return (uintptr_t)w % kVecBytes == 0 && (int64_t)depth * wbytes % kVecBytes == 0;
+    }
+    void choose(Launch& l, bool gated, int rows, int64_t used, bool eight)
+    {
+        // A wave streams four tiles of its own where that gives every CU work enough; with few experts the waves of a
+        // workgroup share two tiles. 128 tokens, top-8 of 128, 2,048 x 768 (768 and 1,024 workgroups): in 16 bits 230
+        // us from 512 workgroups on, 222 from 1,024; in 8 bits, where two tiles hold fewer tokens, 140 and 152.
+        l.slices = ceil_div(rows, (gated ? 32 : 64) * kWaves);
+        l.mode = wide ? kWide : l.lds && used * l.slices >= (eight ? 512 : 1024) ? kStream : kParts;
+        if (l.mode == kWide) l.slices = ceil_div(rows, gated ? 32 : 64);
+        if (l.mode == kParts) l.slices = ceil_div(rows, gated ? 16 : 32);
+    }
 };
 
-static ExpertsVariant experts_variant(const void* w, int wbytes, bool gated, int rows, int depth, int64_t blocks)
+int64_t experts_aux_bytes(bool eight_bit, const ExpertsCall& c)
 {
-    ExpertsVariant v;
-    v.lds = (uintptr_t)w % kVecBytes == 0 && (int64_t)depth * wbytes % kVecBytes == 0 &&
-            (wbytes == 2 || !gated || rows % 16 == 0);
-    // With few experts the four waves of a workgroup share two tiles, so that
-    // there is work for every CU.
-    v.slices = ceil_div(rows, (gated ? 32 : 64) * kWaves);
-    v.whole = v.lds && blocks * v.slices >= 512;
-    if (!v.whole) v.slices = ceil_div(rows, gated ? 16 : 32);
-    return v;
-}
-
-static int64_t experts_blocks(int64_t n, int experts, int dim, int hidden, bool eight_bit)
-{
-    return n > kFindMax ? ExpertsScratch(n, experts, dim, hidden, experts_chunk(eight_bit)).blocks : n;
+    const ExpertsPlan p(eight_bit, c);
+    return ExpertsScratch(c.tokens * c.top_k, c.experts, c.dim, c.hidden, p.chunk).bytes;
 }
 
 int64_t experts_workgroups(bool eight_bit, const ExpertsCall& c)
 {
-    const int64_t blocks = experts_blocks(c.tokens * c.top_k, c.experts, c.dim, c.hidden, eight_bit);
-    const int wbytes = eight_bit ? 1 : 2;
-    const int64_t a = experts_variant(c.w_in, wbytes, true, c.hidden, c.dim, blocks).slices;
-    const int64_t b = experts_variant(c.w_out, wbytes, false, c.dim, c.hidden, blocks).slices;
-    return blocks * (a > b ? a : b);
+    const ExpertsPlan p(eight_bit, c);
+    return p.blocks * (p.in.slices > p.out.slices ? p.in.slices : p.out.slices);
 }
 
 template <typename X, typename W, bool GATED>
-static hipError_t launch_expert_kernel(ExpertArgs a, hipStream_t stream)
+static hipError_t launch_expert_kernel(ExpertArgs a, const ExpertsPlan::Launch& l, hipStream_t stream)
 {
-    const ExpertsVariant v = experts_variant(a.w, sizeof(W), GATED, a.rows, a.depth, a.blocks);
-    a.slices = (int)v.slices;
-    const dim3 grid((unsigned)(a.blocks * v.slices)), block(kThreads);
-    if (v.whole)
-        expert_kernel<X, W, 4, GATED, 1, true><<<grid, block, 0, stream>>>(a);
-    else if (v.lds)
-        expert_kernel<X, W, 2, GATED, kWaves, true><<<grid, block, 0, stream>>>(a);
+    a.slices = (int)l.slices;
+    const dim3 grid((unsigned)(a.blocks * l.slices)), block(kThreads);
+    if (l.mode == kStream)
+        expert_kernel<X, W, GATED, kStream, true><<<grid, block, 0, stream>>>(a);
+    else if (l.mode == kWide)
+        expert_kernel<X, W, GATED, kWide, true><<<grid, block, 0, stream>>>(a);
+    else if (l.lds)
+        expert_kernel<X, W, GATED, kParts, true><<<grid, block, 0, stream>>>(a);
     else
-        expert_kernel<X, W, 2, GATED, kWaves, false><<<grid, block, 0, stream>>>(a);
+        expert_kernel<X, W, GATED, kParts, false><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 template <typename X, typename W>
 static hipError_t experts_typed(const ExpertsCall& c, char* aux, hipStream_t stream)
 {
-    const int n = (int)(c.tokens * c.top_k), chunk = 16 * MostBlocks<W>::value;
-    const ExpertsScratch s(n, c.experts, c.dim, c.hidden, chunk);
+    const int n = (int)(c.tokens * c.top_k);
+    const ExpertsPlan p(sizeof(W) == 1, c);
+    const ExpertsScratch s(n, c.experts, c.dim, c.hidden, p.chunk);
     char *h = aux, *part = aux + s.part_at;
     int32_t* plan = nullptr;
     uint16_t* list = nullptr;
-    const int blocks = (int)experts_blocks(n, c.experts, c.dim, c.hidden, sizeof(W) == 1);
+    const int blocks = (int)p.blocks;
     if (n > kFindMax) {
         plan = reinterpret_cast<int32_t*>(aux + s.plan_at);
         list = reinterpret_cast<uint16_t*>(aux + s.list_at);
-        expert_plan_kernel<<<dim3(1), dim3(kPlanThreads), 0, stream>>>(c.ids, n, c.experts, chunk, blocks, plan, list);
+        expert_plan_kernel<<<dim3(1), dim3(kPlanThreads), 0, stream>>>(c.ids, n, c.experts, p.chunk, blocks, plan, list);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    ExpertArgs a{c.ids, c.x, c.w_in, c.w_in_scale, h, c.x_stride, s.h_stride, plan, list, n, c.top_k, c.experts,
-                 blocks, 0, chunk, c.hidden, c.dim};
-    hipError_t e = launch_expert_kernel<X, W, true>(a, stream);
+    const ExpertArgs a{c.ids, c.x, c.w_in, c.w_in_scale, h, c.x_stride, s.h_stride, plan, list, n, c.top_k, c.experts,
+                       blocks, 0, p.chunk, c.hidden, c.dim};
+    hipError_t e = launch_expert_kernel<X, W, true>(a, p.in, stream);
     if (e != hipSuccess) return e;
-    ExpertArgs b{c.ids, h, c.w_out, c.w_out_scale, part, s.h_stride, s.part_stride, plan, list, n, c.top_k, c.experts,
-                 blocks, 0, chunk, c.dim, c.hidden};
-    e = launch_expert_kernel<X, W, false>(b, stream);
+    const ExpertArgs b{c.ids, h, c.w_out, c.w_out_scale, part, s.h_stride, s.part_stride, plan, list, n, c.top_k,
+                       c.experts, blocks, 0, p.chunk, c.dim, c.hidden};
+    e = launch_expert_kernel<X, W, false>(b, p.out, stream);
     if (e != hipSuccess) return e;
     const int64_t items = c.tokens * ceil_div(c.dim, 4);
     expert_sum_kernel<X><<<dim3((unsigned)ceil_div(items, kThreads)), dim3(kThreads), 0, stream>>>(

@@ -195,6 +195,25 @@ def test_experts(dtype, eight, tokens, experts, top_k, dim, hidden):
                   f"{tokens} tokens, {top_k} of {experts}, {dim} x {hidden}")
 
 
+@pytest.mark.parametrize("dtype,eight", [(torch.bfloat16, False), (torch.float16, False), (torch.bfloat16, True)])
+@pytest.mark.parametrize("tokens,experts,top_k,dim,hidden", [(40, 1, 1, 64, 32), (100, 1, 1, 144, 48), (300, 2, 1, 272, 160),
+                                                            (600, 1, 1, 128, 64), (257, 2, 2, 80, 304),
+                                                            (129, 4, 4, 192, 128), (200, 3, 1, 1040, 16)])
+def test_experts_many_tokens(dtype, eight, tokens, experts, top_k, dim, hidden):
+    # the waves of a workgroup split an expert's tokens: up to 16, 32 and 64 to a wave, and blocks of the most
+    check_experts(layer(tokens, tokens, experts, top_k, dim, hidden, dtype, eight), f"{tokens} tokens, {experts} experts")
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_experts_one_crowded_among_many(eight):
+    # enough experts for every wave to have its own rows, one of them with most of the tokens
+    x, w_in, w_out, ids, weights, s_in, s_out = layer(31, 180, 130, 2, 272, 1040, torch.bfloat16, eight)
+    ids[:150, 0] = 77
+    ids[:40, 1] = 3
+    ids[150:, 1] = 129
+    check_experts((x, w_in, w_out, ids, weights, s_in, s_out), "crowded")
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_experts_wide_enough_for_whole_waves(eight):
     # many experts and rows: every wave streams its own rows over the whole depth
