@@ -19,6 +19,8 @@ namespace ds {
 // lanes rows at once, 16 bytes per lane and step; a wave takes ROWS such groups
 // of rows and holds STEPS steps of each in flight. Outputs are written past the
 // cache: nothing here reads them again, and rows of frequent tokens stay in it.
+// 65,536 tokens of 2,048 bf16: 64-66 us, 351 MB at 5.4 TB/s (one group of rows
+// in flight: 77; with cached stores 79, with past-cache loads 85).
 // ---------------------------------------------------------------------------
 template <typename T, typename ID, int STEPS, int ROWS>
 __global__ __launch_bounds__(kThreads) void embedding_kernel(const T* __restrict__ table, int64_t rows, int64_t dim,

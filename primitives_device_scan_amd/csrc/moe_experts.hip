@@ -25,6 +25,10 @@
 // expert of more, and all where a workgroup's waves split an expert's tokens,
 // take the rounded values alone (both halves for up to 32 tokens made the down
 // products of 256 tokens, top-8 of 256, 5% slower).
+// Measured: 256 tokens, top-8 of 256, 2,048 x 768 in bf16: gate/up 250-260 us,
+// down 142 (2.25 GB in all at 5.6-6.2 TB/s, some of it read twice for crowded
+// experts), plan and sum 5 each. 64 tokens, top-6 of 64, 2,048 x 1,408 in
+// e4m3: 66-73 and 36 us.
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -765,8 +769,10 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
 // Many tokens of one expert: the waves of a workgroup share four tiles and
 // split the tokens, 16 * TT to a wave. The stages of the weights are shared: a
 // wave loads one tile of each, three stages make the ring, and a barrier per
-// stage says that all tiles of it are there and that the stage before the one
-// being overwritten is done with.
+// stage says that all tiles of it are there and that the stage that is to be
+// overwritten is done with. 512 tokens, top-2 of 8, 4,096 x 2,048 in bf16: 215
+// us against 388 with 64 tokens to a workgroup; the tokens' values, which every
+// workgroup reads from the L2, bound it.
 // ---------------------------------------------------------------------------
 constexpr int kWideRing = 3;
 constexpr int kWideOps = kDmaOps / kWaves;  // loads of a wave per stage
