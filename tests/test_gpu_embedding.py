@@ -176,6 +176,26 @@ def test_grad_strides_shape_and_guards():
     assert ds.embedding_grad(dout, ids.cuda(), 0).shape == (0, 64)
 
 
+def test_grad_past_32_bit_offsets():
+    # 2.8G values of dout; then 2.25G values of the gradient
+    n, dim = 70_000, 40_000
+    dout = torch.ones((n, dim), dtype=torch.bfloat16, device="cuda")
+    ids = torch.arange(n, device="cuda") % 5
+    ids[-3:] = 4
+    got = ds.embedding_grad(dout, ids, 6, dtype=torch.float32)
+    assert torch.equal(got[:, 0], torch.bincount(ids, minlength=6).float())
+    assert torch.equal(got, got[:, :1].expand(6, dim))
+    del dout, got
+    rows, dim = 1_100_000, 2048
+    grad = torch.full((rows, dim), 3.0, device="cuda")
+    ids = torch.tensor([rows - 1, 5, 1_048_576, rows - 1], device="cuda")
+    d = normal(9, (4, dim), torch.float32).cuda()
+    got = ds.embedding_grad(d, ids, rows, out=grad)
+    assert torch.equal(got[rows - 1], d[0] + d[3]) and torch.equal(got[5], d[1]) and torch.equal(got[1_048_576], d[2])
+    got[ids] = 0
+    assert not bool(got.any())
+
+
 def test_grad_infinities_stay_in_their_rows():
     dout = torch.ones(200, 8)
     ids = torch.arange(200) % 5

@@ -89,6 +89,22 @@ def test_route_strides_and_bias_that_switches_off():
     assert w.shape == (0, 4) and ids.shape == (0, 4)
 
 
+def test_route_past_32_bit_offsets():
+    tokens, experts = 4_300_000, 511          # 2.2G logits
+    l = torch.zeros((tokens, experts), dtype=torch.bfloat16, device="cuda")
+    l[-2:] = normal(3, (2, experts), torch.bfloat16).cuda()
+    w, ids = ds.moe_route(l, 2)
+    rw, rids = mo.route(l[-2:], None, 2, "softmax", True, 1.0)
+    assert np.array_equal(ids[-2:].cpu().numpy(), rids) and ids[:-2].unique(dim=0).tolist() == [[0, 1]]
+    mo.within(w[-2:], rw, mo.route_terms(l[-2:]) * mo.U * np.abs(rw) + 2.0 ** -120, "last tokens")
+    dw = torch.zeros((tokens, 2), device="cuda")
+    dw[-2:, 0] = 1.0
+    got = ds.moe_route_grad(l, ids, dw)
+    ref, size = mo.route_grad(mo.f64(l[-2:]), rids, np.array([[1.0, 0.0]] * 2), "softmax", True, 1.0)
+    mo.within(got[-2:], ref, 2 * mo.route_terms(l[-2:]) * mo.U * size + mo.rounding(ref, l.dtype), "last gradients")
+    assert not bool(got[:-2].any())
+
+
 def check_route_grad(l, ids, score, renorm, scale, seed, what):
     dw = normal(seed, tuple(ids.shape))
     got = ds.moe_route_grad(l.cuda(), ids.cuda(), dw.cuda(), score=score, renormalize=renorm, scale=scale)
@@ -188,7 +204,7 @@ def check_experts(args, what):
     (1, 1, 1, 1, 1), (1, 4, 2, 64, 32), (1, 300, 8, 128, 48), (2, 3, 3, 7, 5), (5, 8, 2, 130, 33), (16, 4, 1, 256, 128),
     (17, 2, 2, 96, 64), (33, 2, 1, 200, 136), (40, 6, 6, 129, 65), (70, 2, 2, 320, 80), (64, 40, 4, 63, 144),
     (130, 3, 2, 72, 40), (12, 300, 3, 384, 272), (1, 9, 9, 2048, 768), (3, 40, 5, 320, 208), (4, 64, 16, 144, 1040),
-    (2, 20, 10, 528, 512), (4, 4, 1, 16, 16), (20, 5, 3, 160, 48), (9, 1, 1, 80, 304), (90, 4, 2, 256, 96)])
+    (2, 20, 10, 528, 512), (64, 8, 1, 64, 48), (65, 8, 1, 64, 48), (16, 300, 4, 64, 48), (13, 70, 5, 64, 48), (4, 4, 1, 16, 16), (20, 5, 3, 160, 48), (9, 1, 1, 80, 304), (90, 4, 2, 256, 96)])
 def test_experts(dtype, eight, tokens, experts, top_k, dim, hidden):
     say("experts", dtype, eight, tokens, experts, top_k, dim, hidden)
     check_experts(layer(tokens + dim, tokens, experts, top_k, dim, hidden, dtype, eight),
