@@ -277,7 +277,7 @@ int ds_embedding(int dtype, const void* d_table, int64_t rows, int64_t dim, int6
  * d_dout[i] over the i with d_ids[i] = v; ids outside [0, rows) are left out.
  * accumulate 0: every row of d_grad is written, rows that no id names with
  * zeros. accumulate 1: the sums are added to d_grad and other rows are not
- * touched. The positions are sorted by id (by rank up to 8,192 ids, by small
+ * touched. The positions are sorted by id (by rank up to 6,144 ids, by small
  * counting passes over 9 bits up to 262,144, by ds_radix_pass's passes above),
  * so a row's terms are added in the order of the sorted positions, without
  * atomics.
