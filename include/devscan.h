@@ -277,10 +277,10 @@ int ds_embedding(int dtype, const void* d_table, int64_t rows, int64_t dim, int6
  * d_dout[i] over the i with d_ids[i] = v; ids outside [0, rows) are left out.
  * accumulate 0: every row of d_grad is written, rows that no id names with
  * zeros. accumulate 1: the sums are added to d_grad and other rows are not
- * touched. The positions are sorted by id (by rank up to 6,144 ids, by small
- * counting passes over 9 bits up to 262,144, by ds_radix_pass's passes above),
- * so a row's terms are added in the order of the sorted positions, without
- * atomics.
+ * touched. Above 128 ids the positions are sorted by id (by rank up to 8,192,
+ * by small counting passes over 9 bits up to 262,144, by ds_radix_pass's passes
+ * above); a row's terms are added in the order of their positions, without
+ * atomics. Up to 128 ids no scratch is needed.
  *   dtype       of d_dout: DS_FP32, DS_BF16 or DS_FP16
  *   grad_dtype  of d_grad: dtype or DS_FP32
  * n < 2^31, rows < 2^27 (else DS_ERR_TOO_LARGE).

@@ -706,7 +706,7 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
     char* aux = nullptr;
     DevWs dws{nullptr, nullptr, nullptr};
     Workspace* w = nullptr;
-    if (n > 0) {
+    if (plan.bytes) {
         st = get_aux(stream, (size_t)plan.bytes, &aux);
         if (st != DS_OK) return st;
     }

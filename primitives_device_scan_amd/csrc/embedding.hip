@@ -4,7 +4,7 @@
 //   out[i] = scale * table[ids[i]]                 (zero where ids[i] is no row)
 //   grad[v] = scale * sum over i with ids[i] = v of dout[i]    (+ grad[v])
 //
-// The gradient goes by sorted tokens: the positions i are put in order of
+// Up to 128 tokens the gradient is one launch. Above, it goes by sorted tokens: the positions i are put in order of
 // their token (equal tokens in input order), so that each row's terms are
 // consecutive, and are then summed in that order: no atomics on the sums, and
 // the same bits on every run.
@@ -168,9 +168,9 @@ __device__ __forceinline__ uint32_t token_key(ID id, int64_t rows)
     return (int64_t)id >= 0 && (int64_t)id < rows ? (uint32_t)id : (uint32_t)rows;
 }
 
-// 5,000 tokens: 25.7 us for a whole gradient call by rank, 26.6 by the passes
-// below; 6,500: 30.4 and 29.2.
-constexpr int64_t kRankSortMax = 6144;
+// 8,000 tokens of 256 columns: 26.8 us for a whole gradient call by rank, 29.4
+// by the passes below; 9,000: 29.1 and 28.3.
+constexpr int64_t kRankSortMax = 8192;
 constexpr int kRankParts = 16;                     // lanes that count for one token
 constexpr int kRankTokens = kThreads / kRankParts; // tokens per workgroup
 
@@ -201,11 +201,25 @@ __global__ __launch_bounds__(kThreads) void token_rank_sort_kernel(const ID* __r
     const uint32_t i = blockIdx.x * kRankTokens + threadIdx.x / kRankParts, part = threadIdx.x % kRankParts;
     const uint32_t key = i < n ? s_key[i] : 0u;
     uint32_t below = 0;
-    for (uint32_t j = part * 4; j < padded; j += kRankParts * 4) {
+    // the workgroup's tokens lie in one block of 64: before it equal keys count, after it they do not
+    static_assert(64 % kRankTokens == 0 && kRankParts * 4 == 64, "a step is a block of 64 keys");
+    const uint32_t own = blockIdx.x * kRankTokens / 64 * 64;
+    const auto count = [&](uint32_t from, uint32_t to, uint32_t limit) {
+#pragma unroll 4
+        for (uint32_t j = from + part * 4; j < to; j += 64) {
+            const u32x4 k = *reinterpret_cast<const u32x4*>(s_key + j);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q) below += k[q] < limit ? 1u : 0u;
+        }
+    };
+    count(0, own, key + 1);
+    {
+        const uint32_t j = own + part * 4;
         const u32x4 k = *reinterpret_cast<const u32x4*>(s_key + j);
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q) below += k[q] < key + (j + q < i ? 1u : 0u) ? 1u : 0u;
     }
+    count(own + 64, padded, key);
     below += dpp<0x111>(below);  // sums over the row of 16 lanes: row_shr 1, 2, 4, 8
     below += dpp<0x112>(below);
     below += dpp<0x114>(below);
@@ -565,6 +579,102 @@ __global__ __launch_bounds__(kThreads) void embedding_sum_kernel(const T* __rest
         sum_chunk_of_slab<T, O, ADD, false>(dout, grad, a, chunk, c, slab == 0);
 }
 
+// ---------------------------------------------------------------------------
+// Up to kFewMax tokens: one launch, no sorting. A wave has one token's position
+// and one slab; every wave holds all ids, two to a lane. The wave of a row's
+// first position adds up the row's positions, in order, and the clearing waves
+// see which rows have tokens. (Three launches take 14.5 us of the host.)
+// ---------------------------------------------------------------------------
+constexpr int kFewMax = 2 * kWave;
+
+template <typename T, typename O, bool ADD, bool WHOLE>
+__device__ __forceinline__ void sum_positions(const T* __restrict__ dout, O* __restrict__ grad, const GradArgs& a,
+                                              uint32_t row, uint64_t low, uint64_t high, int64_t c)
+{
+    constexpr int N = GradCols<T, O>::value, kAhead = 8;
+    const bool live = c < a.dim;
+    const int64_t col = live ? c : 0, valid = a.dim - col, limit = (a.n - 1) * a.dout_stride + a.dim;
+    float acc[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
+    int count = __builtin_popcountll(low) + __builtin_popcountll(high);
+    for (; count > 0; count -= kAhead) {
+        Pack<T, N> x[kAhead];
+        int at[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            at[k] = low ? __builtin_ctzll(low) : high ? kWave + __builtin_ctzll(high) : at[k ? k - 1 : 0];
+            if (low) low &= low - 1;
+            else high &= high - 1;
+            const int64_t from = at[k] * a.dout_stride + col;
+            if (WHOLE || limit >= N) {
+                x[k] = load_window<T, N>(dout, from, WHOLE ? INT64_MAX : limit);
+            } else {
+                T t[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) t[j] = j < valid ? dout[from + j] : (T)0.0f;
+                __builtin_memcpy(&x[k], t, sizeof(t));
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (k < count) {  // uniform
+                if constexpr (!WHOLE) {
+                    const int64_t over = limit < N ? 0 : at[k] * a.dout_stride + col + N - limit;
+                    if (ballot(over > 0)) shift_down<T, N>(x[k], over > 0 ? (int)over : 0);
+                }
+                T t[N];
+                __builtin_memcpy(t, &x[k], sizeof(t));
+#pragma unroll
+                for (int j = 0; j < N; ++j) acc[j] += (float)t[j];
+            }
+        }
+    }
+    if (!live) return;
+    O* p = grad + (int64_t)row * a.grad_stride + c;
+    float y[N], old[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) old[j] = 0.0f;
+    if constexpr (ADD) load_floats<O, N>(p, valid, old);
+#pragma unroll
+    for (int j = 0; j < N; ++j) y[j] = acc[j] * a.scale + (ADD ? old[j] : 0.0f);
+    store_floats<O, N>(p, valid, y);
+}
+
+template <typename T, typename O, bool ADD, typename ID>
+__global__ __launch_bounds__(kThreads) void embedding_few_kernel(const ID* __restrict__ ids, const T* __restrict__ dout,
+                                                                 O* __restrict__ grad, GradArgs a, int64_t slabs,
+                                                                 ClearArgs clear)
+{
+    constexpr int N = GradCols<T, O>::value;
+    const int lane = lane_id();
+    const uint32_t id0 = lane < a.n ? token_key(ids[lane], a.rows) : (uint32_t)a.rows;
+    const uint32_t id1 = lane + kWave < a.n ? token_key(ids[lane + kWave], a.rows) : (uint32_t)a.rows;
+    if (!ADD && blockIdx.x >= (uint32_t)clear.skip) {
+        const int64_t r0 = clear.first + clear_wave<kThreads>(clear) * clear.per_wave;
+        const int64_t r1 = r0 + clear.per_wave < clear.last ? r0 + clear.per_wave : clear.last;
+        if (r0 >= r1) return;
+        const auto within = [&](uint32_t id) { return (int64_t)id >= r0 && (int64_t)id < r1; };
+        if (clear.stride_bytes == clear.row_bytes && !(ballot(within(id0)) | ballot(within(id1))))
+            return clear_span(clear.grad + r0 * clear.stride_bytes, (r1 - r0) * clear.row_bytes);
+        for (int64_t r = r0; r < r1; ++r)
+            if (!(ballot((int64_t)id0 == r) | ballot((int64_t)id1 == r)))
+                clear_span(clear.grad + r * clear.stride_bytes, clear.row_bytes);
+        return;
+    }
+    const int64_t unit = (int64_t)blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t i = unit / slabs, slab = unit % slabs, c = (slab * kWave + lane) * N;
+    if (i >= a.n) return;
+    const uint32_t row = i < kWave ? readlane(id0, (int)i) : readlane(id1, (int)i - kWave);
+    if (row >= (uint32_t)a.rows) return;
+    const uint64_t low = ballot(id0 == row), high = ballot(id1 == row);
+    if ((low ? __builtin_ctzll(low) : kWave + __builtin_ctzll(high)) != i) return;  // not the row's first position
+    if (a.dim % N == 0 || (slab + 1) * kWave * N <= a.dim)
+        sum_positions<T, O, ADD, true>(dout, grad, a, row, low, high, c);
+    else
+        sum_positions<T, O, ADD, false>(dout, grad, a, row, low, high, c);
+}
+
 // The rows whose runs cross chunks: for each chunk in the list and 128 columns
 // (two per lane), a wave adds the run's part there and the first parts of the
 // chunks that it reaches. kJoinAhead parts are in flight: a frequent token
@@ -707,6 +817,7 @@ EmbeddingGradPlan embedding_grad_plan(ElemKind grad_kind, int64_t n, int64_t row
     p.chunk = sum_chunk(n, p.slabs);
     p.chunks = ceil_div(n, p.chunk);
     p.partial_stride = p.slabs * kWave * per;
+    if (n <= kFewMax) return p;
     int bits = 1;
     while (((int64_t)1 << bits) < rows + 1) ++bits;
     if (n > kTileSortMax) {
@@ -758,6 +869,27 @@ struct Clearing {
     }
 };
 
+// All in one launch, for few tokens.
+template <typename T, typename O, bool ADD>
+static hipError_t embedding_few_typed(const EmbeddingGradPlan& p, const void* ids, bool wide_ids, const void* dout,
+                                      void* grad, const GradArgs& a, Clearing& clear, hipStream_t stream)
+{
+    unsigned blocks = clear.next(ceil_div(a.n * p.slabs, kWaves), kThreads, true, true);
+    // spans of some kilobytes, where rows are short: waves that share a cache line are slow
+    const int64_t each = ceil_div(4 * kPiece, clear.a.row_bytes);
+    if (clear.a.per_wave < each) {
+        clear.a.per_wave = (int)(each < 1024 ? each : 1024);
+        blocks = (unsigned)(clear.a.skip + ceil_div(ceil_div(clear.a.last - clear.a.first, clear.a.per_wave), kWaves));
+    }
+    if (wide_ids)
+        embedding_few_kernel<T, O, ADD><<<dim3(blocks), dim3(kThreads), 0, stream>>>((const int64_t*)ids, (const T*)dout,
+                                                                                     (O*)grad, a, p.slabs, clear.a);
+    else
+        embedding_few_kernel<T, O, ADD><<<dim3(blocks), dim3(kThreads), 0, stream>>>((const int32_t*)ids, (const T*)dout,
+                                                                                     (O*)grad, a, p.slabs, clear.a);
+    return hipGetLastError();
+}
+
 template <typename T, typename O, bool ADD>
 static hipError_t embedding_grad_typed(const EmbeddingGradPlan& p, const void* dout, void* grad, const GradArgs& a,
                                        Clearing& clear, hipStream_t stream)
@@ -793,14 +925,27 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
     const bool tiled = p.tiles > 0;
     uint32_t* crossing = table + p.crossing_at;
     Clearing clear(add, grad, rows, dim, grad_stride, grad_kind == kF32 ? 4 : 2);
-    if (p.radix_bits || n == 0) {
-        const unsigned grid = clear.next(ceil_div(n, kThreads), kThreads, n == 0);
+    if (n <= kFewMax) {
+        const GradArgs a{nullptr, nullptr, n, rows, dim, dout_stride, grad_stride, 0, scale, nullptr, 0, nullptr};
+#define DS_FEW(T, O)                                                                                \
+    return add ? embedding_few_typed<T, O, true>(p, ids, wide_ids, dout, grad, a, clear, stream) \
+               : embedding_few_typed<T, O, false>(p, ids, wide_ids, dout, grad, a, clear, stream)
+        if (kind == kF32 && grad_kind == kF32) DS_FEW(float, float);
+        if (kind == kBF16 && grad_kind == kBF16) DS_FEW(bf16, bf16);
+        if (kind == kBF16 && grad_kind == kF32) DS_FEW(bf16, float);
+        if (kind == kF16 && grad_kind == kF16) DS_FEW(fp16, fp16);
+        if (kind == kF16 && grad_kind == kF32) DS_FEW(fp16, float);
+#undef DS_FEW
+        return hipErrorInvalidValue;
+    }
+    if (p.radix_bits) {
+        const unsigned grid = clear.next(ceil_div(n, kThreads), kThreads);
         if (wide_ids)
             token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int64_t*)ids, n, rows, keys, index, crossing, clear.a);
         else
             token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int32_t*)ids, n, rows, keys, index, crossing, clear.a);
         e = hipGetLastError();
-        if (e != hipSuccess || n == 0) return e;
+        if (e != hipSuccess) return e;
         for (int d = 0; d < p.digits; ++d) {
             e = launch_radix_pass(keys, index, keys2, index2, n, d * p.radix_bits, p.radix_bits, table, ws, spin_limit, stream);
             if (e != hipSuccess) return e;
