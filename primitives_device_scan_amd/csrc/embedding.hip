@@ -941,9 +941,11 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
     if (p.radix_bits) {
         const unsigned grid = clear.next(ceil_div(n, kThreads), kThreads);
         if (wide_ids)
-            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int64_t*)ids, n, rows, keys, index, crossing, clear.a);
+            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int64_t*)ids, n, rows, keys, index,
+                                                                         crossing, clear.a);
         else
-            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int32_t*)ids, n, rows, keys, index, crossing, clear.a);
+            token_keys_kernel<<<dim3(grid), dim3(kThreads), 0, stream>>>((const int32_t*)ids, n, rows, keys, index,
+                                                                         crossing, clear.a);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
         for (int d = 0; d < p.digits; ++d) {
@@ -958,9 +960,11 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
             const void* from = d ? nullptr : ids;
             unsigned grid = clear.next(p.tiles, kTileThreads);
             if (wide_ids)
-                token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)from, a, d, keys, crossing, clear.a);
+                token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int64_t*)from, a, d, keys,
+                                                                                  crossing, clear.a);
             else
-                token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)from, a, d, keys, crossing, clear.a);
+                token_count_kernel<<<dim3(grid), dim3(kTileThreads), 0, stream>>>((const int32_t*)from, a, d, keys,
+                                                                                  crossing, clear.a);
             e = hipGetLastError();
             if (e != hipSuccess) return e;
             grid = clear.next(p.tiles, kTileThreads);

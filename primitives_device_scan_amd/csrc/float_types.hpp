@@ -84,9 +84,8 @@ __device__ __forceinline__ u32x4 load_end(const T* __restrict__ row, int64_t at,
     return u32x4{(uint32_t)lo, (uint32_t)(lo >> 32), (uint32_t)hi, (uint32_t)(hi >> 32)};
 }
 
-// Rounds N floats to T (nearest even) and writes the first `valid` of them
-// (NT: past the cache).
-template <typename T, int N, bool NT = false>
+// Rounds N floats to T (nearest even) and writes the first `valid` of them.
+template <typename T, int N>
 __device__ __forceinline__ void store_floats(T* __restrict__ p, int64_t valid, const float (&x)[N])
 {
     constexpr int kPer = Vec16<T>::kN;
@@ -99,10 +98,7 @@ __device__ __forceinline__ void store_floats(T* __restrict__ p, int64_t valid, c
         for (int v = 0; v < N / kPer; ++v) {
             u32x4 u;
             __builtin_memcpy(&u, t + v * kPer, sizeof(u));
-            if constexpr (NT)
-                __builtin_nontemporal_store(u, reinterpret_cast<typename Vec16<T>::type*>(p + v * kPer));
-            else
-                *reinterpret_cast<typename Vec16<T>::type*>(p + v * kPer) = u;
+            *reinterpret_cast<typename Vec16<T>::type*>(p + v * kPer) = u;
         }
     } else {
 #pragma unroll

@@ -344,7 +344,8 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
             const float d = use_sigmoid ? dw[m] * (chosen[m] > neg_inf() ? sigmoid_slope(chosen[m]) : 0.0f) : dw[m];
             all += dw[m] * q[m];
             for (int i = 0; i < L && m * L + i < top_k; ++i)
-                if (lane == i && id[m] >= 0) __hip_atomic_fetch_add(dp + id[m], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+                if (lane == i && id[m] >= 0)
+                    __hip_atomic_fetch_add(dp + id[m], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
     if (!use_sigmoid) all = group_sum<L>(all);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
