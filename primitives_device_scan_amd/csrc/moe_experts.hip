@@ -25,10 +25,11 @@
 // expert of more, and all where a workgroup's waves split an expert's tokens,
 // take the rounded values alone (both halves for up to 32 tokens made the down
 // products of 256 tokens, top-8 of 256, 5% slower).
-// Measured: 256 tokens, top-8 of 256, 2,048 x 768 in bf16: gate/up 250-260 us,
-// down 142 (2.25 GB in all at 5.6-6.2 TB/s, some of it read twice for crowded
-// experts), plan and sum 5 each. 64 tokens, top-6 of 64, 2,048 x 1,408 in
-// e4m3: 66-73 and 36 us.
+// Measured: 256 tokens, top-8 of 256, 2,048 x 768 in bf16: gate/up 254-259 us
+// (1.50 GB at 5.8-5.9 TB/s; 1.56 GB are fetched, as crowded experts' weights are
+// read again), down 137-139 (0.75 GB at 5.4-5.5), plan and sum 5 each. 64
+// tokens, top-6 of 64, 2,048 x 1,408 in e4m3: 62-66 us (344 MB at 5.2-5.6 TB/s)
+// and 36-37 (172 MB at 4.6-4.8).
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
