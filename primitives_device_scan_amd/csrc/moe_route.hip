@@ -254,11 +254,15 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
 // ---------------------------------------------------------------------------
 // The gradient with respect to the logits, for given ids and d loss / d w:
 // the scores are computed again from the logits, then the chain rule goes
-// through the division by the chosen scores' sum and through the scores. The
-// chosen experts' parts are added up in LDS, choice by choice, so an expert
-// that is named twice has its parts added in their order. Bound by memory:
-// 65,536 tokens of 256 experts in fp32 take 26.5-27.3 us, 138 MB at 5.1 TB/s
-// (51 us with a wave to a token).
+// through the division by the chosen scores' sum and through the scores. For
+// softmax with renorm the two give w_j = softmax of the chosen logits alone and
+//   d / d l_e = sum over j with ids[j] = e of w_j (dw_j - sum_i w_i dw_i):
+// the other logits are not read (they have no part, however much larger they
+// are) and get 0. The chosen experts' parts are added up in LDS, choice by
+// choice, so an expert that is named twice has its parts added in their order.
+// Bound by memory: 65,536 tokens of 256 experts in fp32, top-8: softmax 19.6 us
+// with renorm (the rows written and a line per chosen logit), 25.3 us without
+// (138 MB at 5.4 TB/s; 51 us with a wave to a token); sigmoid 19.5.
 // ---------------------------------------------------------------------------
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __restrict__ logits, int64_t tokens,
@@ -295,11 +299,16 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
             }
         }
     }
-    float l[NV][N], top = neg_inf(), total = 0.0f;
+    float l[NV][N], total = 0.0f;
     float chosen[M];
 #pragma unroll
     for (int m = 0; m < M; ++m) chosen[m] = m * L < top_k && id[m] >= 0 ? (float)row[id[m]] : neg_inf();
-    if (!use_sigmoid) {
+    float top = neg_inf();
+    if (!use_sigmoid && renorm) {
+#pragma unroll
+        for (int m = 0; m < M; ++m) top = chosen[m] > top ? chosen[m] : top;  // false for NaN
+        top = group_max<L>(top);
+    } else if (!use_sigmoid) {
         load_logits<T, L, NV>(row, experts, lane, l);
 #pragma unroll
         for (int v = 0; v < NV; ++v)
@@ -316,12 +325,13 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
         total = group_sum<L>(total);
         total = total > 0.0f || total != total ? 1.0f / total : 0.0f;
     }
-    // the chosen scores
+    // the chosen scores; softmax with renorm: up to a factor that the division by their sum takes away
     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
-            if (chosen[m] > neg_inf()) q[m] = use_sigmoid ? sigmoid(chosen[m]) : exp_sum(chosen[m] - top) * total;
+            if (chosen[m] > neg_inf())
+                q[m] = use_sigmoid ? sigmoid(chosen[m]) : renorm ? expf(chosen[m] - top) : exp_sum(chosen[m] - top) * total;
             sum += q[m];
             dot += dw[m] * q[m];
         }
@@ -341,13 +351,15 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
 #pragma unroll
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
-            const float d = use_sigmoid ? dw[m] * (chosen[m] > neg_inf() ? sigmoid_slope(chosen[m]) : 0.0f) : dw[m];
+            float d = dw[m];
+            if (use_sigmoid) d *= chosen[m] > neg_inf() ? sigmoid_slope(chosen[m]) : 0.0f;
+            else if (renorm) d *= q[m];
             all += dw[m] * q[m];
             for (int i = 0; i < L && m * L + i < top_k; ++i)
                 if (lane == i && id[m] >= 0)
                     __hip_atomic_fetch_add(dp + id[m], d, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
-    if (!use_sigmoid) all = group_sum<L>(all);
+    if (!use_sigmoid && !renorm) all = group_sum<L>(all);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     T* out = dlogits + token * dstride;
 #pragma unroll
@@ -360,7 +372,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
 #pragma unroll
             for (int i = 0; i < 4; ++i) d[j + i] = x[i];
         }
-        if (!use_sigmoid) {
+        if (!use_sigmoid && !renorm) {
 #pragma unroll
             for (int j = 0; j < N; ++j) d[j] = l[v][j] * total * (d[j] - all);
         }
