@@ -318,13 +318,20 @@ int ds_moe_route(int dtype, const void* d_logits, int64_t tokens, int num_expert
  * Gradient of ds_moe_route's weights with respect to the logits (the choice
  * itself has none): d_dlogits[t, e] = sum over j of d_dweights[t, j] *
  * (d weights[t, j] / d logits[t, e]) for the ids given (ids outside
- * [0, num_experts) have no part). Scores are taken over the logits that are
- * neither -infinity nor NaN; the others get 0. With softmax and renormalize 1
+ * [0, num_experts) and of experts that cannot be chosen have no part). d_bias
+ * is the one that ds_moe_route had, or NULL: scores are taken over the experts
+ * that can be chosen with it, the others get 0. With softmax and renormalize 1
  * the weights are the softmax of the chosen logits alone, so no other logit
  * has a part, and all but the chosen experts get exactly 0. All num_experts
  * entries of every row are written, in the logits' type. Other arguments as
  * ds_moe_route.
  */
+int ds_moe_route_grad_biased(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
+                             const float* d_bias, const int32_t* d_ids, const float* d_dweights, int top_k, int score,
+                             int renormalize, float scale, void* d_dlogits, int64_t dlogits_stride,
+                             hipStream_t stream);
+
+/* ds_moe_route_grad_biased without a bias. */
 int ds_moe_route_grad(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
                       const int32_t* d_ids, const float* d_dweights, int top_k, int score, int renormalize,
                       float scale, void* d_dlogits, int64_t dlogits_stride, hipStream_t stream);

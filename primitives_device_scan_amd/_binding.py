@@ -31,7 +31,7 @@ DS_ERR_STREAM_CAPTURING = 8
 
 EXPORTS = ["scan_exclusive", "scan_inclusive", "ds_scan", "ds_scan_seeded", "ds_scan_noalloc", "compact_if",
            "ds_compact_unordered", "ds_radix_pass", "ds_moe_align", "ds_embedding", "ds_embedding_grad",
-           "ds_moe_route", "ds_moe_route_grad", "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan",
+           "ds_moe_route", "ds_moe_route_grad", "ds_moe_route_grad_biased", "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan",
            "ds_tile_pipeline",
            "ds_tile_elems", "ds_scan_tile_elems", "ds_query_timeout", "ds_fail_next_allocations", "ds_set_spin_limit",
            "ds_status_string", "ds_release_workspace", "ds_version"]
@@ -73,6 +73,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ds_moe_route.restype = I
     L.ds_moe_route_grad.argtypes = [I, P, I64, I, I64, P, P, I, I, I, F, P, I64, P]
     L.ds_moe_route_grad.restype = I
+    L.ds_moe_route_grad_biased.argtypes = [I, P, I64, I, I64, P, P, P, I, I, I, F, P, I64, P]
+    L.ds_moe_route_grad_biased.restype = I
     L.ds_moe_experts.argtypes = [I, P, I64, I64, I64, I, P, P, P, P, I, I64, P, P, I, P, I64, P]
     L.ds_moe_experts.restype = I
     L.ds_copy.argtypes = [P, P, I64, P]
@@ -481,9 +483,11 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
 
 
 def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, *, score: str = "softmax",
-                   renormalize: bool = True, scale: float = 1.0, stream=None) -> torch.Tensor:
+                   bias: torch.Tensor | None = None, renormalize: bool = True, scale: float = 1.0,
+                   stream=None) -> torch.Tensor:
     """The gradient of moe_route's weights with respect to its logits, from the ids it chose and the gradient dweights
-    (float32 [tokens, top_k]) of the weights; in the logits' dtype."""
+    (float32 [tokens, top_k]) of the weights, for the score, bias, renormalize and scale that it had; in the logits'
+    dtype."""
     code = _float_code(logits, "logits")
     stride = _check_rows(logits, "logits")
     if ids.dim() != 2:
@@ -492,15 +496,19 @@ def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tens
     top_k = ids.shape[1]
     _check_flat(ids, "ids", torch.int32, (tokens, top_k), logits)
     _check_flat(dweights, "dweights", torch.float32, (tokens, top_k), logits)
+    if bias is not None:
+        _check_flat(bias, "bias", torch.float32, (experts,), logits)
     if score not in SCORES:
         raise ValueError(f"score must be one of {list(SCORES)}")
     if _elsewhere(logits, stream):
-        return _call_elsewhere(lambda: moe_route_grad(logits, ids, dweights, score=score, renormalize=renormalize,
-                                                      scale=scale), logits, stream, (logits, ids, dweights))
+        return _call_elsewhere(lambda: moe_route_grad(logits, ids, dweights, score=score, bias=bias,
+                                                      renormalize=renormalize, scale=scale), logits, stream,
+                               (logits, ids, dweights, bias))
     dlogits = logits.new_empty((tokens, experts))
-    _check(lib.ds_moe_route_grad(code, logits.data_ptr(), tokens, experts, stride, ids.data_ptr(), dweights.data_ptr(),
-                                 top_k, SCORES[score], 1 if renormalize else 0, scale, dlogits.data_ptr(), experts,
-                                 _stream_of(logits)), "ds_moe_route_grad")
+    _check(lib.ds_moe_route_grad_biased(code, logits.data_ptr(), tokens, experts, stride,
+                                        None if bias is None else bias.data_ptr(), ids.data_ptr(), dweights.data_ptr(),
+                                        top_k, SCORES[score], 1 if renormalize else 0, scale, dlogits.data_ptr(),
+                                        experts, _stream_of(logits)), "ds_moe_route_grad")
     return dlogits
 
 

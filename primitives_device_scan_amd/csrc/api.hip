@@ -757,19 +757,28 @@ int ds_moe_route_grad(int dtype, const void* d_logits, int64_t tokens, int num_e
                       const int32_t* d_ids, const float* d_dweights, int top_k, int score, int renormalize,
                       float scale, void* d_dlogits, int64_t dlogits_stride, hipStream_t stream)
 {
+    return ds_moe_route_grad_biased(dtype, d_logits, tokens, num_experts, stride, nullptr, d_ids, d_dweights, top_k,
+                                    score, renormalize, scale, d_dlogits, dlogits_stride, stream);
+}
+
+int ds_moe_route_grad_biased(int dtype, const void* d_logits, int64_t tokens, int num_experts, int64_t stride,
+                             const float* d_bias, const int32_t* d_ids, const float* d_dweights, int top_k, int score,
+                             int renormalize, float scale, void* d_dlogits, int64_t dlogits_stride, hipStream_t stream)
+{
     int st = check_route(dtype, tokens, num_experts, stride, top_k, score, renormalize);
     if (st == DS_OK && dlogits_stride < num_experts) st = DS_ERR_INVALID_VALUE;
     if (st != DS_OK || tokens == 0) return st;
     const int esz = float_bytes(dtype);
-    const Buf bufs[4] = {{d_logits, span_bytes(tokens, num_experts, stride, esz), esz, false},
+    const Buf bufs[5] = {{d_logits, span_bytes(tokens, num_experts, stride, esz), esz, false},
+                         {d_bias, d_bias ? (int64_t)num_experts * 4 : 0, 4, false},
                          {d_ids, tokens * top_k * 4, 4, false},
                          {d_dweights, tokens * top_k * 4, 4, false},
                          {d_dlogits, span_bytes(tokens, num_experts, dlogits_stride, esz), esz, true}};
-    st = check_buffers(bufs, 4);
+    st = check_buffers(bufs, 5);
     if (st != DS_OK) return st;
     const ds::RouteArgs a{tokens, stride, num_experts, top_k, score == DS_SCORE_SIGMOID, renormalize != 0, scale};
-    return ds::launch_moe_route_grad(float_kind(dtype), a, d_logits, d_ids, d_dweights, d_dlogits, dlogits_stride,
-                                     stream) == hipSuccess
+    return ds::launch_moe_route_grad(float_kind(dtype), a, d_logits, d_bias, d_ids, d_dweights, d_dlogits,
+                                     dlogits_stride, stream) == hipSuccess
                ? DS_OK
                : DS_ERR_HIP;
 }

@@ -121,8 +121,9 @@ int route_max_experts();
 int64_t route_blocks(int64_t tokens);
 hipError_t launch_moe_route(ElemKind kind, const RouteArgs& a, const void* logits, const float* bias, float* weights,
                             int32_t* ids, hipStream_t stream);
-hipError_t launch_moe_route_grad(ElemKind kind, const RouteArgs& a, const void* logits, const int32_t* ids,
-                                 const float* dweights, void* dlogits, int64_t dstride, hipStream_t stream);
+hipError_t launch_moe_route_grad(ElemKind kind, const RouteArgs& a, const void* logits, const float* bias,
+                                 const int32_t* ids, const float* dweights, void* dlogits, int64_t dstride,
+                                 hipStream_t stream);
 
 struct ExpertsCall {
     int64_t tokens;

@@ -117,6 +117,23 @@ __device__ __forceinline__ void load_logits(const T* __restrict__ row, int exper
     }
 }
 
+// The bias of experts e0 .. e0 + N - 1 (any value past the last expert).
+template <int N>
+__device__ __forceinline__ void load_bias(const float* __restrict__ bias, int e0, int experts, float (&b)[N])
+{
+    if (experts % N == 0) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+            const f32x4_v v = *reinterpret_cast<const f32x4_a4*>(bias + (e0 < experts ? e0 : 0) + j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[j + i] = v[i];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) b[j] = bias[e0 + j < experts ? e0 + j : 0];
+    }
+}
+
 // ---------------------------------------------------------------------------
 // Selection. A token's keys lie in LDS, in strips of S consecutive experts; lane
 // i of the group knows the largest key of strip i. A choice finds the largest
@@ -155,17 +172,10 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
 #pragma unroll
         for (int j = 0; j < N; ++j) sel[j] = l[v][j];
         if (bias) {
-            if (experts % N == 0) {
+            float b[N];
+            load_bias<N>(bias, e0, experts, b);
 #pragma unroll
-                for (int j = 0; j < N; j += 4) {
-                    const f32x4_v b = *reinterpret_cast<const f32x4_a4*>(bias + (e0 < experts ? e0 : 0) + j);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) sel[j + i] += b[i];
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < N; ++j) sel[j] += bias[e0 + j < experts ? e0 + j : 0];
-            }
+            for (int j = 0; j < N; ++j) sel[j] += b[j];
         }
         // -inf past the last expert, but +inf + -inf is NaN: both keys are kNoKey, which is never chosen
         uint32_t* at = keys + e0 / S * kStrip + e0 % S;
@@ -260,13 +270,15 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
 // the other logits are not read (they have no part, however much larger they
 // are) and get 0. The chosen experts' parts are added up in LDS, choice by
 // choice, so an expert that is named twice has its parts added in their order.
-// Bound by memory: 65,536 tokens of 256 experts in fp32, top-8: softmax 19.6 us
-// with renorm (the rows written and a line per chosen logit), 25.3 us without
-// (138 MB at 5.4 TB/s; 51 us with a wave to a token); sigmoid 19.5.
+// The bias is the router's: it says which experts can be chosen, no more.
+// Bound by memory: 65,536 tokens of 256 experts in fp32, top-8: softmax 19.9 us
+// with renorm (the rows written and a line per chosen logit), 25.7 us without
+// (138 MB at 5.4 TB/s; 51 us with a wave to a token); sigmoid 19.8-20.1.
 // ---------------------------------------------------------------------------
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __restrict__ logits, int64_t tokens,
                                                                   int experts, int64_t stride,
+                                                                  const float* __restrict__ bias,
                                                                   const int32_t* __restrict__ ids,
                                                                   const float* __restrict__ dweights, int top_k,
                                                                   bool use_sigmoid, bool renorm, float scale,
@@ -293,16 +305,22 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
                 id[m] = ids[token * top_k + j];
                 dw[m] = dweights[token * top_k + j] * scale;
             }
-            if (id[m] < 0 || id[m] >= experts) {
-                id[m] = -1;
-                dw[m] = 0.0f;
-            }
+            if (id[m] < 0 || id[m] >= experts) id[m] = -1;
         }
     }
+    // a choice of what cannot be chosen is none: it has no score, and its dw is not looked at
     float l[NV][N], total = 0.0f;
     float chosen[M];
 #pragma unroll
-    for (int m = 0; m < M; ++m) chosen[m] = m * L < top_k && id[m] >= 0 ? (float)row[id[m]] : neg_inf();
+    for (int m = 0; m < M; ++m) {
+        chosen[m] = m * L < top_k && id[m] >= 0 ? (float)row[id[m]] : neg_inf();
+        const float s = bias && m * L < top_k && id[m] >= 0 ? chosen[m] + bias[id[m]] : chosen[m];
+        if (!(s > neg_inf())) {
+            id[m] = -1;
+            dw[m] = 0.0f;
+            chosen[m] = neg_inf();
+        }
+    }
     float top = neg_inf();
     if (!use_sigmoid && renorm) {
 #pragma unroll
@@ -310,6 +328,16 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
         top = group_max<L>(top);
     } else if (!use_sigmoid) {
         load_logits<T, L, NV>(row, experts, lane, l);
+        if (bias) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int e0 = (v * L + lane) * N;
+                float b[N];
+                load_bias<N>(bias, e0, experts, b);
+#pragma unroll
+                for (int j = 0; j < N; ++j) l[v][j] = l[v][j] + b[j] > neg_inf() ? l[v][j] : neg_inf();
+            }
+        }
 #pragma unroll
         for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -330,7 +358,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
 #pragma unroll
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
-            if (chosen[m] > neg_inf())
+            if (id[m] >= 0)
                 q[m] = use_sigmoid ? sigmoid(chosen[m]) : renorm ? expf(chosen[m] - top) : exp_sum(chosen[m] - top) * total;
             sum += q[m];
             dot += dw[m] * q[m];
@@ -352,7 +380,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
             float d = dw[m];
-            if (use_sigmoid) d *= chosen[m] > neg_inf() ? sigmoid_slope(chosen[m]) : 0.0f;
+            if (use_sigmoid) d *= sigmoid_slope(chosen[m]);
             else if (renorm) d *= q[m];
             all += dw[m] * q[m];
             for (int i = 0; i < L && m * L + i < top_k; ++i)
@@ -407,15 +435,15 @@ static hipError_t route_typed(const RouteArgs& a, const void* logits, const floa
 }
 
 template <typename T>
-static hipError_t route_grad_typed(const RouteArgs& a, const void* logits, const int32_t* ids, const float* dweights,
-                                   void* dlogits, int64_t dstride, hipStream_t stream)
+static hipError_t route_grad_typed(const RouteArgs& a, const void* logits, const float* bias, const int32_t* ids,
+                                   const float* dweights, void* dlogits, int64_t dstride, hipStream_t stream)
 {
     constexpr int W = 16 / Vec16<T>::kN;  // vectors for 16 experts to a lane
     const auto launch = [&](auto kernel, int lanes) {
         const int64_t per_block = kWaves * (kWave / lanes);
         kernel<<<dim3((unsigned)((a.tokens + per_block - 1) / per_block)), dim3(kThreads), 0, stream>>>(
-            (const T*)logits, a.tokens, a.experts, a.stride, ids, dweights, a.top_k, a.use_sigmoid, a.renorm, a.scale,
-            (T*)dlogits, dstride);
+            (const T*)logits, a.tokens, a.experts, a.stride, bias, ids, dweights, a.top_k, a.use_sigmoid, a.renorm,
+            a.scale, (T*)dlogits, dstride);
         return hipGetLastError();
     };
     if (a.experts <= 64) return launch(moe_route_grad_kernel<T, 8, W / 2>, 8);
@@ -435,13 +463,14 @@ hipError_t launch_moe_route(ElemKind kind, const RouteArgs& a, const void* logit
     }
 }
 
-hipError_t launch_moe_route_grad(ElemKind kind, const RouteArgs& a, const void* logits, const int32_t* ids,
-                                 const float* dweights, void* dlogits, int64_t dstride, hipStream_t stream)
+hipError_t launch_moe_route_grad(ElemKind kind, const RouteArgs& a, const void* logits, const float* bias,
+                                 const int32_t* ids, const float* dweights, void* dlogits, int64_t dstride,
+                                 hipStream_t stream)
 {
     switch (kind) {
-    case kF32: return route_grad_typed<float>(a, logits, ids, dweights, dlogits, dstride, stream);
-    case kBF16: return route_grad_typed<bf16>(a, logits, ids, dweights, dlogits, dstride, stream);
-    case kF16: return route_grad_typed<fp16>(a, logits, ids, dweights, dlogits, dstride, stream);
+    case kF32: return route_grad_typed<float>(a, logits, bias, ids, dweights, dlogits, dstride, stream);
+    case kBF16: return route_grad_typed<bf16>(a, logits, bias, ids, dweights, dlogits, dstride, stream);
+    case kF16: return route_grad_typed<fp16>(a, logits, bias, ids, dweights, dlogits, dstride, stream);
     default: return hipErrorInvalidValue;
     }
 }

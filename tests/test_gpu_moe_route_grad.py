@@ -55,3 +55,74 @@ def test_renormalised_gradient_far_below_the_largest_logit(dtype, distance, toke
     ids = (ids + experts - top_k).to(torch.int32)
     got, _ = check(l, ids, "softmax", True, 2.5, what=f"{distance} below, {top_k} of {experts}")
     assert not bool(got[:, :experts - top_k].any())   # an expert that was not chosen has no part in the weights
+
+
+def switched_off(experts, seed=2):
+    """A selection bias that takes experts out of the choice."""
+    bias = normal(seed, (experts,), std=0.5)
+    bias[1::5] = float("-inf")
+    bias[3::11] = float("nan")
+    return bias
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("tokens,experts,top_k", [(1, 2, 1), (33, 60, 4), (9, 64, 6), (40, 128, 8), (21, 256, 8),
+                                                  (6, 300, 16), (5, 511, 5)])
+def test_weights_and_gradient_agree_with_a_bias(dtype, score, renorm, tokens, experts, top_k):
+    # experts that the bias switches off have large logits: they must not be in any sum
+    l, bias = normal(tokens + experts, (tokens, experts), std=1.5), switched_off(experts)
+    l[:, 1::5] += 20.0
+    l[0] = float("-inf")
+    l = l.to(dtype)
+    w, ids = ds.moe_route(l.cuda(), top_k, score=score, renormalize=renorm, scale=2.5, bias=bias.cuda())
+    got, want = check(l, ids.cpu(), score, renorm, 2.5, bias, f"{top_k} of {experts}")
+    mo.within(w, want, mo.route_terms(l) * mo.U * np.abs(want) + 2.0 ** -120, "weights")
+    off = ~np.isfinite(f32(bias))
+    assert not bool(got[:, torch.from_numpy(off)].any()) and not bool(got[0].any())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_choices_that_cannot_be_made_have_no_part(score, renorm):
+    # ids that the caller gives: switched off by the bias or by the logit, outside the experts, twice the same
+    l, bias = normal(3, (12, 40), std=1.5), switched_off(40)
+    l[:, 7] = float("-inf")
+    l[:, 8] = float("nan")
+    ids = torch.randint(0, 40, (12, 6), generator=torch.Generator().manual_seed(4)).to(torch.int32)
+    ids[0], ids[1, :3], ids[2, 2], ids[3, 0] = 1, 7, 8, 40
+    ids[4, 1] = ids[4, 0] = 10
+    check(l, ids, score, renorm, 1.5, bias, "given ids")
+    dw = torch.ones(12, 6)
+    dw[(ids == 1) | (ids == 7) | (ids == 8) | (ids == 40)] = float("nan")   # what no weight came from is not looked at
+    got = ds.moe_route_grad(l.cuda(), ids.cuda(), dw.cuda(), score=score, renormalize=renorm, bias=bias.cuda())
+    assert not bool(got.isnan().any()) and not bool(got[0].any())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("biased", [False, True])
+def test_gradient_against_differences_of_the_router(score, renorm, biased):
+    # A symmetric difference of the router's own weights along one direction, at logits far enough apart that the choice
+    # stays. Its error: the step's square times a third of the third derivative along the direction (under 20 |d|^3 for
+    # these sums of products of scores, |d| the largest part), and the weights' error of route_terms over the step.
+    tokens, experts, top_k, step = 16, 40, 5, 2.0 ** -6
+    l = torch.stack([torch.randperm(experts, generator=torch.Generator().manual_seed(t)) for t in range(tokens)]) / 8.0
+    d = normal(9, (tokens, experts)).clamp(-3, 3)
+    bias = None
+    if biased:
+        bias = torch.zeros(experts)
+        bias[2::3] = float("-inf")
+    more = {} if bias is None else {"bias": bias.cuda()}
+    up, ids = ds.moe_route((l + step * d).cuda(), top_k, score=score, renormalize=renorm, **more)
+    down, ids2 = ds.moe_route((l - step * d).cuda(), top_k, score=score, renormalize=renorm, **more)
+    at, ids3 = ds.moe_route(l.cuda(), top_k, score=score, renormalize=renorm, **more)
+    assert torch.equal(ids, ids2) and torch.equal(ids, ids3)
+    dw = normal(10, (tokens, top_k))
+    grad = mo.f64(ds.moe_route_grad(l.cuda(), ids, dw.cuda(), score=score, renormalize=renorm, **more))
+    moved = mo.f64(l + step * d) - mo.f64(l - step * d)
+    slope = ((mo.f64(up) - mo.f64(down)) * mo.f64(dw)).sum(1) / (2 * step)
+    most = np.abs(mo.f64(dw)).sum(1)
+    bound = 20 * step ** 2 * most * np.abs(mo.f64(d)).max(1) ** 3 + mo.route_terms(l) * mo.U * most / step
+    assert bool((np.abs(slope - (grad * moved).sum(1) / (2 * step)) <= bound).all())
