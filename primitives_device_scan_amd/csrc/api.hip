@@ -704,23 +704,15 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
     if (ds::embedding_grad_blocks(plan, n, rows, dim * gsz) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
     std::lock_guard<std::mutex> lock(g_mu);
     char* aux = nullptr;
-    DevWs dws{nullptr, nullptr, nullptr};
-    Workspace* w = nullptr;
     if (plan.bytes) {
         st = get_aux(stream, (size_t)plan.bytes, &aux);
         if (st != DS_OK) return st;
     }
-    if (plan.radix_bits) {
-        const int64_t words = ((int64_t)1 << plan.radix_bits) * ds::sort_table_columns(true, n);
-        st = scan_workspace_u32(stream, words, &dws, &w);
-        if (st != DS_OK) return st;
-        if (w) w->base_captured |= capturing(stream);
-    }
-    const hipError_t e = ds::launch_embedding_grad(float_kind(dtype), float_kind(grad_dtype), plan, d_dout,
-                                                   dout_stride, d_ids, id_bytes == 8, n, rows, dim, scale, d_grad,
-                                                   grad_stride, accumulate != 0, aux, dws, g_spin_limit, stream);
-    if (w) w->lookback_launches += (uint64_t)plan.digits;
-    return e == hipSuccess ? DS_OK : DS_ERR_HIP;
+    return ds::launch_embedding_grad(float_kind(dtype), float_kind(grad_dtype), plan, d_dout, dout_stride, d_ids,
+                                     id_bytes == 8, n, rows, dim, scale, d_grad, grad_stride, accumulate != 0, aux,
+                                     stream) == hipSuccess
+               ? DS_OK
+               : DS_ERR_HIP;
 }
 
 static int check_route(int dtype, int64_t tokens, int num_experts, int64_t stride, int top_k, int score,

@@ -574,7 +574,9 @@ static hipError_t counting_sort_typed(const uint32_t* keys, const uint32_t* vals
                                                                                             groups, tiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    e = launch_lookback_scan(kU32, false, hist, slots, (int64_t)dig.buckets * groups, ws, spin_limit, st);
+    const int64_t words = (int64_t)dig.buckets * groups;
+    e = ws.totals && !ws.status ? launch_three_pass_scan(kU32, false, hist, slots, words, ws, st)
+                                : launch_lookback_scan(kU32, false, hist, slots, words, ws, spin_limit, st);
     if (e != hipSuccess) return e;
     const int bits = dig.buckets > 1 ? 32 - __builtin_clz(dig.buckets - 1) : 0;
 #define DS_SCATTER(BITS)                                                                                      \

@@ -824,6 +824,12 @@ EmbeddingGradPlan embedding_grad_plan(ElemKind grad_kind, int64_t n, int64_t row
         p.radix_bits = 8;
         p.digits = (bits + 7) / 8;
         p.table_words = sort_aux_words(true, n, p.radix_bits);
+        // A table of more than one tile is scanned in three launches, not with the look-back: a wait there that gave up
+        // would leave keys and positions of earlier calls in the scratch, and the sums take both for addresses.
+        // (1,000,003 tokens, three passes: TIMES.)
+        const int64_t words = ((int64_t)1 << p.radix_bits) * sort_table_columns(true, n);
+        if (words > tile_elems(kU32, false, words)) p.totals_words = ceil_div(words, three_pass_tile_elems(4));
+        p.table_words += p.totals_words;
     } else if (n > kRankSortMax) {
         p.digits = (bits + kDigitBits - 1) / kDigitBits;
         p.bits = (bits + p.digits - 1) / p.digits;
@@ -916,7 +922,7 @@ int64_t embedding_grad_blocks(const EmbeddingGradPlan& p, int64_t n, int64_t row
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& p, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
                                  int64_t dim, float scale, void* grad, int64_t grad_stride, bool add, char* aux,
-                                 const DevWs& ws, uint32_t spin_limit, hipStream_t stream)
+                                 hipStream_t stream)
 {
     hipError_t e = hipSuccess;
     uint32_t* table = reinterpret_cast<uint32_t*>(aux);
@@ -948,8 +954,10 @@ hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const Embedd
                                                                          crossing, clear.a);
         e = hipGetLastError();
         if (e != hipSuccess) return e;
+        const int64_t totals_at = sort_aux_words(true, n, p.radix_bits);
+        const DevWs ws{nullptr, nullptr, p.totals_words ? table + totals_at : nullptr};
         for (int d = 0; d < p.digits; ++d) {
-            e = launch_radix_pass(keys, index, keys2, index2, n, d * p.radix_bits, p.radix_bits, table, ws, spin_limit, stream);
+            e = launch_radix_pass(keys, index, keys2, index2, n, d * p.radix_bits, p.radix_bits, table, ws, 1, stream);
             if (e != hipSuccess) return e;
             uint32_t* t = keys; keys = keys2; keys2 = t;
             t = index; index = index2; index2 = t;

@@ -67,7 +67,8 @@ int64_t moe_tile_elems();              // MoE alignment
 int sort_max_buckets();
 
 // table: (1 << bits) * tiles 32-bit words of scratch (the digit-major counts,
-// scanned in place); ws: look-back workspace for a scan of that many words.
+// scanned in place); ws: look-back workspace for a scan of that many words, or
+// totals alone for a scan in three launches that wait for nothing.
 hipError_t launch_radix_pass(const uint32_t* keys, const uint32_t* vals_in, uint32_t* keys_out, uint32_t* vals_out,
                              int64_t n, int shift, int bits, uint32_t* table, const DevWs& ws, uint32_t spin_limit,
                              hipStream_t stream);
@@ -98,6 +99,7 @@ struct EmbeddingGradPlan {
     int64_t slabs, chunks;   // units of work: slabs x chunks
     int64_t partial_stride;  // elements between rows of the crossing runs' parts
     int64_t table_words;     // the passes' table, 32-bit words at the start of the scratch
+    int64_t totals_words;    // of it at its end: tile totals of the radix passes' scan, or 0
     int64_t crossing_at;     // word offset of the list of crossing runs
     int64_t partial_at;      // byte offset of the parts
     int64_t bytes;           // scratch in all
@@ -108,7 +110,7 @@ int64_t embedding_grad_blocks(const EmbeddingGradPlan& plan, int64_t n, int64_t 
 hipError_t launch_embedding_grad(ElemKind kind, ElemKind grad_kind, const EmbeddingGradPlan& plan, const void* dout,
                                  int64_t dout_stride, const void* ids, bool wide_ids, int64_t n, int64_t rows,
                                  int64_t dim, float scale, void* grad, int64_t grad_stride, bool add, char* aux,
-                                 const DevWs& ws, uint32_t spin_limit, hipStream_t stream);
+                                 hipStream_t stream);
 
 // Mixture-of-experts router (float kinds) and experts (16-bit kinds).
 struct RouteArgs {

@@ -87,7 +87,7 @@ __global__ __launch_bounds__(kThreads) void tile_rescan_kernel(const T* in, T* o
     // each vector can be stored as soon as it is scanned.
     T wave_excl;
     (void)tile_reduce<T, S::kItems>(e, wave_excl, s_wave);
-    const T head = offsets[tile] + wave_excl;
+    const T head = (offsets ? offsets[tile] : T(0)) + wave_excl;  // null: the only tile
     if (whole) {
         scan_store_vec<T, V, kThreePassVPT, INCLUSIVE, A16>(out, seg, lane, e, head);
     } else {
@@ -103,13 +103,16 @@ static hipError_t three_pass_typed(bool incl, const void* in, void* out, int64_t
 {
     const int64_t tiles = (n + Shape<T, kThreePassVPT>::kTile - 1) / Shape<T, kThreePassVPT>::kTile;
     if (!ws.totals) return hipErrorInvalidValue;
-    T* totals = (T*)ws.totals;
-    tile_reduce_kernel<T, A16><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>((const T*)in, n, totals);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    scan_totals_kernel<T><<<dim3(1), dim3(kTotalsThreads), 0, st>>>(totals, tiles);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    T* totals = nullptr;
+    if (tiles > 1) {
+        totals = (T*)ws.totals;
+        tile_reduce_kernel<T, A16><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>((const T*)in, n, totals);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        scan_totals_kernel<T><<<dim3(1), dim3(kTotalsThreads), 0, st>>>(totals, tiles);
+        e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (incl)
         tile_rescan_kernel<T, true, A16><<<dim3((unsigned)tiles), dim3(kThreads), 0, st>>>(
             (const T*)in, (T*)out, n, totals);
