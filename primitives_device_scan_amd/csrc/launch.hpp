@@ -36,7 +36,7 @@ hipError_t launch_lookback_blocked(ElemKind kind, bool inclusive, const void* in
 int64_t blocked_tile_elems(int64_t n);
 
 hipError_t launch_three_pass_scan(ElemKind kind, bool inclusive, const void* in, void* out, int64_t n,
-                                  const DevWs& ws, hipStream_t stream);
+                                  const DevWs& ws, hipStream_t stream);  // one tile: one launch, no totals
 
 hipError_t launch_compact(ElemKind kind, const void* in, void* out, int64_t* num_selected, int64_t n,
                           int cmp, uint64_t operand_bits, const DevWs& ws, uint32_t spin_limit,
@@ -68,7 +68,7 @@ int sort_max_buckets();
 
 // table: (1 << bits) * tiles 32-bit words of scratch (the digit-major counts,
 // scanned in place); ws: look-back workspace for a scan of that many words, or
-// totals alone for a scan in three launches that wait for nothing.
+// totals alone for the three-pass scan, which waits for nothing.
 hipError_t launch_radix_pass(const uint32_t* keys, const uint32_t* vals_in, uint32_t* keys_out, uint32_t* vals_out,
                              int64_t n, int shift, int bits, uint32_t* table, const DevWs& ws, uint32_t spin_limit,
                              hipStream_t stream);
