@@ -25,7 +25,8 @@
  * Graph capture. A call records only kernel launches once the workspace of
  * its (device, stream) is large enough, so make one call of at least the
  * captured size on the stream before capturing it; otherwise the call
- * returns DS_ERR_STREAM_CAPTURING and records nothing. Status words carry a
+ * returns DS_ERR_STREAM_CAPTURING and records nothing. A buffer that a graph
+ * has recorded is kept when a later call outgrows it. Status words carry a
  * 30-bit launch number that the kernels advance themselves, and the host
  * clears them every 2^29 eager launches; a captured graph therefore may be
  * replayed at most 2^29 times before ds_release_workspace() (or one eager

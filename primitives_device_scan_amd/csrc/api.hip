@@ -30,15 +30,20 @@ using ds::DevWs;
 
 // Workspace layout: [Ctrl][status: one 128-byte line per tile][totals: 8 B per
 // tile]; `aux` is a separate scratch buffer for the counting-sort tables.
+struct Retired {
+    char* p;
+    int64_t tiles;  // of a `base`; 0 for an `aux`
+};
+
 struct Workspace {
     char* base = nullptr;
     int64_t tile_cap = 0;
     uint64_t lookback_launches = 0;  // launches that stamped an epoch since the last clear
-    bool base_captured = false;   // a graph of ds_embedding_grad holds the address of base
+    bool base_captured = false;   // some graph holds the address of base
     char* aux = nullptr;
     size_t aux_cap = 0;
     bool aux_captured = false;    // some graph holds the address of aux
-    std::vector<char*> retired;   // earlier buffers that graphs hold, freed by ds_release_workspace
+    std::vector<Retired> retired; // earlier buffers that graphs hold, freed by ds_release_workspace
 };
 
 std::mutex g_mu;
@@ -100,13 +105,14 @@ int get_workspace(hipStream_t stream, int64_t tiles, Workspace** out)
     Workspace& w = g_ws[{dev, stream}];
     const bool grow = w.tile_cap < tiles;
     const bool clear = w.lookback_launches >= kEpochClearPeriod;
-    if ((grow || clear) && capturing(stream)) return DS_ERR_STREAM_CAPTURING;
+    const bool recording = capturing(stream);
+    if ((grow || clear) && recording) return DS_ERR_STREAM_CAPTURING;
     if (grow) {
         int64_t cap = w.tile_cap * 2 > tiles ? w.tile_cap * 2 : tiles;
         if (cap < 1024) cap = 1024;
         if (refuse_allocation()) return DS_ERR_OUT_OF_MEMORY;
         if (w.base && w.base_captured) {
-            w.retired.push_back(w.base);  // a replay may still use it
+            w.retired.push_back({w.base, w.tile_cap});  // a replay may still use it
         } else if (w.base) {
             // The old buffer may still be in use by work queued on the stream.
             if (hipStreamSynchronize(stream) != hipSuccess) return DS_ERR_HIP;
@@ -133,6 +139,7 @@ int get_workspace(hipStream_t stream, int64_t tiles, Workspace** out)
             return DS_ERR_HIP;
         w.lookback_launches = 0;
     }
+    w.base_captured |= recording;
     *out = &w;
     return DS_OK;
 }
@@ -151,7 +158,7 @@ int get_aux(hipStream_t stream, size_t bytes, char** out)
         if (cap < ((size_t)1 << 20)) cap = (size_t)1 << 20;
         if (refuse_allocation()) return DS_ERR_OUT_OF_MEMORY;
         if (w.aux && w.aux_captured) {
-            w.retired.push_back(w.aux);  // a replay may still write to it
+            w.retired.push_back({w.aux, 0});  // a replay may still write to it
         } else if (w.aux) {
             if (hipStreamSynchronize(stream) != hipSuccess) return DS_ERR_HIP;
             (void)hipFree(w.aux);
@@ -479,6 +486,24 @@ int ds_tile_pipeline(int dtype, int variant, const void* d_in, void* d_out, int6
                : DS_ERR_HIP;
 }
 
+// Whether a wait on this look-back workspace has given up (sets *gave_up if so).
+static int take_timeout(char* base, int64_t tiles, bool* gave_up)
+{
+    Ctrl* c = reinterpret_cast<Ctrl*>(base);
+    uint32_t flag = 0;
+    if (hipMemcpy(&flag, &c->timeout, sizeof(flag), hipMemcpyDeviceToHost) != hipSuccess) return DS_ERR_HIP;
+    if (!flag) return DS_OK;
+    // A wait that gave up may have let the last tile advance the epoch
+    // before slower tiles read it, so their status words can carry the
+    // next launch's epoch. The stream is idle: clear every status word
+    // (and the flag) so the next launch starts from a clean array.
+    if (hipMemset(base + sizeof(Ctrl), 0, (size_t)tiles * kStatusBytes) != hipSuccess) return DS_ERR_HIP;
+    const uint32_t zero = 0;
+    if (hipMemcpy(&c->timeout, &zero, sizeof(zero), hipMemcpyHostToDevice) != hipSuccess) return DS_ERR_HIP;
+    *gave_up = true;
+    return DS_OK;
+}
+
 int ds_query_timeout(hipStream_t stream, int* timed_out)
 {
     if (!timed_out) return DS_ERR_INVALID_VALUE;
@@ -500,25 +525,20 @@ int ds_query_timeout(hipStream_t stream, int* timed_out)
         }
     }
     auto it = g_ws.find({dev, stream});
-    if (it == g_ws.end() || !it->second.base) {
-        *timed_out = from_scratch;
-        return DS_OK;
+    bool gave_up = false;
+    if (it != g_ws.end()) {
+        Workspace& w = it->second;
+        if (w.base) {
+            const int st = take_timeout(w.base, w.tile_cap, &gave_up);
+            if (st != DS_OK) return st;
+            if (gave_up) w.lookback_launches = 0;
+        }
+        for (const Retired& r : w.retired) {  // graphs may still run on these
+            const int st = r.tiles ? take_timeout(r.p, r.tiles, &gave_up) : DS_OK;
+            if (st != DS_OK) return st;
+        }
     }
-    Workspace& w = it->second;
-    Ctrl* c = reinterpret_cast<Ctrl*>(w.base);
-    uint32_t flag = 0;
-    if (hipMemcpy(&flag, &c->timeout, sizeof(flag), hipMemcpyDeviceToHost) != hipSuccess) return DS_ERR_HIP;
-    if (flag) {
-        // A wait that gave up may have let the last tile advance the epoch
-        // before slower tiles read it, so their status words can carry the
-        // next launch's epoch. The stream is idle: clear every status word
-        // (and the flag) so the next launch starts from a clean array.
-        if (hipMemset(w.base + sizeof(Ctrl), 0, (size_t)w.tile_cap * kStatusBytes) != hipSuccess) return DS_ERR_HIP;
-        const uint32_t zero = 0;
-        if (hipMemcpy(&c->timeout, &zero, sizeof(zero), hipMemcpyHostToDevice) != hipSuccess) return DS_ERR_HIP;
-        w.lookback_launches = 0;
-    }
-    *timed_out = (flag || from_scratch) ? 1 : 0;
+    *timed_out = (gave_up || from_scratch) ? 1 : 0;
     return DS_OK;
 }
 
@@ -820,7 +840,7 @@ void ds_release_workspace(void)
     for (auto& kv : g_ws) {
         if (kv.second.base) (void)hipFree(kv.second.base);
         if (kv.second.aux) (void)hipFree(kv.second.aux);
-        for (char* p : kv.second.retired) (void)hipFree(p);
+        for (const Retired& r : kv.second.retired) (void)hipFree(r.p);
     }
     g_ws.clear();
 }
