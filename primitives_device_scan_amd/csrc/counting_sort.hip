@@ -403,7 +403,8 @@ struct MoeSlots {
 // gbase[e] for MoE: expert e's padded start plus the keys of e in earlier
 // tiles. Thread e takes expert e.
 __device__ __forceinline__ void moe_bases(uint32_t* gbase, uint32_t* s_wave, const uint32_t* __restrict__ slots,
-                                          int64_t tiles, int64_t tile, uint32_t E, const MoeSlots& moe, int64_t n)
+                                          int64_t tiles, int64_t tile, uint32_t E, const MoeSlots& moe, int64_t n,
+                                          int64_t out_cap)
 {
     const uint32_t e = threadIdx.x;
     const uint32_t last = slots[(int64_t)E * tiles - 1] + moe.hist[(int64_t)E * tiles - 1];
@@ -421,7 +422,9 @@ __device__ __forceinline__ void moe_bases(uint32_t* gbase, uint32_t* s_wave, con
         if (e < E) {
             moe.counts[e] = (int32_t)c;
             moe.offsets[e] = (int32_t)off;
-            for (uint32_t j = c; j < r; ++j) moe.sorted[off + j] = (int32_t)n;
+            // (past out_cap only where a wait of the table's scan gave up)
+            for (uint32_t j = c; j < r; ++j)
+                if ((int64_t)(off + j) < out_cap) moe.sorted[off + j] = (int32_t)n;
         }
         if (threadIdx.x == 0) moe.offsets[E] = (int32_t)total;
     }
@@ -447,7 +450,7 @@ __global__ __launch_bounds__(kSortThreads) void digit_scatter_kernel(
     uint32_t key[ITEMS], val[ITEMS];
     const bool whole = load_tile<VALS, ITEMS>(keys, vals_in, n, first, key, val);
     if (moe.hist) {
-        moe_bases(sh.gbase, sh.s_wave, slots, groups, tile, dig.buckets, moe, n);
+        moe_bases(sh.gbase, sh.s_wave, slots, groups, tile, dig.buckets, moe, n, out_cap);
     } else {
         const int64_t g = tile / GROUP;
         const bool later = GROUP > 1 && tile % GROUP != 0;
