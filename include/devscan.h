@@ -26,7 +26,15 @@
  * its (device, stream) is large enough, so make one call of at least the
  * captured size on the stream before capturing it; otherwise the call
  * returns DS_ERR_STREAM_CAPTURING and records nothing. A buffer that a graph
- * has recorded is kept when a later call outgrows it. Status words carry a
+ * has recorded is kept when a later call outgrows it. Scratch in graphs: all
+ * calls recorded on one stream hold that stream's workspace, as its eager calls
+ * do, so graphs recorded on the same stream must not run at the same time, nor
+ * beside an eager call on it, if their calls use a workspace (the scans,
+ * compact_if, ds_radix_pass, ds_moe_align, ds_tile_pipeline, ds_embedding_grad,
+ * ds_moe_experts). The last two also take scratch from the caller
+ * (ds_embedding_grad_scratch, ds_moe_experts_scratch): a graph with scratch of
+ * its own runs beside anything, and needs no call before the capture (the
+ * Python binding records these two that way). Status words carry a
  * 30-bit launch number that the kernels advance themselves, and the host
  * clears them every 2^29 eager launches; a captured graph therefore may be
  * replayed at most 2^29 times before ds_release_workspace() (or one eager
@@ -290,6 +298,19 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
                       float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim, int64_t grad_stride,
                       int accumulate, hipStream_t stream);
 
+/*
+ * ds_embedding_grad with its scratch in memory of the caller's, d_scratch, 256-byte
+ * aligned, of at least ds_embedding_grad_scratch_bytes() (which is 0 where no
+ * scratch is needed or an argument is out of range; DS_ERR_INVALID_VALUE if
+ * scratch_bytes is less). Its contents need not be kept. For calls recorded
+ * into a graph: see "Scratch in graphs" above. d_scratch NULL: ds_embedding_grad.
+ */
+int64_t ds_embedding_grad_scratch_bytes(int grad_dtype, int64_t n, int64_t rows, int64_t dim);
+int ds_embedding_grad_scratch(int dtype, const void* d_dout, int64_t dout_stride, const void* d_ids, int id_bytes,
+                              int64_t n, float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim,
+                              int64_t grad_stride, int accumulate, void* d_scratch, int64_t scratch_bytes,
+                              hipStream_t stream);
+
 /* Score of an expert in ds_moe_route. */
 typedef enum {
     DS_SCORE_SOFTMAX = 0, /* softmax of the logits over the experts that can be chosen */
@@ -364,6 +385,15 @@ int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int6
                    const void* d_w_in, const float* d_w_in_scale, const void* d_w_out, const float* d_w_out_scale,
                    int num_experts, int64_t hidden, const int32_t* d_ids, const float* d_weights, int top_k,
                    void* d_y, int64_t y_stride, hipStream_t stream);
+
+/* ds_moe_experts with its scratch in memory of the caller's, as ds_embedding_grad_scratch. */
+int64_t ds_moe_experts_scratch_bytes(int weight_dtype, int64_t tokens, int64_t dim, int num_experts, int64_t hidden,
+                                     int top_k);
+int ds_moe_experts_scratch(int dtype, const void* d_x, int64_t tokens, int64_t dim, int64_t x_stride, int weight_dtype,
+                           const void* d_w_in, const float* d_w_in_scale, const void* d_w_out,
+                           const float* d_w_out_scale, int num_experts, int64_t hidden, const int32_t* d_ids,
+                           const float* d_weights, int top_k, void* d_y, int64_t y_stride, void* d_scratch,
+                           int64_t scratch_bytes, hipStream_t stream);
 
 /*
  * Copy of nbytes from d_in to d_out with the same launch shape, 16-byte

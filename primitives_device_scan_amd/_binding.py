@@ -31,6 +31,8 @@ DS_ERR_STREAM_CAPTURING = 8
 
 EXPORTS = ["scan_exclusive", "scan_inclusive", "ds_scan", "ds_scan_seeded", "ds_scan_noalloc", "compact_if",
            "ds_compact_unordered", "ds_radix_pass", "ds_moe_align", "ds_embedding", "ds_embedding_grad",
+           "ds_embedding_grad_scratch", "ds_embedding_grad_scratch_bytes", "ds_moe_experts_scratch",
+           "ds_moe_experts_scratch_bytes",
            "ds_moe_route", "ds_moe_route_grad", "ds_moe_route_grad_biased", "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan",
            "ds_tile_pipeline",
            "ds_tile_elems", "ds_scan_tile_elems", "ds_query_timeout", "ds_fail_next_allocations", "ds_set_spin_limit",
@@ -69,6 +71,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ds_embedding.restype = I
     L.ds_embedding_grad.argtypes = [I, P, I64, P, I, I64, F, I, P, I64, I64, I64, I, P]
     L.ds_embedding_grad.restype = I
+    L.ds_embedding_grad_scratch.argtypes = [I, P, I64, P, I, I64, F, I, P, I64, I64, I64, I, P, I64, P]
+    L.ds_embedding_grad_scratch.restype = I
+    L.ds_embedding_grad_scratch_bytes.argtypes = [I, I64, I64, I64]
+    L.ds_embedding_grad_scratch_bytes.restype = I64
     L.ds_moe_route.argtypes = [I, P, I64, I, I64, P, I, I, I, F, P, P, P]
     L.ds_moe_route.restype = I
     L.ds_moe_route_grad.argtypes = [I, P, I64, I, I64, P, P, I, I, I, F, P, I64, P]
@@ -77,6 +83,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ds_moe_route_grad_biased.restype = I
     L.ds_moe_experts.argtypes = [I, P, I64, I64, I64, I, P, P, P, P, I, I64, P, P, I, P, I64, P]
     L.ds_moe_experts.restype = I
+    L.ds_moe_experts_scratch.argtypes = [I, P, I64, I64, I64, I, P, P, P, P, I, I64, P, P, I, P, I64, P, I64, P]
+    L.ds_moe_experts_scratch.restype = I
+    L.ds_moe_experts_scratch_bytes.argtypes = [I, I64, I64, I, I64, I]
+    L.ds_moe_experts_scratch_bytes.restype = I64
     L.ds_copy.argtypes = [P, P, I64, P]
     L.ds_copy.restype = I
     L.ds_bandwidth_pattern.argtypes = [I, I, I, P, P, I64, P]
@@ -370,6 +380,15 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream"):
         return torch._C._cuda_getCurrentRawStream(x.get_device())
 
 
+_recording = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+# A call that is being recorded takes its scratch from the graph's own memory (torch allocates there during a capture, and
+# the graph keeps it): the stream's workspace is shared with every other graph recorded on it and with its eager calls.
+def _scratch_of(x: torch.Tensor, room: int) -> torch.Tensor | None:
+    return x.new_empty(room, dtype=torch.uint8) if room else None
+
+
 def _call_elsewhere(call, x: torch.Tensor, stream, used):
     """call() with x's device and the stream current: outputs are allocated on the stream that the call runs on, and
     tensors that belong to another stream are kept from reuse until the call has run."""
@@ -450,9 +469,14 @@ def embedding_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: f
         grad_stride = _check_rows(out, "out", rows, dim, dout)
         if out.dtype != dtype:
             raise TypeError(f"out must be {dtype}")
-    _check(lib.ds_embedding_grad(code, dout.data_ptr(), stride, ids.data_ptr(), _ID_BYTES[ids.dtype], n, scale,
-                                 _FLOATS[dtype], out.data_ptr(), rows, dim, grad_stride, 1 if accumulate else 0,
-                                 _stream_of(dout)), "ds_embedding_grad")
+    scratch, room = None, 0
+    if _recording():
+        room = lib.ds_embedding_grad_scratch_bytes(_FLOATS[dtype], n, rows, dim)
+        scratch = _scratch_of(dout, room)
+    _check(lib.ds_embedding_grad_scratch(code, dout.data_ptr(), stride, ids.data_ptr(), _ID_BYTES[ids.dtype], n, scale,
+                                         _FLOATS[dtype], out.data_ptr(), rows, dim, grad_stride, 1 if accumulate else 0,
+                                         None if scratch is None else scratch.data_ptr(), room, _stream_of(dout)),
+           "ds_embedding_grad")
     return out
 
 
@@ -553,10 +577,17 @@ def moe_experts(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, ids: t
         y_stride = _check_rows(out, "out", tokens, dim, x)
         if out.dtype != x.dtype:
             raise TypeError("out must have x's dtype")
-    _check(lib.ds_moe_experts(code, x.data_ptr(), tokens, dim, x_stride, DS_FP8_E4M3 if eight else code,
-                              w_in.data_ptr(), w_in_scale.data_ptr() if eight else None, w_out.data_ptr(),
-                              w_out_scale.data_ptr() if eight else None, experts, hidden, ids.data_ptr(),
-                              weights.data_ptr(), top_k, out.data_ptr(), y_stride, _stream_of(x)), "ds_moe_experts")
+    weight_code = DS_FP8_E4M3 if eight else code
+    scratch, room = None, 0
+    if _recording():
+        room = lib.ds_moe_experts_scratch_bytes(weight_code, tokens, dim, experts, hidden, top_k)
+        scratch = _scratch_of(x, room)
+    _check(lib.ds_moe_experts_scratch(code, x.data_ptr(), tokens, dim, x_stride, weight_code, w_in.data_ptr(),
+                                      w_in_scale.data_ptr() if eight else None, w_out.data_ptr(),
+                                      w_out_scale.data_ptr() if eight else None, experts, hidden, ids.data_ptr(),
+                                      weights.data_ptr(), top_k, out.data_ptr(), y_stride,
+                                      None if scratch is None else scratch.data_ptr(), room, _stream_of(x)),
+           "ds_moe_experts")
     return out
 
 

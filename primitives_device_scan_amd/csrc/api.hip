@@ -703,9 +703,35 @@ int ds_embedding(int dtype, const void* d_table, int64_t rows, int64_t dim, int6
                : DS_ERR_HIP;
 }
 
+// The scratch of a call: the caller's, checked against the call's buffers too, or the stream's own.
+static int check_scratch(const void* scratch, int64_t have, int64_t need, const Buf* bufs, int count)
+{
+    if (have < 0 || (scratch && have < need)) return DS_ERR_INVALID_VALUE;
+    if ((uintptr_t)scratch % 256) return DS_ERR_MISALIGNED;
+    for (int i = 0; scratch && i < count; ++i)
+        if (overlaps(scratch, (size_t)need, bufs[i].p, (size_t)bufs[i].bytes)) return DS_ERR_OVERLAP;
+    return DS_OK;
+}
+
 int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const void* d_ids, int id_bytes, int64_t n,
                       float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim, int64_t grad_stride,
                       int accumulate, hipStream_t stream)
+{
+    return ds_embedding_grad_scratch(dtype, d_dout, dout_stride, d_ids, id_bytes, n, scale, grad_dtype, d_grad, rows,
+                                     dim, grad_stride, accumulate, nullptr, 0, stream);
+}
+
+int64_t ds_embedding_grad_scratch_bytes(int grad_dtype, int64_t n, int64_t rows, int64_t dim)
+{
+    if (!float_bytes(grad_dtype) || rows < 1 || dim < 1 || n < 1) return 0;
+    if (n >= ((int64_t)1 << 31) || dim >= ((int64_t)1 << 31) || rows > ds::embedding_most_rows()) return 0;
+    return ds::embedding_grad_plan(float_kind(grad_dtype), n, rows, dim).bytes;
+}
+
+int ds_embedding_grad_scratch(int dtype, const void* d_dout, int64_t dout_stride, const void* d_ids, int id_bytes,
+                              int64_t n, float scale, int grad_dtype, void* d_grad, int64_t rows, int64_t dim,
+                              int64_t grad_stride, int accumulate, void* d_scratch, int64_t scratch_bytes,
+                              hipStream_t stream)
 {
     const int esz = float_bytes(dtype), gsz = float_bytes(grad_dtype);
     if (!esz || !gsz || (grad_dtype != dtype && grad_dtype != DS_FP32)) return DS_ERR_UNSUPPORTED_DTYPE;
@@ -722,9 +748,11 @@ int ds_embedding_grad(int dtype, const void* d_dout, int64_t dout_stride, const 
     if (st != DS_OK) return st;
     const ds::EmbeddingGradPlan plan = ds::embedding_grad_plan(float_kind(grad_dtype), n, rows, dim);
     if (ds::embedding_grad_blocks(plan, n, rows, dim * gsz) > kMaxTiles / 2) return DS_ERR_TOO_LARGE;
+    st = check_scratch(d_scratch, scratch_bytes, plan.bytes, bufs, 3);
+    if (st != DS_OK) return st;
     std::lock_guard<std::mutex> lock(g_mu);
-    char* aux = nullptr;
-    if (plan.bytes) {
+    char* aux = static_cast<char*>(d_scratch);
+    if (plan.bytes && !aux) {
         st = get_aux(stream, (size_t)plan.bytes, &aux);
         if (st != DS_OK) return st;
     }
@@ -800,6 +828,28 @@ int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int6
                    int num_experts, int64_t hidden, const int32_t* d_ids, const float* d_weights, int top_k,
                    void* d_y, int64_t y_stride, hipStream_t stream)
 {
+    return ds_moe_experts_scratch(dtype, d_x, tokens, dim, x_stride, weight_dtype, d_w_in, d_w_in_scale, d_w_out,
+                                  d_w_out_scale, num_experts, hidden, d_ids, d_weights, top_k, d_y, y_stride, nullptr,
+                                  0, stream);
+}
+
+int64_t ds_moe_experts_scratch_bytes(int weight_dtype, int64_t tokens, int64_t dim, int num_experts, int64_t hidden,
+                                     int top_k)
+{
+    if (tokens < 1 || dim < 1 || hidden < 1 || num_experts < 1 || num_experts > ds::experts_max_experts() ||
+        top_k < 1 || dim > DS_EXPERTS_MAX_WIDTH || hidden > DS_EXPERTS_MAX_WIDTH ||
+        tokens > ds::experts_max_assignments() || tokens * top_k > ds::experts_max_assignments())
+        return 0;
+    // weights at any address: whichever launch that leads to
+    return ds::experts_most_aux_bytes(weight_dtype == DS_FP8_E4M3, tokens, (int)dim, num_experts, (int)hidden, top_k);
+}
+
+int ds_moe_experts_scratch(int dtype, const void* d_x, int64_t tokens, int64_t dim, int64_t x_stride, int weight_dtype,
+                           const void* d_w_in, const float* d_w_in_scale, const void* d_w_out,
+                           const float* d_w_out_scale, int num_experts, int64_t hidden, const int32_t* d_ids,
+                           const float* d_weights, int top_k, void* d_y, int64_t y_stride, void* d_scratch,
+                           int64_t scratch_bytes, hipStream_t stream)
+{
     if (dtype != DS_BF16 && dtype != DS_FP16) return DS_ERR_UNSUPPORTED_DTYPE;
     const bool eight = weight_dtype == DS_FP8_E4M3;
     if (weight_dtype != dtype && !eight) return DS_ERR_UNSUPPORTED_DTYPE;
@@ -826,9 +876,12 @@ int ds_moe_experts(int dtype, const void* d_x, int64_t tokens, int64_t dim, int6
     const ds::ExpertsCall call{tokens, (int)dim, (int)hidden, num_experts, top_k, d_x, x_stride, d_w_in, d_w_out,
                                d_w_in_scale, d_w_out_scale, d_ids, d_weights, d_y, y_stride};
     if (ds::experts_workgroups(eight, call) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    const int64_t need = ds::experts_aux_bytes(eight, call);
+    st = check_scratch(d_scratch, scratch_bytes, need, bufs, 8);
+    if (st != DS_OK) return st;
     std::lock_guard<std::mutex> lock(g_mu);
-    char* aux = nullptr;
-    st = get_aux(stream, (size_t)ds::experts_aux_bytes(eight, call), &aux);
+    char* aux = static_cast<char*>(d_scratch);
+    if (!aux) st = get_aux(stream, (size_t)need, &aux);
     if (st != DS_OK) return st;
     return ds::launch_moe_experts(float_kind(dtype), eight, call, aux, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }

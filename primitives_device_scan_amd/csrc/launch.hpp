@@ -142,6 +142,7 @@ struct ExpertsCall {
 int64_t experts_max_assignments();
 int experts_max_experts();
 int64_t experts_aux_bytes(bool eight_bit, const ExpertsCall& call);
+int64_t experts_most_aux_bytes(bool eight_bit, int64_t tokens, int dim, int experts, int hidden, int top_k);
 int64_t experts_workgroups(bool eight_bit, const ExpertsCall& call);  // of the largest launch
 hipError_t launch_moe_experts(ElemKind kind, bool eight_bit, const ExpertsCall& call, char* aux, hipStream_t stream);
 

@@ -1057,12 +1057,14 @@ struct ExpertsPlan {
         in.lds = whole_vectors(c.w_in, c.dim, wbytes) && (!eight_bit || c.hidden % 16 == 0);
         out.lds = whole_vectors(c.w_out, c.hidden, wbytes);
         wide = in.lds && out.lds && n >= kWideTokens * c.experts;
-        chunk = (wide ? 64 : 16) * most;
+        chunk = block_size(wide, most);
         blocks = n > kFindMax ? ExpertsScratch(n, c.experts, c.dim, c.hidden, chunk).blocks : n;
         const int64_t used = n < c.experts ? n : c.experts;  // experts at most; without a plan, other blocks are idle
         choose(in, true, c.hidden, used, eight_bit);
         choose(out, false, c.dim, used, eight_bit);
     }
+
+    static int block_size(bool wide, int most) { return (wide ? 64 : 16) * most; }
 
 private:
     // On average to an expert: 512 tokens, top-6 of 64, 2,048 x 1,408: 346 us wide, 355 not; top-8 of 256: 583 and 490.
@@ -1088,6 +1090,15 @@ int64_t experts_aux_bytes(bool eight_bit, const ExpertsCall& c)
 {
     const ExpertsPlan p(eight_bit, c);
     return ExpertsScratch(c.tokens * c.top_k, c.experts, c.dim, c.hidden, p.chunk).bytes;
+}
+
+// For any alignment of the weights.
+int64_t experts_most_aux_bytes(bool eight_bit, int64_t tokens, int dim, int experts, int hidden, int top_k)
+{
+    const int most = eight_bit ? MostBlocks<fp8>::value : MostBlocks<bf16>::value;
+    const ExpertsScratch narrow(tokens * top_k, experts, dim, hidden, ExpertsPlan::block_size(false, most));
+    const ExpertsScratch wide(tokens * top_k, experts, dim, hidden, ExpertsPlan::block_size(true, most));
+    return narrow.bytes > wide.bytes ? narrow.bytes : wide.bytes;
 }
 
 int64_t experts_workgroups(bool eight_bit, const ExpertsCall& c)
