@@ -342,6 +342,7 @@ __global__ __launch_bounds__(kTileThreads) void token_pass_kernel(const uint32_t
         const uint32_t run = s_count[wave][d[k]];
         if (live && below == 0) s_count[wave][d[k]] = run + (uint32_t)__builtin_popcountll(same);
         rank[k] = run + below;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // the next key's lanes read what these lanes wrote
     }
     __syncthreads();
     uint32_t sum = start;
