@@ -314,7 +314,8 @@ def moe_align(topk_ids: torch.Tensor, num_experts: int, block: int, *, stream=No
     return counts, offsets, sorted_ids
 
 
-# Language-model operators. Their matrices are 2-D tensors whose rows are contiguous; rows may be any distance apart.
+# Language-model operators. Their matrices are 2-D tensors whose rows are contiguous; rows may be any distance apart. They
+# record nothing for autograd and refuse tensors that require grad while it is on; the gradients are calls of their own.
 # Small calls are bound by this code, not by the GPU, so the checks of what is right ask each tensor a few questions and
 # the rest is left to the functions that say what is wrong.
 _FLOATS = {torch.float32: DS_FP32, torch.bfloat16: DS_BF16, torch.float16: DS_FP16}
@@ -366,6 +367,15 @@ def _check_flat(x: torch.Tensor, name: str, dtype, shape, like: torch.Tensor):
         raise ValueError(f"{name} must be on {like.device}")
 
 
+def _refuse_history(*tensors):
+    """These calls record nothing for autograd: a result that looked like any other would lose its gradient."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if getattr(t, "requires_grad", False):
+                raise ValueError("a tensor that requires grad: these calls have no autograd history; detach it or call "
+                                 "them under torch.no_grad(), and use embedding_grad and moe_route_grad for gradients")
+
+
 def _elsewhere(x: torch.Tensor, stream) -> bool:
     """Whether a call on x runs on another stream than the current one of the current device."""
     return stream is not None or x.get_device() != _current_device()
@@ -411,6 +421,7 @@ def embedding(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, out
               stream=None) -> torch.Tensor:
     """scale * table[ids] (int32 or int64 ids of any shape); a row of zeros where an id is no row of the table.
     Returns [*ids.shape, dim]; `out`, if given, is a matrix [ids.numel(), dim] and is returned as it is."""
+    _refuse_history(table, out)
     code = _float_code(table, "table")
     stride = _check_rows(table, "table")
     _check_flat(ids, "ids", _ID_BYTES, None, table)
@@ -442,6 +453,7 @@ def embedding_grad(dout: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: f
     """The gradient of embedding's table [rows, dim] from the gradient dout of its output ([*ids.shape, dim], or
     [ids.numel(), dim] with rows any distance apart). `dtype` is dout's (the default) or float32. accumulate: the sums
     are added to `out`; otherwise every row is written, into `out` if it is given."""
+    _refuse_history(dout, out)
     if not isinstance(dout, torch.Tensor) or dout.dim() < 1:
         raise ValueError("dout must be a GPU tensor")
     if dout.dim() != 2:
@@ -486,6 +498,7 @@ def moe_route(logits: torch.Tensor, top_k: int, *, score: str = "softmax", bias:
     returns (weights float32, ids int32), both [tokens, top_k], best first. weights = scale * score, where score is
     "softmax" over the experts that can be chosen or "sigmoid", with renormalize divided by its sum over the chosen.
     Experts at -inf or NaN cannot be chosen; where fewer than top_k can, the rest is id -1 with weight 0."""
+    _refuse_history(logits, bias)
     code = _float_code(logits, "logits")
     stride = _check_rows(logits, "logits")
     tokens, experts = logits.shape
@@ -512,6 +525,7 @@ def moe_route_grad(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tens
     """The gradient of moe_route's weights with respect to its logits, from the ids it chose and the gradient dweights
     (float32 [tokens, top_k]) of the weights, for the score, bias, renormalize and scale that it had; in the logits'
     dtype."""
+    _refuse_history(logits, dweights, bias)
     code = _float_code(logits, "logits")
     stride = _check_rows(logits, "logits")
     if ids.dim() != 2:
@@ -545,6 +559,7 @@ def moe_experts(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, ids: t
     [experts, dim, hidden] in x's dtype, or float8_e4m3fn with a float32 scale for every block of 128 x 128
     ([experts, ceil(rows / 128), ceil(columns / 128)]); ids int32, weights float32 [tokens, top_k]. Choices outside
     [0, experts) are left out."""
+    _refuse_history(x, w_in, w_out, weights, w_in_scale, w_out_scale, out)
     code = _float_code(x, "x")
     if code == DS_FP32:
         raise TypeError("x must be bfloat16 or float16")
