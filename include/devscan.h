@@ -326,7 +326,8 @@ typedef enum {
  * token, the top_k experts that can be chosen, by s from the largest, equal s
  * by the lower index, to d_ids[t * top_k + j], and scale times their scores
  * (ds_score, of l without the bias; with renormalize 1 divided by the sum of
- * the token's chosen scores, or 0 if that sum is 0) to d_weights. Where fewer
+ * the token's chosen scores, or 0 if that sum is 0: a sigmoid below 2^-150 is 0
+ * in 32 bits) to d_weights. Where fewer
  * than top_k can be chosen the rest is id -1, weight 0, which ds_moe_align and
  * ds_moe_experts drop.
  *   dtype  of the logits: DS_FP32, DS_BF16 or DS_FP16

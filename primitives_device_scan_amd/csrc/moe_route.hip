@@ -70,7 +70,25 @@ __device__ __forceinline__ float key_value(uint32_t k)
 }
 template <int L> __device__ __forceinline__ float group_max(float x) { return key_value(group_max<L>(order_key(x))); }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// By the exponential that does not overflow, so that scores go down to 2^-149.
+__device__ __forceinline__ float sigmoid(float x)
+{
+    const float e = expf(-fabsf(x));
+    return (x >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+
+// Shares of chosen scores, whose largest logit is `top`. Softmax scores are
+// exp(x - top) up to a factor that the division takes away, and so are sigmoid
+// scores where all are small (1 + e^x is 1 in 32 bits), which keeps their bits
+// where the scores themselves run out of them. Below kNoScore a sigmoid rounds
+// to 0 in 32 bits: no share.
+constexpr float kSmallScore = -80.0f;
+constexpr float kNoScore = -103.9721f;  // ln 2^-150
+__device__ __forceinline__ float share_score(float x, float top, bool use_sigmoid)
+{
+    if (use_sigmoid && top >= kSmallScore) return sigmoid(x);
+    return use_sigmoid && top < kNoScore ? 0.0f : expf(x - top);
+}
 
 // exp(x) for the sums over all experts: 2^(x log2 e), off by at most 1.5 |x| +
 // 2 steps of 2^-24, relative (the product's two roundings), where the library
@@ -242,11 +260,14 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
         chosen[j] = x;
         most = x > most ? x : most;
     }
-    if (!use_sigmoid && renorm) top = group_max<L>(most);
+    if (renorm) top = group_max<L>(most);
     float sum = 0.0f;
     for (int j = lane; j < top_k; j += L) {
         const float x = chosen[j];
-        const float p = choice[j] == kNone ? 0.0f : use_sigmoid ? sigmoid(x) : expf(x - top);
+        const float p = choice[j] == kNone ? 0.0f
+                        : renorm           ? share_score(x, top, use_sigmoid)
+                        : use_sigmoid      ? sigmoid(x)
+                                           : expf(x - top);
         chosen[j] = p;
         sum += p;
     }
@@ -264,16 +285,16 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
 // ---------------------------------------------------------------------------
 // The gradient with respect to the logits, for given ids and d loss / d w:
 // the scores are computed again from the logits, then the chain rule goes
-// through the division by the chosen scores' sum and through the scores. For
-// softmax with renorm the two give w_j = softmax of the chosen logits alone and
-//   d / d l_e = sum over j with ids[j] = e of w_j (dw_j - sum_i w_i dw_i):
-// the other logits are not read (they have no part, however much larger they
-// are) and get 0. The chosen experts' parts are added up in LDS, choice by
+// through the division by the chosen scores' sum and through the scores. With
+// renorm the two give
+//   d / d l_e = sum over j with ids[j] = e of w_j (dw_j - sum_i w_i dw_i),
+// times 1 - sigmoid(l_e) for sigmoid scores: the other logits are not read
+// (they have no part, however much larger they are) and get 0. The chosen experts' parts are added up in LDS, choice by
 // choice, so an expert that is named twice has its parts added in their order.
 // The bias is the router's: it says which experts can be chosen, no more.
 // Bound by memory: 65,536 tokens of 256 experts in fp32, top-8: softmax 19.9 us
 // with renorm (the rows written and a line per chosen logit), 25.7 us without
-// (138 MB at 5.4 TB/s; 51 us with a wave to a token); sigmoid 19.8-20.1.
+// (138 MB at 5.4 TB/s; 51 us with a wave to a token); sigmoid 19.9-20.2.
 // ---------------------------------------------------------------------------
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __restrict__ logits, int64_t tokens,
@@ -322,7 +343,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
         }
     }
     float top = neg_inf();
-    if (!use_sigmoid && renorm) {
+    if (renorm) {
 #pragma unroll
         for (int m = 0; m < M; ++m) top = chosen[m] > top ? chosen[m] : top;  // false for NaN
         top = group_max<L>(top);
@@ -353,13 +374,15 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
         total = group_sum<L>(total);
         total = total > 0.0f || total != total ? 1.0f / total : 0.0f;
     }
-    // the chosen scores; softmax with renorm: up to a factor that the division by their sum takes away
+    // the chosen scores; with renorm as share_score gives them
     float sum = 0.0f, dot = 0.0f;
 #pragma unroll
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
             if (id[m] >= 0)
-                q[m] = use_sigmoid ? sigmoid(chosen[m]) : renorm ? expf(chosen[m] - top) : exp_sum(chosen[m] - top) * total;
+                q[m] = renorm        ? share_score(chosen[m], top, use_sigmoid)
+                       : use_sigmoid ? sigmoid(chosen[m])
+                                     : exp_sum(chosen[m] - top) * total;
             sum += q[m];
             dot += dw[m] * q[m];
         }
@@ -380,8 +403,8 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
             float d = dw[m];
-            if (use_sigmoid) d *= sigmoid_slope(chosen[m]);
-            else if (renorm) d *= q[m];
+            if (renorm) d *= use_sigmoid ? q[m] / (1.0f + expf(chosen[m])) : q[m];  // d log sigmoid = 1 - sigmoid
+            else if (use_sigmoid) d *= sigmoid_slope(chosen[m]);
             all += dw[m] * q[m];
             for (int i = 0; i < L && m * L + i < top_k; ++i)
                 if (lane == i && id[m] >= 0)

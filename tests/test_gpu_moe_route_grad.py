@@ -126,3 +126,18 @@ def test_gradient_against_differences_of_the_router(score, renorm, biased):
     most = np.abs(mo.f64(dw)).sum(1)
     bound = 20 * step ** 2 * most * np.abs(mo.f64(d)).max(1) ** 3 + mo.route_terms(l) * mo.U * most / step
     assert bool((np.abs(slope - (grad * moved).sum(1) / (2 * step)) <= bound).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("low", [-80.0, -87.0, -89.0, -95.0, -102.0])
+def test_renormalised_sigmoid_scores_of_very_negative_logits(dtype, low):
+    # scores down to 2^-149 are numbers of 32 bits, and their shares are held relative to the largest
+    l = (low + normal(7, (20, 48)).clamp(-1, 1)).to(dtype)
+    w, ids = ds.moe_route(l.cuda(), 6, score="sigmoid", renormalize=True, scale=2.5)
+    _, want = check(l, ids.cpu(), "sigmoid", True, 2.5, what=f"sigmoid around {low}")
+    mo.within(w, want, mo.route_terms(l) * mo.U * np.abs(want), "weights")
+    # below half of that they are 0, and so are the weights and their gradient
+    l = torch.full((3, 9), -104.5, dtype=dtype)
+    w, ids = ds.moe_route(l.cuda(), 4, score="sigmoid", renormalize=True)
+    got = ds.moe_route_grad(l.cuda(), ids, torch.ones_like(w), score="sigmoid", renormalize=True)
+    assert ids.tolist() == [[0, 1, 2, 3]] * 3 and not bool(w.any()) and not bool(got.any())
