@@ -90,10 +90,27 @@ __device__ __forceinline__ float share_score(float x, float top, bool use_sigmoi
     return use_sigmoid && top < kNoScore ? 0.0f : expf(x - top);
 }
 
-// exp(x) for the sums over all experts: 2^(x log2 e), off by at most 1.5 |x| +
-// 2 steps of 2^-24, relative (the product's two roundings), where the library
-// function takes five times the instructions; 0 below 2^-126.
+// exp(x) for the router's sum over all experts: 2^(x log2 e), off by at most
+// 1.5 |x| + 2 steps of 2^-24, relative (the product's two roundings), where the
+// library function takes five times the instructions; 0 below 2^-126. In a sum
+// that has a term of 1 that is at most a step per term.
 __device__ __forceinline__ float exp_sum(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+
+// exp(x) for the gradient, x <= 0, where it is each element's own factor: what
+// the product x log2 e loses, and log2 e as a float, is put back, since 2^(t + r)
+// = 2^t (1 + r ln 2) for small r: 3 steps. Where the gradient is rounded to 16
+// bits, exp_sum: its 130 steps at most are a thirtieth of that rounding in fp16,
+// less in bf16. (65,536 tokens of 256 experts, no renormalising: fp32 25.7 us
+// with exp_sum, 26.6 with this; bf16 15.9 and 17.4.)
+template <typename T>
+__device__ __forceinline__ float exp_factor(float x)
+{
+    if constexpr (sizeof(T) == 2) return exp_sum(x);
+    x = x < -200.0f ? -200.0f : x;  // 0 all the same, and t stays finite
+    const float t = x * 1.44269504f, r = __builtin_fmaf(x, 1.925963e-8f, __builtin_fmaf(x, 1.44269504f, -t));
+    const float p = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(p, r * 0.693147181f, p);
+}
 
 // sigmoid(x) (1 - sigmoid(x)) without the difference from 1, which loses its
 // digits for large x; 0 at both infinities.
@@ -293,8 +310,8 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
 // choice, so an expert that is named twice has its parts added in their order.
 // The bias is the router's: it says which experts can be chosen, no more.
 // Bound by memory: 65,536 tokens of 256 experts in fp32, top-8: softmax 19.9 us
-// with renorm (the rows written and a line per chosen logit), 25.7 us without
-// (138 MB at 5.4 TB/s; 51 us with a wave to a token); sigmoid 19.9-20.2.
+// with renorm (the rows written and a line per chosen logit), 26.6 us without
+// (138 MB at 5.2 TB/s; 51 us with a wave to a token); sigmoid 19.9-20.2.
 // ---------------------------------------------------------------------------
 template <typename T, int L, int NV>
 __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __restrict__ logits, int64_t tokens,
@@ -368,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
         for (int v = 0; v < NV; ++v)
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                l[v][j] = l[v][j] > neg_inf() ? exp_sum(l[v][j] - top) : 0.0f;
+                l[v][j] = l[v][j] > neg_inf() ? exp_factor<T>(l[v][j] - top) : 0.0f;
                 total += l[v][j];
             }
         total = group_sum<L>(total);
@@ -382,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
             if (id[m] >= 0)
                 q[m] = renorm        ? share_score(chosen[m], top, use_sigmoid)
                        : use_sigmoid ? sigmoid(chosen[m])
-                                     : exp_sum(chosen[m] - top) * total;
+                                     : exp_factor<T>(chosen[m] - top) * total;
             sum += q[m];
             dot += dw[m] * q[m];
         }

@@ -141,3 +141,17 @@ def test_renormalised_sigmoid_scores_of_very_negative_logits(dtype, low):
     w, ids = ds.moe_route(l.cuda(), 4, score="sigmoid", renormalize=True)
     got = ds.moe_route_grad(l.cuda(), ids, torch.ones_like(w), score="sigmoid", renormalize=True)
     assert ids.tolist() == [[0, 1, 2, 3]] * 3 and not bool(w.any()) and not bool(got.any())
+
+
+def test_gradient_of_small_scores_keeps_32_bits():
+    # Multiples of 1/16: every difference from the largest logit is exact, so only the exponentials (4 steps each way),
+    # the sum of 8 scores and 16 products, quotients and differences count: 8 + 2 * 4 + 16 steps, relative. Few choices,
+    # the largest expert's: its weight's gradient is p_e (0 - p_0), with p_0 next to 1.
+    l = torch.randint(-80 * 16, -20 * 16, (4000, 8), generator=torch.Generator().manual_seed(6)) / 16.0
+    l[:, 0] = 0.0
+    ids = torch.zeros(4000, 1, dtype=torch.int32)
+    got = mo.f64(ds.moe_route_grad(l.cuda(), ids.cuda(), torch.ones(4000, 1).cuda(), renormalize=False))[:, 1:]
+    _, ref, _, _ = ro.weights_and_grad(f32(l), None, ids.numpy(), np.ones((4000, 1)), "softmax", False, 1.0)
+    worst = (np.abs(got - ref[:, 1:]) / np.abs(ref[:, 1:])).max() / mo.U
+    say("small scores: off by %.1f steps" % worst)
+    assert worst <= 32
