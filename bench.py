@@ -32,8 +32,9 @@ seeded (datagen). Prints one JSON line:
 Other modes (their own JSON line): --ceiling (the access-pattern table:
 read, write, copy and read-all/write-half at 4 to 112 KiB per workgroup,
 contiguous and 4 KiB-interleaved, warm and cold), --tile-lds (the pages' LDS
-block-scan experiment), --profile-only [--cold] [--pattern ...] (launches
-without timing, for rocprofv3).
+block-scan experiment), --operators [NAME,...] (the cases of
+perf/operators.py through the library), --profile-only [--cold]
+[--pattern ...] [--operators ...] (launches without timing, for rocprofv3).
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--no-compact] [--no-sort]
 """
@@ -227,6 +228,60 @@ def tile_lds_experiment(args):
     print(json.dumps({"mode": "tile_lds", "n": n, "dtype": "fp32", "tile": 4096, "threads": 1024,
                       "copy_us": round(copy_ms * 1e3, 1), "copy_gbs": round(copy_gbs, 1), "rows": rows,
                       "lookback_scan_us_same_input": round(lb_ms * 1e3, 1)}), flush=True)
+
+
+def operators_experiment(args):
+    """The language-model operators: the cases of perf/operators.py (all, or
+    those named) through the library. A case's time is the median of five runs
+    of --steps passes, on three prepared inputs in turn, one event pair around a
+    run; bytes and operations are what the case cannot do without (its `work`).
+    --profile-only: nine passes per case, an erfinv kernel before and after
+    them, nothing timed."""
+    import importlib.util
+    import statistics
+
+    import torch
+
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    ops = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ops)
+    ops.own = True
+    cases = [c for c in ops.listed() if args.operators == "all" or c["name"] in args.operators.split(",")]
+    if not cases:
+        print(f"--operators: no case is named {args.operators}", file=sys.stderr)
+        sys.exit(2)
+    torch.cuda.set_device(0)
+    mark = torch.zeros(8, device="cuda")
+    rows = []
+    for c in cases:
+        states = [ops.prepare(c, seed) for seed in range(3)]
+        for s in states * 3:
+            ops.run(s)
+        torch.cuda.synchronize()
+        log(f"{c['name']}")
+        if args.profile_only:
+            mark.erfinv_()
+            for s in states * 3:
+                ops.run(s)
+            mark.erfinv_()
+            torch.cuda.synchronize()
+            continue
+        times = []
+        for _ in range(5):
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            begin.record()
+            for i in range(args.steps):
+                ops.run(states[i % 3])
+            end.record()
+            end.synchronize()
+            times.append(begin.elapsed_time(end) * 1e3 / args.steps)
+        us, work = statistics.median(times), ops.work(c)
+        rows.append({"case": c["name"], "us": round(us, 2), "gbs": round(work["bytes"] / us * 1e-3, 1),
+                     "tflops": round(work["flops"] / us * 1e-6, 3)})
+        del states
+        torch.cuda.empty_cache()
+    if not args.profile_only:
+        print(json.dumps({"mode": "operators", "steps": args.steps, "data": "synthetic", "rows": rows}), flush=True)
 
 
 def ceiling_experiment(args):
@@ -424,6 +479,9 @@ def main():
                     help="the pages' LDS block-scan experiment instead of the main bench (own JSON line)")
     ap.add_argument("--ceiling", action="store_true",
                     help="the access-pattern ceiling table instead of the main bench (own JSON line)")
+    ap.add_argument("--operators", nargs="?", const="all", default=None, metavar="NAME,...",
+                    help="the language-model operators' cases (all, or those named) instead of the main bench (own "
+                         "JSON line); with --profile-only their launches alone")
     ap.add_argument("--cold", action="store_true",
                     help="with --profile-only: a 1 GiB read before every scan launch (the cold protocol)")
     ap.add_argument("--algo", default="default",
@@ -447,6 +505,8 @@ def main():
         return tile_lds_experiment(args)
     if args.ceiling:
         return ceiling_experiment(args)
+    if args.operators:
+        return operators_experiment(args)
     if args.profile_only and args.pattern:
         return profile_pattern(args)
     if args.profile_only and args.workload == "radix":
