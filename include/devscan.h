@@ -366,11 +366,14 @@ int ds_moe_route_grad(int dtype, const void* d_logits, int64_t tokens, int num_e
  * step): y[t] = sum over j < top_k of d_weights[t, j] * w_out[e] h, with
  * e = d_ids[t, j] and h = silu(w_in[e][0 .. hidden) x[t]) * (w_in[e][hidden ..
  * 2 hidden) x[t]); choices outside [0, num_experts) are left out. A used
- * expert's weights are streamed once for up to 64 of its tokens (128 or 256
- * where experts have 32 or more on average); all products are summed in 32
- * bits. The down products take h in `dtype`: as its rounded value and the
- * rounded rest for an expert of up to eight tokens, the rounded value alone
- * otherwise (so in fp16 an h above 65,504 becomes infinite).
+ * expert's weights are streamed once for every 64 of its tokens (8-bit weights:
+ * 32); for every 32 (16) where there are few workgroups, or rows that do not
+ * start on 16-byte boundaries; for every 256 (128) where experts have 32 or
+ * more tokens on average. All products are summed in 32 bits. The down products
+ * take h in `dtype`: as its rounded value and the rounded rest for an expert of
+ * up to eight tokens in the call, the rounded value alone otherwise, so a
+ * token's last bits go by how many tokens its experts have. In fp16 an h above
+ * 65,504 becomes infinite.
  *   dtype         DS_BF16 or DS_FP16, of x [tokens, dim] and y [tokens, dim]
  *   weight_dtype  dtype, or DS_FP8_E4M3 with scales
  *   d_w_in        [num_experts, 2 * hidden, dim], contiguous

@@ -22,9 +22,12 @@
 // kept as its rounded value and the rounded rest, and a token has two columns
 // in the down products. That costs nothing for an expert of up to eight tokens
 // (blocks are 16 columns wide, and the weights' bytes bound these products); an
-// expert of more, and all where a workgroup's waves split an expert's tokens,
-// take the rounded values alone (both halves for up to 32 tokens made the down
-// products of 256 tokens, top-8 of 256, 5% slower).
+// expert of more takes the rounded values alone. A relative error of 0.0016
+// becomes one of 0.0021-0.0024 in bf16 (whose own rounding is 0.0016), and a
+// token's last bits go by how many tokens its expert has. Both halves for every
+// token were measured: 256 tokens, top-8 of 256, 2,048 x 768: 400 -> 415 us; 64,
+// top-6 of 64, 2,048 x 1,408 in e4m3: 107 -> 125; 512, top-2 of 8, 4,096 x 2,048:
+// 253 -> 286; 300, top-2 of 20, 1,000 x 777: 61 -> 77.
 // Measured: 256 tokens, top-8 of 256, 2,048 x 768 in bf16: gate/up 254-259 us
 // (1.50 GB at 5.8-5.9 TB/s; 1.56 GB are fetched, as crowded experts' weights are
 // read again), down 137-139 (0.75 GB at 5.4-5.5), plan and sum 5 each. 64
@@ -895,7 +898,7 @@ struct WideProduct {
     }
 };
 
-template <typename X, typename W, int TT, bool GATED>
+template <typename X, typename W, int TT, bool GATED, bool SPLIT>
 __device__ __forceinline__ void expert_wide(const ExpertArgs& a, int expert, const uint16_t* list, int first, int count,
                                             int group, char* s_mem)
 {
@@ -906,13 +909,13 @@ __device__ __forceinline__ void expert_wide(const ExpertArgs& a, int expert, con
     clear_sums(acc);
     int assign[TT];
     const X* tok[TT];
-    find_columns<X, TT, GATED, false>(a, list, first + wave * 16 * TT, count, lane, assign, tok);
+    find_columns<X, TT, GATED, SPLIT>(a, list, first + wave * (SPLIT ? 8 : 16) * TT, count, lane, assign, tok);
     const Tiles<W, 4, GATED, true> t(a, expert, row0, lane);
     const W* tile = wave == 0 ? t.tile[0] : wave == 1 ? t.tile[1] : wave == 2 ? t.tile[2] : t.tile[3];
     const int last = wave == 0 ? t.last[0] : wave == 1 ? t.last[1] : wave == 2 ? t.last[2] : t.last[3];
     WideProduct<X, W, TT> p(tile, last, a.depth, tok, t.sc, (lds_char*)s_mem, lane, wave);
     p.run(a.depth / Stage<W, 4>::kSegVals, acc);
-    write_results<X, 4, TT, GATED, false>(a, assign, row0, lane, acc);
+    write_results<X, 4, TT, GATED, SPLIT>(a, assign, row0, lane, acc);
 }
 
 // Blocks of 16 tokens that a wave holds at once, as registers allow (256 at two
@@ -926,6 +929,8 @@ template <typename W, int RT = 4> struct MostBlocks {
 // over the whole depth (kStream); all waves on one tile set, each with a part of
 // the depth (kParts) or of the tokens (kWide).
 enum ExpertMode { kStream, kParts, kWide };
+
+constexpr int kSplitTokens = 8;  // of an expert, at most, for h in two halves: a block of 16 columns
 
 template <typename X, typename W, bool GATED, ExpertMode MODE, bool LDS>
 __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
@@ -950,15 +955,20 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
         if (f.count == 0) return;
         list = s_list;
     }
+    // halves of h for all tokens of an expert or for none, whatever their order in the list
+    const bool split = !GATED && f.all && f.count <= kSplitTokens;
     if constexpr (MODE == kWide) {
+        if constexpr (!GATED) {
+            if (split) return expert_wide<X, W, 1, GATED, true>(a, f.expert, list, 0, f.count, slice, s_mem);
+        }
         for (int first = 0; first < f.count; first += 64 * kMost) {
             const int left = f.count - first;
             if (left > 32 * kMost)
-                expert_wide<X, W, kMost, GATED>(a, f.expert, list, first, f.count, slice, s_mem);
+                expert_wide<X, W, kMost, GATED, false>(a, f.expert, list, first, f.count, slice, s_mem);
             else if (kMost > 2 && left > 64)
-                expert_wide<X, W, kMost / 2, GATED>(a, f.expert, list, first, f.count, slice, s_mem);
+                expert_wide<X, W, kMost / 2, GATED, false>(a, f.expert, list, first, f.count, slice, s_mem);
             else
-                expert_wide<X, W, 1, GATED>(a, f.expert, list, first, f.count, slice, s_mem);
+                expert_wide<X, W, 1, GATED, false>(a, f.expert, list, first, f.count, slice, s_mem);
         }
     } else {
         int first = 0;
@@ -970,8 +980,7 @@ __global__ __launch_bounds__(kThreads, 2) void expert_kernel(ExpertArgs a)
         constexpr std::integral_constant<int, kMost> most{};
         constexpr std::integral_constant<int, kMiddle> middle{};
         if constexpr (!GATED) {
-            // halves for all tokens of an expert or for none, whatever their order in the list
-            if (f.all && f.count <= 8) return pass(std::integral_constant<int, 1>{}, std::true_type{});
+            if (split) return pass(std::integral_constant<int, 1>{}, std::true_type{});
         }
         for (; f.count - first > (kMost > 1 ? 8 * kMost : 0); first += 16 * kMost) pass(most, std::false_type{});
         if constexpr (kMost > 1) {
