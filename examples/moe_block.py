@@ -3,9 +3,10 @@
     python examples/moe_block.py [--tokens 64] [--steps 20]
 
 The decoding step looks the tokens up, routes them and runs the experts. The training step trains the router and the
-table (the experts are frozen): the gradient of the routing weights goes back through the router to its matrix and to
-the token embeddings, whose rows are accumulated in 32 bits over micro-batches. Weights and tokens are random; the
-router's own product is a plain matrix product and left to torch.
+table by a loss of the routing weights alone, as a router is distilled or balanced: its gradient goes back through the
+router to its matrix and to the token embeddings, whose rows are accumulated in 32 bits over micro-batches. (A loss of
+the experts' output has a path through the experts too, and there is no backward pass of theirs here.) Weights, tokens
+and d loss / d weights are random; the router's own product is a plain matrix product and left to torch.
 """
 from __future__ import annotations
 
@@ -48,7 +49,8 @@ def decode_step(block: Block, ids: torch.Tensor):
 
 
 def train_step(block: Block, ids: torch.Tensor, weight_grad: torch.Tensor):
-    """Adds a micro-batch's gradients to the block's, for d loss / d weights = weight_grad [tokens, top_k]."""
+    """Adds a micro-batch's gradients to the block's, for a loss of the routing weights with d loss / d weights =
+    weight_grad [tokens, top_k]."""
     x = ds.embedding(block.table, ids, scale=block.scale)
     logits = x.float() @ block.router
     _, chosen = ds.moe_route(logits, block.top_k)

@@ -4,10 +4,10 @@
 //   out[i] = scale * table[ids[i]]                 (zero where ids[i] is no row)
 //   grad[v] = scale * sum over i with ids[i] = v of dout[i]    (+ grad[v])
 //
-// Up to 128 tokens the gradient is one launch. Above, it goes by sorted tokens: the positions i are put in order of
-// their token (equal tokens in input order), so that each row's terms are
-// consecutive, and are then summed in that order: no atomics on the sums, and
-// the same bits on every run.
+// Up to 128 tokens the gradient is one launch. Above, it goes by sorted tokens:
+// the positions i are put in order of their token (equal tokens in input
+// order), so that each row's terms are consecutive, and are then summed in that
+// order: no atomics on the sums, and the same bits on every run.
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -681,7 +681,10 @@ __global__ __launch_bounds__(kThreads) void embedding_few_kernel(const ID* __res
 // chunks that it reaches. kJoinAhead parts are in flight: a frequent token
 // fills hundreds of chunks, most runs two. (A workgroup per item, the parts
 // split over its waves, took twice as long: most items are short, and it is
-// their number that counts.)
+// their number that counts.) A row that has all tokens is one such chain, and
+// its terms come in one wave per 128 columns: 65,536 tokens of 256 columns take
+// 107 us then, 81 with half of them on one row, 49 spread over 50,000 rows;
+// 1,000,003 tokens 1,290, 790 and 280.
 constexpr int kJoinCols = 2;
 constexpr int kJoinAhead = 16;
 

@@ -28,11 +28,11 @@
 // token were measured: 256 tokens, top-8 of 256, 2,048 x 768: 400 -> 415 us; 64,
 // top-6 of 64, 2,048 x 1,408 in e4m3: 107 -> 125; 512, top-2 of 8, 4,096 x 2,048:
 // 253 -> 286; 300, top-2 of 20, 1,000 x 777: 61 -> 77.
-// Measured: 256 tokens, top-8 of 256, 2,048 x 768 in bf16: gate/up 254-259 us
-// (1.50 GB at 5.8-5.9 TB/s; 1.56 GB are fetched, as crowded experts' weights are
-// read again), down 137-139 (0.75 GB at 5.4-5.5), plan and sum 5 each. 64
-// tokens, top-6 of 64, 2,048 x 1,408 in e4m3: 62-66 us (344 MB at 5.2-5.6 TB/s)
-// and 36-37 (172 MB at 4.6-4.8).
+// Measured: 256 tokens, top-8 of 256, 2,048 x 768 in bf16: gate/up 246-252 us
+// (1.50 GB at 6.0-6.1 TB/s; 1.56 GB are fetched, as crowded experts' weights are
+// read again), down 135-138 (0.75 GB at 5.4-5.6), plan and sum 5 each. 64
+// tokens, top-6 of 64, 2,048 x 1,408 in e4m3: 58-65 us (344 MB at 5.3-5.9 TB/s)
+// and 35-36 (172 MB at 4.7-4.9).
 #include "device_scan.hpp"
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -780,9 +780,10 @@ __device__ __forceinline__ void expert_block(const ExpertArgs& a, int expert, co
 // split the tokens, 16 * TT to a wave. The stages of the weights are shared: a
 // wave loads one tile of each, three stages make the ring, and a barrier per
 // stage says that all tiles of it are there and that the stage that is to be
-// overwritten is done with. 512 tokens, top-2 of 8, 4,096 x 2,048 in bf16: 215
-// us against 388 with 64 tokens to a workgroup; the tokens' values, which every
-// workgroup reads from the L2, bound it.
+// overwritten is done with. 512 tokens, top-2 of 8, 4,096 x 2,048 in bf16: 178
+// us where the experts have equal shares, 247-253 where the r-th has 1 / r of the
+// first's (225 for half the tokens with 64 to a workgroup, 154 with this); the
+// tokens' values, which every workgroup reads from the L2, bound it.
 // ---------------------------------------------------------------------------
 constexpr int kWideRing = 3;
 constexpr int kWideOps = kDmaOps / kWaves;  // loads of a wave per stage
@@ -1076,7 +1077,10 @@ struct ExpertsPlan {
     static int block_size(bool wide, int most) { return (wide ? 64 : 16) * most; }
 
 private:
-    // On average to an expert: 512 tokens, top-6 of 64, 2,048 x 1,408: 346 us wide, 355 not; top-8 of 256: 583 and 490.
+    // Assignments to an expert on average. In 16 bits: 48 (512 tokens, top-6 of 64, 2,048 x 1,408) 327 us wide and 455
+    // not; 24 (256 of these) 287 and 297; 16 (512 tokens, top-8 of 256, 2,048 x 768) 567 and 473; 32 (1,024 of these)
+    // 641 and 586, but 32 of few experts (128 tokens, top-2 of 8, 4,096 x 2,048) 120 and 127. In 8 bits the two meet at
+    // 64 for many experts (308 and 304; 48: 268 and 250), at 16 for few (66 and 67; 32: 87 and 116). 32 is between.
     static constexpr int64_t kWideTokens = 32;
 
     static bool whole_vectors(const void* w, int depth, int wbytes)
