@@ -306,8 +306,9 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(const T* __restrict
 // renorm the two give
 //   d / d l_e = sum over j with ids[j] = e of w_j (dw_j - sum_i w_i dw_i),
 // times 1 - sigmoid(l_e) for sigmoid scores: the other logits are not read
-// (they have no part, however much larger they are) and get 0. The chosen experts' parts are added up in LDS, choice by
-// choice, so an expert that is named twice has its parts added in their order.
+// (they have no part, however much larger they are) and get 0. The chosen
+// experts' parts are added up in LDS, choice by choice, so an expert that is
+// named twice has its parts added in their order.
 // The bias is the router's: it says which experts can be chosen, no more.
 // Bound by memory: 65,536 tokens of 256 experts in fp32, top-8: softmax 19.9 us
 // with renorm (the rows written and a line per chosen logit), 26.6 us without
@@ -401,15 +402,20 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
                        : use_sigmoid ? sigmoid(chosen[m])
                                      : exp_factor<T>(chosen[m] - top) * total;
             sum += q[m];
-            dot += dw[m] * q[m];
         }
-    if (renorm) {
+    if (renorm) {  // shares, and dw less its mean over them; the sum may be too small for dw to be divided by it
         sum = group_sum<L>(sum);
         sum = sum > 0.0f || sum != sum ? sum : 1.0f;
-        dot = group_sum<L>(dot) / sum;
 #pragma unroll
         for (int m = 0; m < M; ++m)
-            if (id[m] >= 0) dw[m] = (dw[m] - dot) / sum;
+            if (m * L < top_k) {
+                q[m] /= sum;
+                dot += dw[m] * q[m];
+            }
+        dot = group_sum<L>(dot);
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+            if (id[m] >= 0) dw[m] -= dot;
     }
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -420,7 +426,7 @@ __global__ __launch_bounds__(kThreads) void moe_route_grad_kernel(const T* __res
     for (int m = 0; m < M; ++m)
         if (m * L < top_k) {
             float d = dw[m];
-            if (renorm) d *= use_sigmoid ? q[m] / (1.0f + expf(chosen[m])) : q[m];  // d log sigmoid = 1 - sigmoid
+            if (renorm) d *= use_sigmoid ? q[m] / (1.0f + expf(chosen[m])) : q[m];  // 1 - sigmoid: d log sigmoid
             else if (use_sigmoid) d *= sigmoid_slope(chosen[m]);
             all += dw[m] * q[m];
             for (int i = 0; i < L && m * L + i < top_k; ++i)

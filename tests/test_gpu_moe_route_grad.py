@@ -155,3 +155,15 @@ def test_gradient_of_small_scores_keeps_32_bits():
     worst = (np.abs(got - ref[:, 1:]) / np.abs(ref[:, 1:])).max() / mo.U
     say("small scores: off by %.1f steps" % worst)
     assert worst <= 32
+
+
+@pytest.mark.parametrize("low", [-20.0, -60.0, -79.0])
+def test_large_weight_gradients_of_small_sigmoid_scores(low):
+    # the scores' sum is as small as 2^-115: a share, not dw, is divided by it
+    l = low + normal(11, (20, 48)).clamp(-1, 1)
+    _, ids = ds.moe_route(l.cuda(), 6, score="sigmoid")
+    dw = normal(12, (20, 6)) * 2.0 ** 20
+    got = ds.moe_route_grad(l.cuda(), ids, dw.cuda(), score="sigmoid")
+    n = ids.cpu().numpy()
+    _, ref, size, spread = ro.weights_and_grad(f32(l), None, n, mo.f64(dw), "sigmoid", True, 1.0)
+    mo.within(got, ref, ro.grad_bound(ref, size, spread, n, l.dtype, True, "sigmoid"), f"around {low}")
