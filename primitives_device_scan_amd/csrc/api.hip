@@ -28,13 +28,15 @@ namespace {
 using ds::Ctrl;
 using ds::DevWs;
 
-// Workspace layout: [Ctrl][status: one 128-byte line per tile][totals: 8 B per
-// tile]; `aux` is a separate scratch buffer for the counting-sort tables.
+// An earlier buffer of a workspace that graphs hold.
 struct Retired {
     char* p;
     int64_t tiles;  // of a `base`; 0 for an `aux`
 };
 
+// Workspace layout: [Ctrl][status: one 128-byte line per tile][totals: 8 B per
+// tile]; `aux` is a separate scratch buffer, for the counting-sort tables and
+// for what ds_embedding_grad and ds_moe_experts keep between their launches.
 struct Workspace {
     char* base = nullptr;
     int64_t tile_cap = 0;
@@ -43,7 +45,7 @@ struct Workspace {
     char* aux = nullptr;
     size_t aux_cap = 0;
     bool aux_captured = false;    // some graph holds the address of aux
-    std::vector<Retired> retired; // earlier buffers that graphs hold, freed by ds_release_workspace
+    std::vector<Retired> retired; // freed by ds_release_workspace
 };
 
 std::mutex g_mu;
