@@ -32,10 +32,9 @@ DS_ERR_STREAM_CAPTURING = 8
 EXPORTS = ["scan_exclusive", "scan_inclusive", "ds_scan", "ds_scan_seeded", "ds_scan_noalloc", "compact_if",
            "ds_compact_unordered", "ds_radix_pass", "ds_moe_align", "ds_embedding", "ds_embedding_grad",
            "ds_embedding_grad_scratch", "ds_embedding_grad_scratch_bytes", "ds_moe_experts_scratch",
-           "ds_moe_experts_scratch_bytes",
-           "ds_moe_route", "ds_moe_route_grad", "ds_moe_route_grad_biased", "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan",
-           "ds_tile_pipeline",
-           "ds_tile_elems", "ds_scan_tile_elems", "ds_query_timeout", "ds_fail_next_allocations", "ds_set_spin_limit",
+           "ds_moe_experts_scratch_bytes", "ds_moe_route", "ds_moe_route_grad", "ds_moe_route_grad_biased",
+           "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan", "ds_tile_pipeline", "ds_tile_elems",
+           "ds_scan_tile_elems", "ds_query_timeout", "ds_fail_next_allocations", "ds_set_spin_limit",
            "ds_status_string", "ds_release_workspace", "ds_version"]
 TILE_OF = {"scan_exclusive": 0, "scan_inclusive": 1, "three_pass": 2, "compact": 3, "lds_tile_scan": 4,
            "counting_sort": 5, "counting_sort_values": 6, "moe_align": 7}
