@@ -404,6 +404,133 @@ int ds_moe_experts_scratch(int dtype, const void* d_x, int64_t tokens, int64_t d
                            int64_t scratch_bytes, hipStream_t stream);
 
 /*
+ * Operators on ragged batches: what a prefix sum over lengths or counts serves
+ * in a language model. Matrices, sums and errors as for the operators above;
+ * offsets and lengths are read on the device, so no call waits for the host.
+ */
+
+/* Gate of the gated recurrence. */
+typedef enum {
+    DS_GATE_DECAY = 0,  /* a = g, of magnitude at most 1 */
+    DS_GATE_LOG = 1,    /* a = exp(g), g at most 0 */
+    DS_GATE_SIGMOID = 2 /* a = 1 / (1 + exp(-g)) */
+} ds_gate;
+
+/*
+ * Gated linear recurrence over packed sequences, channel by channel:
+ * h_t = a_t h_{t-1} + b_t, with a_t from the gate g_t (ds_gate) and b_t = x_t, or
+ * (1 - a_t) x_t with mix 1. Sequence s holds the rows [d_offsets[s],
+ * d_offsets[s + 1]) of the matrices and starts from d_initial[s] (d_initial
+ * NULL: 0); h after its last row goes to d_final[s] unless d_final is NULL (an
+ * empty sequence passes its initial state on). Rows before d_offsets[0] and from
+ * d_offsets[sequences] on are neither read nor written. d_offsets NULL: one
+ * sequence of all rows.
+ *   dtype      DS_FP32, DS_BF16 or DS_FP16, of d_gate, d_x and d_h [tokens, dim]
+ *   d_offsets  sequences + 1 offsets that do not decrease (others are cut to
+ *              [0, tokens]; what is computed then is not defined)
+ *   d_initial, d_final  [sequences, dim] in fp32, contiguous
+ * States are held in 32 bits and rounded as they are written to d_h; a gate near
+ * 1 keeps 1 - a to 32 bits. Gates of magnitude above 1 may overflow products
+ * over many steps; once a state is infinite or NaN so are the later ones of its
+ * sequence and channel. d_scratch: as in ds_embedding_grad_scratch, of at least
+ * ds_gated_scan_scratch_bytes(dtype, tokens, dim) bytes; NULL: the stream's
+ * workspace. tokens, dim, sequences < 2^31 (else DS_ERR_TOO_LARGE).
+ */
+int64_t ds_gated_scan_scratch_bytes(int dtype, int64_t tokens, int64_t dim);
+int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride,
+                  int64_t tokens, int64_t dim, const int32_t* d_offsets, int64_t sequences, int form, int mix,
+                  const float* d_initial, void* d_h, int64_t h_stride, float* d_final, void* d_scratch,
+                  int64_t scratch_bytes, hipStream_t stream);
+
+/*
+ * Gradient of ds_gated_scan, from its states d_h as it wrote them and the
+ * gradients d_dh of them and d_dfinal of the last ones (NULL: 0). With
+ * G_t = dh_t + a_{t+1} G_{t+1} (plus dfinal at a sequence's last row):
+ * dx_t = G_t, or (1 - a_t) G_t with mix; dgate_t = G_t (h_{t-1}, or
+ * h_{t-1} - x_t with mix) da/dg; dinitial = a G of the first row (an empty
+ * sequence's is its dfinal). d_x is read with mix alone and may else be NULL;
+ * d_dinitial may be NULL. Rows outside the sequences are not written. Other
+ * arguments and the scratch as ds_gated_scan.
+ */
+int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const void* d_h, int64_t h_stride,
+                       const void* d_dh, int64_t dh_stride, const void* d_x, int64_t x_stride, int64_t tokens,
+                       int64_t dim, const int32_t* d_offsets, int64_t sequences, int form, int mix,
+                       const float* d_initial, const float* d_dfinal, void* d_dgate, int64_t dgate_stride,
+                       void* d_dx, int64_t dx_stride, float* d_dinitial, void* d_scratch, int64_t scratch_bytes,
+                       hipStream_t stream);
+
+/*
+ * One token for each of `rows` sequences whose states lie in a pool: row i takes
+ * slot d_slots[i] (d_slots NULL: slot i) of d_state [pool, dim] in fp32, rows
+ * state_stride apart, through ds_gated_scan's step, in place, and d_h[i] is the
+ * new state in the matrices' type. A row whose slot lies outside [0, pool) is a
+ * row of zeros and changes no state. Rows that name the same slot are its tokens
+ * in the order of the rows.
+ */
+int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride, int64_t rows,
+                  int64_t dim, const int32_t* d_slots, float* d_state, int64_t pool, int64_t state_stride, int form,
+                  int mix, void* d_h, int64_t h_stride, hipStream_t stream);
+
+/*
+ * Matrix products grouped by expert: rows [d_offsets[e], d_offsets[e + 1]) of a
+ * batch of m rows belong to expert e with the matrix W_e = d_w[e] (rows x cols),
+ * and y_r = W_e x_r, or with transposed 1 (the gradient of the inputs)
+ * y_r = W_e^T x_r. Rows outside all groups are not written.
+ *   dtype      DS_BF16 or DS_FP16, of x, w and y
+ *   d_x        [x_rows, cols] (transposed: rows), rows x_stride apart
+ *   d_w        [num_experts, rows, cols], contiguous
+ *   d_offsets  num_experts + 1 offsets that do not decrease, as ds_moe_align or
+ *              an exclusive scan of counts gives them (cut to [0, m])
+ *   d_index    NULL: row r of the batch is row r of x (x_rows >= m, else
+ *              DS_ERR_INVALID_VALUE). Else m entries, as ds_moe_align's
+ *              d_sorted_ids: it is row d_index[r] / top_k of x, a row of zeros
+ *              where that lies outside x (padding)
+ *   d_y        [m, rows] (transposed: cols), rows y_stride apart
+ * Sums in 32 bits. num_experts <= 8,192; m, x_rows < 2^31, rows and cols at most
+ * DS_EXPERTS_MAX_WIDTH (else DS_ERR_TOO_LARGE).
+ */
+int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stride, const void* d_w, int num_experts,
+                      int64_t rows, int64_t cols, int transposed, const int32_t* d_offsets, int64_t m,
+                      const int32_t* d_index, int top_k, void* d_y, int64_t y_stride, hipStream_t stream);
+
+/*
+ * Gradient of the matrices of ds_grouped_matmul: d_dw[e] = the sum over its
+ * group's rows r of dy_r x_r^T (added to d_dw with accumulate 1; else an expert
+ * without rows gets zeros), from d_dy [m, rows] and the x, index and offsets
+ * that the product had.
+ *   grad_dtype  of d_dw [num_experts, rows, cols]: dtype or DS_FP32
+ * The same on every run. Other arguments as ds_grouped_matmul.
+ */
+int ds_grouped_matmul_grad(int dtype, const void* d_dy, int64_t m, int64_t dy_stride, const void* d_x, int64_t x_rows,
+                           int64_t x_stride, const int32_t* d_offsets, int num_experts, const int32_t* d_index,
+                           int top_k, int64_t rows, int64_t cols, int grad_dtype, void* d_dw, int accumulate,
+                           hipStream_t stream);
+
+/*
+ * Page tables and slot maps of a step, for caches that are held in pages of
+ * `page` tokens. Request r has d_context[r] tokens in the cache, in the pages
+ * d_tables[r, 0 .. ceil(context / page)), and d_new[r] tokens now (negative
+ * numbers count as 0). Pages that they need beyond those are taken from the end
+ * of the free list, d_free[*d_count - 1] first, request by request, and entered
+ * into the tables; where none is left the entry is -1, and entries past the
+ * table's width are dropped. Writes
+ *   d_offsets    [requests + 1] the exclusive sums of d_new, a packed batch's
+ *                offsets (sums below 2^31)
+ *   d_slots      [tokens] int64: token i of request r is to be kept at
+ *                table[r, p / page] * page + p % page, p = context + i; -1 where
+ *                it has no page
+ *   d_positions  [tokens] its p
+ *   d_left       [1] the free pages that are left; negative: so many were missing
+ * Entries of d_slots and d_positions behind the last token are -1 and 0; tokens
+ * past `tokens` are left out of them. *d_count counts as cut to [0, capacity]. Calls again with the same inputs give the same
+ * results. requests, tokens, capacity < 2^31 (else DS_ERR_TOO_LARGE).
+ */
+int ds_page_slots(const int32_t* d_context, const int32_t* d_new, int64_t requests, int32_t* d_tables, int64_t width,
+                  int64_t table_stride, const int32_t* d_free, int64_t capacity, const int32_t* d_count, int page,
+                  int32_t* d_offsets, int64_t* d_slots, int32_t* d_positions, int64_t tokens, int32_t* d_left,
+                  hipStream_t stream);
+
+/*
  * Copy of nbytes from d_in to d_out with the same launch shape, 16-byte
  * accesses and tile size (128 KiB) as the 4-byte scan: the practical
  * bandwidth ceiling the scan is measured against (the "copy, no scan" row of

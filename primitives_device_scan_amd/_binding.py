@@ -33,7 +33,8 @@ EXPORTS = ["scan_exclusive", "scan_inclusive", "ds_scan", "ds_scan_seeded", "ds_
            "ds_compact_unordered", "ds_radix_pass", "ds_moe_align", "ds_embedding", "ds_embedding_grad",
            "ds_embedding_grad_scratch", "ds_embedding_grad_scratch_bytes", "ds_moe_experts_scratch",
            "ds_moe_experts_scratch_bytes", "ds_moe_route", "ds_moe_route_grad", "ds_moe_route_grad_biased",
-           "ds_moe_experts", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan", "ds_tile_pipeline", "ds_tile_elems",
+           "ds_moe_experts", "ds_gated_scan", "ds_gated_scan_scratch_bytes", "ds_gated_scan_grad", "ds_gated_step",
+           "ds_grouped_matmul", "ds_grouped_matmul_grad", "ds_page_slots", "ds_copy", "ds_bandwidth_pattern", "ds_tile_scan", "ds_tile_pipeline", "ds_tile_elems",
            "ds_scan_tile_elems", "ds_query_timeout", "ds_fail_next_allocations", "ds_set_spin_limit",
            "ds_status_string", "ds_release_workspace", "ds_version"]
 TILE_OF = {"scan_exclusive": 0, "scan_inclusive": 1, "three_pass": 2, "compact": 3, "lds_tile_scan": 4,
@@ -86,6 +87,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ds_moe_experts_scratch.restype = I
     L.ds_moe_experts_scratch_bytes.argtypes = [I, I64, I64, I, I64, I]
     L.ds_moe_experts_scratch_bytes.restype = I64
+    L.ds_gated_scan_scratch_bytes.argtypes = [I, I64, I64]
+    L.ds_gated_scan_scratch_bytes.restype = I64
+    L.ds_gated_scan.argtypes = [I, P, I64, P, I64, I64, I64, P, I64, I, I, P, P, I64, P, P, I64, P]
+    L.ds_gated_scan.restype = I
+    L.ds_gated_scan_grad.argtypes = [I, P, I64, P, I64, P, I64, P, I64, I64, I64, P, I64, I, I, P, P, P, I64, P, I64, P,
+                                     P, I64, P]
+    L.ds_gated_scan_grad.restype = I
+    L.ds_gated_step.argtypes = [I, P, I64, P, I64, I64, I64, P, P, I64, I64, I, I, P, I64, P]
+    L.ds_gated_step.restype = I
+    L.ds_grouped_matmul.argtypes = [I, P, I64, I64, P, I, I64, I64, I, P, I64, P, I, P, I64, P]
+    L.ds_grouped_matmul.restype = I
+    L.ds_grouped_matmul_grad.argtypes = [I, P, I64, I64, P, I64, I64, P, I, P, I, I64, I64, I, P, I, P]
+    L.ds_grouped_matmul_grad.restype = I
+    L.ds_page_slots.argtypes = [P, P, I64, P, I64, I64, P, I64, P, I, P, P, P, I64, P, P]
+    L.ds_page_slots.restype = I
     L.ds_copy.argtypes = [P, P, I64, P]
     L.ds_copy.restype = I
     L.ds_bandwidth_pattern.argtypes = [I, I, I, P, P, I64, P]
@@ -372,7 +388,8 @@ def _refuse_history(*tensors):
         for t in tensors:
             if getattr(t, "requires_grad", False):
                 raise ValueError("a tensor that requires grad: these calls have no autograd history; detach it or call "
-                                 "them under torch.no_grad(), and use embedding_grad and moe_route_grad for gradients")
+                                 "them under torch.no_grad(), and use embedding_grad, moe_route_grad, gated_scan_grad and "
+                                 "grouped_matmul_grad for gradients")
 
 
 def _elsewhere(x: torch.Tensor, stream) -> bool:
@@ -603,6 +620,264 @@ def moe_experts(x: torch.Tensor, w_in: torch.Tensor, w_out: torch.Tensor, ids: t
                                       None if scratch is None else scratch.data_ptr(), room, _stream_of(x)),
            "ds_moe_experts")
     return out
+
+
+# Operators on ragged batches. Offsets and lengths stay on the GPU: no call waits for the host.
+GATES = {"decay": 0, "log": 1, "sigmoid": 2}
+
+
+def _ptr(x: torch.Tensor | None):
+    return None if x is None else x.data_ptr()
+
+
+def _check_like(x: torch.Tensor, name: str, like: torch.Tensor, what: str) -> int:
+    """x is a matrix of like's shape, dtype and device, with contiguous rows; returns its row stride."""
+    stride = _check_rows(x, name, like.shape[0], like.shape[1], like)
+    if x.dtype != like.dtype:
+        raise TypeError(f"{name} must have {what}'s dtype")
+    return stride
+
+
+def _check_sequences(offsets: torch.Tensor | None, like: torch.Tensor) -> int:
+    if offsets is None:
+        return 1
+    _check_flat(offsets, "offsets", torch.int32, None, like)
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must hold one entry more than there are sequences")
+    return offsets.numel() - 1
+
+
+def gated_scan(gate: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor | None = None, *, form: str = "sigmoid",
+               mix: bool = False, initial: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+    """A gated linear recurrence over packed sequences: h_t = a_t h_{t-1} + x_t, with mix a_t h_{t-1} + (1 - a_t) x_t.
+    gate and x are [tokens, dim]; a_t is the gate ("decay"), its exponential ("log", gates at most 0) or its sigmoid.
+    Sequence s holds the rows offsets[s] to offsets[s + 1] (int32 [sequences + 1]; None: all rows are one sequence) and
+    starts from initial[s] (float32 [sequences, dim], or None for 0). Returns (h, final): h [tokens, dim] in x's dtype,
+    into `out` if it is given (rows outside the sequences are not written), and final float32 [sequences, dim], the
+    states after each sequence's last row."""
+    _refuse_history(gate, x, initial, out)
+    code = _float_code(x, "x")
+    x_stride = _check_rows(x, "x")
+    gate_stride = _check_like(gate, "gate", x, "x")
+    if form not in GATES:
+        raise ValueError(f"form must be one of {list(GATES)}")
+    sequences = _check_sequences(offsets, x)
+    tokens, dim = x.shape
+    if initial is not None:
+        _check_flat(initial, "initial", torch.float32, (sequences, dim), x)
+    if _elsewhere(x, stream):
+        return _call_elsewhere(lambda: gated_scan(gate, x, offsets, form=form, mix=mix, initial=initial, out=out), x,
+                               stream, (gate, x, offsets, initial, out))
+    if out is None:
+        out = x.new_empty((tokens, dim))
+        stride = dim
+    else:
+        stride = _check_like(out, "out", x, "x")
+    final = x.new_empty((sequences, dim), dtype=torch.float32)
+    scratch, room = None, 0
+    if _recording():
+        room = lib.ds_gated_scan_scratch_bytes(code, tokens, dim)
+        scratch = _scratch_of(x, room)
+    _check(lib.ds_gated_scan(code, gate.data_ptr(), gate_stride, x.data_ptr(), x_stride, tokens, dim, _ptr(offsets),
+                             sequences, GATES[form], 1 if mix else 0, _ptr(initial), out.data_ptr(), stride,
+                             final.data_ptr(), _ptr(scratch), room, _stream_of(x)), "ds_gated_scan")
+    return out, final
+
+
+def gated_scan_grad(gate: torch.Tensor, h: torch.Tensor, dh: torch.Tensor, offsets: torch.Tensor | None = None, *,
+                    x: torch.Tensor | None = None, form: str = "sigmoid", mix: bool = False,
+                    initial: torch.Tensor | None = None, dfinal: torch.Tensor | None = None, stream=None):
+    """The gradients of gated_scan's gate, x and initial states, from its gate, the h that it gave, the gradient dh of h
+    and dfinal of the final states (float32 [sequences, dim], or None for 0). With mix it needs x too. Returns (dgate,
+    dx, dinitial), the first two in h's dtype (rows outside the sequences are not written), dinitial float32."""
+    _refuse_history(gate, h, dh, x, initial, dfinal)
+    code = _float_code(h, "h")
+    h_stride = _check_rows(h, "h")
+    gate_stride = _check_like(gate, "gate", h, "h")
+    dh_stride = _check_like(dh, "dh", h, "h")
+    if mix and x is None:
+        raise ValueError("with mix the gradient needs x")
+    x_stride = _check_like(x, "x", h, "h") if mix else 0
+    if form not in GATES:
+        raise ValueError(f"form must be one of {list(GATES)}")
+    sequences = _check_sequences(offsets, h)
+    tokens, dim = h.shape
+    for name, t in (("initial", initial), ("dfinal", dfinal)):
+        if t is not None:
+            _check_flat(t, name, torch.float32, (sequences, dim), h)
+    if _elsewhere(h, stream):
+        return _call_elsewhere(lambda: gated_scan_grad(gate, h, dh, offsets, x=x, form=form, mix=mix, initial=initial,
+                                                       dfinal=dfinal), h, stream,
+                               (gate, h, dh, offsets, x, initial, dfinal))
+    dgate, dx = h.new_empty((tokens, dim)), h.new_empty((tokens, dim))
+    dinitial = h.new_empty((sequences, dim), dtype=torch.float32)
+    scratch, room = None, 0
+    if _recording():
+        room = lib.ds_gated_scan_scratch_bytes(code, tokens, dim)
+        scratch = _scratch_of(h, room)
+    _check(lib.ds_gated_scan_grad(code, gate.data_ptr(), gate_stride, h.data_ptr(), h_stride, dh.data_ptr(), dh_stride,
+                                  x.data_ptr() if mix else None, x_stride, tokens, dim, _ptr(offsets), sequences,
+                                  GATES[form], 1 if mix else 0, _ptr(initial), _ptr(dfinal), dgate.data_ptr(), dim,
+                                  dx.data_ptr(), dim, dinitial.data_ptr(), _ptr(scratch), room, _stream_of(h)),
+           "ds_gated_scan_grad")
+    return dgate, dx, dinitial
+
+
+def gated_step(gate: torch.Tensor, x: torch.Tensor, state: torch.Tensor, slots: torch.Tensor | None = None, *,
+               form: str = "sigmoid", mix: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gated_scan's step for one token of each of several sequences, their states held in a pool: state[slots[i]]
+    (float32 [pool, dim]; slots int32 [rows], None: row i's slot is i) takes row i of gate and x [rows, dim], in place,
+    and the new state is returned in x's dtype. A row whose slot is none of the pool's is zeros; rows of one slot are its
+    tokens in their order."""
+    _refuse_history(gate, x, state, out)
+    code = _float_code(x, "x")
+    x_stride = _check_rows(x, "x")
+    gate_stride = _check_like(gate, "gate", x, "x")
+    rows, dim = x.shape
+    state_stride = _check_rows(state, "state", None, dim, x)
+    if state.dtype != torch.float32:
+        raise TypeError("state must be float32")
+    pool = state.shape[0]
+    if slots is not None:
+        _check_flat(slots, "slots", torch.int32, (rows,), x)
+    elif pool < rows:
+        raise ValueError("without slots every row needs a state of its own")
+    if form not in GATES:
+        raise ValueError(f"form must be one of {list(GATES)}")
+    if _elsewhere(x, stream):
+        return _call_elsewhere(lambda: gated_step(gate, x, state, slots, form=form, mix=mix, out=out), x, stream,
+                               (gate, x, state, slots, out))
+    if out is None:
+        out = x.new_empty((rows, dim))
+        stride = dim
+    else:
+        stride = _check_like(out, "out", x, "x")
+    _check(lib.ds_gated_step(code, gate.data_ptr(), gate_stride, x.data_ptr(), x_stride, rows, dim, _ptr(slots),
+                             state.data_ptr(), pool, state_stride, GATES[form], 1 if mix else 0, out.data_ptr(), stride,
+                             _stream_of(x)), "ds_gated_step")
+    return out
+
+
+def _check_batch(x: torch.Tensor, offsets: torch.Tensor, index: torch.Tensor | None, top_k: int):
+    """(experts, rows of the batch) that offsets and index give."""
+    _check_flat(offsets, "offsets", torch.int32, None, x)
+    if offsets.dim() != 1 or offsets.numel() < 1:
+        raise ValueError("offsets must hold one entry more than there are experts")
+    if index is None:
+        return offsets.numel() - 1, x.shape[0]
+    _check_flat(index, "index", torch.int32, None, x)
+    if top_k < 1:
+        raise ValueError("top_k must be at least 1")
+    return offsets.numel() - 1, index.numel()
+
+
+def _sixteen_bit(x: torch.Tensor, name: str) -> int:
+    code = _float_code(x, name)
+    if code == DS_FP32:
+        raise TypeError(f"{name} must be bfloat16 or float16")
+    return code
+
+
+def grouped_matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, index: torch.Tensor | None = None,
+                   top_k: int = 1, transposed: bool = False, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Products grouped by expert: rows offsets[e] to offsets[e + 1] of the batch (int32 [experts + 1], of moe_align or
+    an exclusive scan of counts) are multiplied by w[e] (w [experts, rows, cols], bfloat16 or float16): y = x @ w[e].T,
+    with transposed y = x @ w[e], the gradient of the inputs. The batch is x, or with index (int32, moe_align's
+    sorted_ids) the rows index // top_k of x, zeros where there is no such row. Returns y [rows of the batch, rows]
+    ([.., cols] with transposed), into `out` if it is given; rows outside the groups are not written."""
+    _refuse_history(x, w, out)
+    code = _sixteen_bit(x, "x")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError("w must be [experts, rows, cols]")
+    experts, m = _check_batch(x, offsets, index, top_k)
+    rows, cols = w.shape[1:]
+    _check_flat(w, "w", x.dtype, (experts, rows, cols), x)
+    x_stride = _check_rows(x, "x", None, rows if transposed else cols)
+    width = cols if transposed else rows
+    if _elsewhere(x, stream):
+        return _call_elsewhere(lambda: grouped_matmul(x, w, offsets, index=index, top_k=top_k, transposed=transposed,
+                                                      out=out), x, stream, (x, w, offsets, index, out))
+    if out is None:
+        out = x.new_empty((m, width))
+        stride = width
+    else:
+        stride = _check_rows(out, "out", m, width, x)
+        if out.dtype != x.dtype:
+            raise TypeError("out must have x's dtype")
+    _check(lib.ds_grouped_matmul(code, x.data_ptr(), x.shape[0], x_stride, w.data_ptr(), experts, rows, cols,
+                                 1 if transposed else 0, offsets.data_ptr(), m, _ptr(index), top_k, out.data_ptr(),
+                                 stride, _stream_of(x)), "ds_grouped_matmul")
+    return out
+
+
+def grouped_matmul_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, *, index: torch.Tensor | None = None,
+                        top_k: int = 1, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                        accumulate: bool = False, stream=None) -> torch.Tensor:
+    """The gradient of grouped_matmul's w [experts, rows, cols]: for each expert dy.T @ x over its rows of the batch,
+    from the gradient dy [rows of the batch, rows] of the products and the x, offsets, index and top_k that they had.
+    `dtype` is x's (the default) or float32. accumulate: added to `out`; otherwise all of it is written, zeros for an
+    expert without rows, into `out` if it is given."""
+    _refuse_history(dy, x, out)
+    code = _sixteen_bit(x, "x")
+    x_stride = _check_rows(x, "x")
+    experts, m = _check_batch(x, offsets, index, top_k)
+    dy_stride = _check_rows(dy, "dy", m, None, x)
+    if dy.dtype != x.dtype:
+        raise TypeError("dy must have x's dtype")
+    rows, cols = dy.shape[1], x.shape[1]
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if dtype is None:
+        dtype = x.dtype if out is None else out.dtype
+    if dtype != x.dtype and dtype != torch.float32:
+        raise TypeError("the gradient's dtype must be x's or float32")
+    if _elsewhere(x, stream):
+        return _call_elsewhere(lambda: grouped_matmul_grad(dy, x, offsets, index=index, top_k=top_k, dtype=dtype,
+                                                           out=out, accumulate=accumulate), x, stream,
+                               (dy, x, offsets, index, out))
+    if out is None:
+        out = x.new_empty((experts, rows, cols), dtype=dtype)
+    else:
+        _check_flat(out, "out", dtype, (experts, rows, cols), x)
+    _check(lib.ds_grouped_matmul_grad(code, dy.data_ptr(), m, dy_stride, x.data_ptr(), x.shape[0], x_stride,
+                                      offsets.data_ptr(), experts, _ptr(index), top_k, rows, cols, _FLOATS[dtype],
+                                      out.data_ptr(), 1 if accumulate else 0, _stream_of(x)), "ds_grouped_matmul_grad")
+    return out
+
+
+def page_slots(context: torch.Tensor, new: torch.Tensor, tables: torch.Tensor, free: torch.Tensor, count: torch.Tensor,
+               page: int, tokens: int, *, stream=None):
+    """Page tables and slot maps of a step. Request r has context[r] tokens in a cache held in pages of `page` tokens,
+    listed in tables[r] (int32 [requests, width], rows any distance apart), and new[r] tokens now. Pages that they need
+    are taken from the end of the free list (free int32 [capacity], its first count[0] entries) and entered into tables
+    in place, -1 where none is left. Returns (offsets int32 [requests + 1], the packed batch's; slots int64 [tokens],
+    where each of its tokens is to be kept, -1 for one without a page and for the rest of the batch; positions int32
+    [tokens], 0 there; left int32 [1], the count for the next step, negative if pages were missing). All arguments but
+    page and tokens, the size of the batch, are on the GPU."""
+    _check_flat(context, "context", torch.int32, None, context)
+    if context.dim() != 1:
+        raise ValueError("context must be [requests]")
+    requests = context.numel()
+    _check_flat(new, "new", torch.int32, (requests,), context)
+    stride = _check_rows(tables, "tables", requests, None, context)
+    if tables.dtype != torch.int32:
+        raise TypeError("tables must be int32")
+    _check_flat(free, "free", torch.int32, None, context)
+    _check_flat(count, "count", torch.int32, (1,), context)
+    if page < 1 or tokens < 0:
+        raise ValueError("page must be at least 1 and tokens at least 0")
+    if _elsewhere(context, stream):
+        return _call_elsewhere(lambda: page_slots(context, new, tables, free, count, page, tokens), context, stream,
+                               (context, new, tables, free, count))
+    offsets = context.new_empty(requests + 1)
+    slots = context.new_empty(tokens, dtype=torch.int64)
+    positions = context.new_empty(tokens)
+    left = context.new_empty(1)
+    _check(lib.ds_page_slots(context.data_ptr(), new.data_ptr(), requests, tables.data_ptr(), tables.shape[1], stride,
+                             free.data_ptr(), free.numel(), count.data_ptr(), page, offsets.data_ptr(), slots.data_ptr(),
+                             positions.data_ptr(), tokens, left.data_ptr(), _stream_of(context)), "ds_page_slots")
+    return offsets, slots, positions, left
 
 
 def copy(src: torch.Tensor, dst: torch.Tensor, *, stream=None) -> torch.Tensor:

@@ -888,6 +888,196 @@ int ds_moe_experts_scratch(int dtype, const void* d_x, int64_t tokens, int64_t d
     return ds::launch_moe_experts(float_kind(dtype), eight, call, aux, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
 
+// Operators on ragged batches.
+static constexpr int64_t kMost31 = ((int64_t)1 << 31) - 1;
+
+static int check_gated(int dtype, int64_t tokens, int64_t dim, const int32_t* offsets, int64_t sequences, int form,
+                       int mix)
+{
+    if (!float_bytes(dtype)) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (tokens < 0 || dim < 0 || sequences < 0 || form < DS_GATE_DECAY || form > DS_GATE_SIGMOID ||
+        (mix != 0 && mix != 1) || (!offsets && sequences != 1))
+        return DS_ERR_INVALID_VALUE;
+    return tokens > kMost31 || dim > kMost31 || sequences > kMost31 ? DS_ERR_TOO_LARGE : DS_OK;
+}
+
+int64_t ds_gated_scan_scratch_bytes(int dtype, int64_t tokens, int64_t dim)
+{
+    if (!float_bytes(dtype) || tokens < 1 || dim < 1 || tokens > kMost31 || dim > kMost31) return 0;
+    return 0;
+}
+
+int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride,
+                  int64_t tokens, int64_t dim, const int32_t* d_offsets, int64_t sequences, int form, int mix,
+                  const float* d_initial, void* d_h, int64_t h_stride, float* d_final, void* d_scratch,
+                  int64_t scratch_bytes, hipStream_t stream)
+{
+    int st = check_gated(dtype, tokens, dim, d_offsets, sequences, form, mix);
+    if (st == DS_OK && (gate_stride < dim || x_stride < dim || h_stride < dim)) st = DS_ERR_INVALID_VALUE;
+    if (st != DS_OK || dim == 0 || sequences == 0) return st;
+    const int esz = float_bytes(dtype);
+    const int64_t states = span_bytes(sequences, dim, dim, 4);
+    const Buf bufs[6] = {{d_gate, span_bytes(tokens, dim, gate_stride, esz), esz, false},
+                         {d_x, span_bytes(tokens, dim, x_stride, esz), esz, false},
+                         {d_offsets, d_offsets ? (sequences + 1) * 4 : 0, 4, false},
+                         {d_initial, d_initial ? states : 0, 4, false},
+                         {d_h, span_bytes(tokens, dim, h_stride, esz), esz, true},
+                         {d_final, d_final ? states : 0, 4, true}};
+    st = check_buffers(bufs, 6);
+    if (st != DS_OK) return st;
+    const ds::GatedScan a{d_gate, d_x, d_h, gate_stride, x_stride, h_stride, tokens, dim, d_offsets, sequences, form,
+                          mix != 0, d_initial, d_final};
+    if (ds::gated_scan_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    st = check_scratch(d_scratch, scratch_bytes, ds_gated_scan_scratch_bytes(dtype, tokens, dim), bufs, 6);
+    if (st != DS_OK) return st;
+    return ds::launch_gated_scan(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
+int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const void* d_h, int64_t h_stride,
+                       const void* d_dh, int64_t dh_stride, const void* d_x, int64_t x_stride, int64_t tokens,
+                       int64_t dim, const int32_t* d_offsets, int64_t sequences, int form, int mix,
+                       const float* d_initial, const float* d_dfinal, void* d_dgate, int64_t dgate_stride,
+                       void* d_dx, int64_t dx_stride, float* d_dinitial, void* d_scratch, int64_t scratch_bytes,
+                       hipStream_t stream)
+{
+    int st = check_gated(dtype, tokens, dim, d_offsets, sequences, form, mix);
+    if (st == DS_OK && (gate_stride < dim || h_stride < dim || dh_stride < dim || (mix && x_stride < dim) ||
+                        dgate_stride < dim || dx_stride < dim))
+        st = DS_ERR_INVALID_VALUE;
+    if (st != DS_OK || dim == 0 || sequences == 0) return st;
+    const int esz = float_bytes(dtype);
+    const int64_t states = span_bytes(sequences, dim, dim, 4);
+    const Buf bufs[10] = {{d_gate, span_bytes(tokens, dim, gate_stride, esz), esz, false},
+                          {d_h, span_bytes(tokens, dim, h_stride, esz), esz, false},
+                          {d_dh, span_bytes(tokens, dim, dh_stride, esz), esz, false},
+                          {d_x, mix ? span_bytes(tokens, dim, x_stride, esz) : 0, esz, false},
+                          {d_offsets, d_offsets ? (sequences + 1) * 4 : 0, 4, false},
+                          {d_initial, d_initial ? states : 0, 4, false},
+                          {d_dfinal, d_dfinal ? states : 0, 4, false},
+                          {d_dgate, span_bytes(tokens, dim, dgate_stride, esz), esz, true},
+                          {d_dx, span_bytes(tokens, dim, dx_stride, esz), esz, true},
+                          {d_dinitial, d_dinitial ? states : 0, 4, true}};
+    st = check_buffers(bufs, 10);
+    if (st != DS_OK) return st;
+    const ds::GatedScanGrad a{{d_gate, d_x, const_cast<void*>(d_h), gate_stride, x_stride, h_stride, tokens, dim,
+                               d_offsets, sequences, form, mix != 0, d_initial, nullptr},
+                              d_dh, d_dgate, d_dx, dh_stride, dgate_stride, dx_stride, d_dfinal, d_dinitial};
+    if (ds::gated_scan_blocks(a.s) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    st = check_scratch(d_scratch, scratch_bytes, ds_gated_scan_scratch_bytes(dtype, tokens, dim), bufs, 10);
+    if (st != DS_OK) return st;
+    return ds::launch_gated_scan_grad(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
+int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride, int64_t rows,
+                  int64_t dim, const int32_t* d_slots, float* d_state, int64_t pool, int64_t state_stride, int form,
+                  int mix, void* d_h, int64_t h_stride, hipStream_t stream)
+{
+    const int esz = float_bytes(dtype);
+    if (!esz) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (rows < 0 || dim < 0 || pool < 0 || form < DS_GATE_DECAY || form > DS_GATE_SIGMOID || (mix != 0 && mix != 1) ||
+        gate_stride < dim || x_stride < dim || h_stride < dim || state_stride < dim || (!d_slots && pool < rows))
+        return DS_ERR_INVALID_VALUE;
+    if (rows == 0 || dim == 0) return DS_OK;
+    if (rows > kMost31 || dim > kMost31 || pool > kMost31) return DS_ERR_TOO_LARGE;
+    const Buf bufs[5] = {{d_gate, span_bytes(rows, dim, gate_stride, esz), esz, false},
+                         {d_x, span_bytes(rows, dim, x_stride, esz), esz, false},
+                         {d_slots, d_slots ? rows * 4 : 0, 4, false},
+                         {d_state, span_bytes(pool, dim, state_stride, 4), 4, true},
+                         {d_h, span_bytes(rows, dim, h_stride, esz), esz, true}};
+    const int st = check_buffers(bufs, 5);
+    if (st != DS_OK) return st;
+    const ds::GatedStep a{d_gate, d_x, d_h, gate_stride, x_stride, h_stride, rows, dim, d_slots, d_state, pool,
+                          state_stride, form, mix != 0};
+    if (ds::gated_step_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    return ds::launch_gated_step(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
+// What the product and the gradient of its matrices have in common.
+static int check_grouped(int dtype, int64_t x_rows, int num_experts, int64_t rows, int64_t cols, int64_t m,
+                         const int32_t* index, int top_k)
+{
+    if (dtype != DS_BF16 && dtype != DS_FP16) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (x_rows < 0 || m < 0 || rows < 0 || cols < 0 || num_experts < 0 || num_experts > ds::experts_max_experts() ||
+        (index ? top_k < 1 : x_rows < m))
+        return DS_ERR_INVALID_VALUE;
+    return m > kMost31 || x_rows > kMost31 || rows > DS_EXPERTS_MAX_WIDTH || cols > DS_EXPERTS_MAX_WIDTH
+               ? DS_ERR_TOO_LARGE
+               : DS_OK;
+}
+
+int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stride, const void* d_w, int num_experts,
+                      int64_t rows, int64_t cols, int transposed, const int32_t* d_offsets, int64_t m,
+                      const int32_t* d_index, int top_k, void* d_y, int64_t y_stride, hipStream_t stream)
+{
+    int st = check_grouped(dtype, x_rows, num_experts, rows, cols, m, d_index, top_k);
+    if (st != DS_OK) return st;
+    if (transposed != 0 && transposed != 1) return DS_ERR_INVALID_VALUE;
+    const int64_t depth = transposed ? rows : cols, out = transposed ? cols : rows;
+    if (x_stride < depth || y_stride < out) return DS_ERR_INVALID_VALUE;
+    if (num_experts == 0 || m == 0 || out == 0) return DS_OK;
+    const Buf bufs[5] = {{d_x, span_bytes(x_rows, depth, x_stride, 2), 2, false},
+                         {d_w, span_bytes(num_experts * rows, cols, cols, 2), 2, false},
+                         {d_offsets, ((int64_t)num_experts + 1) * 4, 4, false},
+                         {d_index, d_index ? m * 4 : 0, 4, false},
+                         {d_y, span_bytes(m, out, y_stride, 2), 2, true}};
+    st = check_buffers(bufs, 5);
+    if (st != DS_OK) return st;
+    const ds::Grouped a{d_x, d_w, d_y, nullptr, x_rows, x_stride, y_stride, m, d_offsets, d_index, num_experts,
+                        top_k, rows, cols, transposed != 0, false};
+    if (ds::grouped_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    return ds::launch_grouped_matmul(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
+int ds_grouped_matmul_grad(int dtype, const void* d_dy, int64_t m, int64_t dy_stride, const void* d_x, int64_t x_rows,
+                           int64_t x_stride, const int32_t* d_offsets, int num_experts, const int32_t* d_index,
+                           int top_k, int64_t rows, int64_t cols, int grad_dtype, void* d_dw, int accumulate,
+                           hipStream_t stream)
+{
+    int st = check_grouped(dtype, x_rows, num_experts, rows, cols, m, d_index, top_k);
+    if (st != DS_OK) return st;
+    if (grad_dtype != dtype && grad_dtype != DS_FP32) return DS_ERR_UNSUPPORTED_DTYPE;
+    if (dy_stride < rows || x_stride < cols || (accumulate != 0 && accumulate != 1)) return DS_ERR_INVALID_VALUE;
+    if (num_experts == 0 || rows == 0 || cols == 0 || (m == 0 && accumulate)) return DS_OK;
+    const int gsz = float_bytes(grad_dtype);
+    const Buf bufs[5] = {{d_dy, span_bytes(m, rows, dy_stride, 2), 2, false},
+                         {d_x, span_bytes(x_rows, cols, x_stride, 2), 2, false},
+                         {d_offsets, ((int64_t)num_experts + 1) * 4, 4, false},
+                         {d_index, d_index ? m * 4 : 0, 4, false},
+                         {d_dw, span_bytes(num_experts * rows, cols, cols, gsz), gsz, true}};
+    st = check_buffers(bufs, 5);
+    if (st != DS_OK) return st;
+    const ds::Grouped a{d_x, nullptr, const_cast<void*>(d_dy), d_dw, x_rows, x_stride, dy_stride, m, d_offsets,
+                        d_index, num_experts, top_k, rows, cols, false, accumulate != 0};
+    if (ds::grouped_grad_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    return ds::launch_grouped_matmul_grad(float_kind(dtype), float_kind(grad_dtype), a, stream) == hipSuccess
+               ? DS_OK
+               : DS_ERR_HIP;
+}
+
+int ds_page_slots(const int32_t* d_context, const int32_t* d_new, int64_t requests, int32_t* d_tables, int64_t width,
+                  int64_t table_stride, const int32_t* d_free, int64_t capacity, const int32_t* d_count, int page,
+                  int32_t* d_offsets, int64_t* d_slots, int32_t* d_positions, int64_t tokens, int32_t* d_left,
+                  hipStream_t stream)
+{
+    if (requests < 0 || width < 0 || table_stride < width || capacity < 0 || page < 1 || tokens < 0)
+        return DS_ERR_INVALID_VALUE;
+    if (requests > kMost31 || width > kMost31 || capacity > kMost31 || tokens > kMost31) return DS_ERR_TOO_LARGE;
+    const Buf bufs[9] = {{d_context, requests * 4, 4, false},
+                         {d_new, requests * 4, 4, false},
+                         {d_tables, span_bytes(requests, width, table_stride, 4), 4, true},
+                         {d_free, capacity * 4, 4, false},
+                         {d_count, 4, 4, false},
+                         {d_offsets, (requests + 1) * 4, 4, true},
+                         {d_slots, tokens * 8, 8, true},
+                         {d_positions, tokens * 4, 4, true},
+                         {d_left, 4, 4, true}};
+    const int st = check_buffers(bufs, 9);
+    if (st != DS_OK) return st;
+    const ds::PageSlots a{d_context, d_new, requests, d_tables, width, table_stride, d_free, capacity, d_count, page,
+                          d_offsets, d_slots, d_positions, tokens, d_left};
+    return ds::launch_page_slots(a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+}
+
 void ds_release_workspace(void)
 {
     std::lock_guard<std::mutex> lock(g_mu);

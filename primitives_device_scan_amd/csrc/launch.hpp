@@ -146,6 +146,77 @@ int64_t experts_most_aux_bytes(bool eight_bit, int64_t tokens, int dim, int expe
 int64_t experts_workgroups(bool eight_bit, const ExpertsCall& call);  // of the largest launch
 hipError_t launch_moe_experts(ElemKind kind, bool eight_bit, const ExpertsCall& call, char* aux, hipStream_t stream);
 
+// Ragged batches. Gated recurrence over packed sequences (float kinds); strides
+// are elements between rows.
+struct GatedScan {
+    const void *gate, *x;       // x: the gradient reads it with mix alone
+    void* h;                    // the scan writes it, the gradient reads it
+    int64_t gate_stride, x_stride, h_stride, tokens, dim;
+    const int32_t* offsets;     // [sequences + 1], or null: one sequence of all tokens
+    int64_t sequences;
+    int form;                   // GateForm
+    bool mix;                   // inputs weighted by 1 - a
+    const float* initial;       // [sequences, dim] or null
+    float* final;               // [sequences, dim] or null
+};
+struct GatedScanGrad {
+    GatedScan s;                // final is not used
+    const void* dh;
+    void *dgate, *dx;
+    int64_t dh_stride, dgate_stride, dx_stride;
+    const float* dfinal;        // [sequences, dim] or null
+    float* dinitial;            // [sequences, dim] or null
+};
+struct GatedStep {
+    const void *gate, *x;
+    void* h;
+    int64_t gate_stride, x_stride, h_stride, rows, dim;
+    const int32_t* slots;       // or null: row i's slot is i
+    float* state;
+    int64_t pool, state_stride;
+    int form;
+    bool mix;
+};
+int64_t gated_scan_blocks(const GatedScan& a);  // workgroups
+int64_t gated_step_blocks(const GatedStep& a);
+hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, hipStream_t stream);
+hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, hipStream_t stream);
+hipError_t launch_gated_step(ElemKind kind, const GatedStep& a, hipStream_t stream);
+
+// Products grouped by expert (16-bit kinds) and the gradient of their weights.
+struct Grouped {
+    const void *x, *w;
+    void *y, *dw;               // y: the products, or the gradient's dy, which it reads
+    int64_t x_rows, x_stride, y_stride, m;
+    const int32_t* offsets;     // [experts + 1]
+    const int32_t* index;       // [m] or null
+    int experts, top_k;
+    int64_t rows, cols;         // of an expert's matrix
+    bool transposed, accumulate;
+};
+int64_t grouped_blocks(const Grouped& a);  // workgroups
+int64_t grouped_grad_blocks(const Grouped& a);
+hipError_t launch_grouped_matmul(ElemKind kind, const Grouped& a, hipStream_t stream);
+hipError_t launch_grouped_matmul_grad(ElemKind kind, ElemKind grad_kind, const Grouped& a, hipStream_t stream);
+
+// Page tables and slot maps of a batch of requests.
+struct PageSlots {
+    const int32_t *context, *fresh;  // [requests]: tokens in the cache, tokens of this step
+    int64_t requests;
+    int32_t* tables;                 // [requests, width], table_stride apart
+    int64_t width, table_stride;
+    const int32_t* free_pages;       // [capacity], *count of them free, taken from the end
+    int64_t capacity;
+    const int32_t* count;
+    int page;
+    int32_t* offsets;                // [requests + 1]
+    int64_t* slots;                  // [tokens]
+    int32_t* positions;              // [tokens]
+    int64_t tokens;
+    int32_t* left;
+};
+hipError_t launch_page_slots(const PageSlots& a, hipStream_t stream);
+
 // Exclusive scan of `count` tile totals in place (one workgroup, carried sum).
 hipError_t launch_scan_totals(ElemKind kind, void* totals, int64_t count, hipStream_t stream);
 
