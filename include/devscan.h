@@ -416,6 +416,8 @@ typedef enum {
     DS_GATE_SIGMOID = 2 /* a = 1 / (1 + exp(-g)) */
 } ds_gate;
 
+#define DS_GATED_MAX_STRIDE 1048576
+
 /*
  * Gated linear recurrence over packed sequences, channel by channel:
  * h_t = a_t h_{t-1} + b_t, with a_t from the gate g_t (ds_gate) and b_t = x_t, or
@@ -433,10 +435,15 @@ typedef enum {
  * 1 keeps 1 - a to 32 bits. Gates of magnitude above 1 may overflow products
  * over many steps; once a state is infinite or NaN so are the later ones of its
  * sequence and channel. d_scratch: as in ds_embedding_grad_scratch, of at least
- * ds_gated_scan_scratch_bytes(dtype, tokens, dim) bytes; NULL: the stream's
- * workspace. tokens, dim, sequences < 2^31 (else DS_ERR_TOO_LARGE).
+ * ds_gated_scan_scratch_bytes(dtype, 0, tokens, dim) bytes; NULL: the stream's
+ * workspace. tokens, sequences < 2^31, distances between rows at most
+ * DS_GATED_MAX_STRIDE (else DS_ERR_TOO_LARGE).
+ *
+ * Rows are worked on in tiles, and a tile that continues a sequence waits for the
+ * tiles before it, as the scans do ("Bounded waits"). Should such a wait give up,
+ * the rest of the sequence is NaN.
  */
-int64_t ds_gated_scan_scratch_bytes(int dtype, int64_t tokens, int64_t dim);
+int64_t ds_gated_scan_scratch_bytes(int dtype, int grad, int64_t tokens, int64_t dim);
 int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride,
                   int64_t tokens, int64_t dim, const int32_t* d_offsets, int64_t sequences, int form, int mix,
                   const float* d_initial, void* d_h, int64_t h_stride, float* d_final, void* d_scratch,
@@ -450,7 +457,8 @@ int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void
  * h_{t-1} - x_t with mix) da/dg; dinitial = a G of the first row (an empty
  * sequence's is its dfinal). d_x is read with mix alone and may else be NULL;
  * d_dinitial may be NULL. Rows outside the sequences are not written. Other
- * arguments and the scratch as ds_gated_scan.
+ * arguments and the scratch (of ds_gated_scan_scratch_bytes(dtype, 1, tokens,
+ * dim) bytes) as ds_gated_scan.
  */
 int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const void* d_h, int64_t h_stride,
                        const void* d_dh, int64_t dh_stride, const void* d_x, int64_t x_stride, int64_t tokens,

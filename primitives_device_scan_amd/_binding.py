@@ -87,7 +87,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.ds_moe_experts_scratch.restype = I
     L.ds_moe_experts_scratch_bytes.argtypes = [I, I64, I64, I, I64, I]
     L.ds_moe_experts_scratch_bytes.restype = I64
-    L.ds_gated_scan_scratch_bytes.argtypes = [I, I64, I64]
+    L.ds_gated_scan_scratch_bytes.argtypes = [I, I, I64, I64]
     L.ds_gated_scan_scratch_bytes.restype = I64
     L.ds_gated_scan.argtypes = [I, P, I64, P, I64, I64, I64, P, I64, I, I, P, P, I64, P, P, I64, P]
     L.ds_gated_scan.restype = I
@@ -676,7 +676,7 @@ def gated_scan(gate: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor | None
     final = x.new_empty((sequences, dim), dtype=torch.float32)
     scratch, room = None, 0
     if _recording():
-        room = lib.ds_gated_scan_scratch_bytes(code, tokens, dim)
+        room = lib.ds_gated_scan_scratch_bytes(code, 0, tokens, dim)
         scratch = _scratch_of(x, room)
     _check(lib.ds_gated_scan(code, gate.data_ptr(), gate_stride, x.data_ptr(), x_stride, tokens, dim, _ptr(offsets),
                              sequences, GATES[form], 1 if mix else 0, _ptr(initial), out.data_ptr(), stride,
@@ -713,7 +713,7 @@ def gated_scan_grad(gate: torch.Tensor, h: torch.Tensor, dh: torch.Tensor, offse
     dinitial = h.new_empty((sequences, dim), dtype=torch.float32)
     scratch, room = None, 0
     if _recording():
-        room = lib.ds_gated_scan_scratch_bytes(code, tokens, dim)
+        room = lib.ds_gated_scan_scratch_bytes(code, 1, tokens, dim)
         scratch = _scratch_of(h, room)
     _check(lib.ds_gated_scan_grad(code, gate.data_ptr(), gate_stride, h.data_ptr(), h_stride, dh.data_ptr(), dh_stride,
                                   x.data_ptr() if mix else None, x_stride, tokens, dim, _ptr(offsets), sequences,

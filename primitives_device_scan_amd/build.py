@@ -19,7 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libdevscan.so")
 SOURCES = ["scan_lookback.hip", "scan_blocked.hip", "scan_three_pass.hip", "compact.hip", "compact_unordered.hip", "counting_sort.hip", "copy.hip", "tile_lds.hip", "embedding.hip",
-           "moe_route.hip", "moe_experts.hip", "gated_scan.hip", "grouped_matmul.hip", "page_slots.hip", "api.hip"]
+           "moe_route.hip", "moe_experts.hip", "gated_scan.hip", "gated_scan_grad.hip", "grouped_matmul.hip", "page_slots.hip", "api.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

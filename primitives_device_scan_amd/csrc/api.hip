@@ -4,6 +4,7 @@
 
 #include <stdlib.h>
 
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -898,13 +899,39 @@ static int check_gated(int dtype, int64_t tokens, int64_t dim, const int32_t* of
     if (tokens < 0 || dim < 0 || sequences < 0 || form < DS_GATE_DECAY || form > DS_GATE_SIGMOID ||
         (mix != 0 && mix != 1) || (!offsets && sequences != 1))
         return DS_ERR_INVALID_VALUE;
-    return tokens > kMost31 || dim > kMost31 || sequences > kMost31 ? DS_ERR_TOO_LARGE : DS_OK;
+    return tokens > kMost31 || sequences > kMost31 ? DS_ERR_TOO_LARGE : DS_OK;
 }
 
-int64_t ds_gated_scan_scratch_bytes(int dtype, int64_t tokens, int64_t dim)
+// Distances between rows that the recurrence's 32-bit offsets within a tile can take.
+static int check_gated_strides(std::initializer_list<int64_t> strides, int64_t dim)
 {
-    if (!float_bytes(dtype) || tokens < 1 || dim < 1 || tokens > kMost31 || dim > kMost31) return 0;
-    return 0;
+    for (const int64_t s : strides)
+        if (s < dim) return DS_ERR_INVALID_VALUE;
+    for (const int64_t s : strides)
+        if (s > DS_GATED_MAX_STRIDE) return DS_ERR_TOO_LARGE;
+    return DS_OK;
+}
+
+static int64_t gated_scratch(const ds::GatedPlan& plan) { return (plan.words * 8 + 15) / 16 * 16; }
+
+int64_t ds_gated_scan_scratch_bytes(int dtype, int grad, int64_t tokens, int64_t dim)
+{
+    if (!float_bytes(dtype) || tokens < 1 || dim < 1 || tokens > kMost31 || dim > DS_GATED_MAX_STRIDE) return 0;
+    return gated_scratch(ds::gated_plan(float_kind(dtype), grad != 0, tokens, dim));
+}
+
+// The words of a scan or its gradient, in the call's scratch.
+static int gated_words(const ds::GatedPlan& plan, void* d_scratch, int64_t scratch_bytes, const Buf* bufs, int count,
+                       hipStream_t stream, uint64_t** words)
+{
+    const int64_t need = gated_scratch(plan);
+    if (plan.tiles * plan.cblocks > kMaxTiles) return DS_ERR_TOO_LARGE;
+    int st = check_scratch(d_scratch, scratch_bytes, need, bufs, count);
+    if (st != DS_OK) return st;
+    char* aux = static_cast<char*>(d_scratch);
+    if (need && !aux) st = get_aux(stream, (size_t)need, &aux);
+    *words = reinterpret_cast<uint64_t*>(aux);
+    return st;
 }
 
 int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride,
@@ -913,7 +940,7 @@ int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void
                   int64_t scratch_bytes, hipStream_t stream)
 {
     int st = check_gated(dtype, tokens, dim, d_offsets, sequences, form, mix);
-    if (st == DS_OK && (gate_stride < dim || x_stride < dim || h_stride < dim)) st = DS_ERR_INVALID_VALUE;
+    if (st == DS_OK) st = check_gated_strides({gate_stride, x_stride, h_stride}, dim);
     if (st != DS_OK || dim == 0 || sequences == 0) return st;
     const int esz = float_bytes(dtype);
     const int64_t states = span_bytes(sequences, dim, dim, 4);
@@ -927,10 +954,13 @@ int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void
     if (st != DS_OK) return st;
     const ds::GatedScan a{d_gate, d_x, d_h, gate_stride, x_stride, h_stride, tokens, dim, d_offsets, sequences, form,
                           mix != 0, d_initial, d_final};
-    if (ds::gated_scan_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
-    st = check_scratch(d_scratch, scratch_bytes, ds_gated_scan_scratch_bytes(dtype, tokens, dim), bufs, 6);
+    const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), false, tokens, dim);
+    std::lock_guard<std::mutex> lock(g_mu);
+    uint64_t* words = nullptr;
+    st = gated_words(plan, d_scratch, scratch_bytes, bufs, 6, stream, &words);
     if (st != DS_OK) return st;
-    return ds::launch_gated_scan(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+    return ds::launch_gated_scan(float_kind(dtype), a, plan, words, g_spin_limit, stream) == hipSuccess ? DS_OK
+                                                                                                        : DS_ERR_HIP;
 }
 
 int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const void* d_h, int64_t h_stride,
@@ -941,9 +971,8 @@ int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const
                        hipStream_t stream)
 {
     int st = check_gated(dtype, tokens, dim, d_offsets, sequences, form, mix);
-    if (st == DS_OK && (gate_stride < dim || h_stride < dim || dh_stride < dim || (mix && x_stride < dim) ||
-                        dgate_stride < dim || dx_stride < dim))
-        st = DS_ERR_INVALID_VALUE;
+    if (st == DS_OK)
+        st = check_gated_strides({gate_stride, h_stride, dh_stride, mix ? x_stride : dim, dgate_stride, dx_stride}, dim);
     if (st != DS_OK || dim == 0 || sequences == 0) return st;
     const int esz = float_bytes(dtype);
     const int64_t states = span_bytes(sequences, dim, dim, 4);
@@ -962,10 +991,14 @@ int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const
     const ds::GatedScanGrad a{{d_gate, d_x, const_cast<void*>(d_h), gate_stride, x_stride, h_stride, tokens, dim,
                                d_offsets, sequences, form, mix != 0, d_initial, nullptr},
                               d_dh, d_dgate, d_dx, dh_stride, dgate_stride, dx_stride, d_dfinal, d_dinitial};
-    if (ds::gated_scan_blocks(a.s) > kMaxTiles) return DS_ERR_TOO_LARGE;
-    st = check_scratch(d_scratch, scratch_bytes, ds_gated_scan_scratch_bytes(dtype, tokens, dim), bufs, 10);
+    const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), true, tokens, dim);
+    std::lock_guard<std::mutex> lock(g_mu);
+    uint64_t* words = nullptr;
+    st = gated_words(plan, d_scratch, scratch_bytes, bufs, 10, stream, &words);
     if (st != DS_OK) return st;
-    return ds::launch_gated_scan_grad(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
+    return ds::launch_gated_scan_grad(float_kind(dtype), a, plan, words, g_spin_limit, stream) == hipSuccess
+               ? DS_OK
+               : DS_ERR_HIP;
 }
 
 int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride, int64_t rows,

@@ -5,11 +5,13 @@
 // more than the roundings of the state itself (which go both ways). So gates
 // that come as sigmoids or exponentials are held as the smaller of a and 1 - a:
 // v = a, or v = -(1 - a) where 0.5 <= a <= 1, marked by the sign bit (a = 1 is
-// -0.0). A step is then fma(v, h, b), plus h where the sign bit is set.
+// -0.0, a = 0 is +0.0). a h is then v h, plus h where the sign bit is set.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "float_types.hpp"
 
 namespace ds {
 
@@ -17,14 +19,38 @@ enum GateForm { kDecay = 0, kLog = 1, kSigmoid = 2 };
 
 __device__ __forceinline__ bool gate_keeps(float v) { return (int)__builtin_bit_cast(uint32_t, v) < 0; }
 
-template <GateForm FORM>
+// exp(-|g|) to some 2^-23 of itself: the product with log2(e) is taken in two
+// parts, since its rounding alone would be |g| 2^-24 of the result, the same
+// for every step of a channel whose gate stays where it is. In bf16 (8 bits)
+// the product with log2(e) cut to 16 bits is exact.
+template <typename T>
+__device__ __forceinline__ float exp_minus(float g)
+{
+    constexpr float kLn2 = 0.69314718f;
+    const float m = -__builtin_fabsf(g);
+    float e, rest;
+    if constexpr (__is_same(T, bf16)) {
+        constexpr float kHi = 1.44268798828125f;
+        e = __builtin_amdgcn_exp2f(m * kHi);
+        rest = m * (float)((1.4426950408889634 - 1.44268798828125) * kLn2);
+    } else {
+        constexpr float kHi = 1.4426950408889634f;
+        const float p = m * kHi;
+        e = __builtin_amdgcn_exp2f(p);
+        rest = __builtin_fmaf(m, (float)(1.4426950408889634 - (double)kHi), __builtin_fmaf(m, kHi, -p)) * kLn2;
+    }
+    // far gates' rest may be infinite or NaN where e is 0; a NaN gate is one in e
+    return __builtin_fmaf(e, __builtin_amdgcn_fmed3f(rest, -0.002f, 0.002f), e);
+}
+
+// v of a gate g that came in type T
+template <typename T, GateForm FORM>
 __device__ __forceinline__ float gate_of(float g)
 {
-    constexpr float kLog2e = 1.44269504f;
     if constexpr (FORM == kDecay) return g;
     if constexpr (FORM == kSigmoid) {
         // s = sigmoid(-|g|) <= 0.5: a itself for g < 0, 1 - a otherwise
-        const float e = __builtin_amdgcn_exp2f(-__builtin_fabsf(g) * kLog2e);
+        const float e = exp_minus<T>(g);
         return __builtin_copysignf(e * __builtin_amdgcn_rcpf(1.0f + e), -g);
     }
     if constexpr (FORM == kLog) {
@@ -41,17 +67,26 @@ __device__ __forceinline__ float gate_of(float g)
         p = __builtin_fmaf(p, g, 0.5f);
         p = __builtin_fmaf(p, g, 1.0f);
         const float near = -__builtin_fabsf(p * g);
-        return g <= 0.0f && g > -0.6931f ? near : __builtin_amdgcn_exp2f(g * kLog2e);
+        return g <= 0.0f && g > -0.6931f ? near : __builtin_amdgcn_exp2f(g * 1.44269504f);
     }
 }
 
-// a h + b
+// a h
 template <GateForm FORM>
-__device__ __forceinline__ float step_of(float v, float h, float b)
+__device__ __forceinline__ float keep_of(float v, float h)
 {
-    const float y = __builtin_fmaf(v, h, b);
-    if constexpr (FORM == kDecay) return y;
-    return y + (gate_keeps(v) ? h : 0.0f);
+    if constexpr (FORM == kDecay) return v * h;
+    return __builtin_fmaf(v, h, gate_keeps(v) ? h : 0.0f);
+}
+
+// a h + x, or with MIX a h + (1 - a) x, which is h - (1 - a) (h - x) or
+// x + a (h - x), whichever has the smaller factor
+template <GateForm FORM, bool MIX>
+__device__ __forceinline__ float step_of(float v, float h, float x)
+{
+    if constexpr (FORM == kDecay) return __builtin_fmaf(v, h, MIX ? (1.0f - v) * x : x);
+    if constexpr (MIX) return __builtin_fmaf(v, h - x, gate_keeps(v) ? h : x);
+    return keep_of<FORM>(v, h) + x;
 }
 
 // 1 - a (near 0 for a log gate above 0, a > 1, it has a's own 32 bits)

@@ -4,65 +4,100 @@
 //   a_t = g_t, exp(g_t) or sigmoid(g_t)          b_t = x_t, or (1 - a_t) x_t
 //   h_t = a_t h_{t-1} + b_t                      h before a sequence: its initial state, or 0
 //
-// It is a scan: steps (a, b) followed by (a', b') are the step (a a', a' b + b').
-#include "float_types.hpp"
-#include "gate.hpp"
-#include "launch.hpp"
+// The scan itself (see gated.hpp for how it is cut up) and the step for single
+// tokens; the gradient is in gated_scan_grad.hip.
+#include "gated.hpp"
 
 namespace ds {
 
-// Sequence s's tokens [first, end), inside [0, tokens) whatever the offsets say.
-__device__ __forceinline__ void sequence_range(const GatedScan& a, int64_t s, int64_t& first, int64_t& end)
+template <typename T, int V, GateForm FORM, bool MIX, int TQ>
+__global__ __launch_bounds__(kThreads, 2) void gated_scan_kernel(GatedScan a, GatedWords w)
 {
-    first = a.offsets ? min(max((int64_t)a.offsets[s], (int64_t)0), a.tokens) : 0;
-    end = a.offsets ? min(max((int64_t)a.offsets[s + 1], first), a.tokens) : a.tokens;
-}
-
-template <typename T, GateForm FORM, bool MIX>
-__global__ __launch_bounds__(kThreads) void gated_scan_kernel(GatedScan a)
-{
-    const int64_t cblocks = (a.dim + kThreads - 1) / kThreads;
-    const int64_t s = blockIdx.x / cblocks, c = blockIdx.x % cblocks * kThreads + threadIdx.x;
-    if (c >= a.dim) return;
-    int64_t first, end;
-    sequence_range(a, s, first, end);
-    float h = a.initial ? a.initial[s * a.dim + c] : 0.0f;
-    for (int64_t t = first; t < end; ++t) {
-        const float v = gate_of<FORM>((float)static_cast<const T*>(a.gate)[t * a.gate_stride + c]);
-        const float x = (float)static_cast<const T*>(a.x)[t * a.x_stride + c];
-        h = step_of<FORM>(v, h, MIX ? rest_of<FORM>(v) * x : x);
-        static_cast<T*>(a.h)[t * a.h_stride + c] = (T)h;
-    }
-    if (a.final) a.final[s * a.dim + c] = h;
-}
-
-template <typename T, GateForm FORM, bool MIX>
-__global__ __launch_bounds__(kThreads) void gated_scan_grad_kernel(GatedScanGrad a)
-{
-    const int64_t cblocks = (a.s.dim + kThreads - 1) / kThreads;
-    const int64_t s = blockIdx.x / cblocks, c = blockIdx.x % cblocks * kThreads + threadIdx.x;
-    if (c >= a.s.dim) return;
-    int64_t first, end;
-    sequence_range(a.s, s, first, end);
-    float total = a.dfinal ? a.dfinal[s * a.s.dim + c] : 0.0f;  // what reaches h_t from later steps
-    for (int64_t t = end - 1; t >= first; --t) {
-        const float v = gate_of<FORM>((float)static_cast<const T*>(a.s.gate)[t * a.s.gate_stride + c]);
-        float before = 0.0f;
-        if (t > first)
-            before = (float)static_cast<const T*>(a.s.h)[(t - 1) * a.s.h_stride + c];
-        else if (a.s.initial)
-            before = a.s.initial[s * a.s.dim + c];
-        total += (float)static_cast<const T*>(a.dh)[t * a.dh_stride + c];
-        float dx = total;
-        if (MIX) {
-            dx *= rest_of<FORM>(v);
-            before -= (float)static_cast<const T*>(a.s.x)[t * a.s.x_stride + c];
+    constexpr int kRows = kSub * TQ, kSpan = kLanes * V;
+    __shared__ float s_a[kSub][kSpan], s_b[kSub][kSpan];
+    __shared__ int s_new[kSub], s_seq[kRows + 2];
+    const Place<V> p(a.dim);
+    const int part = (int)threadIdx.x / kLanes, at = (int)threadIdx.x % kLanes * V;
+    const int64_t tiles = gridDim.x / p.cblocks, row0 = p.tile * kRows, mine = row0 + part * TQ;
+    if (a.tokens > 0) {
+        const int64_t left = a.tokens - mine;  // rows of this part that there are, or more
+        const Rows<const T> gate(static_cast<const T*>(a.gate), a.gate_stride, row0, part * TQ, p.channel);
+        const Rows<const T> in(static_cast<const T*>(a.x), a.x_stride, row0, part * TQ, p.channel);
+        Cells<T, V> g[TQ] = {}, x[TQ] = {};
+        if (row0 + kRows <= a.tokens) {
+#pragma unroll
+            for (int k = 0; k < TQ; ++k) {
+                g[k].load(gate.at(k), gate.bytes);
+                x[k].load(in.at(k), in.bytes);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < TQ; ++k)
+                if (k < left) {
+                    g[k].load(gate.at(k), gate.bytes);
+                    x[k].load(in.at(k), in.bytes);
+                }
         }
-        static_cast<T*>(a.dx)[t * a.dx_stride + c] = (T)dx;
-        static_cast<T*>(a.dgate)[t * a.dgate_stride + c] = (T)(total * before * slope_of<FORM>(v));
-        total = step_of<FORM>(v, total, 0.0f);
+        const bool inside = find_sequences<kRows>(a, row0, s_seq);
+        // bit k: row k of this part is the first, the last, or none of a sequence
+        uint32_t first = 0, last = 0, none = 0;
+        if (!inside)
+            for (int k = 0; k < TQ; ++k) {
+                const int s = s_seq[part * TQ + k + 1];
+                none |= (uint32_t)(s < 0) << k;
+                first |= (uint32_t)(s >= 0 && s != s_seq[part * TQ + k]) << k;
+                last |= (uint32_t)(s >= 0 && s != s_seq[part * TQ + k + 2]) << k;
+            }
+        const auto initial = [&](int k, float (&h)[V]) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] = 0.0f;
+            if (a.initial) load_states(a.initial + (int64_t)s_seq[part * TQ + k + 1] * a.dim + p.channel, h);
+        };
+        float v[TQ][V], pa[V], h[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            pa[i] = 1.0f;
+            h[i] = 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < TQ; ++k) {
+            if (first >> k & 1) initial(k, h);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                v[k][i] = gate_of<T, FORM>(g[k][i]);
+                h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
+                pa[i] = keep_of<FORM>(v[k][i], pa[i]);
+            }
+            pin(v[k]);
+            x[k].pin();
+        }
+        store_states(&s_a[part][at], pa);
+        store_states(&s_b[part][at], h);
+        if (at == 0) s_new[part] = first != 0;
+        __syncthreads();
+        join_parts<kSpan>(s_a, s_b, s_new, p.tile, tiles, p.cblock, p.cblocks, s_seq[1] >= 0 && s_seq[0] == s_seq[1], w);
+        __syncthreads();
+        load_states(&s_a[part][at], h);
+        const Rows<T> to(static_cast<T*>(a.h), a.h_stride, row0, part * TQ, p.channel);
+#pragma unroll
+        for (int k = 0; k < TQ; ++k) {
+            if (first >> k & 1) initial(k, h);
+            Cells<T, V> out;
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
+            out.set(h);
+            if (p.live && !(none >> k & 1)) out.store(to.at(k), to.bytes);
+            if (p.live && (last >> k & 1) && a.final)
+                store_states(a.final + (int64_t)s_seq[part * TQ + k + 1] * a.dim + p.channel, h);
+        }
     }
-    if (a.dinitial) a.dinitial[s * a.s.dim + c] = total;
+    pass_empty(a, p, a.initial, a.final);
+}
+
+__global__ __launch_bounds__(kThreads) void gated_clear_kernel(u32x4* words, int64_t count)
+{
+    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < count; i += (int64_t)gridDim.x * kThreads)
+        words[i] = u32x4{0, 0, 0, 0};
 }
 
 // A workgroup takes one row's columns. Rows whose slot an earlier row names are
@@ -88,9 +123,8 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
     float h = c < a.dim ? *state : 0.0f;
     for (;;) {
         if (c < a.dim) {
-            const float v = gate_of<FORM>((float)static_cast<const T*>(a.gate)[i * a.gate_stride + c]);
-            const float x = (float)static_cast<const T*>(a.x)[i * a.x_stride + c];
-            h = step_of<FORM>(v, h, MIX ? rest_of<FORM>(v) * x : x);
+            const float v = gate_of<T, FORM>((float)static_cast<const T*>(a.gate)[i * a.gate_stride + c]);
+            h = step_of<FORM, MIX>(v, h, (float)static_cast<const T*>(a.x)[i * a.x_stride + c]);
             static_cast<T*>(a.h)[i * a.h_stride + c] = (T)h;
         }
         if (!a.slots) break;
@@ -112,51 +146,35 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
     if (c < a.dim) *state = h;
 }
 
-int64_t gated_scan_blocks(const GatedScan& a) { return (a.dim + kThreads - 1) / kThreads * a.sequences; }
+GatedPlan gated_plan(ElemKind kind, bool grad, int64_t tokens, int64_t dim)
+{
+    return gated_plan_of(kind, grad, tokens, dim);
+}
+
 int64_t gated_step_blocks(const GatedStep& a) { return (a.dim + kThreads - 1) / kThreads * a.rows; }
 
-template <typename F> static void with_form(int form, bool mix, F&& f)
+GatedWords clear_words(const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit, hipStream_t stream)
 {
-    const auto go = [&](auto fm) {
-        if (mix)
-            f(fm, std::true_type{});
-        else
-            f(fm, std::false_type{});
-    };
-    if (form == kDecay)
-        go(std::integral_constant<GateForm, kDecay>{});
-    else if (form == kLog)
-        go(std::integral_constant<GateForm, kLog>{});
-    else
-        go(std::integral_constant<GateForm, kSigmoid>{});
+    if (plan.words) {
+        const int64_t vecs = (plan.words + 1) / 2, blocks = (vecs + kThreads - 1) / kThreads;
+        gated_clear_kernel<<<dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(kThreads), 0, stream>>>(
+            reinterpret_cast<u32x4*>(scratch), vecs);
+    }
+    return GatedWords{scratch, scratch + plan.pair_words, spin_limit};
 }
 
-template <typename F> static hipError_t with_type(ElemKind kind, int form, bool mix, F&& f)
+hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan& plan, uint64_t* scratch,
+                             uint32_t spin_limit, hipStream_t stream)
 {
-    with_form(form, mix, [&](auto fm, auto mx) {
-        if (kind == kF32)
-            f(float{}, fm, mx);
-        else if (kind == kBF16)
-            f(bf16{}, fm, mx);
-        else
-            f(fp16{}, fm, mx);
-    });
-    return hipGetLastError();
-}
-
-hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, hipStream_t stream)
-{
+    const GatedWords w = clear_words(plan, scratch, spin_limit, stream);
+    const dim3 grid((unsigned)(plan.tiles * plan.cblocks)), block(kThreads);
     return with_type(kind, a.form, a.mix, [&](auto t, auto fm, auto mx) {
-        gated_scan_kernel<decltype(t), decltype(fm)::value, decltype(mx)::value>
-            <<<dim3((unsigned)gated_scan_blocks(a)), dim3(kThreads), 0, stream>>>(a);
-    });
-}
-
-hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, hipStream_t stream)
-{
-    return with_type(kind, a.s.form, a.s.mix, [&](auto t, auto fm, auto mx) {
-        gated_scan_grad_kernel<decltype(t), decltype(fm)::value, decltype(mx)::value>
-            <<<dim3((unsigned)gated_scan_blocks(a.s)), dim3(kThreads), 0, stream>>>(a);
+        using T = decltype(t);
+        if (vector_of(kind, a.dim) == 1)
+            gated_scan_kernel<T, 1, decltype(fm)::value, decltype(mx)::value, kScanRows<T>><<<grid, block, 0, stream>>>(a, w);
+        else
+            gated_scan_kernel<T, Vec16<T>::kN, decltype(fm)::value, decltype(mx)::value, kScanRows<T>>
+                <<<grid, block, 0, stream>>>(a, w);
     });
 }
 

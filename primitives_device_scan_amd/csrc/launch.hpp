@@ -177,10 +177,20 @@ struct GatedStep {
     int form;
     bool mix;
 };
-int64_t gated_scan_blocks(const GatedScan& a);  // workgroups
-int64_t gated_step_blocks(const GatedStep& a);
-hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, hipStream_t stream);
-hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, hipStream_t stream);
+struct GatedPlan {
+    int64_t tiles, cblocks;         // workgroups: tiles x cblocks
+    int64_t pair_words, words;      // 64-bit words of scratch: tiles' pairs, and in all (0: one tile)
+};
+struct GatedWords {
+    uint64_t *pairs, *entries;
+    uint32_t spin_limit;
+};
+GatedPlan gated_plan(ElemKind kind, bool grad, int64_t tokens, int64_t dim);
+int64_t gated_step_blocks(const GatedStep& a);  // workgroups
+hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan& plan, uint64_t* scratch,
+                             uint32_t spin_limit, hipStream_t stream);
+hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, const GatedPlan& plan, uint64_t* scratch,
+                                  uint32_t spin_limit, hipStream_t stream);
 hipError_t launch_gated_step(ElemKind kind, const GatedStep& a, hipStream_t stream);
 
 // Products grouped by expert (16-bit kinds) and the gradient of their weights.

@@ -21,16 +21,17 @@ def test_gated_scan_refusals(lib):
     assert f(gate=A + 2) == MIS and f(x=B + 1) == MIS and f(off=C + 2) == MIS and f(init=D + 2) == MIS and f(final=F + 1) == MIS
     assert f(h=A + 32) == OVL and f(h=B) == OVL and f(final=D) == OVL and f(final=E + 64) == OVL and f(h=C - 64) == OVL
     assert f(t=1 << 31) == BIG and f(d=1 << 31, gs=1 << 31, xs=1 << 31, hs=1 << 31) == BIG and f(n=1 << 31) == BIG
+    assert f(t=1, hs=(1 << 20) + 1) == BIG
     assert f(ws=G, room=-1) == INV and f(ws=G + 8, room=1 << 40) == MIS
     big = dict(dtype=BF16, gate=0x100000000000, x=0x200000000000, h=0x300000000000, t=1 << 16, d=4096, gs=4096, xs=4096, hs=4096)
-    need = lib.ds_gated_scan_scratch_bytes(BF16, 1 << 16, 4096)
-    if need:
-        assert f(**big, ws=G, room=need - 1) == INV and f(**big, ws=0x100000000100, room=need) == OVL
+    need = lib.ds_gated_scan_scratch_bytes(BF16, 0, 1 << 16, 4096)
+    assert need > 0 and f(**big, ws=G, room=need - 1) == INV and f(**big, ws=0x100000000100, room=need) == OVL
 
 
 def test_gated_scan_scratch_bytes(lib):
     f = lib.ds_gated_scan_scratch_bytes
-    assert f(F32, 0, 8) == 0 and f(F32, 8, 0) == 0 and f(0, 8, 8) == 0 and f(F32, 1 << 31, 8) == 0 and f(BF16, 1, 2048) == 0
+    assert f(F32, 0, 0, 8) == 0 and f(F32, 1, 8, 0) == 0 and f(0, 0, 8, 8) == 0 and f(F32, 0, 1 << 31, 8) == 0
+    assert f(BF16, 0, 1, 2048) == 0 and f(BF16, 1, 4000, 2048) > 0
 
 
 def test_gated_scan_grad_refusals(lib):
