@@ -494,7 +494,7 @@ int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void
  *              d_sorted_ids: it is row d_index[r] / top_k of x, a row of zeros
  *              where that lies outside x (padding)
  *   d_y        [m, rows] (transposed: cols), rows y_stride apart
- * Sums in 32 bits. num_experts <= 8,192; m, x_rows < 2^31, rows and cols at most
+ * Sums in 32 bits. num_experts <= 2,048; m, x_rows < 2^31, rows and cols at most
  * DS_EXPERTS_MAX_WIDTH (else DS_ERR_TOO_LARGE).
  */
 int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stride, const void* d_w, int num_experts,

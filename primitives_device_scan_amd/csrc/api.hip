@@ -1030,12 +1030,20 @@ static int check_grouped(int dtype, int64_t x_rows, int num_experts, int64_t row
                          const int32_t* index, int top_k)
 {
     if (dtype != DS_BF16 && dtype != DS_FP16) return DS_ERR_UNSUPPORTED_DTYPE;
-    if (x_rows < 0 || m < 0 || rows < 0 || cols < 0 || num_experts < 0 || num_experts > ds::experts_max_experts() ||
+    if (x_rows < 0 || m < 0 || rows < 0 || cols < 0 || num_experts < 0 || num_experts > ds::grouped_most_experts() ||
         (index ? top_k < 1 : x_rows < m))
         return DS_ERR_INVALID_VALUE;
     return m > kMost31 || x_rows > kMost31 || rows > DS_EXPERTS_MAX_WIDTH || cols > DS_EXPERTS_MAX_WIDTH
                ? DS_ERR_TOO_LARGE
                : DS_OK;
+}
+
+// Division by top_k without one: with 2^shift >= top_k, magic = floor(2^32 (2^shift - top_k) / top_k) + 1.
+static void set_divisor(ds::Grouped& a)
+{
+    const uint64_t d = a.index ? (uint64_t)a.top_k : 1;
+    while (((uint64_t)1 << a.shift) < d) ++a.shift;
+    a.magic = (uint32_t)(((((uint64_t)1 << a.shift) - d) << 32) / d + 1);
 }
 
 int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stride, const void* d_w, int num_experts,
@@ -1055,9 +1063,9 @@ int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stri
                          {d_y, span_bytes(m, out, y_stride, 2), 2, true}};
     st = check_buffers(bufs, 5);
     if (st != DS_OK) return st;
-    const ds::Grouped a{d_x, d_w, d_y, nullptr, x_rows, x_stride, y_stride, m, d_offsets, d_index, num_experts,
-                        top_k, rows, cols, transposed != 0, false};
-    if (ds::grouped_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    ds::Grouped a{d_x, d_w, d_y, nullptr, x_rows, x_stride, y_stride, m, d_offsets, d_index, num_experts, top_k, rows,
+                  cols, x_rows ? depth : 0, transposed != 0, false, 0, 0};
+    set_divisor(a);
     return ds::launch_grouped_matmul(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
 
@@ -1079,9 +1087,10 @@ int ds_grouped_matmul_grad(int dtype, const void* d_dy, int64_t m, int64_t dy_st
                          {d_dw, span_bytes(num_experts * rows, cols, cols, gsz), gsz, true}};
     st = check_buffers(bufs, 5);
     if (st != DS_OK) return st;
-    const ds::Grouped a{d_x, nullptr, const_cast<void*>(d_dy), d_dw, x_rows, x_stride, dy_stride, m, d_offsets,
-                        d_index, num_experts, top_k, rows, cols, false, accumulate != 0};
-    if (ds::grouped_grad_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    // without rows of x every sum is empty, as with groups without rows
+    ds::Grouped a{d_x, nullptr, const_cast<void*>(d_dy), d_dw, x_rows, x_stride, dy_stride, x_rows ? m : 0, d_offsets,
+                  d_index, num_experts, top_k, rows, cols, 0, false, accumulate != 0, 0, 0};
+    set_divisor(a);
     return ds::launch_grouped_matmul_grad(float_kind(dtype), float_kind(grad_dtype), a, stream) == hipSuccess
                ? DS_OK
                : DS_ERR_HIP;

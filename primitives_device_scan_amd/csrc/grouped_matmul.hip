@@ -6,26 +6,59 @@
 //
 // Row r of the batch is row r of x, or, with an index, row index[r] / top_k of
 // it (zeros where that is no row): the batch that the MoE alignment orders.
+//
+// All three are C[m, n] = sum over k of A[m, k] B[n, k], with operands whose
+// memory runs along k (rows of the batch, rows of W) or across it (W transposed,
+// both operands of dW, whose k are rows of the batch). A workgroup of four waves
+// makes a tile of C, 2 x 2 waves of TM x TN blocks of 32 x 32 (the matrix
+// instructions' 32 x 32 x 16), from stages of 32 k in LDS.
+//
+// Operands whose rows start on 16 bytes and whose lengths are whole segments of
+// 16 bytes go to LDS by loads that write it directly, three stages ahead of the
+// one that is multiplied, in one stream over all of a workgroup's tiles. One
+// barrier to a stage; the reads of the next 16 k lie between the matrix
+// instructions of the last. Other operands go through registers (RowsOdd).
+//
+// In LDS an operand along k has 64 bytes of each row, row r's segment s at
+// s ^ (r / 2) mod 4; one across k has lines of all rows, line k's segment s at
+// s ^ 2 (k mod 4), and is turned as it is read (ds_read_b64_tr_b16). In both
+// orders the lanes that are served together lie in different banks.
+//
+// Workgroups stay and take one tile after another; each finds the experts' tiles
+// by a prefix sum of its own over the groups. Workgroup i runs on XCD i % 8: each
+// XCD takes a contiguous run of tiles, so that what its tiles share is in its L2.
+#include <type_traits>
+
 #include "float_types.hpp"
 #include "launch.hpp"
 
 namespace ds {
 
-typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
 
-__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c)
+template <typename T>
+__device__ __forceinline__ f32x16 mma32(const u32x4& a, const u32x4& b, f32x16 c)
 {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    if constexpr (__is_same(T, bf16))
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                       0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0,
+                                                      0);
 }
-__device__ __forceinline__ f32x4 mma(f16x8 a, f16x8 b, f32x4 c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-template <typename T> struct Vec8;
-template <> struct Vec8<bf16> { using type = bf16x8; };
-template <> struct Vec8<fp16> { using type = f16x8; };
+
+constexpr int kDepth = 32;           // k of a stage
+constexpr int kBlockBytes = 4096;    // of a stage, for 64 rows of an operand
+constexpr int kRing = 4;             // stages in LDS
+constexpr int kMostGroups = 2048;
+constexpr int kXcds = 8;
+
+// What lanes that have nothing to load read instead.
+static __device__ __align__(16) uint32_t zeros[4];
 
 __device__ __forceinline__ void group_range(const Grouped& a, int e, int64_t& first, int64_t& end)
 {
@@ -33,151 +66,677 @@ __device__ __forceinline__ void group_range(const Grouped& a, int e, int64_t& fi
     end = min(max((int64_t)a.offsets[e + 1], first), a.m);
 }
 
-// The row of x that row r of the batch is, or -1.
+// The row of x that an entry of the index names, or -1; entry / top_k by a
+// product (n < 2^31: (n + mulhi(n, magic)) >> shift).
+__device__ __forceinline__ int32_t row_of_entry(const Grouped& a, int32_t i)
+{
+    const uint32_t n = (uint32_t)i, t = (n + __umulhi(n, a.magic)) >> a.shift;
+    const bool none = (i < 0) | ((int64_t)t >= a.x_rows);
+    return none ? -1 : (int32_t)t;
+}
 __device__ __forceinline__ int64_t batch_row(const Grouped& a, int64_t r)
 {
-    if (!a.index) return r;
-    const int64_t i = a.index[r];
-    const int64_t t = i / a.top_k;
-    return i >= 0 && t < a.x_rows ? t : -1;
+    return a.index ? row_of_entry(a, a.index[r]) : r;
 }
 
-constexpr int kTile = 64, kDepth = 32, kPad = 8;
-
-// C (64 x 64) of a workgroup's four waves, each a 32 x 32 quarter.
-template <typename T, typename LA, typename LB, typename ST>
-__device__ __forceinline__ void tile_product(int64_t depth, LA&& load_a, LB&& load_b, ST&& store)
+// This lane's 8 k of one row: of block `b` of 32 rows from `first` on, half `kk`
+// of the stage, from an operand of 64 R rows.
+template <int R, bool ACROSS>
+__device__ __forceinline__ u32x4 read_fragment(const lds_char* stage, int first, int b, int kk, int lane)
 {
-    __shared__ T sa[kTile][kDepth + kPad], sb[kTile][kDepth + kPad];
-    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
-    f32x4 acc[2][2] = {};
-    for (int64_t k0 = 0; k0 < depth; k0 += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += kThreads) {
-            sa[i / kDepth][i % kDepth] = load_a(i / kDepth, k0 + i % kDepth);
-            sb[i / kDepth][i % kDepth] = load_b(i / kDepth, k0 + i % kDepth);
+    if constexpr (!ACROSS) {
+        const int r = first + lane % 32;
+        return *reinterpret_cast<const __attribute__((address_space(3))) u32x4*>(
+            stage + r * 64 + (((kk * 2 + lane / 32) ^ (r >> 1)) & 3) * 16 + b * 32 * 64);
+    } else {
+        // of 16 lanes, lanes 4 j .. 4 j + 3 name 16 rows of line j, and each lane
+        // receives what four lines have of its own row
+        const int j = lane % 16 / 4, line = kk * 16 + lane / 32 * 8 + j;
+        const int row = first + 32 * b + lane / 16 % 2 * 16 + lane % 4 * 4;
+        const lds_char* const at = stage + line * (128 * R) + (row / 8 ^ j * 2) * 16 + row % 8 * 2;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 4 * 128 * R));
+        u32x4 v;
+        __builtin_memcpy(&v, &lo, 8);
+        __builtin_memcpy(reinterpret_cast<char*>(&v) + 8, &hi, 8);
+        return v;
+    }
+}
+
+enum GroupedOp { kProduct = 0, kTransposed = 1, kGradient = 2 };
+
+// A tile of C and where its operands are.
+struct Tile {
+    int m0, n0;           // in y: row of the batch, column; in dW_e: row, column
+    int e, first, end;    // the expert and its rows
+    int depth;
+    bool there;
+};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// The tile of this workgroup's turn: workgroup i of XCD i % 8 takes every
+// (grid / 8)-th tile of the XCD's contiguous run. -1: none left.
+__device__ __forceinline__ int tile_of_turn(int turn, int tiles)
+{
+    const int run = (tiles + kXcds - 1) / kXcds, per = (int)gridDim.x / kXcds;
+    const int at = (int)blockIdx.x / kXcds + turn * per, tile = (int)blockIdx.x % kXcds * run + at;
+    return at < run && tile < tiles ? tile : -1;
+}
+
+// s_first[e] = blocks of `size` rows in the groups before e; returns all of them.
+__device__ __forceinline__ int count_blocks(const Grouped& a, int size, int* s_first)
+{
+    __shared__ int s_wave[kWaves];
+    int before = 0;
+    for (int base = 0; base < a.experts; base += kThreads) {
+        const int e = base + (int)threadIdx.x;
+        int n = 0;
+        if (e < a.experts) {
+            int64_t first, end;
+            group_range(a, e, first, end);
+            n = (int)((end - first + size - 1) / size);
         }
+        const int to = wave_inclusive_scan(n);
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                typename Vec8<T>::type va, vb;
-                __builtin_memcpy(&va, &sa[wave / 2 * 32 + i * 16 + lane % 16][lane / 16 * 8], 16);
-                __builtin_memcpy(&vb, &sb[wave % 2 * 32 + j * 16 + lane % 16][lane / 16 * 8], 16);
-                acc[i][j] = mma(va, vb, acc[i][j]);
-            }
+        if (lane_id() == kWave - 1) s_wave[threadIdx.x / kWave] = to;
         __syncthreads();
+        int from = before;
+        for (int w = 0; w < kWaves; ++w) {
+            if (w < (int)threadIdx.x / kWave) from += s_wave[w];
+            before += s_wave[w];
+        }
+        if (e < a.experts) s_first[e] = from + to - n;
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                store(wave / 2 * 32 + i * 16 + lane / 16 * 4 + k, wave % 2 * 32 + j * 16 + lane % 16, acc[i][j][k]);
+    __syncthreads();
+    return uniform(before);
 }
 
-template <typename T, bool TRANSPOSED>
-__global__ __launch_bounds__(kThreads) void grouped_kernel(Grouped a)
+// Columns and depth of C; the gradient's C is rows x cols and its depth the group's rows.
+template <GroupedOp OP> __device__ __forceinline__ int64_t width_of(const Grouped& a) { return OP == kProduct ? a.rows : a.cols; }
+
+template <GroupedOp OP, int M, int N>
+__device__ __forceinline__ int count_tiles(const Grouped& a, int* s_first)
 {
-    const int64_t out = TRANSPOSED ? a.cols : a.rows, depth = TRANSPOSED ? a.rows : a.cols;
-    const int64_t ntiles = (out + kTile - 1) / kTile;
-    int64_t mt = blockIdx.x / ntiles;
-    const int64_t n0 = blockIdx.x % ntiles * kTile;
-    int e = 0;
-    int64_t first = 0, end = 0;
-    for (;; ++e) {
-        if (e == a.experts) return;
-        group_range(a, e, first, end);
-        const int64_t tiles = (end - first + kTile - 1) / kTile;
-        if (mt < tiles) break;
-        mt -= tiles;
-    }
-    const int64_t m0 = first + mt * kTile;
-    const T* x = static_cast<const T*>(a.x);
-    const T* w = static_cast<const T*>(a.w) + (int64_t)e * a.rows * a.cols;
-    T* y = static_cast<T*>(a.y);
-    tile_product<T>(
-        depth,
-        [&](int i, int64_t k) {
-            const int64_t r = m0 + i < end ? batch_row(a, m0 + i) : -1;
-            return r >= 0 && k < depth ? x[r * a.x_stride + k] : (T)0.0f;
-        },
-        [&](int j, int64_t k) {
-            if (n0 + j >= out || k >= depth) return (T)0.0f;
-            return TRANSPOSED ? w[k * a.cols + n0 + j] : w[(n0 + j) * a.cols + k];
-        },
-        [&](int i, int j, float v) {
-            if (m0 + i < end && n0 + j < out) y[(m0 + i) * a.y_stride + n0 + j] = (T)v;
-        });
+    const int wide = (int)((width_of<OP>(a) + N - 1) / N);
+    if constexpr (OP == kGradient) return a.experts * (int)((a.rows + M - 1) / M) * wide;
+    return count_blocks(a, M, s_first) * wide;
 }
 
-template <typename T, typename G>
-__global__ __launch_bounds__(kThreads) void grouped_grad_kernel(Grouped a)
+template <GroupedOp OP, int M, int N>
+__device__ __forceinline__ Tile find_tile(const Grouped& a, int turn, int tiles, const int* s_first)
 {
-    const int64_t tr = (a.rows + kTile - 1) / kTile, tc = (a.cols + kTile - 1) / kTile;
-    const int e = (int)(blockIdx.x / (tr * tc));
-    const int64_t i0 = blockIdx.x / tc % tr * kTile, j0 = blockIdx.x % tc * kTile;
+    Tile t = {};
+    const int tile = tile_of_turn(turn, tiles);
+    t.there = tile >= 0;
+    if (!t.there) return t;
+    const int wide = (int)((width_of<OP>(a) + N - 1) / N), block = tile / wide;
+    t.n0 = tile % wide * N;
+    int in = block;  // the block among the expert's
+    if constexpr (OP == kGradient) {
+        const int high = (int)((a.rows + M - 1) / M);
+        t.e = block / high;
+        in = block % high;
+    } else {
+        int e = 0, over = a.experts;  // the last group with s_first <= block: the one with rows
+        while (over - e > 1) {
+            const int mid = (e + over) >> 1;
+            if (uniform(s_first[mid]) <= block)
+                e = mid;
+            else
+                over = mid;
+        }
+        t.e = e;
+        in -= uniform(s_first[e]);
+    }
     int64_t first, end;
-    group_range(a, e, first, end);
-    const T *x = static_cast<const T*>(a.x), *dy = static_cast<const T*>(a.y);
-    G* dw = static_cast<G*>(a.dw) + (int64_t)e * a.rows * a.cols;
-    tile_product<T>(
-        end - first,
-        [&](int i, int64_t k) { return i0 + i < a.rows && first + k < end ? dy[(first + k) * a.y_stride + i0 + i] : (T)0.0f; },
-        [&](int j, int64_t k) {
-            const int64_t r = j0 + j < a.cols && first + k < end ? batch_row(a, first + k) : -1;
-            return r >= 0 ? x[r * a.x_stride + j0 + j] : (T)0.0f;
-        },
-        [&](int i, int j, float v) {
-            if (i0 + i >= a.rows || j0 + j >= a.cols) return;
-            G* p = dw + (i0 + i) * a.cols + j0 + j;
-            *p = (G)(a.accumulate ? v + (float)*p : v);
-        });
+    group_range(a, t.e, first, end);
+    t.first = uniform((int)first);
+    t.end = uniform((int)end);
+    t.m0 = OP == kGradient ? in * M : t.first + in * M;
+    t.depth = OP == kGradient ? t.end - t.first : (int)a.depth;
+    return t;
 }
 
-int64_t grouped_blocks(const Grouped& a)
+// The rows of x that rows `row[i]` of the tile are; inside the group whatever
+// they are, and where the index names none, some row that is there (its products
+// are not kept).
+template <int N>
+__device__ __forceinline__ void group_rows(const Grouped& a, const Tile& t, int (&row)[N])
 {
-    const int64_t out = a.transposed ? a.cols : a.rows;
-    return ((a.m + kTile - 1) / kTile + a.experts) * ((out + kTile - 1) / kTile);
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = min(t.m0 + row[i], t.end - 1);
+    if (!a.index) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = a.index[row[i]];
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = max(row_of_entry(a, row[i]), 0);
 }
 
-int64_t grouped_grad_blocks(const Grouped& a)
+// 16 bytes a lane straight into LDS, 1 KiB from `to` on. As the compiler's own
+// instruction it would make each read of LDS wait for all of these that came
+// before, since it cannot tell the ring's slots apart; stage_there() has the waits.
+__device__ __forceinline__ void load_to_lds(const char* from, lds_char* to)
 {
-    return (int64_t)a.experts * ((a.rows + kTile - 1) / kTile) * ((a.cols + kTile - 1) / kTile);
+    const uint32_t at = (uint32_t)(uintptr_t)to;  // uniform
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(from) : "m0");
 }
 
-template <typename T> static void launch_typed(const Grouped& a, hipStream_t stream)
+// ---------------------------------------------------------------------------
+// Operands that LDS takes directly. Each of a wave's R loads of a stage brings 1
+// KiB: 16 rows of 64 bytes along k, or 8 / R lines across it.
+// ---------------------------------------------------------------------------
+template <typename T, int R, bool ACROSS> struct Rows {
+    const char* p[R];      // this lane's 16 bytes at k = 0 (across k: of its line)
+    int k[ACROSS ? R : 1]; // their k in a stage
+    int64_t step;          // bytes from one stage to the next
+
+    // along k: rows `stride` apart; rows_of turns the tile's rows into theirs
+    template <typename F>
+    __device__ __forceinline__ void begin_along(const T* base, int64_t stride, F&& rows_of)
+    {
+        const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
+        const int seg = (lane % 4) ^ (lane / 8 % 4);  // (row / 2) % 4 = (lane / 8) % 4
+        k[0] = seg * 8;
+        step = kDepth * (int)sizeof(T);
+        int row[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) row[i] = (wave * R + i) * 16 + lane / 4;
+        rows_of(row);
+#pragma unroll
+        for (int i = 0; i < R; ++i) p[i] = reinterpret_cast<const char*>(base + row[i] * stride + seg * 8);
+    }
+    // across k: lines `stride` apart from `base` on, of `length` elements
+    __device__ __forceinline__ void begin_across(const T* base, int64_t stride, int64_t from, int64_t length)
+    {
+        const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
+        step = kDepth * stride * (int)sizeof(T);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            k[i] = (wave * R + i) * (8 / R) + lane / (8 * R);
+            const int64_t at = from + (lane % (8 * R) ^ k[i] % 4 * 2) * 8;
+            p[i] = reinterpret_cast<const char*>(base + k[i] * stride + min(at, length - 8));
+        }
+    }
+    // the i-th load of a stage; left: k from its first on, what lies past them is 0
+    __device__ __forceinline__ void issue(int i, lds_char* stage, int left)
+    {
+        const int wave = uniform((int)threadIdx.x / kWave);
+        const char* from = p[i];
+        if (k[ACROSS ? i : 0] >= left) from = reinterpret_cast<const char*>(zeros);
+        load_to_lds(from, stage + (wave * R + i) * 1024);
+        p[i] += step;
+    }
+};
+
+// Lines across k that an index names: a wave's 8 lines of a stage are 8
+// successive entries, which it reads into scalar registers a stage ahead.
+template <typename T, int R> struct IndexedRows {
+    int first, end;   // the group's entries
+    int32_t entry[8];
+    int64_t from, length;
+    __device__ __forceinline__ void begin(const Grouped& g, const Tile& t, int64_t from_, int64_t length_)
+    {
+        first = t.first;
+        end = t.end;
+        from = from_;
+        length = length_;
+        fetch(g, 0);
+    }
+    __device__ __forceinline__ void fetch(const Grouped& g, int k0)
+    {
+        const auto* const index = (const __attribute__((address_space(4))) int32_t*)g.index;
+        const int wave = uniform((int)threadIdx.x / kWave);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) entry[i] = index[max(min(first + k0 + wave * 8 + i, end - 1), 0)];
+    }
+    __device__ __forceinline__ void issue(const Grouped& g, int i, lds_char* stage, int left)
+    {
+        const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
+        const int part = lane / (8 * R), k = (wave * R + i) * (8 / R) + part;
+        constexpr int W = 8 / R;  // lines of a load
+        int32_t e = part & 1 ? entry[i * W + 1] : entry[i * W];
+        if constexpr (W >= 4) {
+            const int32_t f = part & 1 ? entry[i * W + 3] : entry[i * W + 2];
+            e = part & 2 ? f : e;
+        }
+        if constexpr (W == 8) {
+            const int32_t f = part & 1 ? entry[5] : entry[4], h = part & 1 ? entry[7] : entry[6];
+            e = part & 4 ? (part & 2 ? h : f) : e;
+        }
+        const int32_t row = row_of_entry(g, e);
+        const int64_t at = min(from + (lane % (8 * R) ^ k % 4 * 2) * 8, length - 8);
+        const char* p = reinterpret_cast<const char*>(g.x) + (row * g.x_stride + at) * (int)sizeof(T);
+        const bool none = (row < 0) | (k >= left);
+        p = none ? reinterpret_cast<const char*>(zeros) : p;
+        load_to_lds(p, stage + (wave * R + i) * 1024);
+    }
+};
+
+// One sum. Those of 256 blocks a wave lie in accumulation registers and are moved
+// one by one as they are written: left to the compiler they are all moved before
+// the first, and what the tiles' loop holds is spilled for it. settle() has to
+// come between the last matrix instruction and the first of these.
+template <bool MOVED>
+__device__ __forceinline__ float sum_of(float acc)
 {
-    const dim3 grid((unsigned)grouped_blocks(a)), block(kThreads);
+    if constexpr (!MOVED) return acc;
+    float v;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(v) : "a"(acc));
+    return v;
+}
+__device__ __forceinline__ void settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A wave's part of C: lane l has, of block (j, i), row m = l % 32 and the columns
+// n = 8 q + 4 (l / 32) + 0 .. 3 for q = 0 .. 3. `rows`, `cols`: of C from the
+// tile on; WHOLE: cols is a multiple of 4.
+template <typename G, int TM, int TN, bool WHOLE>
+__device__ __forceinline__ void write_tile(const f32x16 (&acc)[TN][TM], G* c, int64_t stride, int rows, int cols, bool add,
+                                           uint32_t kept)
+{
+    const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
+    const int m0 = wave / 2 * 32 * TM + lane % 32, n0 = wave % 2 * 32 * TN + lane / 32 * 4;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        if (m0 + 32 * i >= rows) continue;
+        G* const row = c + (m0 + 32 * i) * stride + n0;
+        const bool keep = kept >> i & 1;
+        int left = cols - n0;
+        asm volatile("" : "+v"(left));  // compared anew for each row: kept masks would not fit
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = 32 * j + 8 * q;
+                if (WHOLE ? n < left : n + 4 <= left) {
+                    G g[4];
+                    float v[4];
+                    if (add) __builtin_memcpy(g, row + n, sizeof(g));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float sum = sum_of<(TM * TN > 4)>(acc[j][i][4 * q + k]);
+                        v[k] = keep ? sum : 0.0f;
+                        g[k] = (G)(add ? v[k] + (float)g[k] : v[k]);
+                    }
+                    __builtin_memcpy(row + n, g, sizeof(g));
+                } else if (!WHOLE) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (n + k < left) {
+                            const float v = keep ? acc[j][i][4 * q + k] : 0.0f;
+                            row[n + k] = (G)(add ? v + (float)row[n + k] : v);
+                        }
+                }
+            }
+    }
+}
+
+template <typename T, typename G, int TM, int TN, GroupedOp OP, bool WHOLE>
+__device__ __forceinline__ void write_out(const Grouped& a, const Tile& t, const f32x16 (&acc)[TN][TM])
+{
+    if constexpr (OP == kGradient) {
+        G* const c = static_cast<G*>(a.dw) + ((int64_t)t.e * a.rows + t.m0) * a.cols + t.n0;
+        const int rows = (int)a.rows - t.m0, cols = (int)a.cols - t.n0;
+        if (!a.accumulate)
+            write_tile<G, TM, TN, WHOLE>(acc, c, a.cols, rows, cols, false, ~0u);
+        else if (t.depth > 0)
+            write_tile<G, TM, TN, WHOLE>(acc, c, a.cols, rows, cols, true, ~0u);
+    } else {
+        uint32_t kept = ~0u;  // bit i: row i of this lane is one that the index names
+        if (a.index)
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int r = t.m0 + (int)threadIdx.x / (2 * kWave) * 32 * TM + lane_id() % 32 + 32 * i;
+                if (row_of_entry(a, a.index[min(r, t.end - 1)]) < 0) kept &= ~(1u << i);
+            }
+        write_tile<G, TM, TN, WHOLE>(acc, static_cast<G*>(a.y) + t.m0 * a.y_stride + t.n0, a.y_stride, t.end - t.m0,
+                                     (int)width_of<OP>(a) - t.n0, false, kept);
+    }
+}
+
+template <typename T, typename G, int TM, int TN, GroupedOp OP, bool INDEXED>
+__global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(Grouped a)
+{
+    constexpr int kM = 64 * TM, kN = 64 * TN, kStage = (TM + TN) * kBlockBytes, kLoads = TM + TN;
+    __shared__ __align__(128) char ring[kRing * kStage];
+    __shared__ int s_first[OP == kGradient ? 1 : kMostGroups];
+    const int tiles = count_tiles<OP, kM, kN>(a, s_first);
+    const auto tile_at = [&](int turn) { return find_tile<OP, kM, kN>(a, turn, tiles, s_first); };
+    Tile now = tile_at(0), ahead = now;
+    if (!now.there) return;
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
+    const int am = wave / 2 * 32 * TM, bn = wave % 2 * 32 * TN;
+
+    // The stream of stages: `ahead` and its k are three stages before what is multiplied.
+    Rows<T, TM, OP == kGradient> ra;
+    typename std::conditional<INDEXED, IndexedRows<T, TN>, Rows<T, TN, OP != kProduct>>::type rb;
+    int ahead_turn = 0, ahead_k = 0;
+    const auto begin = [&] {
+        const T* const w = static_cast<const T*>(a.w) + (int64_t)ahead.e * a.rows * a.cols;
+        const T* const x = static_cast<const T*>(a.x);
+        if constexpr (OP == kGradient) {
+            ra.begin_across(static_cast<const T*>(a.y) + ahead.first * a.y_stride, a.y_stride, ahead.m0, a.rows);
+            if constexpr (INDEXED)
+                rb.begin(a, ahead, ahead.n0, a.cols);
+            else
+                rb.begin_across(x + ahead.first * a.x_stride, a.x_stride, ahead.n0, a.cols);
+        } else {
+            ra.begin_along(x, a.x_stride, [&](int (&row)[TM]) { group_rows(a, ahead, row); });
+            if constexpr (OP == kTransposed)
+                rb.begin_across(w, a.cols, ahead.n0, a.cols);
+            else
+                rb.begin_along(w, a.cols, [&](int (&row)[TN]) {
+#pragma unroll
+                    for (int i = 0; i < TN; ++i) row[i] = min(ahead.n0 + row[i], (int)a.rows - 1);
+                });
+        }
+    };
+    const auto issue = [&](int i, int slot) {  // one of kLoads of a stage
+        lds_char* const stage = (lds_char*)(ring + slot * kStage);
+        const int left = ahead.depth - ahead_k;
+        if (i < TM)
+            ra.issue(i, stage, left);
+        else if constexpr (INDEXED)
+            rb.issue(a, i - TM, stage + TM * kBlockBytes, left);
+        else
+            rb.issue(i - TM, stage + TM * kBlockBytes, left);
+    };
+    const auto next = [&] {  // once the tile's last stage is on its way
+        if (ahead_k < ahead.depth || !ahead.there) return;
+        ahead = tile_at(++ahead_turn);  // none left: depth 0, zeros
+        ahead_k = 0;
+        if (ahead.there) begin();
+    };
+    u32x4 fa[2][TM], fb[2][TN];
+    const auto read = [&](int i, int slot, int kk) {  // one of kLoads fragments
+        const lds_char* const stage = (const lds_char*)(ring + slot * kStage);
+        if (i < TM)
+            fa[kk][i] = read_fragment<TM, OP == kGradient>(stage, am, i, kk, lane);
+        else
+            fb[kk][i - TM] = read_fragment<TN, OP != kProduct>(stage + TM * kBlockBytes, bn, i - TM, kk, lane);
+    };
+    f32x16 acc[TN][TM];
+    // The products of half `kk`, and between them, each in its place, `count` other steps.
+    const auto multiply = [&](int kk, auto count, auto&& step) {
+        constexpr int kSteps = decltype(count)::value, kEach = (kSteps + TM * TN - 1) / (TM * TN);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int t = 0; t < TM * TN; ++t) {
+            acc[t / TM][t % TM] = mma32<T>(fb[kk][t / TM], fa[kk][t % TM], acc[t / TM][t % TM]);
+#pragma unroll
+            for (int i = t * kEach; i < (t + 1) * kEach; ++i)
+                if (i < kSteps) step(i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // At most the two stages after the next are still to come; this wave's reads
+    // are done, so that after the barrier the slot they were of may be filled.
+    const auto stage_there = [&] {
+        if constexpr (kLoads == 8)
+            asm volatile("s_waitcnt vmcnt(16) lgkmcnt(0)" ::: "memory");
+        else if constexpr (kLoads == 4)
+            asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+        else
+            asm volatile("s_waitcnt vmcnt(4) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    static_assert(kLoads == 8 || kLoads == 4 || kLoads == 2, "the waits above");
+
+    begin();
+    for (int slot = 0; slot < kRing - 1; ++slot) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) issue(i, slot);
+        ahead_k += kDepth;
+        if constexpr (INDEXED) rb.fetch(a, ahead_k);
+        next();
+    }
+    stage_there();
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) read(i, 0, 0);
+    int slot = 0, turn = 0;
+    for (;;) {
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) acc[j][i][k] = 0.0f;
+        for (int k0 = 0; k0 < now.depth || k0 == 0; k0 += kDepth) {
+            const int free = (slot + kRing - 1) % kRing;
+            multiply(0, std::integral_constant<int, 2 * kLoads>{}, [&](int i) {
+                if (i < kLoads)
+                    read(i, slot, 1);
+                else
+                    issue(i - kLoads, free);
+            });
+            ahead_k += kDepth;
+            stage_there();
+            slot = (slot + 1) % kRing;
+            if constexpr (INDEXED) rb.fetch(a, ahead_k);
+            multiply(1, std::integral_constant<int, kLoads>{}, [&](int i) { read(i, slot, 0); });
+            next();
+        }
+        settle();
+        write_out<T, G, TM, TN, OP, true>(a, now, acc);
+        now = tile_at(++turn);
+        if (!now.there) break;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+}
+
+// ---------------------------------------------------------------------------
+// Operands of any alignment and length, through registers.
+// ---------------------------------------------------------------------------
+// 8 elements of a line from `at` on, 0 past its end, from one load inside it.
+template <typename T>
+__device__ __forceinline__ u32x4 load_odd(const T* line, int64_t at, int64_t length, bool there)
+{
+    if (length < 8) {  // uniform
+        u32x4 v = {0, 0, 0, 0};
+        if (there && at < length) v = load_end<T>(line, at, length);
+        return v;
+    }
+    const u32x4 v = load_end<T>(line, at, length);
+    return there ? v : u32x4{0, 0, 0, 0};
+}
+
+template <typename T, int R, bool ACROSS> struct RowsOdd {
+    const T* line[R];  // along k: the row's; across: of k in the first stage
+    bool there[R];
+    int64_t from, length;
+    u32x4 staged[R];
+    static __device__ __forceinline__ int place(int i) { return ACROSS ? (i * kThreads + (int)threadIdx.x) / (8 * R) : i * 64 + (int)threadIdx.x / 4; }
+    static __device__ __forceinline__ int segment(int i) { return ACROSS ? (i * kThreads + (int)threadIdx.x) % (8 * R) : (int)threadIdx.x % 4; }
+    // line_of(place, &there): a line that is there in any case
+    template <typename F>
+    __device__ __forceinline__ void load(int k0, int depth, F&& line_of)
+    {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            bool is = true;
+            const T* const l = line_of(place(i), is);
+            staged[i] = load_odd<T>(l, ACROSS ? from + segment(i) * 8 : k0 + segment(i) * 8, ACROSS ? length : depth, is);
+        }
+    }
+    __device__ __forceinline__ void put(lds_char* stage) const
+    {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int p = place(i), s = segment(i);
+            lds_char* const to = ACROSS ? stage + p * (128 * R) + (s ^ p % 4 * 2) * 16 : stage + p * 64 + ((s ^ (p >> 1)) & 3) * 16;
+            *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(to) = staged[i];
+        }
+    }
+};
+
+template <typename T, typename G, int TM, int TN, GroupedOp OP>
+__global__ __launch_bounds__(kThreads, 2) void grouped_odd_kernel(Grouped a)
+{
+    constexpr int kM = 64 * TM, kN = 64 * TN, kStage = (TM + TN) * kBlockBytes;
+    __shared__ __align__(128) char ring[2 * kStage];
+    __shared__ int s_first[OP == kGradient ? 1 : kMostGroups];
+    const int tiles = count_tiles<OP, kM, kN>(a, s_first);
+    const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
+    const int am = wave / 2 * 32 * TM, bn = wave % 2 * 32 * TN;
+    const T* const x = static_cast<const T*>(a.x);
+    for (int turn = 0;; ++turn) {
+        const Tile t = find_tile<OP, kM, kN>(a, turn, tiles, s_first);
+        if (!t.there) break;
+        const T* const w = static_cast<const T*>(a.w) + (int64_t)t.e * a.rows * a.cols;
+        RowsOdd<T, TM, OP == kGradient> ra;
+        RowsOdd<T, TN, OP != kProduct> rb;
+        ra.from = t.m0;
+        ra.length = a.rows;
+        rb.from = t.n0;
+        rb.length = a.cols;
+        int xrow[TM];  // of the rows that this thread loads
+        if constexpr (OP != kGradient) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) xrow[i] = RowsOdd<T, TM, false>::place(i);
+            group_rows(a, t, xrow);
+        }
+        const auto load = [&](int k0) {
+            if constexpr (OP == kGradient) {
+                ra.load(k0, t.depth, [&](int k, bool& is) {
+                    is = k0 + k < t.depth;
+                    return static_cast<const T*>(a.y) + (t.first + min(k0 + k, t.depth - 1)) * a.y_stride;
+                });
+                rb.load(k0, t.depth, [&](int k, bool& is) {
+                    const int64_t r = batch_row(a, t.first + min(k0 + k, t.depth - 1));
+                    is = k0 + k < t.depth && r >= 0;
+                    return x + max(r, (int64_t)0) * a.x_stride;
+                });
+            } else {
+                int i = 0;
+                ra.load(k0, t.depth, [&](int, bool&) { return x + xrow[i++] * a.x_stride; });
+                if constexpr (OP == kTransposed)
+                    rb.load(k0, t.depth, [&](int k, bool& is) {
+                        is = k0 + k < t.depth;
+                        return w + (int64_t)min(k0 + k, t.depth - 1) * a.cols;
+                    });
+                else
+                    rb.load(k0, t.depth, [&](int n, bool&) { return w + min((int64_t)t.n0 + n, a.rows - 1) * a.cols; });
+            }
+        };
+        const auto put = [&](int slot) {
+            ra.put((lds_char*)(ring + slot * kStage));
+            rb.put((lds_char*)(ring + slot * kStage + TM * kBlockBytes));
+        };
+        f32x16 acc[TN][TM] = {};
+        if (t.depth > 0) {
+            load(0);
+            __syncthreads();  // the tile before is done with the slots
+            put(0);
+            for (int k0 = 0, slot = 0; k0 < t.depth; k0 += kDepth, slot ^= 1) {
+                const bool more = k0 + kDepth < t.depth;
+                if (more) load(k0 + kDepth);
+                __syncthreads();
+                const lds_char* const stage = (const lds_char*)(ring + slot * kStage);
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    u32x4 fa[TM], fb[TN];
+#pragma unroll
+                    for (int i = 0; i < TM; ++i) fa[i] = read_fragment<TM, OP == kGradient>(stage, am, i, kk, lane);
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+                        fb[j] = read_fragment<TN, OP != kProduct>(stage + TM * kBlockBytes, bn, j, kk, lane);
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+#pragma unroll
+                        for (int i = 0; i < TM; ++i) acc[j][i] = mma32<T>(fb[j], fa[i], acc[j][i]);
+                }
+                if (more) put(slot ^ 1);
+            }
+        }
+        write_out<T, G, TM, TN, OP, false>(a, t, acc);
+    }
+}
+
+int grouped_most_experts() { return kMostGroups; }
+
+constexpr int kCus = 256;
+
+// Tiles of C in tiles of m x n, at most (a product's go by the lengths of the groups).
+static int64_t most_tiles(GroupedOp op, const Grouped& a, int m, int n)
+{
+    const int64_t wide = ((op == kProduct ? a.rows : a.cols) + n - 1) / n;
+    if (op == kGradient) return a.experts * ((a.rows + m - 1) / m) * wide;
+    return ((a.m + m - 1) / m + (a.experts < a.m ? a.experts : a.m)) * wide;
+}
+
+static dim3 resident(int64_t tiles, int per_cu)
+{
+    const int64_t most = (int64_t)kCus * per_cu, need = (tiles + kXcds - 1) / kXcds * kXcds;
+    return dim3((unsigned)(need < most ? need : most));
+}
+
+template <typename T, typename G, GroupedOp OP> static void launch_op(const Grouped& a, hipStream_t stream)
+{
+    const auto even = [](const void* p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; };
+    const dim3 block(kThreads);
+    const bool whole = a.rows % 8 == 0 && a.cols % 8 == 0 && a.x_rows > 0 && even(a.x, a.x_stride) &&
+                       (OP == kGradient ? even(a.y, a.y_stride) : even(a.w, 0) && a.depth > 0);
+    if (!whole) {
+        grouped_odd_kernel<T, G, 1, 2, OP><<<resident(most_tiles(OP, a, 64, 128), 2), block, 0, stream>>>(a);
+        return;
+    }
+    const auto go = [&](auto tm, auto indexed) {
+        constexpr int R = decltype(tm)::value;
+        const dim3 grid = resident(most_tiles(OP, a, 64 * R, 64 * R), R == 4 ? 1 : R == 2 ? 2 : 4);
+        grouped_kernel<T, G, R, R, OP, decltype(indexed)::value><<<grid, block, 0, stream>>>(a);
+    };
+    const auto sized = [&](auto indexed) {
+        if (most_tiles(OP, a, 256, 256) >= 2 * kCus)
+            go(std::integral_constant<int, 4>{}, indexed);
+        else if (most_tiles(OP, a, 128, 128) >= 2 * kCus)
+            go(std::integral_constant<int, 2>{}, indexed);
+        else
+            go(std::integral_constant<int, 1>{}, indexed);
+    };
+    if constexpr (OP == kGradient) {
+        if (a.index) {
+            sized(std::true_type{});
+            return;
+        }
+    }
+    sized(std::false_type{});
+}
+
+template <typename T> static void launch_product(const Grouped& a, hipStream_t stream)
+{
     if (a.transposed)
-        grouped_kernel<T, true><<<grid, block, 0, stream>>>(a);
+        launch_op<T, T, kTransposed>(a, stream);
     else
-        grouped_kernel<T, false><<<grid, block, 0, stream>>>(a);
+        launch_op<T, T, kProduct>(a, stream);
 }
 
 hipError_t launch_grouped_matmul(ElemKind kind, const Grouped& a, hipStream_t stream)
 {
     if (kind == kBF16)
-        launch_typed<bf16>(a, stream);
+        launch_product<bf16>(a, stream);
     else
-        launch_typed<fp16>(a, stream);
+        launch_product<fp16>(a, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_grouped_matmul_grad(ElemKind kind, ElemKind grad_kind, const Grouped& a, hipStream_t stream)
 {
-    const dim3 grid((unsigned)grouped_grad_blocks(a)), block(kThreads);
     if (kind == kBF16) {
         if (grad_kind == kF32)
-            grouped_grad_kernel<bf16, float><<<grid, block, 0, stream>>>(a);
+            launch_op<bf16, float, kGradient>(a, stream);
         else
-            grouped_grad_kernel<bf16, bf16><<<grid, block, 0, stream>>>(a);
+            launch_op<bf16, bf16, kGradient>(a, stream);
     } else {
         if (grad_kind == kF32)
-            grouped_grad_kernel<fp16, float><<<grid, block, 0, stream>>>(a);
+            launch_op<fp16, float, kGradient>(a, stream);
         else
-            grouped_grad_kernel<fp16, fp16><<<grid, block, 0, stream>>>(a);
+            launch_op<fp16, fp16, kGradient>(a, stream);
     }
     return hipGetLastError();
 }

@@ -202,10 +202,11 @@ struct Grouped {
     const int32_t* index;       // [m] or null
     int experts, top_k;
     int64_t rows, cols;         // of an expert's matrix
+    int64_t depth;              // of a product: cols, transposed rows; 0 if x has no rows
     bool transposed, accumulate;
+    uint32_t magic, shift;      // i / top_k = (i + mulhi(i, magic)) >> shift for 0 <= i < 2^31
 };
-int64_t grouped_blocks(const Grouped& a);  // workgroups
-int64_t grouped_grad_blocks(const Grouped& a);
+int grouped_most_experts();
 hipError_t launch_grouped_matmul(ElemKind kind, const Grouped& a, hipStream_t stream);
 hipError_t launch_grouped_matmul_grad(ElemKind kind, ElemKind grad_kind, const Grouped& a, hipStream_t stream);
 

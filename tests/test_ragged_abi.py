@@ -73,7 +73,7 @@ def test_grouped_refusals(lib):
     def f(dtype=BF16, x=A, xr=20, xs=16, w=B, e=3, rows=24, cols=16, tr=0, off=C, m=30, index=D, k=2, y=E, ys=24):
         return lib.ds_grouped_matmul(dtype, x, xr, xs, w, e, rows, cols, tr, off, m, index, k, y, ys, None)
     assert f(dtype=F32) == DTY and f(dtype=FP8) == DTY and f(dtype=0) == DTY
-    assert f(xr=-1) == INV and f(e=-1) == INV and f(e=8193) == INV and f(rows=-1) == INV and f(cols=-1) == INV and f(m=-1) == INV
+    assert f(xr=-1) == INV and f(e=-1) == INV and f(e=2049) == INV and f(rows=-1) == INV and f(cols=-1) == INV and f(m=-1) == INV
     assert f(tr=2) == INV and f(k=0) == INV and f(xs=15) == INV and f(ys=23) == INV and f(tr=1) == INV  # a row of x is 24 long then
     assert f(index=None) == INV                                    # 20 rows for a batch of 30
     for name in ("x", "w", "off", "y"):
