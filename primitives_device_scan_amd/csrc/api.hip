@@ -1044,6 +1044,8 @@ static void set_divisor(ds::Grouped& a)
     const uint64_t d = a.index ? (uint64_t)a.top_k : 1;
     while (((uint64_t)1 << a.shift) < d) ++a.shift;
     a.magic = (uint32_t)(((((uint64_t)1 << a.shift) - d) << 32) / d + 1);
+    const uint64_t all = (uint64_t)a.x_rows * d;
+    a.entries = (uint32_t)(all < ((uint64_t)1 << 31) ? all : (uint64_t)1 << 31);
 }
 
 int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stride, const void* d_w, int num_experts,
@@ -1064,7 +1066,7 @@ int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stri
     st = check_buffers(bufs, 5);
     if (st != DS_OK) return st;
     ds::Grouped a{d_x, d_w, d_y, nullptr, x_rows, x_stride, y_stride, m, d_offsets, d_index, num_experts, top_k, rows,
-                  cols, x_rows ? depth : 0, transposed != 0, false, 0, 0};
+                  cols, x_rows ? depth : 0, transposed != 0, false, 0, 0, 0};
     set_divisor(a);
     return ds::launch_grouped_matmul(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
@@ -1089,7 +1091,7 @@ int ds_grouped_matmul_grad(int dtype, const void* d_dy, int64_t m, int64_t dy_st
     if (st != DS_OK) return st;
     // without rows of x every sum is empty, as with groups without rows
     ds::Grouped a{d_x, nullptr, const_cast<void*>(d_dy), d_dw, x_rows, x_stride, dy_stride, x_rows ? m : 0, d_offsets,
-                  d_index, num_experts, top_k, rows, cols, 0, false, accumulate != 0, 0, 0};
+                  d_index, num_experts, top_k, rows, cols, 0, false, accumulate != 0, 0, 0, 0};
     set_divisor(a);
     return ds::launch_grouped_matmul_grad(float_kind(dtype), float_kind(grad_dtype), a, stream) == hipSuccess
                ? DS_OK

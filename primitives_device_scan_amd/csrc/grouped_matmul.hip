@@ -28,6 +28,7 @@
 // by a prefix sum of its own over the groups. Workgroup i runs on XCD i % 8: each
 // XCD takes a contiguous run of tiles, so that what its tiles share is in its L2.
 #include <type_traits>
+#include <utility>
 
 #include "float_types.hpp"
 #include "launch.hpp"
@@ -58,7 +59,8 @@ constexpr int kMostGroups = 2048;
 constexpr int kXcds = 8;
 
 // What lanes that have nothing to load read instead.
-static __device__ __align__(16) uint32_t zeros[4];
+static __device__ __align__(16) uint32_t zeros[128];  // a line of a tile
+
 
 __device__ __forceinline__ void group_range(const Grouped& a, int e, int64_t& first, int64_t& end)
 {
@@ -67,12 +69,11 @@ __device__ __forceinline__ void group_range(const Grouped& a, int e, int64_t& fi
 }
 
 // The row of x that an entry of the index names, or -1; entry / top_k by a
-// product (n < 2^31: (n + mulhi(n, magic)) >> shift).
+// product (for 0 <= n < 2^31).
 __device__ __forceinline__ int32_t row_of_entry(const Grouped& a, int32_t i)
 {
     const uint32_t n = (uint32_t)i, t = (n + __umulhi(n, a.magic)) >> a.shift;
-    const bool none = (i < 0) | ((int64_t)t >= a.x_rows);
-    return none ? -1 : (int32_t)t;
+    return n < a.entries ? (int32_t)t : -1;
 }
 __device__ __forceinline__ int64_t batch_row(const Grouped& a, int64_t r)
 {
@@ -226,6 +227,15 @@ __device__ __forceinline__ void load_to_lds(const char* from, lds_char* to)
 // Operands that LDS takes directly. Each of a wave's R loads of a stage brings 1
 // KiB: 16 rows of 64 bytes along k, or 8 / R lines across it.
 // ---------------------------------------------------------------------------
+struct Issuer {
+    int wave;
+    const char* none;  // zeros
+    __device__ __forceinline__ Issuer() : wave(uniform((int)threadIdx.x / kWave)), none(reinterpret_cast<const char*>(zeros))
+    {
+        asm volatile("" : "+s"(wave), "+s"(none));  // not worked out anew at each use
+    }
+};
+
 template <typename T, int R, bool ACROSS> struct Rows {
     const char* p[R];      // this lane's 16 bytes at k = 0 (across k: of its line)
     int k[ACROSS ? R : 1]; // their k in a stage
@@ -259,57 +269,65 @@ template <typename T, int R, bool ACROSS> struct Rows {
         }
     }
     // the i-th load of a stage; left: k from its first on, what lies past them is 0
-    __device__ __forceinline__ void issue(int i, lds_char* stage, int left)
+    __device__ __forceinline__ void issue(const Issuer& by, int i, lds_char* stage, int left)
     {
-        const int wave = uniform((int)threadIdx.x / kWave);
-        const char* from = p[i];
-        if (k[ACROSS ? i : 0] >= left) from = reinterpret_cast<const char*>(zeros);
-        load_to_lds(from, stage + (wave * R + i) * 1024);
+        const char* const from = k[ACROSS ? i : 0] >= left ? by.none : p[i];
+        load_to_lds(from, stage + (by.wave * R + i) * 1024);
         p[i] += step;
     }
 };
 
 // Lines across k that an index names: a wave's 8 lines of a stage are 8
-// successive entries, which it reads into scalar registers a stage ahead.
+// successive entries. They are read and turned into addresses in scalar
+// registers, a stage ahead, and a lane only chooses between them.
 template <typename T, int R> struct IndexedRows {
-    int first, end;   // the group's entries
+    static constexpr int W = 8 / R;  // lines of a load
+    int first, depth;                // the group's entries, from this wave's first on, and all of them
     int32_t entry[8];
-    int64_t from, length;
-    __device__ __forceinline__ void begin(const Grouped& g, const Tile& t, int64_t from_, int64_t length_)
+    const char* line[8];             // at the tile's first column; zeros where there is no row
+    int most;                        // bytes from there to the last segment that there is
+    const char* x;
+    __device__ __forceinline__ void begin(const Grouped& g, const Issuer& by, const Tile& t, int from, int length)
     {
-        first = t.first;
-        end = t.end;
-        from = from_;
-        length = length_;
+        first = t.first + by.wave * 8;
+        depth = t.depth - by.wave * 8;
+        most = (length - 8 - from) * (int)sizeof(T);
+        x = static_cast<const char*>(g.x) + from * (int64_t)sizeof(T);
         fetch(g, 0);
+        find(g, by);
     }
+    // k0: of the stage
     __device__ __forceinline__ void fetch(const Grouped& g, int k0)
     {
-        const auto* const index = (const __attribute__((address_space(4))) int32_t*)g.index;
-        const int wave = uniform((int)threadIdx.x / kWave);
+        const auto* const index = (const __attribute__((address_space(4))) int32_t*)g.index + first + k0;
+        if (k0 + 8 <= depth) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) entry[i] = index[max(min(first + k0 + wave * 8 + i, end - 1), 0)];
+            for (int i = 0; i < 8; ++i) entry[i] = index[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) entry[i] = k0 + i < depth ? index[i] : -1;
+        }
     }
-    __device__ __forceinline__ void issue(const Grouped& g, int i, lds_char* stage, int left)
+    template <int I> __device__ __forceinline__ void find_one(const Grouped& g, const Issuer& by)
     {
-        const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
-        const int part = lane / (8 * R), k = (wave * R + i) * (8 / R) + part;
-        constexpr int W = 8 / R;  // lines of a load
-        int32_t e = part & 1 ? entry[i * W + 1] : entry[i * W];
-        if constexpr (W >= 4) {
-            const int32_t f = part & 1 ? entry[i * W + 3] : entry[i * W + 2];
-            e = part & 2 ? f : e;
-        }
-        if constexpr (W == 8) {
-            const int32_t f = part & 1 ? entry[5] : entry[4], h = part & 1 ? entry[7] : entry[6];
-            e = part & 4 ? (part & 2 ? h : f) : e;
-        }
-        const int32_t row = row_of_entry(g, e);
-        const int64_t at = min(from + (lane % (8 * R) ^ k % 4 * 2) * 8, length - 8);
-        const char* p = reinterpret_cast<const char*>(g.x) + (row * g.x_stride + at) * (int)sizeof(T);
-        const bool none = (row < 0) | (k >= left);
-        p = none ? reinterpret_cast<const char*>(zeros) : p;
-        load_to_lds(p, stage + (wave * R + i) * 1024);
+        const uint32_t n = (uint32_t)entry[I], t = (n + __umulhi(n, g.magic)) >> g.shift;
+        const char* const at = x + (int64_t)t * (g.x_stride * (int64_t)sizeof(T));
+        line[I] = n < g.entries ? at : by.none;
+    }
+    __device__ __forceinline__ void find(const Grouped& g, const Issuer& by)
+    {
+        find_one<0>(g, by), find_one<1>(g, by), find_one<2>(g, by), find_one<3>(g, by);
+        find_one<4>(g, by), find_one<5>(g, by), find_one<6>(g, by), find_one<7>(g, by);
+    }
+    template <int I> __device__ __forceinline__ void issue(const Issuer& by, lds_char* stage)
+    {
+        const int lane = lane_id(), part = lane / (8 * R), k = (by.wave * R + I) * W + part;
+        const auto pick = [](bool second, const char* a, const char* b) { return second ? b : a; };
+        const char* e = pick(part & 1, line[I * W], line[I * W + 1]);
+        if constexpr (W >= 4) e = pick(part & 2, e, pick(part & 1, line[I * W + 2], line[I * W + 3]));
+        if constexpr (W == 8)
+            e = pick(part & 4, e, pick(part & 2, pick(part & 1, line[4], line[5]), pick(part & 1, line[6], line[7])));
+        load_to_lds(e + min((lane % (8 * R) ^ k % 4 * 2) * kVecBytes, most), stage + (by.wave * R + I) * 1024);
     }
 };
 
@@ -399,6 +417,16 @@ __device__ __forceinline__ void write_out(const Grouped& a, const Tile& t, const
     }
 }
 
+// f(0), .. f(N - 1) with each number known to the compiler, so that what it picks stays in registers.
+template <typename F, int... I> __device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F> __device__ __forceinline__ void for_each(F&& f)
+{
+    each_of(std::make_integer_sequence<int, N>{}, f);
+}
+
 template <typename T, typename G, int TM, int TN, GroupedOp OP, bool INDEXED>
 __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(Grouped a)
 {
@@ -412,6 +440,7 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
     const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
     const int am = wave / 2 * 32 * TM, bn = wave % 2 * 32 * TN;
 
+    const Issuer by;
     // The stream of stages: `ahead` and its k are three stages before what is multiplied.
     Rows<T, TM, OP == kGradient> ra;
     typename std::conditional<INDEXED, IndexedRows<T, TN>, Rows<T, TN, OP != kProduct>>::type rb;
@@ -422,7 +451,7 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
         if constexpr (OP == kGradient) {
             ra.begin_across(static_cast<const T*>(a.y) + ahead.first * a.y_stride, a.y_stride, ahead.m0, a.rows);
             if constexpr (INDEXED)
-                rb.begin(a, ahead, ahead.n0, a.cols);
+                rb.begin(a, by, ahead, ahead.n0, a.cols);
             else
                 rb.begin_across(x + ahead.first * a.x_stride, a.x_stride, ahead.n0, a.cols);
         } else {
@@ -436,15 +465,16 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
                 });
         }
     };
-    const auto issue = [&](int i, int slot) {  // one of kLoads of a stage
+    const auto issue = [&](auto step, int slot) {  // one of kLoads of a stage
+        constexpr int i = decltype(step)::value;
         lds_char* const stage = (lds_char*)(ring + slot * kStage);
         const int left = ahead.depth - ahead_k;
-        if (i < TM)
-            ra.issue(i, stage, left);
+        if constexpr (i < TM)
+            ra.issue(by, i, stage, left);
         else if constexpr (INDEXED)
-            rb.issue(a, i - TM, stage + TM * kBlockBytes, left);
+            rb.template issue<i - TM>(by, stage + TM * kBlockBytes);
         else
-            rb.issue(i - TM, stage + TM * kBlockBytes, left);
+            rb.issue(by, i - TM, stage + TM * kBlockBytes, left);
     };
     const auto next = [&] {  // once the tile's last stage is on its way
         if (ahead_k < ahead.depth || !ahead.there) return;
@@ -453,26 +483,31 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
         if (ahead.there) begin();
     };
     u32x4 fa[2][TM], fb[2][TN];
-    const auto read = [&](int i, int slot, int kk) {  // one of kLoads fragments
+    const auto read = [&](auto step, int slot, auto half) {  // one of kLoads fragments
+        constexpr int i = decltype(step)::value, kk = decltype(half)::value;
         const lds_char* const stage = (const lds_char*)(ring + slot * kStage);
-        if (i < TM)
+        if constexpr (i < TM)
             fa[kk][i] = read_fragment<TM, OP == kGradient>(stage, am, i, kk, lane);
         else
             fb[kk][i - TM] = read_fragment<TN, OP != kProduct>(stage + TM * kBlockBytes, bn, i - TM, kk, lane);
     };
+    constexpr std::integral_constant<int, 0> kFirst;
+    constexpr std::integral_constant<int, 1> kSecond;
     f32x16 acc[TN][TM];
-    // The products of half `kk`, and between them, each in its place, `count` other steps.
-    const auto multiply = [&](int kk, auto count, auto&& step) {
-        constexpr int kSteps = decltype(count)::value, kEach = (kSteps + TM * TN - 1) / (TM * TN);
+    // The products of a half, and between them, each in its place, `count` other steps.
+    const auto multiply = [&](auto half, auto count, auto&& step) {
+        constexpr int kk = decltype(half)::value, kSteps = decltype(count)::value;
+        constexpr int kEach = (kSteps + TM * TN - 1) / (TM * TN);
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int t = 0; t < TM * TN; ++t) {
-            acc[t / TM][t % TM] = mma32<T>(fb[kk][t / TM], fa[kk][t % TM], acc[t / TM][t % TM]);
-#pragma unroll
-            for (int i = t * kEach; i < (t + 1) * kEach; ++i)
-                if (i < kSteps) step(i);
+        for_each<TM * TN>([&](auto at) {
+            constexpr int t = decltype(at)::value, j = t / TM, i = t % TM;
+            acc[j][i] = mma32<T>(fb[kk][j], fa[kk][i], acc[j][i]);
+            for_each<kEach>([&](auto s) {
+                constexpr int n = t * kEach + decltype(s)::value;
+                if constexpr (n < kSteps) step(std::integral_constant<int, n>{});
+            });
             __builtin_amdgcn_sched_barrier(0);
-        }
+        });
     };
     // At most the two stages after the next are still to come; this wave's reads
     // are done, so that after the barrier the slot they were of may be filled.
@@ -490,15 +525,16 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
 
     begin();
     for (int slot = 0; slot < kRing - 1; ++slot) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) issue(i, slot);
+        for_each<kLoads>([&](auto i) { issue(i, slot); });
         ahead_k += kDepth;
-        if constexpr (INDEXED) rb.fetch(a, ahead_k);
+        if constexpr (INDEXED) {
+            rb.fetch(a, ahead_k);
+            rb.find(a, by);
+        }
         next();
     }
     stage_there();
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) read(i, 0, 0);
+    for_each<kLoads>([&](auto i) { read(i, 0, kFirst); });
     int slot = 0, turn = 0;
     for (;;) {
 #pragma unroll
@@ -509,17 +545,22 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
                 for (int k = 0; k < 16; ++k) acc[j][i][k] = 0.0f;
         for (int k0 = 0; k0 < now.depth || k0 == 0; k0 += kDepth) {
             const int free = (slot + kRing - 1) % kRing;
-            multiply(0, std::integral_constant<int, 2 * kLoads>{}, [&](int i) {
-                if (i < kLoads)
-                    read(i, slot, 1);
+            if constexpr (INDEXED) rb.fetch(a, ahead_k + kDepth);
+            multiply(kFirst, std::integral_constant<int, 2 * kLoads>{}, [&](auto i) {
+                if constexpr (decltype(i)::value < kLoads)
+                    read(i, slot, kSecond);
                 else
-                    issue(i - kLoads, free);
+                    issue(std::integral_constant<int, decltype(i)::value - kLoads>{}, free);
             });
             ahead_k += kDepth;
             stage_there();
             slot = (slot + 1) % kRing;
-            if constexpr (INDEXED) rb.fetch(a, ahead_k);
-            multiply(1, std::integral_constant<int, kLoads>{}, [&](int i) { read(i, slot, 0); });
+            multiply(kSecond, std::integral_constant<int, kLoads + (INDEXED ? 8 : 0)>{}, [&](auto i) {
+                if constexpr (decltype(i)::value < kLoads)
+                    read(i, slot, kFirst);
+                else if constexpr (INDEXED)
+                    rb.template find_one<decltype(i)::value - kLoads>(a, by);
+            });
             next();
         }
         settle();

@@ -205,6 +205,7 @@ struct Grouped {
     int64_t depth;              // of a product: cols, transposed rows; 0 if x has no rows
     bool transposed, accumulate;
     uint32_t magic, shift;      // i / top_k = (i + mulhi(i, magic)) >> shift for 0 <= i < 2^31
+    uint32_t entries;           // index entries below this name a row of x
 };
 int grouped_most_experts();
 hipError_t launch_grouped_matmul(ElemKind kind, const Grouped& a, hipStream_t stream);
