@@ -1068,6 +1068,7 @@ int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stri
     ds::Grouped a{d_x, d_w, d_y, nullptr, x_rows, x_stride, y_stride, m, d_offsets, d_index, num_experts, top_k, rows,
                   cols, x_rows ? depth : 0, transposed != 0, false, 0, 0, 0};
     set_divisor(a);
+    if (ds::grouped_tiles(a, false) > kMost31) return DS_ERR_TOO_LARGE;
     return ds::launch_grouped_matmul(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
 
@@ -1093,6 +1094,7 @@ int ds_grouped_matmul_grad(int dtype, const void* d_dy, int64_t m, int64_t dy_st
     ds::Grouped a{d_x, nullptr, const_cast<void*>(d_dy), d_dw, x_rows, x_stride, dy_stride, x_rows ? m : 0, d_offsets,
                   d_index, num_experts, top_k, rows, cols, 0, false, accumulate != 0, 0, 0, 0};
     set_divisor(a);
+    if (ds::grouped_tiles(a, true) > kMost31) return DS_ERR_TOO_LARGE;
     return ds::launch_grouped_matmul_grad(float_kind(dtype), float_kind(grad_dtype), a, stream) == hipSuccess
                ? DS_OK
                : DS_ERR_HIP;

@@ -116,17 +116,15 @@ struct Tile {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// The tile of this workgroup's turn: workgroup i of XCD i % 8 takes every
-// (grid / 8)-th tile of the XCD's contiguous run. -1: none left.
-__device__ __forceinline__ int tile_of_turn(int turn, int tiles)
-{
-    const int run = (tiles + kXcds - 1) / kXcds, per = (int)gridDim.x / kXcds;
-    const int at = (int)blockIdx.x / kXcds + turn * per, tile = (int)blockIdx.x % kXcds * run + at;
-    return at < run && tile < tiles ? tile : -1;
-}
+// The tiles of this workgroup: every `step`-th of [at, end).
+struct Turns {
+    int at, end, step;
+};
 
-// s_first[e] = blocks of `size` rows in the groups before e; returns all of them.
-__device__ __forceinline__ int count_blocks(const Grouped& a, int size, int* s_first)
+// s_first[e] = the sum of of_rows(group's rows) over the groups before e; returns
+// that over all.
+template <typename F>
+__device__ __forceinline__ int sum_groups(const Grouped& a, int* s_first, F&& of_rows)
 {
     __shared__ int s_wave[kWaves];
     int before = 0;
@@ -136,7 +134,7 @@ __device__ __forceinline__ int count_blocks(const Grouped& a, int size, int* s_f
         if (e < a.experts) {
             int64_t first, end;
             group_range(a, e, first, end);
-            n = (int)((end - first + size - 1) / size);
+            n = of_rows((int)(end - first));
         }
         const int to = wave_inclusive_scan(n);
         __syncthreads();
@@ -153,42 +151,75 @@ __device__ __forceinline__ int count_blocks(const Grouped& a, int size, int* s_f
     return uniform(before);
 }
 
-// Columns and depth of C; the gradient's C is rows x cols and its depth the group's rows.
-template <GroupedOp OP> __device__ __forceinline__ int64_t width_of(const Grouped& a) { return OP == kProduct ? a.rows : a.cols; }
-
-template <GroupedOp OP, int M, int N>
-__device__ __forceinline__ int count_tiles(const Grouped& a, int* s_first)
+// The last group with s_first <= v.
+__device__ __forceinline__ int group_at(const int* s_first, int groups, int v)
 {
-    const int wide = (int)((width_of<OP>(a) + N - 1) / N);
-    if constexpr (OP == kGradient) return a.experts * (int)((a.rows + M - 1) / M) * wide;
-    return count_blocks(a, M, s_first) * wide;
+    int e = 0, over = groups;
+    while (over - e > 1) {
+        const int mid = (e + over) >> 1;
+        if (uniform(s_first[mid]) <= v)
+            e = mid;
+        else
+            over = mid;
+    }
+    return e;
+}
+
+// Columns of C; the gradient's C is rows x cols and its depth the group's rows.
+template <GroupedOp OP> __device__ __forceinline__ int width_of(const Grouped& a)
+{
+    return (int)(OP == kProduct ? a.rows : a.cols);
+}
+
+// Fills s_first and deals out the tiles. Workgroup i runs on XCD i % 8. A
+// product's tiles all cost the same, and each XCD takes an eighth of them. A
+// tile of the gradient costs its group's stages and some for its start and end:
+// the XCDs' runs end where eighths of that cost do (64 experts whose lengths
+// differ by a factor of 8, 65,536 rows in all, 1,536 x 2,048: 589 us with equal
+// numbers of tiles, 534 so).
+template <GroupedOp OP, int M, int N>
+__device__ __forceinline__ Turns deal_tiles(const Grouped& a, int* s_first)
+{
+    constexpr int kTileCost = 4;  // of a tile beside its stages, in stages
+    const int xcd = (int)blockIdx.x % kXcds, among = (int)blockIdx.x / kXcds, per = (int)gridDim.x / kXcds;
+    const int wide = (width_of<OP>(a) + N - 1) / N;
+    int from, to;
+    if constexpr (OP == kGradient) {
+        const int each = ((int)a.rows + M - 1) / M * wide;  // tiles of a group
+        const int64_t cost = sum_groups(a, s_first, [](int rows) { return (rows + kDepth - 1) / kDepth + kTileCost; });
+        const auto tile_at = [&](int64_t v) {  // the first tile that starts at v of the cost or behind it
+            const int e = group_at(s_first, a.experts, (int)v), first = uniform(s_first[e]);
+            const int own = (e + 1 < a.experts ? uniform(s_first[e + 1]) : (int)cost) - first;
+            return e * each + (int)(((v - first) * each + own - 1) / own);
+        };
+        from = xcd == 0 ? 0 : tile_at(cost * xcd / kXcds);
+        to = xcd == kXcds - 1 ? a.experts * each : tile_at(cost * (xcd + 1) / kXcds);
+    } else {
+        const int tiles = sum_groups(a, s_first, [](int rows) { return (rows + M - 1) / M; }) * wide;
+        const int run = (tiles + kXcds - 1) / kXcds;
+        from = xcd * run;
+        to = min(from + run, tiles);
+    }
+    return Turns{from + among, to, per};
 }
 
 template <GroupedOp OP, int M, int N>
-__device__ __forceinline__ Tile find_tile(const Grouped& a, int turn, int tiles, const int* s_first)
+__device__ __forceinline__ Tile find_tile(const Grouped& a, const Turns& turns, int turn, const int* s_first)
 {
     Tile t = {};
-    const int tile = tile_of_turn(turn, tiles);
-    t.there = tile >= 0;
+    const int tile = turns.at + turn * turns.step;
+    t.there = tile < turns.end;
     if (!t.there) return t;
-    const int wide = (int)((width_of<OP>(a) + N - 1) / N), block = tile / wide;
+    const int wide = (width_of<OP>(a) + N - 1) / N, block = tile / wide;
     t.n0 = tile % wide * N;
     int in = block;  // the block among the expert's
     if constexpr (OP == kGradient) {
-        const int high = (int)((a.rows + M - 1) / M);
+        const int high = ((int)a.rows + M - 1) / M;
         t.e = block / high;
         in = block % high;
     } else {
-        int e = 0, over = a.experts;  // the last group with s_first <= block: the one with rows
-        while (over - e > 1) {
-            const int mid = (e + over) >> 1;
-            if (uniform(s_first[mid]) <= block)
-                e = mid;
-            else
-                over = mid;
-        }
-        t.e = e;
-        in -= uniform(s_first[e]);
+        t.e = group_at(s_first, a.experts, block);
+        in -= uniform(s_first[t.e]);
     }
     int64_t first, end;
     group_range(a, t.e, first, end);
@@ -413,7 +444,7 @@ __device__ __forceinline__ void write_out(const Grouped& a, const Tile& t, const
                 if (row_of_entry(a, a.index[min(r, t.end - 1)]) < 0) kept &= ~(1u << i);
             }
         write_tile<G, TM, TN, WHOLE>(acc, static_cast<G*>(a.y) + t.m0 * a.y_stride + t.n0, a.y_stride, t.end - t.m0,
-                                     (int)width_of<OP>(a) - t.n0, false, kept);
+                                     width_of<OP>(a) - t.n0, false, kept);
     }
 }
 
@@ -432,9 +463,9 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
 {
     constexpr int kM = 64 * TM, kN = 64 * TN, kStage = (TM + TN) * kBlockBytes, kLoads = TM + TN;
     __shared__ __align__(128) char ring[kRing * kStage];
-    __shared__ int s_first[OP == kGradient ? 1 : kMostGroups];
-    const int tiles = count_tiles<OP, kM, kN>(a, s_first);
-    const auto tile_at = [&](int turn) { return find_tile<OP, kM, kN>(a, turn, tiles, s_first); };
+    __shared__ int s_first[kMostGroups];
+    const Turns turns = deal_tiles<OP, kM, kN>(a, s_first);
+    const auto tile_at = [&](int turn) { return find_tile<OP, kM, kN>(a, turns, turn, s_first); };
     Tile now = tile_at(0), ahead = now;
     if (!now.there) return;
     const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
@@ -621,13 +652,13 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_odd_kernel(Grouped a)
 {
     constexpr int kM = 64 * TM, kN = 64 * TN, kStage = (TM + TN) * kBlockBytes;
     __shared__ __align__(128) char ring[2 * kStage];
-    __shared__ int s_first[OP == kGradient ? 1 : kMostGroups];
-    const int tiles = count_tiles<OP, kM, kN>(a, s_first);
+    __shared__ int s_first[kMostGroups];
+    const Turns turns = deal_tiles<OP, kM, kN>(a, s_first);
     const int lane = lane_id(), wave = uniform((int)threadIdx.x / kWave);
     const int am = wave / 2 * 32 * TM, bn = wave % 2 * 32 * TN;
     const T* const x = static_cast<const T*>(a.x);
     for (int turn = 0;; ++turn) {
-        const Tile t = find_tile<OP, kM, kN>(a, turn, tiles, s_first);
+        const Tile t = find_tile<OP, kM, kN>(a, turns, turn, s_first);
         if (!t.there) break;
         const T* const w = static_cast<const T*>(a.w) + (int64_t)t.e * a.rows * a.cols;
         RowsOdd<T, TM, OP == kGradient> ra;
@@ -709,6 +740,11 @@ static int64_t most_tiles(GroupedOp op, const Grouped& a, int m, int n)
     const int64_t wide = ((op == kProduct ? a.rows : a.cols) + n - 1) / n;
     if (op == kGradient) return a.experts * ((a.rows + m - 1) / m) * wide;
     return ((a.m + m - 1) / m + (a.experts < a.m ? a.experts : a.m)) * wide;
+}
+
+int64_t grouped_tiles(const Grouped& a, bool gradient)
+{
+    return most_tiles(gradient ? kGradient : a.transposed ? kTransposed : kProduct, a, 64, 64);
 }
 
 static dim3 resident(int64_t tiles, int per_cu)

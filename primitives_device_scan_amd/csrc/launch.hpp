@@ -208,6 +208,7 @@ struct Grouped {
     uint32_t entries;           // index entries below this name a row of x
 };
 int grouped_most_experts();
+int64_t grouped_tiles(const Grouped& a, bool gradient);  // the most that a call works on
 hipError_t launch_grouped_matmul(ElemKind kind, const Grouped& a, hipStream_t stream);
 hipError_t launch_grouped_matmul_grad(ElemKind kind, ElemKind grad_kind, const Grouped& a, hipStream_t stream);
 
