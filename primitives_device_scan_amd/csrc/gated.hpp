@@ -10,9 +10,15 @@
 // which the group before published. Which pairs are joined is fixed by the
 // positions, so results do not depend on which tile was first. A sequence's
 // first row starts anew: a tile that has one needs no earlier state behind it.
+// Tiles of one sequence alone are held in registers; of a tile in which sequences
+// meet, the rows are read a second time, two or four at a time, which costs few
+// registers (the same code for both needed more than there are and spilled).
 //
-// Words between workgroups are 64 bits, a value and a mark of what it is, so
-// that a value needs no order with a flag; a launch before clears them. Tile t
+// Words between workgroups are 64 bits, a pair or a state and which of them it is
+// in one, so that a value needs no order with a flag; a launch before clears them
+// and finds each tile's sequence. A wave waits with one lane to an earlier tile
+// and reads all its channels' words once they are there (each channel polling its
+// own words kept the fabric busy: @@POLL@@). Tile t
 // waits for lower tiles only, which are dispatched before it, and every wait
 // ends after the spin limit (the state is NaN then).
 #pragma once
@@ -29,7 +35,6 @@ namespace ds {
 constexpr int kLanes = 16;                              // lanes side by side in a row
 constexpr int kSub = kThreads / kLanes;                 // parts of a tile's rows
 constexpr int kGroup = 8;                               // tiles to a group
-constexpr uint32_t kPair = 1, kState = 2;               // marks: a pair (A, B), or B alone, a state
 
 // V elements of T at any element alignment, as they lie in memory. An address
 // is a row that all lanes have in common and a lane's bytes from it (32 bits:
@@ -44,6 +49,13 @@ template <typename T, int V> struct Cells {
     __device__ __forceinline__ void store(T* row, uint32_t bytes) const
     {
         *reinterpret_cast<At*>(reinterpret_cast<char*>(row) + bytes) = raw;
+    }
+    __device__ __forceinline__ void fill(T x)
+    {
+        T t[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = x;
+        __builtin_memcpy(&raw, t, sizeof(t));
     }
     __device__ __forceinline__ float operator[](int i) const
     {
@@ -128,64 +140,79 @@ template <typename T> struct Rows {
     __device__ __forceinline__ T* at(int k) const { return row + k * stride; }
 };
 
-__device__ __forceinline__ uint64_t marked(uint32_t mark, float v)
+// A word: 0 while there is nothing, else B and above it A (no NaN but one, its
+// bits turned by kTurn, so that they are never 0), or kState and a state.
+constexpr uint32_t kTurn = 0x7fffffffu, kState = 1;
+__device__ __forceinline__ uint64_t pair_word(float a, float b)
 {
-    return (uint64_t)mark << 32 | __builtin_bit_cast(uint32_t, v);
+    const uint32_t bits = a == a ? __builtin_bit_cast(uint32_t, a) : 0x7fc00000u;
+    return (uint64_t)(bits ^ kTurn) << 32 | __builtin_bit_cast(uint32_t, b);
 }
+__device__ __forceinline__ uint64_t state_word(float h) { return (uint64_t)kState << 32 | __builtin_bit_cast(uint32_t, h); }
+__device__ __forceinline__ float first_of(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)(w >> 32) ^ kTurn); }
+__device__ __forceinline__ float second_of(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); }
 
 // The state that enters tile `tile` in this thread's channel, from the words of
-// the tiles before it. `pairs`, `entries`: this channel's words, of the pairs
-// (two) and of the states that enter groups; `step` words to the next tile's.
+// the tiles before it in its group and of the group; all lanes of a wave call
+// it. `pairs`, `entries`: this channel's words, `step` words to the next tile's.
 __device__ __forceinline__ float entering_state(uint64_t* pairs, uint64_t* entries, int64_t step, int64_t tile,
                                                 uint32_t spin_limit)
 {
-    constexpr int kBatch = 4;
+    const int lane = lane_id();
     const int64_t group = tile / kGroup;
+    const int before = (int)(tile - group * kGroup);  // tiles of the group; word `before` is the group's own
+    // lane l: word l of the wave's first channel
+    uint64_t* const first = reinterpret_cast<uint64_t*>(readlane((uint64_t)(uintptr_t)pairs, 0));
+    uint64_t* const entry = reinterpret_cast<uint64_t*>(readlane((uint64_t)(uintptr_t)entries, 0));
+    uint64_t* const mine = lane < before ? first + (tile - 1 - lane) * step : entry + group * step;
     uint32_t polls = 0;
-    float a = 1.0f, b = 0.0f;  // the steps from after tile j up to this one
-    for (int64_t j = tile - 1; j >= group * kGroup; j -= kBatch) {
-        uint64_t wa[kBatch], wb[kBatch];
-        for (;;) {
-            bool ready = true;
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int64_t at = max(j - i, group * kGroup) * step;
-                wa[i] = status_load(pairs + 2 * at);
-                wb[i] = status_load(pairs + 2 * at + 1);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                ready &= (uint32_t)(wb[i] >> 32) == kState || ((wa[i] >> 32) && (wb[i] >> 32));
-            if (ready) break;
-            if (++polls >= spin_limit) return __builtin_nanf("");
-            __builtin_amdgcn_s_sleep(1);
-        }
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (j - i < group * kGroup) break;
-            b = __builtin_fmaf(a, __builtin_bit_cast(float, (uint32_t)wb[i]), b);
-            if ((uint32_t)(wb[i] >> 32) == kState) return b;
-            a *= __builtin_bit_cast(float, (uint32_t)wa[i]);
-        }
-    }
+    int need;  // words 0 .. need: up to the first state
     for (;;) {
-        const uint64_t w = status_load(entries + group * step);
-        if (w >> 32) return __builtin_fmaf(a, __builtin_bit_cast(float, (uint32_t)w), b);
+        const uint32_t mark = lane <= before ? (uint32_t)(status_load(mine) >> 32) : kState;
+        const uint64_t there = ballot(mark != 0), states = ballot(mark == kState);
+        need = min(before, __builtin_ctzll(states | (uint64_t)1 << before));
+        const uint64_t wanted = ((uint64_t)2 << need) - 1;
+        if ((there & wanted) == wanted) break;
         if (++polls >= spin_limit) return __builtin_nanf("");
         __builtin_amdgcn_s_sleep(1);
     }
+    uint64_t w[kGroup];
+    for (;;) {
+        bool there = true;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            if (i <= need) w[i] = status_load(i < before ? pairs + (tile - 1 - i) * step : entries + group * step);
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) there &= i > need || (w[i] >> 32) != 0;
+        if (ballot(!there) == 0) break;
+        if (++polls >= spin_limit) return __builtin_nanf("");
+    }
+    float a = 1.0f, b = 0.0f;  // the steps from after word i up to this tile
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+        if (i > need) break;
+        b = __builtin_fmaf(a, second_of(w[i]), b);
+        a *= first_of(w[i]);
+    }
+    return b;
 }
 
+// Where a tile's first row's state comes from.
+enum Enter { kNone, kGiven, kBefore };  // nowhere (all parts' states are their own), `given`, the tile before
+
 // From the parts' pairs in s_a, s_b (s_new: the part starts anew) to the state
-// that enters each part, which replaces its A. `needs`: a state enters the tile.
-template <int SPAN>
-__device__ __forceinline__ void join_parts(float (&s_a)[kSub][SPAN], float (&s_b)[kSub][SPAN], const int (&s_new)[kSub],
-                                           int64_t tile, int64_t tiles, int64_t cblock, int64_t cblocks, bool needs,
-                                           const GatedWords& w)
+// that enters each part, which replaces its A. `given`: a state for each channel,
+// or null for 0.
+template <int V>
+__device__ __forceinline__ void join_parts(float (&s_a)[kSub][kLanes * V], float (&s_b)[kSub][kLanes * V],
+                                           const int (&s_new)[kSub], const Place<V>& p, int64_t tiles, int64_t dim,
+                                           Enter enter, const float* given, const GatedWords& w)
 {
+    constexpr int kSpan = kLanes * V;
     const int i = (int)threadIdx.x;
-    if (i >= SPAN) return;
-    float a = 1.0f, b = 0.0f;
+    if (i >= kSpan) return;
+    float a = 1.0f, b = 0.0f, h = 0.0f;
+    if (enter == kGiven && given) h = given[min(p.cblock * kSpan + i / V * V, dim - V) + i % V];
     bool anew = false;
 #pragma unroll 4
     for (int q = 0; q < kSub; ++q) {
@@ -193,17 +220,17 @@ __device__ __forceinline__ void join_parts(float (&s_a)[kSub][SPAN], float (&s_b
         a *= s_a[q][i];
         anew |= s_new[q] != 0;
     }
-    const int64_t step = cblocks * SPAN;
-    uint64_t* const pairs = w.pairs + 2 * (cblock * SPAN + i);
-    uint64_t* const entries = w.entries + cblock * SPAN + i;
-    float h = 0.0f;
     if (tiles > 1) {
-        uint64_t* const mine = pairs + 2 * tile * step;
-        if (!anew) status_store(mine, marked(kPair, a));
-        status_store(mine + 1, marked(anew ? kState : kPair, b));
-        if (needs) h = entering_state(pairs, entries, step, tile, w.spin_limit);
-        if (tile % kGroup == kGroup - 1 && tile + 1 < tiles)
-            status_store(entries + (tile / kGroup + 1) * step, marked(kState, anew ? b : __builtin_fmaf(a, h, b)));
+        const int64_t step = p.cblocks * kSpan;
+        uint64_t* const pairs = w.pairs + p.cblock * kSpan + i;
+        uint64_t* const entries = w.entries + p.cblock * kSpan + i;
+        const bool known = anew || enter == kGiven;  // what leaves does not depend on the tiles before
+        const float leaving = anew ? b : __builtin_fmaf(a, h, b);
+        status_store(pairs + p.tile * step, known ? state_word(leaving) : pair_word(a, b));
+        if (enter == kBefore) h = entering_state(pairs, entries, step, p.tile, w.spin_limit);
+        if (p.tile % kGroup == kGroup - 1 && p.tile + 1 < tiles)
+            status_store(entries + (p.tile / kGroup + 1) * step,
+                         state_word(known ? leaving : __builtin_fmaf(a, h, b)));
     }
 #pragma unroll 4
     for (int q = 0; q < kSub; ++q) {
@@ -213,19 +240,46 @@ __device__ __forceinline__ void join_parts(float (&s_a)[kSub][SPAN], float (&s_b
     }
 }
 
-// The sequences of rows row0 - 1 .. row0 + ROWS into s_seq; true if they are all
-// the same one.
-template <int ROWS>
-__device__ __forceinline__ bool find_sequences(const GatedScan& a, int64_t row0, int (&s_seq)[ROWS + 2])
+// A tile's one sequence, or none (-1: sequences meet in it, or it has rows of
+// none), and whether it begins at the tile's first row and ends at its last.
+struct TileInfo {
+    int32_t sequence;
+    uint32_t ends;  // 1: begins here, 2: ends here
+};
+__device__ __forceinline__ TileInfo tile_info(const GatedScan& a, int64_t row0, int rows)
 {
-    const int first = sequence_of(a, row0 - 1);
-    bool same = first >= 0;
-    for (int i = threadIdx.x; i < ROWS + 2; i += kThreads) {
-        const int s = sequence_of(a, row0 - 1 + i);
-        s_seq[i] = s;
-        same &= s == first;
-    }
-    return __syncthreads_and(same);
+    const int64_t last = min(row0 + rows, a.tokens) - 1;
+    const int s = sequence_of(a, row0), before = sequence_of(a, row0 - 1), after = sequence_of(a, last + 1);
+    TileInfo t;
+    t.sequence = s >= 0 && sequence_of(a, last) == s ? s : -1;
+    t.ends = (before != s ? 1u : 0u) | (after != s ? 2u : 0u);
+    return t;
+}
+// ... from the launch before, or of the only tile
+__device__ __forceinline__ TileInfo info_of(const GatedScan& a, const GatedWords& w, int64_t tiles, int64_t at, int rows)
+{
+    TileInfo t;
+    if (tiles > 1)
+        t = reinterpret_cast<const TileInfo*>(w.infos)[at];
+    else
+        t = tile_info(a, 0, rows);
+    t.sequence = __builtin_amdgcn_readfirstlane(t.sequence);
+    t.ends = (uint32_t)__builtin_amdgcn_readfirstlane((int)t.ends);
+    return t;
+}
+
+// A gate that keeps the state as it is, for rows past the end.
+template <typename T, GateForm FORM> __device__ __forceinline__ T open_gate()
+{
+    return (T)(FORM == kSigmoid ? __builtin_inff() : FORM == kLog ? 0.0f : 1.0f);
+}
+
+// The sequences of rows row0 - 1 .. row0 + ROWS into s_seq.
+template <int ROWS>
+__device__ __forceinline__ void find_sequences(const GatedScan& a, int64_t row0, int (&s_seq)[ROWS + 2])
+{
+    for (int i = threadIdx.x; i < ROWS + 2; i += kThreads) s_seq[i] = sequence_of(a, row0 - 1 + i);
+    __syncthreads();
 }
 
 // Sequences without rows: `to` gets `from`, or 0.
@@ -246,7 +300,7 @@ __device__ __forceinline__ void pass_empty(const GatedScan& a, const Place<V>& p
 }
 
 // Rows of a part: what the registers hold at two workgroups to a CU.
-template <typename T> constexpr int kScanRows = sizeof(T) == 4 ? 16 : 12;
+template <typename T> constexpr int kScanRows = 8;
 template <typename T> constexpr int kGradRows = 8;
 
 inline int vector_of(ElemKind kind, int64_t dim)
@@ -263,8 +317,10 @@ inline GatedPlan gated_plan_of(ElemKind kind, bool grad, int64_t tokens, int64_t
     GatedPlan p;
     p.tiles = tokens > 0 ? (tokens + rows - 1) / rows : 1;
     p.cblocks = (dim + span - 1) / span;
-    p.pair_words = p.tiles > 1 ? 2 * p.tiles * p.cblocks * span : 0;
-    p.words = p.tiles > 1 ? p.pair_words + (p.tiles + kGroup - 1) / kGroup * p.cblocks * span : 0;
+    p.pair_words = p.tiles > 1 ? p.tiles * p.cblocks * span : 0;
+    p.rows = rows;
+    p.entry_words = p.tiles > 1 ? (p.tiles + kGroup - 1) / kGroup * p.cblocks * span : 0;
+    p.words = p.tiles > 1 ? p.pair_words + p.entry_words + p.tiles : 0;
     return p;
 }
 
@@ -298,7 +354,8 @@ template <typename F> hipError_t with_type(ElemKind kind, int form, bool mix, F&
 }
 
 
-// The words of a call in its scratch, cleared.
-GatedWords clear_words(const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit, hipStream_t stream);
+// The words of a call in its scratch, cleared, and its tiles' sequences.
+GatedWords begin_words(const GatedScan& a, const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit,
+                       hipStream_t stream);
 
 }  // namespace ds

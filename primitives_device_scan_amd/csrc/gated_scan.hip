@@ -11,7 +11,7 @@
 namespace ds {
 
 template <typename T, int V, GateForm FORM, bool MIX, int TQ>
-__global__ __launch_bounds__(kThreads, 2) void gated_scan_kernel(GatedScan a, GatedWords w)
+__global__ __launch_bounds__(kThreads, 3) void gated_scan_kernel(GatedScan a, GatedWords w)
 {
     constexpr int kRows = kSub * TQ, kSpan = kLanes * V;
     __shared__ float s_a[kSub][kSpan], s_b[kSub][kSpan];
@@ -20,84 +20,126 @@ __global__ __launch_bounds__(kThreads, 2) void gated_scan_kernel(GatedScan a, Ga
     const int part = (int)threadIdx.x / kLanes, at = (int)threadIdx.x % kLanes * V;
     const int64_t tiles = gridDim.x / p.cblocks, row0 = p.tile * kRows, mine = row0 + part * TQ;
     if (a.tokens > 0) {
-        const int64_t left = a.tokens - mine;  // rows of this part that there are, or more
         const Rows<const T> gate(static_cast<const T*>(a.gate), a.gate_stride, row0, part * TQ, p.channel);
         const Rows<const T> in(static_cast<const T*>(a.x), a.x_stride, row0, part * TQ, p.channel);
-        Cells<T, V> g[TQ] = {}, x[TQ] = {};
-        if (row0 + kRows <= a.tokens) {
-#pragma unroll
-            for (int k = 0; k < TQ; ++k) {
-                g[k].load(gate.at(k), gate.bytes);
-                x[k].load(in.at(k), in.bytes);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < TQ; ++k)
-                if (k < left) {
-                    g[k].load(gate.at(k), gate.bytes);
-                    x[k].load(in.at(k), in.bytes);
-                }
-        }
-        const bool inside = find_sequences<kRows>(a, row0, s_seq);
-        // bit k: row k of this part is the first, the last, or none of a sequence
-        uint32_t first = 0, last = 0, none = 0;
-        if (!inside)
-            for (int k = 0; k < TQ; ++k) {
-                const int s = s_seq[part * TQ + k + 1];
-                none |= (uint32_t)(s < 0) << k;
-                first |= (uint32_t)(s >= 0 && s != s_seq[part * TQ + k]) << k;
-                last |= (uint32_t)(s >= 0 && s != s_seq[part * TQ + k + 2]) << k;
-            }
-        const auto initial = [&](int k, float (&h)[V]) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) h[i] = 0.0f;
-            if (a.initial) load_states(a.initial + (int64_t)s_seq[part * TQ + k + 1] * a.dim + p.channel, h);
-        };
-        float v[TQ][V], pa[V], h[V];
+        const Rows<T> to(static_cast<T*>(a.h), a.h_stride, row0, part * TQ, p.channel);
+        const TileInfo info = info_of(a, w, tiles, p.tile, kRows);
+        float pa[V], h[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             pa[i] = 1.0f;
             h[i] = 0.0f;
         }
+        const auto publish = [&](bool anew, Enter enter, const float* given) {
+            store_states(&s_a[part][at], pa);
+            store_states(&s_b[part][at], h);
+            if (at == 0) s_new[part] = anew;
+            __syncthreads();
+            join_parts<V>(s_a, s_b, s_new, p, tiles, a.dim, enter, given, w);
+            __syncthreads();
+            load_states(&s_a[part][at], h);
+        };
+        if (info.sequence >= 0) {
+            const int64_t states = (int64_t)info.sequence * a.dim;
+            const bool whole = row0 + kRows <= a.tokens;
+            Cells<T, V> g[TQ], x[TQ];
+            if (whole) {
 #pragma unroll
-        for (int k = 0; k < TQ; ++k) {
-            if (first >> k & 1) initial(k, h);
+                for (int k = 0; k < TQ; ++k) {
+                    g[k].load(gate.at(k), gate.bytes);
+                    x[k].load(in.at(k), in.bytes);
+                }
+            } else {  // rows past the end leave the state as it is
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                v[k][i] = gate_of<T, FORM>(g[k][i]);
-                h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
-                pa[i] = keep_of<FORM>(v[k][i], pa[i]);
+                for (int k = 0; k < TQ; ++k) {
+                    g[k].fill(open_gate<T, FORM>());
+                    x[k].fill((T)0.0f);
+                    if (mine + k < a.tokens) {
+                        g[k].load(gate.at(k), gate.bytes);
+                        x[k].load(in.at(k), in.bytes);
+                    }
+                }
             }
-            pin(v[k]);
-            x[k].pin();
-        }
-        store_states(&s_a[part][at], pa);
-        store_states(&s_b[part][at], h);
-        if (at == 0) s_new[part] = first != 0;
-        __syncthreads();
-        join_parts<kSpan>(s_a, s_b, s_new, p.tile, tiles, p.cblock, p.cblocks, s_seq[1] >= 0 && s_seq[0] == s_seq[1], w);
-        __syncthreads();
-        load_states(&s_a[part][at], h);
-        const Rows<T> to(static_cast<T*>(a.h), a.h_stride, row0, part * TQ, p.channel);
+            float v[TQ][V];
 #pragma unroll
-        for (int k = 0; k < TQ; ++k) {
-            if (first >> k & 1) initial(k, h);
-            Cells<T, V> out;
+            for (int k = 0; k < TQ; ++k) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
-            out.set(h);
-            if (p.live && !(none >> k & 1)) out.store(to.at(k), to.bytes);
-            if (p.live && (last >> k & 1) && a.final)
-                store_states(a.final + (int64_t)s_seq[part * TQ + k + 1] * a.dim + p.channel, h);
+                for (int i = 0; i < V; ++i) {
+                    v[k][i] = gate_of<T, FORM>(g[k][i]);
+                    h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
+                    pa[i] = keep_of<FORM>(v[k][i], pa[i]);
+                }
+                pin(v[k]);
+                x[k].pin();
+            }
+            publish(false, info.ends & 1 ? kGiven : kBefore, a.initial ? a.initial + states : nullptr);
+#pragma unroll
+            for (int k = 0; k < TQ; ++k) {
+                Cells<T, V> out;
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
+                out.set(h);
+                if (p.live && (whole || mine + k < a.tokens)) out.store(to.at(k), to.bytes);
+            }
+            if ((info.ends & 2) && part == kSub - 1 && p.live && a.final) store_states(a.final + states + p.channel, h);
+        } else {
+            find_sequences<kRows>(a, row0, s_seq);
+            // f(row of the part, its sequence, gate, x) for the part's rows that belong to one
+            const auto rows = [&](auto&& f) {
+#pragma unroll 1
+                for (int k0 = 0; k0 < TQ; k0 += 4) {
+                    Cells<T, V> g[4], x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (mine + k0 + j < a.tokens) {
+                            g[j].load(gate.at(k0 + j), gate.bytes);
+                            x[j].load(in.at(k0 + j), in.bytes);
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int row = part * TQ + k0 + j, s = s_seq[row + 1];
+                        if (s < 0) continue;
+                        if (s_seq[row] != s) {  // the first of its sequence
+#pragma unroll
+                            for (int i = 0; i < V; ++i) h[i] = 0.0f;
+                            if (a.initial) load_states(a.initial + (int64_t)s * a.dim + p.channel, h);
+                        }
+                        f(k0 + j, row, s, g[j], x[j]);
+                    }
+                }
+            };
+            static_assert(TQ % 4 == 0, "four rows at a time");
+            bool anew = false;
+            rows([&](int, int row, int s, const Cells<T, V>& g, const Cells<T, V>& x) {
+                anew |= s_seq[row] != s;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float v = gate_of<T, FORM>(g[i]);
+                    h[i] = step_of<FORM, MIX>(v, h[i], x[i]);
+                    pa[i] = keep_of<FORM>(v, pa[i]);
+                }
+            });
+            publish(anew, s_seq[1] >= 0 && s_seq[0] == s_seq[1] ? kBefore : kNone, nullptr);
+            rows([&](int k, int row, int s, const Cells<T, V>& g, const Cells<T, V>& x) {
+                Cells<T, V> out;
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[i] = step_of<FORM, MIX>(gate_of<T, FORM>(g[i]), h[i], x[i]);
+                out.set(h);
+                if (!p.live) return;
+                out.store(to.at(k), to.bytes);
+                if (s_seq[row + 2] != s && a.final) store_states(a.final + (int64_t)s * a.dim + p.channel, h);
+            });
         }
     }
     pass_empty(a, p, a.initial, a.final);
 }
 
-__global__ __launch_bounds__(kThreads) void gated_clear_kernel(u32x4* words, int64_t count)
+__global__ __launch_bounds__(kThreads) void gated_begin_kernel(GatedScan a, u32x4* words, int64_t count, TileInfo* infos,
+                                                               int64_t tiles, int rows)
 {
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < count; i += (int64_t)gridDim.x * kThreads)
-        words[i] = u32x4{0, 0, 0, 0};
+    const int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x, all = (int64_t)gridDim.x * kThreads;
+    for (int64_t i = at; i < count; i += all) words[i] = u32x4{0, 0, 0, 0};
+    for (int64_t i = at; i < tiles; i += all) infos[i] = tile_info(a, i * rows, rows);
 }
 
 // A workgroup takes one row's columns. Rows whose slot an earlier row names are
@@ -153,20 +195,24 @@ GatedPlan gated_plan(ElemKind kind, bool grad, int64_t tokens, int64_t dim)
 
 int64_t gated_step_blocks(const GatedStep& a) { return (a.dim + kThreads - 1) / kThreads * a.rows; }
 
-GatedWords clear_words(const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit, hipStream_t stream)
+GatedWords begin_words(const GatedScan& a, const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit,
+                       hipStream_t stream)
 {
+    uint64_t* const entries = scratch + plan.pair_words;
+    uint64_t* const infos = entries + plan.entry_words;
     if (plan.words) {
-        const int64_t vecs = (plan.words + 1) / 2, blocks = (vecs + kThreads - 1) / kThreads;
-        gated_clear_kernel<<<dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(kThreads), 0, stream>>>(
-            reinterpret_cast<u32x4*>(scratch), vecs);
+        const int64_t vecs = (plan.pair_words + plan.entry_words) / 2;  // both even
+        const int64_t most = vecs > plan.tiles ? vecs : plan.tiles, blocks = (most + kThreads - 1) / kThreads;
+        gated_begin_kernel<<<dim3((unsigned)(blocks < 1024 ? blocks : 1024)), dim3(kThreads), 0, stream>>>(
+            a, reinterpret_cast<u32x4*>(scratch), vecs, reinterpret_cast<TileInfo*>(infos), plan.tiles, (int)plan.rows);
     }
-    return GatedWords{scratch, scratch + plan.pair_words, spin_limit};
+    return GatedWords{scratch, entries, infos, spin_limit};
 }
 
 hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan& plan, uint64_t* scratch,
                              uint32_t spin_limit, hipStream_t stream)
 {
-    const GatedWords w = clear_words(plan, scratch, spin_limit, stream);
+    const GatedWords w = begin_words(a, plan, scratch, spin_limit, stream);
     const dim3 grid((unsigned)(plan.tiles * plan.cblocks)), block(kThreads);
     return with_type(kind, a.form, a.mix, [&](auto t, auto fm, auto mx) {
         using T = decltype(t);

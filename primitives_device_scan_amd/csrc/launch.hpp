@@ -178,11 +178,11 @@ struct GatedStep {
     bool mix;
 };
 struct GatedPlan {
-    int64_t tiles, cblocks;         // workgroups: tiles x cblocks
-    int64_t pair_words, words;      // 64-bit words of scratch: tiles' pairs, and in all (0: one tile)
+    int64_t tiles, cblocks, rows;   // workgroups: tiles (of so many rows) x cblocks
+    int64_t pair_words, entry_words, words;  // 64-bit words of scratch: tiles' pairs, groups' states, in all (0: one tile)
 };
 struct GatedWords {
-    uint64_t *pairs, *entries;
+    uint64_t *pairs, *entries, *infos;
     uint32_t spin_limit;
 };
 GatedPlan gated_plan(ElemKind kind, bool grad, int64_t tokens, int64_t dim);
