@@ -917,7 +917,10 @@ static int64_t gated_scratch(const ds::GatedPlan& plan) { return (plan.words * 8
 int64_t ds_gated_scan_scratch_bytes(int dtype, int grad, int64_t tokens, int64_t dim)
 {
     if (!float_bytes(dtype) || tokens < 1 || dim < 1 || tokens > kMost31 || dim > DS_GATED_MAX_STRIDE) return 0;
-    return gated_scratch(ds::gated_plan(float_kind(dtype), grad != 0, tokens, dim));
+    // of either kind of input
+    const int64_t plain = gated_scratch(ds::gated_plan(float_kind(dtype), grad != 0, false, tokens, dim));
+    const int64_t mixed = gated_scratch(ds::gated_plan(float_kind(dtype), grad != 0, true, tokens, dim));
+    return plain > mixed ? plain : mixed;
 }
 
 // The words of a scan or its gradient, in the call's scratch.
@@ -954,7 +957,7 @@ int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void
     if (st != DS_OK) return st;
     const ds::GatedScan a{d_gate, d_x, d_h, gate_stride, x_stride, h_stride, tokens, dim, d_offsets, sequences, form,
                           mix != 0, d_initial, d_final};
-    const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), false, tokens, dim);
+    const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), false, mix != 0, tokens, dim);
     std::lock_guard<std::mutex> lock(g_mu);
     uint64_t* words = nullptr;
     st = gated_words(plan, d_scratch, scratch_bytes, bufs, 6, stream, &words);
@@ -991,7 +994,7 @@ int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const
     const ds::GatedScanGrad a{{d_gate, d_x, const_cast<void*>(d_h), gate_stride, x_stride, h_stride, tokens, dim,
                                d_offsets, sequences, form, mix != 0, d_initial, nullptr},
                               d_dh, d_dgate, d_dx, dh_stride, dgate_stride, dx_stride, d_dfinal, d_dinitial};
-    const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), true, tokens, dim);
+    const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), true, mix != 0, tokens, dim);
     std::lock_guard<std::mutex> lock(g_mu);
     uint64_t* words = nullptr;
     st = gated_words(plan, d_scratch, scratch_bytes, bufs, 10, stream, &words);

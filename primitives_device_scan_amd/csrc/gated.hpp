@@ -41,14 +41,21 @@ constexpr int kGroup = 8;                               // tiles to a group
 // kMostStride), so that a tile's many addresses take scalar registers.
 template <typename T, int V> struct Cells {
     typename std::conditional<V == 1, T, u32x4>::type raw;
-    using At = typename std::conditional<V == 1, T, typename Vec16<T>::type>::type;
     __device__ __forceinline__ void load(const T* row, uint32_t bytes)
     {
-        raw = *reinterpret_cast<const At*>(reinterpret_cast<const char*>(row) + bytes);
+        const char* const p = reinterpret_cast<const char*>(row) + bytes;
+        if constexpr (V == 1)
+            raw = *reinterpret_cast<const T*>(p);
+        else
+            raw = *reinterpret_cast<const typename Vec16<T>::type*>(p);
     }
     __device__ __forceinline__ void store(T* row, uint32_t bytes) const
     {
-        *reinterpret_cast<At*>(reinterpret_cast<char*>(row) + bytes) = raw;
+        char* const p = reinterpret_cast<char*>(row) + bytes;
+        if constexpr (V == 1)
+            *reinterpret_cast<T*>(p) = raw;
+        else
+            *reinterpret_cast<typename Vec16<T>::type*>(p) = raw;
     }
     __device__ __forceinline__ void fill(T x)
     {
@@ -264,6 +271,7 @@ __device__ __forceinline__ TileInfo info_of(const GatedScan& a, const GatedWords
     else
         t = tile_info(a, 0, rows);
     t.sequence = __builtin_amdgcn_readfirstlane(t.sequence);
+    if (t.sequence >= a.sequences) t.sequence = -1;  // it indexes the states: never past them
     t.ends = (uint32_t)__builtin_amdgcn_readfirstlane((int)t.ends);
     return t;
 }
@@ -301,7 +309,8 @@ __device__ __forceinline__ void pass_empty(const GatedScan& a, const Place<V>& p
 
 // Rows of a part: what the registers hold at two workgroups to a CU.
 template <typename T> constexpr int kScanRows = 8;
-template <typename T> constexpr int kGradRows = 8;
+template <typename T, bool MIX> constexpr int kGradRows = sizeof(T) == 2 && MIX ? 4 : 8;
+template <typename T, bool MIX> constexpr int kGradPerCu = sizeof(T) == 2 && MIX ? 3 : 2;
 
 inline int vector_of(ElemKind kind, int64_t dim)
 {
@@ -309,11 +318,12 @@ inline int vector_of(ElemKind kind, int64_t dim)
     return dim < v ? 1 : v;
 }
 
-inline GatedPlan gated_plan_of(ElemKind kind, bool grad, int64_t tokens, int64_t dim)
+inline GatedPlan gated_plan_of(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t dim)
 {
-    const int64_t rows = kSub * (grad ? (kind == kF32 ? kGradRows<float> : kGradRows<bf16>)
-                                       : (kind == kF32 ? kScanRows<float> : kScanRows<bf16>)),
-                  span = (int64_t)kLanes * vector_of(kind, dim);
+    const int part = !grad              ? (kind == kF32 ? kScanRows<float> : kScanRows<bf16>)
+                     : kind == kF32 ? (mix ? kGradRows<float, true> : kGradRows<float, false>)
+                                    : (mix ? kGradRows<bf16, true> : kGradRows<bf16, false>);
+    const int64_t rows = kSub * part, span = (int64_t)kLanes * vector_of(kind, dim);
     GatedPlan p;
     p.tiles = tokens > 0 ? (tokens + rows - 1) / rows : 1;
     p.cblocks = (dim + span - 1) / span;

@@ -188,9 +188,9 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
     if (c < a.dim) *state = h;
 }
 
-GatedPlan gated_plan(ElemKind kind, bool grad, int64_t tokens, int64_t dim)
+GatedPlan gated_plan(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t dim)
 {
-    return gated_plan_of(kind, grad, tokens, dim);
+    return gated_plan_of(kind, grad, mix, tokens, dim);
 }
 
 int64_t gated_step_blocks(const GatedStep& a) { return (a.dim + kThreads - 1) / kThreads * a.rows; }

@@ -12,7 +12,7 @@ namespace ds {
 // row t - 1 is S = a_t G_t, with G_t = dh_t + S of row t + 1 (or dfinal), so the
 // scan's pairs need no row but their own.
 template <typename T, int V, GateForm FORM, bool MIX, int TQ>
-__global__ __launch_bounds__(kThreads, 2) void gated_scan_grad_kernel(GatedScanGrad a, GatedWords w)
+__global__ __launch_bounds__(kThreads, (kGradPerCu<T, MIX>)) void gated_scan_grad_kernel(GatedScanGrad a, GatedWords w)
 {
     constexpr int kRows = kSub * TQ, kSpan = kLanes * V;
     __shared__ float s_a[kSub][kSpan], s_b[kSub][kSpan];
@@ -198,9 +198,9 @@ hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, const G
     return with_type(kind, a.s.form, a.s.mix, [&](auto t, auto fm, auto mx) {
         using T = decltype(t);
         if (vector_of(kind, a.s.dim) == 1)
-            gated_scan_grad_kernel<T, 1, decltype(fm)::value, decltype(mx)::value, kGradRows<T>><<<grid, block, 0, stream>>>(a, w);
+            gated_scan_grad_kernel<T, 1, decltype(fm)::value, decltype(mx)::value, kGradRows<T, decltype(mx)::value>><<<grid, block, 0, stream>>>(a, w);
         else
-            gated_scan_grad_kernel<T, Vec16<T>::kN, decltype(fm)::value, decltype(mx)::value, kGradRows<T>>
+            gated_scan_grad_kernel<T, Vec16<T>::kN, decltype(fm)::value, decltype(mx)::value, kGradRows<T, decltype(mx)::value>>
                 <<<grid, block, 0, stream>>>(a, w);
     });
 }

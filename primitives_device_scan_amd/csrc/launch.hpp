@@ -185,7 +185,7 @@ struct GatedWords {
     uint64_t *pairs, *entries, *infos;
     uint32_t spin_limit;
 };
-GatedPlan gated_plan(ElemKind kind, bool grad, int64_t tokens, int64_t dim);
+GatedPlan gated_plan(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t dim);
 int64_t gated_step_blocks(const GatedStep& a);  // workgroups
 hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan& plan, uint64_t* scratch,
                              uint32_t spin_limit, hipStream_t stream);
