@@ -97,6 +97,27 @@ __device__ __forceinline__ float rest_of(float v)
     return gate_keeps(v) ? -v : 1.0f - v;
 }
 
+// The product of gates, in the same form: a near 1 is held as 1 - a, which is the
+// sum of (1 - a_t) times the product before; a product of 1,000 gates near 1 that is
+// rounded 1,000 times would be 1e-6 off. DECAY (whose gates may be negative) has
+// the product alone.
+template <GateForm FORM> struct Product {
+    float a = 1.0f, rest = 0.0f;
+    __device__ __forceinline__ void step(float v)
+    {
+        // a sigmoid's v > 0 is a gate below 0.5, and so is the product then: `rest` does not count
+        if constexpr (FORM == kSigmoid) rest = __builtin_fmaf(-v, a, rest);
+        if constexpr (FORM == kLog) rest = __builtin_fmaf(rest_of<FORM>(v), a, rest);
+        a = keep_of<FORM>(v, a);
+    }
+    // v of all of them; NaN stays NaN
+    __device__ __forceinline__ float value() const
+    {
+        if constexpr (FORM == kDecay) return a;
+        return a >= 0.5f && a <= 1.0f ? __builtin_copysignf(rest, -1.0f) : __builtin_fabsf(a);
+    }
+};
+
 // d a / d g
 template <GateForm FORM>
 __device__ __forceinline__ float slope_of(float v)

@@ -162,6 +162,7 @@ __device__ __forceinline__ float second_of(uint64_t w) { return __builtin_bit_ca
 // The state that enters tile `tile` in this thread's channel, from the words of
 // the tiles before it in its group and of the group; all lanes of a wave call
 // it. `pairs`, `entries`: this channel's words, `step` words to the next tile's.
+template <GateForm FORM>
 __device__ __forceinline__ float entering_state(uint64_t* pairs, uint64_t* entries, int64_t step, int64_t tile,
                                                 uint32_t spin_limit)
 {
@@ -183,7 +184,7 @@ __device__ __forceinline__ float entering_state(uint64_t* pairs, uint64_t* entri
         if (++polls >= spin_limit) return __builtin_nanf("");
         __builtin_amdgcn_s_sleep(1);
     }
-    uint64_t w[kGroup];
+    uint64_t w[kGroup] = {};
     for (;;) {
         bool there = true;
 #pragma unroll
@@ -194,23 +195,21 @@ __device__ __forceinline__ float entering_state(uint64_t* pairs, uint64_t* entri
         if (ballot(!there) == 0) break;
         if (++polls >= spin_limit) return __builtin_nanf("");
     }
-    float a = 1.0f, b = 0.0f;  // the steps from after word i up to this tile
+    float h = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) {
-        if (i > need) break;
-        b = __builtin_fmaf(a, second_of(w[i]), b);
-        a *= first_of(w[i]);
-    }
-    return b;
+    for (int i = kGroup - 1; i >= 0; --i)
+        if (i <= need)
+            h = (uint32_t)(w[i] >> 32) == kState ? second_of(w[i]) : keep_of<FORM>(first_of(w[i]), h) + second_of(w[i]);
+    return h;
 }
 
 // Where a tile's first row's state comes from.
 enum Enter { kNone, kGiven, kBefore };  // nowhere (all parts' states are their own), `given`, the tile before
 
-// From the parts' pairs in s_a, s_b (s_new: the part starts anew) to the state
+// From the parts' pairs in s_a (as Product has them), s_b (s_new: the part starts anew) to the state
 // that enters each part, which replaces its A. `given`: a state for each channel,
 // or null for 0.
-template <int V>
+template <int V, GateForm FORM>
 __device__ __forceinline__ void join_parts(float (&s_a)[kSub][kLanes * V], float (&s_b)[kSub][kLanes * V],
                                            const int (&s_new)[kSub], const Place<V>& p, int64_t tiles, int64_t dim,
                                            Enter enter, const float* given, const GatedWords& w)
@@ -218,13 +217,14 @@ __device__ __forceinline__ void join_parts(float (&s_a)[kSub][kLanes * V], float
     constexpr int kSpan = kLanes * V;
     const int i = (int)threadIdx.x;
     if (i >= kSpan) return;
-    float a = 1.0f, b = 0.0f, h = 0.0f;
+    Product<FORM> all;
+    float b = 0.0f, h = 0.0f;
     if (enter == kGiven && given) h = given[min(p.cblock * kSpan + i / V * V, dim - V) + i % V];
     bool anew = false;
 #pragma unroll 4
     for (int q = 0; q < kSub; ++q) {
-        b = s_new[q] ? s_b[q][i] : __builtin_fmaf(s_a[q][i], b, s_b[q][i]);
-        a *= s_a[q][i];
+        b = (s_new[q] ? 0.0f : keep_of<FORM>(s_a[q][i], b)) + s_b[q][i];
+        all.step(s_a[q][i]);
         anew |= s_new[q] != 0;
     }
     if (tiles > 1) {
@@ -232,16 +232,16 @@ __device__ __forceinline__ void join_parts(float (&s_a)[kSub][kLanes * V], float
         uint64_t* const pairs = w.pairs + p.cblock * kSpan + i;
         uint64_t* const entries = w.entries + p.cblock * kSpan + i;
         const bool known = anew || enter == kGiven;  // what leaves does not depend on the tiles before
-        const float leaving = anew ? b : __builtin_fmaf(a, h, b);
+        const float a = all.value(), leaving = anew ? b : keep_of<FORM>(a, h) + b;
         status_store(pairs + p.tile * step, known ? state_word(leaving) : pair_word(a, b));
-        if (enter == kBefore) h = entering_state(pairs, entries, step, p.tile, w.spin_limit);
+        if (enter == kBefore) h = entering_state<FORM>(pairs, entries, step, p.tile, w.spin_limit);
         if (p.tile % kGroup == kGroup - 1 && p.tile + 1 < tiles)
             status_store(entries + (p.tile / kGroup + 1) * step,
-                         state_word(known ? leaving : __builtin_fmaf(a, h, b)));
+                         state_word(known ? leaving : keep_of<FORM>(a, h) + b));
     }
 #pragma unroll 4
     for (int q = 0; q < kSub; ++q) {
-        const float to = s_new[q] ? s_b[q][i] : __builtin_fmaf(s_a[q][i], h, s_b[q][i]);
+        const float to = (s_new[q] ? 0.0f : keep_of<FORM>(s_a[q][i], h)) + s_b[q][i];
         s_a[q][i] = h;
         h = to;
     }

@@ -24,18 +24,19 @@ __global__ __launch_bounds__(kThreads, 3) void gated_scan_kernel(GatedScan a, Ga
         const Rows<const T> in(static_cast<const T*>(a.x), a.x_stride, row0, part * TQ, p.channel);
         const Rows<T> to(static_cast<T*>(a.h), a.h_stride, row0, part * TQ, p.channel);
         const TileInfo info = info_of(a, w, tiles, p.tile, kRows);
-        float pa[V], h[V];
+        Product<FORM> all[V];
+        float h[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            pa[i] = 1.0f;
-            h[i] = 0.0f;
-        }
+        for (int i = 0; i < V; ++i) h[i] = 0.0f;
         const auto publish = [&](bool anew, Enter enter, const float* given) {
+            float pa[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) pa[i] = all[i].value();
             store_states(&s_a[part][at], pa);
             store_states(&s_b[part][at], h);
             if (at == 0) s_new[part] = anew;
             __syncthreads();
-            join_parts<V>(s_a, s_b, s_new, p, tiles, a.dim, enter, given, w);
+            join_parts<V, FORM>(s_a, s_b, s_new, p, tiles, a.dim, enter, given, w);
             __syncthreads();
             load_states(&s_a[part][at], h);
         };
@@ -67,7 +68,7 @@ __global__ __launch_bounds__(kThreads, 3) void gated_scan_kernel(GatedScan a, Ga
                 for (int i = 0; i < V; ++i) {
                     v[k][i] = gate_of<T, FORM>(g[k][i]);
                     h[i] = step_of<FORM, MIX>(v[k][i], h[i], x[k][i]);
-                    pa[i] = keep_of<FORM>(v[k][i], pa[i]);
+                    all[i].step(v[k][i]);
                 }
                 pin(v[k]);
                 x[k].pin();
@@ -116,7 +117,7 @@ __global__ __launch_bounds__(kThreads, 3) void gated_scan_kernel(GatedScan a, Ga
                 for (int i = 0; i < V; ++i) {
                     const float v = gate_of<T, FORM>(g[i]);
                     h[i] = step_of<FORM, MIX>(v, h[i], x[i]);
-                    pa[i] = keep_of<FORM>(v, pa[i]);
+                    all[i].step(v);
                 }
             });
             publish(anew, s_seq[1] >= 0 && s_seq[0] == s_seq[1] ? kBefore : kNone, nullptr);

@@ -30,18 +30,19 @@ __global__ __launch_bounds__(kThreads, (kGradPerCu<T, MIX>)) void gated_scan_gra
         const Rows<T> to_gate(static_cast<T*>(a.dgate), a.dgate_stride, row0, top, p.channel);
         const Rows<T> to_x(static_cast<T*>(a.dx), a.dx_stride, row0, top, p.channel);
         const TileInfo info = info_of(a.s, w, tiles, tile, kRows);
-        float pa[V], s[V];
+        Product<FORM> all[V];
+        float s[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            pa[i] = 1.0f;
-            s[i] = 0.0f;
-        }
+        for (int i = 0; i < V; ++i) s[i] = 0.0f;
         const auto publish = [&](bool anew, Enter enter, const float* given) {
+            float pa[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) pa[i] = all[i].value();
             store_states(&s_a[part][at], pa);
             store_states(&s_b[part][at], s);
             if (at == 0) s_new[part] = anew;
             __syncthreads();
-            join_parts<V>(s_a, s_b, s_new, p, tiles, a.s.dim, enter, given, w);
+            join_parts<V, FORM>(s_a, s_b, s_new, p, tiles, a.s.dim, enter, given, w);
             __syncthreads();
             load_states(&s_a[part][at], s);
         };
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(kThreads, (kGradPerCu<T, MIX>)) void gated_scan_gra
                 for (int i = 0; i < V; ++i) {
                     v[k][i] = gate_of<T, FORM>(g[k][i]);
                     s[i] = keep_of<FORM>(v[k][i], s[i] + dh[k][i]);
-                    pa[i] = keep_of<FORM>(v[k][i], pa[i]);
+                    all[i].step(v[k][i]);
                 }
                 pin(v[k]);
                 dh[k].pin();
@@ -166,7 +167,7 @@ __global__ __launch_bounds__(kThreads, (kGradPerCu<T, MIX>)) void gated_scan_gra
                 for (int i = 0; i < V; ++i) {
                     const float v = gate_of<T, FORM>(g[i]);
                     s[i] = keep_of<FORM>(v, s[i] + dh[i]);
-                    pa[i] = keep_of<FORM>(v, pa[i]);
+                    all[i].step(v);
                 }
             });
             publish(anew, s_seq[kRows] >= 0 && s_seq[kRows + 1] == s_seq[kRows] ? kBefore : kNone, nullptr);
