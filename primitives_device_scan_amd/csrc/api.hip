@@ -1024,7 +1024,7 @@ int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void
     if (st != DS_OK) return st;
     const ds::GatedStep a{d_gate, d_x, d_h, gate_stride, x_stride, h_stride, rows, dim, d_slots, d_state, pool,
                           state_stride, form, mix != 0};
-    if (ds::gated_step_blocks(a) > kMaxTiles) return DS_ERR_TOO_LARGE;
+    if (ds::gated_step_blocks(float_kind(dtype), a) > kMaxTiles) return DS_ERR_TOO_LARGE;
     return ds::launch_gated_step(float_kind(dtype), a, stream) == hipSuccess ? DS_OK : DS_ERR_HIP;
 }
 

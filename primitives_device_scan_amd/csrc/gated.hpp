@@ -64,6 +64,14 @@ template <typename T, int V> struct Cells {
         for (int i = 0; i < V; ++i) t[i] = x;
         __builtin_memcpy(&raw, t, sizeof(t));
     }
+    __device__ __forceinline__ void put(int k, T x)
+    {
+        T t[V];
+        __builtin_memcpy(t, &raw, sizeof(t));
+#pragma unroll
+        for (int i = 0; i < V; ++i) t[i] = i == k ? x : t[i];
+        __builtin_memcpy(&raw, t, sizeof(t));
+    }
     __device__ __forceinline__ float operator[](int i) const
     {
         T t[V];

@@ -143,50 +143,92 @@ __global__ __launch_bounds__(kThreads) void gated_begin_kernel(GatedScan a, u32x
     for (int64_t i = at; i < tiles; i += all) infos[i] = tile_info(a, i * rows, rows);
 }
 
-// A workgroup takes one row's columns. Rows whose slot an earlier row names are
-// that slot's next tokens: the first such row's workgroups do them, in order.
-template <typename T, GateForm FORM, bool MIX>
+// A workgroup takes one row's columns, V to a thread. Rows whose slot an earlier
+// row names are that slot's next tokens: the first such row's workgroups do them,
+// in order. All slots are looked through for that while the row's data is loaded
+// (n slots by each of n rows: nothing for the few thousand sequences of a step).
+template <typename T, int V, GateForm FORM, bool MIX>
 __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
 {
-    const int64_t cblocks = (a.dim + kThreads - 1) / kThreads;
+    const int64_t wide = (int64_t)blockDim.x * V, cblocks = (a.dim + wide - 1) / wide;
     int64_t i = blockIdx.x / cblocks;
-    const int64_t c = blockIdx.x % cblocks * kThreads + threadIdx.x;
+    const int64_t c = blockIdx.x % cblocks * wide + (int64_t)threadIdx.x * V;
+    const int here = (int)min((int64_t)V, a.dim - c);  // this thread's columns, or none
+    const auto each = [&](auto&& whole, auto&& one) {
+        if (here == V)
+            whole();
+        else
+            for (int k = 0; k < here; ++k) one(k);
+    };
     const int64_t slot = a.slots ? a.slots[i] : i;
-    const bool used = slot >= 0 && slot < a.pool;
-    if (!used) {
-        if (c < a.dim) static_cast<T*>(a.h)[i * a.h_stride + c] = (T)0.0f;
+    if (slot < 0 || slot >= a.pool) {
+        T* const h = static_cast<T*>(a.h) + i * a.h_stride + c;
+        Cells<T, V> zero;
+        zero.fill((T)0.0f);
+        each([&] { zero.store(h, 0); }, [&](int k) { h[k] = (T)0.0f; });
         return;
     }
-    if (a.slots) {
-        int earlier = 0;
-        for (int64_t j = threadIdx.x; j < i; j += kThreads) earlier |= a.slots[j] == slot;
-        if (__syncthreads_or(earlier)) return;
-    }
     float* const state = a.state + slot * a.state_stride + c;
-    float h = c < a.dim ? *state : 0.0f;
+    const T* const gate = static_cast<const T*>(a.gate) + c;
+    const T* const in = static_cast<const T*>(a.x) + c;
+    Cells<T, V> g, x;
+    float h[V];
+    g.fill((T)0.0f);
+    x.fill((T)0.0f);
+    const auto load = [&] {
+        each(
+            [&] {
+                g.load(gate + i * a.gate_stride, 0);
+                x.load(in + i * a.x_stride, 0);
+            },
+            [&](int k) {
+                g.put(k, gate[i * a.gate_stride + k]);
+                x.put(k, in[i * a.x_stride + k]);
+            });
+    };
+    load();
+#pragma unroll
+    for (int k = 0; k < V; ++k) h[k] = 0.0f;
+    each([&] { load_states(state, h); },
+         [&](int k) {
+#pragma unroll
+             for (int j = 0; j < V; ++j)
+                 if (j == k) h[j] = state[k];
+         });
+    __shared__ int s_first, s_next;  // the first row of this slot; the next one after i
+    const auto find_rows = [&](int64_t from) {
+        if (threadIdx.x == 0) s_first = s_next = INT32_MAX;
+        __syncthreads();
+        for (int64_t j = from + threadIdx.x; j < a.rows; j += blockDim.x)
+            if (a.slots[j] == slot && j != i) atomicMin(j < i ? &s_first : &s_next, (int)j);
+        __syncthreads();
+    };
+    int next = INT32_MAX;
+    if (a.slots) {
+        find_rows(0);
+        if (s_first != INT32_MAX) return;  // an earlier row's workgroups do this one
+        next = s_next;
+    }
     for (;;) {
-        if (c < a.dim) {
-            const float v = gate_of<T, FORM>((float)static_cast<const T*>(a.gate)[i * a.gate_stride + c]);
-            h = step_of<FORM, MIX>(v, h, (float)static_cast<const T*>(a.x)[i * a.x_stride + c]);
-            static_cast<T*>(a.h)[i * a.h_stride + c] = (T)h;
-        }
-        if (!a.slots) break;
-        // the next row of this slot
-        __shared__ int s_next;
-        if (threadIdx.x == 0) s_next = INT32_MAX;
-        __syncthreads();
-        for (int64_t j = i + 1 + threadIdx.x; j < a.rows; j += kThreads)
-            if (a.slots[j] == slot) {
-                atomicMin(&s_next, (int)j);
-                break;
-            }
-        __syncthreads();
-        const int next = s_next;
-        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < V; ++k) h[k] = step_of<FORM, MIX>(gate_of<T, FORM>(g[k]), h[k], x[k]);
+        T* const to = static_cast<T*>(a.h) + i * a.h_stride + c;
+        Cells<T, V> out;
+        out.set(h);
+        each([&] { out.store(to, 0); }, [&](int k) { to[k] = (T)out[k]; });
         if (next == INT32_MAX) break;
         i = next;
+        load();
+        __syncthreads();  // all have read s_next
+        find_rows(i + 1);
+        next = s_next;
     }
-    if (c < a.dim) *state = h;
+    each([&] { store_states(state, h); },
+         [&](int k) {
+#pragma unroll
+             for (int j = 0; j < V; ++j)
+                 if (j == k) state[k] = h[j];
+         });
 }
 
 GatedPlan gated_plan(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t dim)
@@ -194,7 +236,19 @@ GatedPlan gated_plan(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t
     return gated_plan_of(kind, grad, mix, tokens, dim);
 }
 
-int64_t gated_step_blocks(const GatedStep& a) { return (a.dim + kThreads - 1) / kThreads * a.rows; }
+// Threads to a workgroup of a step: those that a row needs, in whole waves.
+static int step_threads(const GatedStep& a, int v)
+{
+    const int64_t need = (a.dim + v - 1) / v;
+    return need >= kThreads ? kThreads : (int)((need + kWave - 1) / kWave * kWave);
+}
+
+int64_t gated_step_blocks(ElemKind kind, const GatedStep& a)
+{
+    const int v = vector_of(kind, a.dim);
+    const int64_t wide = (int64_t)step_threads(a, v) * v;
+    return (a.dim + wide - 1) / wide * a.rows;
+}
 
 GatedWords begin_words(const GatedScan& a, const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit,
                        hipStream_t stream)
@@ -227,9 +281,14 @@ hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan&
 
 hipError_t launch_gated_step(ElemKind kind, const GatedStep& a, hipStream_t stream)
 {
+    const int v = vector_of(kind, a.dim);
+    const dim3 grid((unsigned)gated_step_blocks(kind, a)), block(step_threads(a, v));
     return with_type(kind, a.form, a.mix, [&](auto t, auto fm, auto mx) {
-        gated_step_kernel<decltype(t), decltype(fm)::value, decltype(mx)::value>
-            <<<dim3((unsigned)gated_step_blocks(a)), dim3(kThreads), 0, stream>>>(a);
+        using T = decltype(t);
+        if (v == 1)
+            gated_step_kernel<T, 1, decltype(fm)::value, decltype(mx)::value><<<grid, block, 0, stream>>>(a);
+        else
+            gated_step_kernel<T, Vec16<T>::kN, decltype(fm)::value, decltype(mx)::value><<<grid, block, 0, stream>>>(a);
     });
 }
 

@@ -186,7 +186,7 @@ struct GatedWords {
     uint32_t spin_limit;
 };
 GatedPlan gated_plan(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t dim);
-int64_t gated_step_blocks(const GatedStep& a);  // workgroups
+int64_t gated_step_blocks(ElemKind kind, const GatedStep& a);  // workgroups
 hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan& plan, uint64_t* scratch,
                              uint32_t spin_limit, hipStream_t stream);
 hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, const GatedPlan& plan, uint64_t* scratch,

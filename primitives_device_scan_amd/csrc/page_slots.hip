@@ -19,79 +19,77 @@ namespace ds {
 constexpr int kPageThreads = 1024;
 constexpr int kPageWaves = kPageThreads / kWave;
 
-// The last i of [0, n) with first[i] <= v, where first[0] <= v and first does
-// not decrease.
-__device__ __forceinline__ int last_at_most(const int64_t* first, int n, int64_t v)
-{
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (first[mid] <= v)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
+// A request's tokens and pages before it in its chunk of requests: sums of 1,024
+// numbers below 2^31 may need 64 bits.
+struct Before {
+    int64_t tokens, pages;
+};
 
 __global__ __launch_bounds__(kPageThreads) void page_slots_kernel(PageSlots a)
 {
-    __shared__ int64_t s_tokens[kPageThreads + 1], s_pages[kPageThreads + 1];  // first of each request in the chunk
-    __shared__ int64_t s_wave[2][kPageWaves];
-    __shared__ int32_t s_context[kPageThreads];
+    __shared__ Before s_first[kPageThreads], s_wave[kPageWaves];
+    __shared__ uint32_t s_context[kPageThreads];
     const int lane = lane_id(), wave = (int)threadIdx.x / kWave;
     const int64_t top = min(max((int64_t)*a.count, (int64_t)0), a.capacity) - 1;
-    const int64_t page = a.page;
+    const uint32_t page = (uint32_t)a.page;
     const auto free_page = [&](int64_t q) { return q <= top ? a.free_pages[top - q] : -1; };
+    const auto pages_of = [&](uint32_t tokens) { return tokens / page + (tokens % page != 0); };
+    // the last request i of the chunk's `here` with s_first[i].*what <= v
+    const auto owner = [&](int64_t Before::*what, int here, int64_t v) {
+        int lo = 0, hi = here;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_first[mid].*what <= v)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
     int64_t tokens = 0, pages = 0;  // of the requests before the chunk
     for (int64_t base = 0; base < a.requests; base += kPageThreads) {
         const int64_t r = base + threadIdx.x;
         const int here = (int)min((int64_t)kPageThreads, a.requests - base);
-        const int64_t context = r < a.requests ? max(a.context[r], 0) : 0;
-        const int64_t fresh = r < a.requests ? max(a.fresh[r], 0) : 0;
-        const int64_t held = (context + page - 1) / page;
-        const int64_t need = (context + fresh + page - 1) / page - held;
-        const int64_t tokens_to = wave_inclusive_scan(fresh), pages_to = wave_inclusive_scan(need);
-        if (lane == kWave - 1) {
-            s_wave[0][wave] = tokens_to;
-            s_wave[1][wave] = pages_to;
-        }
+        const uint32_t context = r < a.requests ? (uint32_t)max(a.context[r], 0) : 0u;
+        const uint32_t fresh = r < a.requests ? (uint32_t)max(a.fresh[r], 0) : 0u;
+        const uint32_t need = pages_of(context + fresh) - pages_of(context);
+        const int64_t tokens_to = wave_inclusive_scan((int64_t)fresh), pages_to = wave_inclusive_scan((int64_t)need);
+        if (lane == kWave - 1) s_wave[wave] = {tokens_to, pages_to};
+        s_context[threadIdx.x] = context;
         __syncthreads();
-        int64_t t0 = tokens, p0 = pages;
+        const int64_t first_token = tokens, first_page = pages;
+        int64_t t0 = tokens_to - fresh, p0 = pages_to - need;
         for (int w = 0; w < kPageWaves; ++w) {
-            if (w < wave) {
-                t0 += s_wave[0][w];
-                p0 += s_wave[1][w];
-            }
-            tokens += s_wave[0][w];
-            pages += s_wave[1][w];
+            const Before n = s_wave[w];
+            t0 += w < wave ? n.tokens : 0;
+            p0 += w < wave ? n.pages : 0;
+            tokens += n.tokens;
+            pages += n.pages;
         }
-        s_tokens[threadIdx.x] = t0 + tokens_to - fresh;
-        s_pages[threadIdx.x] = p0 + pages_to - need;
-        s_context[threadIdx.x] = (int32_t)context;
-        if (blockIdx.x == 0 && r < a.requests)
-            a.offsets[r] = (int32_t)min(t0 + tokens_to - fresh, (int64_t)INT32_MAX);
+        t0 += first_token;
+        p0 += first_page;
+        s_first[threadIdx.x] = {t0, p0};
+        if (blockIdx.x == 0 && r < a.requests) a.offsets[r] = (int32_t)min(t0, (int64_t)INT32_MAX);
         __syncthreads();
-        const int64_t first_token = s_tokens[0], first_page = s_pages[0];
         // pages that the chunk's requests take
         for (int64_t q = first_page + blockIdx.x * kPageThreads + threadIdx.x; q < pages;
              q += (int64_t)gridDim.x * kPageThreads) {
-            const int i = last_at_most(s_pages, here, q);
-            const int64_t col = (s_context[i] + page - 1) / page + q - s_pages[i];
+            const int i = owner(&Before::pages, here, q);
+            const int64_t col = pages_of(s_context[i]) + (q - s_first[i].pages);
             if (col < a.width) a.tables[(base + i) * a.table_stride + col] = free_page(q);
         }
         // their tokens
         const int64_t end = min(tokens, a.tokens);
         for (int64_t t = first_token + blockIdx.x * kPageThreads + threadIdx.x; t < end;
              t += (int64_t)gridDim.x * kPageThreads) {
-            const int i = last_at_most(s_tokens, here, t);
-            const int64_t position = s_context[i] + t - s_tokens[i];
-            const int64_t col = position / page, own = (s_context[i] + page - 1) / page;
-            int64_t id = -1;
+            const int i = owner(&Before::tokens, here, t);
+            const uint32_t position = s_context[i] + (uint32_t)(t - s_first[i].tokens);
+            const uint32_t col = position / page, own = pages_of(s_context[i]);
+            int32_t id = -1;
             if (col < a.width)
-                id = col < own ? a.tables[(base + i) * a.table_stride + col] : free_page(s_pages[i] + col - own);
-            a.slots[t] = id < 0 ? -1 : id * page + position % page;
-            a.positions[t] = (int32_t)min(position, (int64_t)INT32_MAX);
+                id = col < own ? a.tables[(base + i) * a.table_stride + col] : free_page(s_first[i].pages + (col - own));
+            a.slots[t] = id < 0 ? -1 : (int64_t)id * page + position % page;
+            a.positions[t] = (int32_t)min(position, (uint32_t)INT32_MAX);
         }
         __syncthreads();
     }
