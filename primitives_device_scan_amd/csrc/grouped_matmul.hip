@@ -431,6 +431,14 @@ __device__ __forceinline__ void write_out(const Grouped& a, const Tile& t, const
     if constexpr (OP == kGradient) {
         G* const c = static_cast<G*>(a.dw) + ((int64_t)t.e * a.rows + t.m0) * a.cols + t.n0;
         const int rows = (int)a.rows - t.m0, cols = (int)a.cols - t.n0;
+        if (WHOLE && t.depth == 0) {  // whole lines of zeros (64 experts of 1,536 x 2,048, 8 of them used: 146 -> 87 us)
+            if (a.accumulate) return;
+            constexpr int kPer = Vec16<G>::kN, kWide = 64 * TN / kPer;
+            for (int i = threadIdx.x; i < 64 * TM * kWide; i += kThreads)
+                if (i / kWide < rows && i % kWide * kPer < cols)
+                    *reinterpret_cast<typename Vec16<G>::type*>(c + i / kWide * a.cols + i % kWide * kPer) = u32x4{0, 0, 0, 0};
+            return;
+        }
         if (!a.accumulate)
             write_tile<G, TM, TN, WHOLE>(acc, c, a.cols, rows, cols, false, ~0u);
         else if (t.depth > 0)
@@ -603,46 +611,51 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Operands of any alignment and length, through registers.
+// Operands of any alignment and length, through registers, kAhead stages ahead
+// (1,003 tokens, top-2 of 20, 777 x 1,000 transposed in fp16: 41 us one stage
+// ahead, 23 so).
 // ---------------------------------------------------------------------------
-// 8 elements of a line from `at` on, 0 past its end, from one load inside it.
-template <typename T>
-__device__ __forceinline__ u32x4 load_odd(const T* line, int64_t at, int64_t length, bool there)
-{
-    if (length < 8) {  // uniform
-        u32x4 v = {0, 0, 0, 0};
-        if (there && at < length) v = load_end<T>(line, at, length);
-        return v;
-    }
-    const u32x4 v = load_end<T>(line, at, length);
-    return there ? v : u32x4{0, 0, 0, 0};
-}
+constexpr int kAhead = 4;
 
 template <typename T, int R, bool ACROSS> struct RowsOdd {
-    const T* line[R];  // along k: the row's; across: of k in the first stage
-    bool there[R];
-    int64_t from, length;
-    u32x4 staged[R];
+    int64_t from, length;  // across k: the tile's first element of a line, and a line's elements
+    u32x4 staged[kAhead][R];
+    uint32_t there[kAhead];  // bit i: piece i is of a line that there is
     static __device__ __forceinline__ int place(int i) { return ACROSS ? (i * kThreads + (int)threadIdx.x) / (8 * R) : i * 64 + (int)threadIdx.x / 4; }
     static __device__ __forceinline__ int segment(int i) { return ACROSS ? (i * kThreads + (int)threadIdx.x) % (8 * R) : (int)threadIdx.x % 4; }
-    // line_of(place, &there): a line that is there in any case
+    __device__ __forceinline__ int64_t element(int i, int k0) const { return (ACROSS ? from : k0) + segment(i) * 8; }
+    // line_of(place, &there): a line that is there in any case. A piece that ends
+    // past its line is loaded from the line's last 16 bytes, and moved down only
+    // as it is put into LDS, so that loading waits for nothing.
     template <typename F>
-    __device__ __forceinline__ void load(int k0, int depth, F&& line_of)
+    __device__ __forceinline__ void load(int set, int k0, int depth, F&& line_of)
     {
+        const int64_t all = ACROSS ? length : depth;
+        there[set] = 0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             bool is = true;
             const T* const l = line_of(place(i), is);
-            staged[i] = load_odd<T>(l, ACROSS ? from + segment(i) * 8 : k0 + segment(i) * 8, ACROSS ? length : depth, is);
+            there[set] |= (uint32_t)is << i;
+            const int64_t at = element(i, k0);
+            if (all >= 8)  // uniform
+                staged[set][i] = *reinterpret_cast<const typename Vec16<T>::type*>(l + min(at, all - 8));
+            else
+                staged[set][i] = at < all ? load_end<T>(l, at, all) : u32x4{0, 0, 0, 0};
         }
     }
-    __device__ __forceinline__ void put(lds_char* stage) const
+    __device__ __forceinline__ void put(int set, int k0, int depth, lds_char* stage) const
     {
+        const int64_t all = ACROSS ? length : depth;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             const int p = place(i), s = segment(i);
+            const int64_t at = element(i, k0);
+            u32x4 v = staged[set][i];
+            if (all >= 8 && at > all - 8) v = move_down<T>(v, at - (all - 8));
+            if (!(there[set] >> i & 1)) v = u32x4{0, 0, 0, 0};
             lds_char* const to = ACROSS ? stage + p * (128 * R) + (s ^ p % 4 * 2) * 16 : stage + p * 64 + ((s ^ (p >> 1)) & 3) * 16;
-            *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(to) = staged[i];
+            *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(to) = v;
         }
     }
 };
@@ -673,45 +686,48 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_odd_kernel(Grouped a)
             for (int i = 0; i < TM; ++i) xrow[i] = RowsOdd<T, TM, false>::place(i);
             group_rows(a, t, xrow);
         }
-        const auto load = [&](int k0) {
+        const auto load = [&](int set, int k0) {
             if constexpr (OP == kGradient) {
-                ra.load(k0, t.depth, [&](int k, bool& is) {
+                ra.load(set, k0, t.depth, [&](int k, bool& is) {
                     is = k0 + k < t.depth;
                     return static_cast<const T*>(a.y) + (t.first + min(k0 + k, t.depth - 1)) * a.y_stride;
                 });
-                rb.load(k0, t.depth, [&](int k, bool& is) {
+                rb.load(set, k0, t.depth, [&](int k, bool& is) {
                     const int64_t r = batch_row(a, t.first + min(k0 + k, t.depth - 1));
                     is = k0 + k < t.depth && r >= 0;
                     return x + max(r, (int64_t)0) * a.x_stride;
                 });
             } else {
                 int i = 0;
-                ra.load(k0, t.depth, [&](int, bool&) { return x + xrow[i++] * a.x_stride; });
+                ra.load(set, k0, t.depth, [&](int, bool&) { return x + xrow[i++] * a.x_stride; });
                 if constexpr (OP == kTransposed)
-                    rb.load(k0, t.depth, [&](int k, bool& is) {
+                    rb.load(set, k0, t.depth, [&](int k, bool& is) {
                         is = k0 + k < t.depth;
                         return w + (int64_t)min(k0 + k, t.depth - 1) * a.cols;
                     });
                 else
-                    rb.load(k0, t.depth, [&](int n, bool&) { return w + min((int64_t)t.n0 + n, a.rows - 1) * a.cols; });
+                    rb.load(set, k0, t.depth, [&](int n, bool&) { return w + min((int64_t)t.n0 + n, a.rows - 1) * a.cols; });
             }
         };
-        const auto put = [&](int slot) {
-            ra.put((lds_char*)(ring + slot * kStage));
-            rb.put((lds_char*)(ring + slot * kStage + TM * kBlockBytes));
-        };
         f32x16 acc[TN][TM] = {};
-        if (t.depth > 0) {
-            load(0);
-            __syncthreads();  // the tile before is done with the slots
-            put(0);
-            for (int k0 = 0, slot = 0; k0 < t.depth; k0 += kDepth, slot ^= 1) {
-                const bool more = k0 + kDepth < t.depth;
-                if (more) load(k0 + kDepth);
+        const int stages = (t.depth + kDepth - 1) / kDepth;
+        __syncthreads();  // the tile before is done with the slots
+        for_each<kAhead>([&](auto u) {
+            constexpr int set = decltype(u)::value;
+            if (set < stages) load(set, set * kDepth);
+        });
+        for (int s0 = 0; s0 < stages; s0 += kAhead)
+            for_each<kAhead>([&](auto u) {
+                constexpr int set = decltype(u)::value;
+                const int s = s0 + set;
+                if (s >= stages) return;  // uniform
+                lds_char* const stage = (lds_char*)(ring + set % 2 * kStage);
+                ra.put(set, s * kDepth, t.depth, stage);  // all are done with the slot: two stages ago it was read, one ago there was a barrier
+                rb.put(set, s * kDepth, t.depth, stage + TM * kBlockBytes);
+                if (s + kAhead < stages) load(set, (s + kAhead) * kDepth);
                 __syncthreads();
-                const lds_char* const stage = (const lds_char*)(ring + slot * kStage);
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
+                for_each<2>([&](auto half) {
+                    constexpr int kk = decltype(half)::value;
                     u32x4 fa[TM], fb[TN];
 #pragma unroll
                     for (int i = 0; i < TM; ++i) fa[i] = read_fragment<TM, OP == kGradient>(stage, am, i, kk, lane);
@@ -722,10 +738,8 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_odd_kernel(Grouped a)
                     for (int j = 0; j < TN; ++j)
 #pragma unroll
                         for (int i = 0; i < TM; ++i) acc[j][i] = mma32<T>(fb[j], fa[i], acc[j][i]);
-                }
-                if (more) put(slot ^ 1);
-            }
-        }
+                });
+            });
         write_out<T, G, TM, TN, OP, false>(a, t, acc);
     }
 }
@@ -768,10 +782,19 @@ template <typename T, typename G, GroupedOp OP> static void launch_op(const Grou
         const dim3 grid = resident(most_tiles(OP, a, 64 * R, 64 * R), R == 4 ? 1 : R == 2 ? 2 : 4);
         grouped_kernel<T, G, R, R, OP, decltype(indexed)::value><<<grid, block, 0, stream>>>(a);
     };
+    // Tiles of 256 where there are enough of them: two for each CU in a product
+    // (65,536 rows of 64 experts, 1,536 x 2,048: 449 us against 613 with tiles of
+    // 128; at 544 tiles 103 and 105, at 384 tiles 64 and 55), four in a gradient
+    // whose groups have 512 rows on average (that gradient: 518 and 744 us; 512
+    // tiles 74 and 58; 1,024 tiles of 128 rows 81 and 69). Tiles of 128 down to half
+    // a tile for each CU in a product (192 tiles 14.2 us, with tiles of 64 16.9; 108
+    // tiles 18.8 and 14.6), a tile in a gradient (512: 17.5 and 20.7; 64: 42 and 27).
     const auto sized = [&](auto indexed) {
-        if (most_tiles(OP, a, 256, 256) >= 2 * kCus)
+        const int64_t large = most_tiles(OP, a, 256, 256), medium = most_tiles(OP, a, 128, 128);
+        const bool deep = OP != kGradient || a.m / 512 >= a.experts;
+        if (deep && large >= (OP == kGradient ? 4 : 2) * kCus)
             go(std::integral_constant<int, 4>{}, indexed);
-        else if (most_tiles(OP, a, 128, 128) >= 2 * kCus)
+        else if (medium >= (OP == kGradient ? kCus : kCus / 2))
             go(std::integral_constant<int, 2>{}, indexed);
         else
             go(std::integral_constant<int, 1>{}, indexed);

@@ -181,3 +181,97 @@ def test_graph_and_streams(lengths):
         torch.cuda.synchronize()
         for out in (*outs, eager):
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# Sizes that take the larger tiles, several tiles to a workgroup, groups of very different lengths; the 64-bit sums on the GPU
+# ---------------------------------------------------------------------------------------------------------------------
+def big_reference(x, w, dy, offsets, index, top_k, transposed):
+    """(y, bound, dw, bound) in 64 bits, from products of whole groups."""
+    rows = x if index is None else torch.cat([x, torch.zeros_like(x[:1])])[
+        torch.where(index < 0, len(x), torch.div(index, top_k, rounding_mode="floor")).clamp(max=len(x)).long()]
+    rows, dy = rows.double(), dy.double()
+    y = torch.zeros((len(rows), w.shape[1 if not transposed else 2]), dtype=torch.float64, device="cuda")
+    ye, dw = torch.zeros_like(y), torch.zeros((len(w), dy.shape[1], x.shape[1]), dtype=torch.float64, device="cuda")
+    dwe = torch.zeros_like(dw)
+    for e in range(len(w)):
+        part = slice(offsets[e], offsets[e + 1])
+        if offsets[e + 1] > offsets[e]:
+            m = w[e].double() if transposed else w[e].double().T.contiguous()
+            y[part], ye[part] = rows[part] @ m, rows[part].abs() @ m.abs() * (len(m) + 2)
+            d = dy[part].T.contiguous()
+            dw[e], dwe[e] = d @ rows[part], d.abs() @ rows[part].abs() * (offsets[e + 1] - offsets[e] + 2)
+    return y, 2 * ro.U * ye, dw, 2 * ro.U * dwe
+
+
+def big_close(got, want, err, dtype, what):
+    bad = (got.double() - want).abs() > ro.rounded(err, want, dtype)
+    assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+BIG = [(520, 264, [700, 0, 1, 257, 3000] + [130] * 250, 8), (1032, 1024, [2100, 9, 4000, 33, 2050, 0, 500, 8000], 0),
+       (264, 520, [5] * 300 + [0] * 20 + [700], 3), (128, 136, [1000, 1, 300], 0), (2056, 1032, [600] * 16, 16),
+       (2056, 2056, [600] * 14 + [3000, 0], 2), (1031, 517, [300, 0, 900, 1], 5)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("rows,cols,lengths,behind", BIG, ids=[f"{r}x{c}-{len(g)}" for r, c, g, _ in BIG])
+def test_large(rows, cols, lengths, behind, gather, dtype):
+    offsets, m = setting(lengths, 0, behind)
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    rand_ = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)
+    tokens, top_k = (m // 3 + 5, 3) if gather else (m, 1)
+    index = choose(m, tokens, top_k, 3).cuda() if gather else None
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    w, dy = rand_(len(lengths), rows, cols), rand_(m, rows)
+    end = offsets[-1]
+    for transposed in (False, True):
+        x = rand_(tokens, rows if transposed else cols)
+        kw = dict(index=index, top_k=top_k)
+        want, err, dw, dwe = big_reference(x, w, dy if not transposed else rand_(m, 1), offsets, index, top_k, transposed)
+        out = torch.full((m, want.shape[1]), 77.0, dtype=dtype, device="cuda")
+        ds.grouped_matmul(x, w, off, transposed=transposed, out=out, **kw)
+        big_close(out[:end], want[:end], err[:end], dtype, f"transposed {transposed}")
+        assert (out[end:] == 77).all()
+        if not transposed:
+            big_close(ds.grouped_matmul_grad(dy, x, off, **kw), dw, dwe, dtype, "gradient")
+            old = torch.randn(dw.shape, generator=g, device="cuda")
+            got = ds.grouped_matmul_grad(dy, x, off, out=old.clone(), accumulate=True, **kw)
+            big_close(got, dw + old.double(), dwe + 2 * ro.U * old.abs().double(), torch.float32, "added gradient")
+
+
+def test_most_experts_and_one_more():
+    off = torch.arange(2049, dtype=torch.int32, device="cuda")
+    x, w = rand(2048, 16, dtype=torch.bfloat16, seed=1).cuda(), rand(2048, 8, 16, dtype=torch.bfloat16, seed=2).cuda()
+    want = (x.double()[:, None] * w.double()).sum(2)
+    err = 2 * ro.U * 18 * (x.double().abs()[:, None] * w.double().abs()).sum(2)
+    big_close(ds.grouped_matmul(x, w, off), want, err, torch.bfloat16, "2,048 experts")
+    dy = rand(2048, 8, dtype=torch.bfloat16, seed=3).cuda()
+    big_close(ds.grouped_matmul_grad(dy, x, off), dy.double()[:, :, None] * x.double()[:, None], torch.zeros(1, device="cuda"),
+              torch.bfloat16, "gradient")
+    with pytest.raises(ds.DevscanError):
+        ds.grouped_matmul(x, torch.zeros((2049, 8, 16), dtype=torch.bfloat16, device="cuda"),
+                          torch.zeros(2050, dtype=torch.int32, device="cuda"))
+
+
+def test_rows_past_32_bit_offsets():
+    """x, y and the matrices each beyond 4 GiB: 2^21 rows of 1,056 columns, two of them used at either end."""
+    n, cols, rows = (1 << 21) + 40, 1056, 64
+    x = torch.zeros((n, cols), dtype=torch.bfloat16, device="cuda")
+    x[:3] = x[-3:] = 1
+    w = rand(2, rows, cols, dtype=torch.bfloat16, seed=2).cuda()
+    off = torch.tensor([0, n - 20, n], dtype=torch.int32, device="cuda")
+    y = ds.grouped_matmul(x, w, off)
+    want = w.double().sum(2)
+    err = 2 * ro.U * (cols + 2) * w.double().abs().sum(2)
+    big_close(y[:3], want[:1].expand(3, -1), err[:1], torch.bfloat16, "first")
+    big_close(y[-3:], want[1:].expand(3, -1), err[1:], torch.bfloat16, "last")
+    assert (y[3:-3] == 0).all()
+    index = torch.tensor([n - 1, 0, n - 2, n], dtype=torch.int32, device="cuda")
+    y = ds.grouped_matmul(x, w, torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda"), index=index)
+    big_close(y[:3], torch.stack([want[0], want[1], want[1]]), err.amax(0, keepdim=True), torch.bfloat16, "index")
+    assert (y[3] == 0).all()
+    dy = torch.ones((4, rows), dtype=torch.bfloat16, device="cuda")
+    dw = ds.grouped_matmul_grad(dy, x, torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda"), index=index)
+    assert (dw[0] == 1).all() and (dw[1] == 2).all()
