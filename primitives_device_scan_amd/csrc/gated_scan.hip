@@ -85,20 +85,19 @@ __global__ __launch_bounds__(kThreads, 3) void gated_scan_kernel(GatedScan a, Ga
             if ((info.ends & 2) && part == kSub - 1 && p.live && a.final) store_states(a.final + states + p.channel, h);
         } else {
             find_sequences<kRows>(a, row0, s_seq);
-            constexpr int kBatch = TQ % 4 == 0 ? 4 : 2;
             // f(row of the part, its sequence, gate, x) for the part's rows that belong to one
             const auto rows = [&](auto&& f) {
 #pragma unroll 1
-                for (int k0 = 0; k0 < TQ; k0 += kBatch) {
-                    Cells<T, V> g[kBatch], x[kBatch];
+                for (int k0 = 0; k0 < TQ; k0 += 4) {
+                    Cells<T, V> g[4], x[4];
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j)
+                    for (int j = 0; j < 4; ++j)
                         if (mine + k0 + j < a.tokens) {
                             g[j].load(gate.at(k0 + j), gate.bytes);
                             x[j].load(in.at(k0 + j), in.bytes);
                         }
 #pragma unroll
-                    for (int j = 0; j < kBatch; ++j) {
+                    for (int j = 0; j < 4; ++j) {
                         const int row = part * TQ + k0 + j, s = s_seq[row + 1];
                         if (s < 0) continue;
                         if (s_seq[row] != s) {  // the first of its sequence
@@ -110,6 +109,7 @@ __global__ __launch_bounds__(kThreads, 3) void gated_scan_kernel(GatedScan a, Ga
                     }
                 }
             };
+            static_assert(TQ % 4 == 0, "four rows at a time");
             bool anew = false;
             rows([&](int, int row, int s, const Cells<T, V>& g, const Cells<T, V>& x) {
                 anew |= s_seq[row] != s;
