@@ -924,10 +924,9 @@ int64_t ds_gated_scan_scratch_bytes(int dtype, int grad, int64_t tokens, int64_t
 }
 
 // The words of a scan or its gradient, in the call's scratch.
-static int gated_words(const ds::GatedPlan& plan, void* d_scratch, int64_t scratch_bytes, const Buf* bufs, int count,
-                       hipStream_t stream, uint64_t** words)
+static int gated_words(const ds::GatedPlan& plan, int64_t need, void* d_scratch, int64_t scratch_bytes,
+                       const Buf* bufs, int count, hipStream_t stream, uint64_t** words)
 {
-    const int64_t need = gated_scratch(plan);
     if (plan.tiles * plan.cblocks > kMaxTiles) return DS_ERR_TOO_LARGE;
     int st = check_scratch(d_scratch, scratch_bytes, need, bufs, count);
     if (st != DS_OK) return st;
@@ -960,7 +959,8 @@ int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void
     const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), false, mix != 0, tokens, dim);
     std::lock_guard<std::mutex> lock(g_mu);
     uint64_t* words = nullptr;
-    st = gated_words(plan, d_scratch, scratch_bytes, bufs, 6, stream, &words);
+    st = gated_words(plan, ds_gated_scan_scratch_bytes(dtype, 0, tokens, dim), d_scratch, scratch_bytes, bufs, 6, stream,
+                     &words);
     if (st != DS_OK) return st;
     return ds::launch_gated_scan(float_kind(dtype), a, plan, words, g_spin_limit, stream) == hipSuccess ? DS_OK
                                                                                                         : DS_ERR_HIP;
@@ -997,7 +997,8 @@ int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const
     const ds::GatedPlan plan = ds::gated_plan(float_kind(dtype), true, mix != 0, tokens, dim);
     std::lock_guard<std::mutex> lock(g_mu);
     uint64_t* words = nullptr;
-    st = gated_words(plan, d_scratch, scratch_bytes, bufs, 10, stream, &words);
+    st = gated_words(plan, ds_gated_scan_scratch_bytes(dtype, 1, tokens, dim), d_scratch, scratch_bytes, bufs, 10, stream,
+                     &words);
     if (st != DS_OK) return st;
     return ds::launch_gated_scan_grad(float_kind(dtype), a, plan, words, g_spin_limit, stream) == hipSuccess
                ? DS_OK

@@ -288,3 +288,82 @@ def test_graph_and_streams(n):
         for out in (*outs, eager):
             assert all(torch.equal(a, b) for a, b in zip(out, want))
     assert not ds.query_timeout()
+
+
+# ---------------------------------------------------------------------------------------------------------------------
+# Many tiles and groups of tiles, the caller's scratch, a wait that gives up, matrices and states beyond 4 GiB
+# ---------------------------------------------------------------------------------------------------------------------
+LONG = [0, 7000, 7000, 7129, 20_021]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+@pytest.mark.parametrize("form,mix", [("log", False), ("sigmoid", True)])
+def test_many_tiles(form, mix, dtype):
+    check_scan(20_030, 136, LONG, dtype, form, mix, initial=True)
+    check_grad(20_030, 136, LONG, dtype, form, mix, given=True)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_scratch_of_the_callers(dtype):
+    n, d, code = 3001, 136, {torch.float32: ds.DS_FP32, torch.bfloat16: ds.DS_BF16, torch.float16: ds.DS_FP16}[dtype]
+    gate, x, dh = (t.cuda() for t in make(n, d, dtype, "sigmoid"))
+    want, final = ds.gated_scan(gate, x)
+    grads = ds.gated_scan_grad(gate, want, dh)
+    stream = torch.cuda.current_stream().cuda_stream
+    for grad in (0, 1):
+        room = ds.lib.ds_gated_scan_scratch_bytes(code, grad, n, d)
+        assert room > 0 and ds.lib.ds_gated_scan_scratch_bytes(code, grad, 5, d) == 0
+        buf = torch.full((room + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+        outs = [torch.empty_like(t) for t in ((want, final) if grad == 0 else grads)]
+        for r in (room, room - 1):
+            if grad == 0:
+                st = ds.lib.ds_gated_scan(code, gate.data_ptr(), d, x.data_ptr(), d, n, d, None, 1, ds.GATES["sigmoid"], 0,
+                                          None, outs[0].data_ptr(), d, outs[1].data_ptr(), buf.data_ptr() + 256, r, stream)
+            else:
+                st = ds.lib.ds_gated_scan_grad(code, gate.data_ptr(), d, want.data_ptr(), d, dh.data_ptr(), d, None, 0, n, d,
+                                               None, 1, ds.GATES["sigmoid"], 0, None, None, outs[0].data_ptr(), d,
+                                               outs[1].data_ptr(), d, outs[2].data_ptr(), buf.data_ptr() + 256, r, stream)
+            assert (st == ds.DS_OK) == (r == room)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, (want, final) if grad == 0 else grads))
+        assert bool((buf[:256] == 0x5A).all()) and bool((buf[256 + room:] == 0x5A).all())
+
+
+def test_after_a_give_up():
+    """Every wave ends; what the wait would have given is NaN, what needs no wait is right, and so is the next call."""
+    n, d, offsets = 9000, 256, [0, 5000, 5100, 9000]
+    gate, x, dh = (t.cuda() for t in make(n, d, torch.float32, "sigmoid"))
+    o = off(offsets)
+    want = ds.gated_scan(gate, x, o)
+    grads = ds.gated_scan_grad(gate, want[0], dh, o)
+    ds.set_spin_limit(1)
+    try:
+        got, got_grads = ds.gated_scan(gate, x, o), ds.gated_scan_grad(gate, want[0], dh, o)
+        torch.cuda.synchronize()
+    finally:
+        ds.set_spin_limit(0)
+    for a, b in zip((*got, *got_grads), (*want, *grads)):
+        assert bool((torch.isnan(a) | (a == b)).all())
+    assert torch.equal(got[0][:128], want[0][:128]) and torch.equal(got[0][5000:5100], want[0][5000:5100])
+    again = (*ds.gated_scan(gate, x, o), *ds.gated_scan_grad(gate, want[0], dh, o))
+    assert all(torch.equal(a, b) for a, b in zip(again, (*want, *grads)))
+
+
+def test_matrices_and_states_past_4_gib():
+    """Gates of 0 forget everything: h is x, dx is dh and dgate dh h_{t-1}, bit for bit."""
+    n, d = (1 << 21) + 40, 1056
+    x = torch.randn((n, d), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda", dtype=torch.bfloat16)
+    gate = torch.zeros_like(x)
+    h, final = ds.gated_scan(gate, x, off([0, n - 200, n]), form="decay")
+    assert torch.equal(h, x) and torch.equal(final[1], x[-1].float())
+    dgate, dx, _ = ds.gated_scan_grad(gate, h, x, off([0, n - 200, n]), form="decay")
+    assert torch.equal(dx, x)
+    before = torch.cat([torch.zeros_like(h[:1]), h[n - 300:n - 201], torch.zeros_like(h[:1]), h[n - 200:-1]])
+    assert torch.equal(dgate[n - 299:], (x[n - 299:].float() * before[1:].float()).to(torch.bfloat16))
+    del h, dgate, dx, gate
+    pool = torch.zeros(((1 << 20) + 5, 1030), device="cuda")
+    pool[-1], pool[0] = 3.0, 5.0
+    got = ds.gated_step(torch.ones((3, 1030), device="cuda"), torch.ones((3, 1030), device="cuda"), pool,
+                        torch.tensor([len(pool) - 1, 0, len(pool) - 1], dtype=torch.int32, device="cuda"), form="decay")
+    assert got[:, 0].tolist() == [4.0, 6.0, 5.0] and (got == got[:, :1]).all()
+    assert (pool[-1] == 5).all() and (pool[0] == 6).all() and pool.sum().item() == 11 * 1030
