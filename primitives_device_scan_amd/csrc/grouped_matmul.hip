@@ -122,33 +122,34 @@ struct Turns {
 };
 
 // s_first[e] = the sum of of_rows(group's rows) over the groups before e; returns
-// that over all.
+// that over all. Both are cut to `most`, which groups that do not overlap never
+// pass: offsets that decrease may name all rows for each expert.
 template <typename F>
-__device__ __forceinline__ int sum_groups(const Grouped& a, int* s_first, F&& of_rows)
+__device__ __forceinline__ int sum_groups(const Grouped& a, int* s_first, int64_t most, F&& of_rows)
 {
-    __shared__ int s_wave[kWaves];
-    int before = 0;
+    __shared__ int64_t s_wave[kWaves];
+    int64_t before = 0;
     for (int base = 0; base < a.experts; base += kThreads) {
         const int e = base + (int)threadIdx.x;
-        int n = 0;
+        int64_t n = 0;
         if (e < a.experts) {
             int64_t first, end;
             group_range(a, e, first, end);
             n = of_rows((int)(end - first));
         }
-        const int to = wave_inclusive_scan(n);
+        const int64_t to = wave_inclusive_scan(n);
         __syncthreads();
         if (lane_id() == kWave - 1) s_wave[threadIdx.x / kWave] = to;
         __syncthreads();
-        int from = before;
+        int64_t from = before;
         for (int w = 0; w < kWaves; ++w) {
             if (w < (int)threadIdx.x / kWave) from += s_wave[w];
             before += s_wave[w];
         }
-        if (e < a.experts) s_first[e] = from + to - n;
+        if (e < a.experts) s_first[e] = (int)min(from + to - n, most);
     }
     __syncthreads();
-    return uniform(before);
+    return uniform((int)min(before, most));
 }
 
 // The last group with s_first <= v.
@@ -186,7 +187,8 @@ __device__ __forceinline__ Turns deal_tiles(const Grouped& a, int* s_first)
     int from, to;
     if constexpr (OP == kGradient) {
         const int each = ((int)a.rows + M - 1) / M * wide;  // tiles of a group
-        const int64_t cost = sum_groups(a, s_first, [](int rows) { return (rows + kDepth - 1) / kDepth + kTileCost; });
+        const int64_t cost = sum_groups(a, s_first, a.m / kDepth + (1 + kTileCost) * (int64_t)a.experts,
+                                        [](int rows) { return (rows + kDepth - 1) / kDepth + kTileCost; });
         const auto tile_at = [&](int64_t v) {  // the first tile that starts at v of the cost or behind it
             const int e = group_at(s_first, a.experts, (int)v), first = uniform(s_first[e]);
             const int own = (e + 1 < a.experts ? uniform(s_first[e + 1]) : (int)cost) - first;
@@ -195,7 +197,7 @@ __device__ __forceinline__ Turns deal_tiles(const Grouped& a, int* s_first)
         from = xcd == 0 ? 0 : tile_at(cost * xcd / kXcds);
         to = xcd == kXcds - 1 ? a.experts * each : tile_at(cost * (xcd + 1) / kXcds);
     } else {
-        const int tiles = sum_groups(a, s_first, [](int rows) { return (rows + M - 1) / M; }) * wide;
+        const int tiles = sum_groups(a, s_first, a.m / M + a.experts, [](int rows) { return (rows + M - 1) / M; }) * wide;
         const int run = (tiles + kXcds - 1) / kXcds;
         from = xcd * run;
         to = min(from + run, tiles);

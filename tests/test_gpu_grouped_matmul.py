@@ -275,3 +275,30 @@ def test_rows_past_32_bit_offsets():
     dy = torch.ones((4, rows), dtype=torch.bfloat16, device="cuda")
     dw = ds.grouped_matmul_grad(dy, x, torch.tensor([0, 1, 4], dtype=torch.int32, device="cuda"), index=index)
     assert (dw[0] == 1).all() and (dw[1] == 2).all()
+
+
+@pytest.mark.parametrize("stride", [8, 11])
+def test_offsets_that_name_all_rows_for_each_expert(stride):
+    """1,024 times 2^29 rows: more blocks of rows than 31 bits count, of offsets that decrease. Undefined results, all inside."""
+    m, guard = 1 << 29, 4096
+    x = torch.ones((m * stride,), dtype=torch.bfloat16, device="cuda").view(m, stride)[:, :8]
+    w = torch.ones((2048, 8, 8), dtype=torch.bfloat16, device="cuda")
+    buf = torch.full((m + 2 * guard, 8), 77.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([0, m] * 1024 + [0], dtype=torch.int32, device="cuda")
+    ds.grouped_matmul(x, w, off, out=buf[guard:-guard])
+    assert (buf[:guard] == 77).all() and (buf[-guard:] == 77).all()
+    assert bool(((buf == 77) | (buf == 8)).all())
+
+
+def test_no_rows_of_x():
+    """Only padding: rows of zeros, and a gradient of zeros, from an x without rows."""
+    x = torch.zeros((0, 24), dtype=torch.bfloat16, device="cuda")
+    w, dy = rand(3, 16, 24, dtype=torch.bfloat16, seed=1).cuda(), rand(40, 16, dtype=torch.bfloat16, seed=2).cuda()
+    off = torch.tensor([0, 16, 16, 32], dtype=torch.int32, device="cuda")
+    index = torch.arange(40, dtype=torch.int32, device="cuda")
+    out = torch.full((40, 16), 77.0, dtype=torch.bfloat16, device="cuda")
+    y = ds.grouped_matmul(x, w, off, index=index, top_k=2, out=out)
+    assert (y[:32] == 0).all() and (y[32:] == 77).all()
+    assert (ds.grouped_matmul_grad(dy, x, off, index=index, top_k=2) == 0).all()
+    old = torch.ones((3, 16, 24), device="cuda")
+    assert (ds.grouped_matmul_grad(dy, x, off, index=index, top_k=2, out=old, accumulate=True) == 1).all()
