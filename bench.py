@@ -33,7 +33,7 @@ Other modes (their own JSON line): --ceiling (the access-pattern table:
 read, write, copy and read-all/write-half at 4 to 112 KiB per workgroup,
 contiguous and 4 KiB-interleaved, warm and cold), --tile-lds (the pages' LDS
 block-scan experiment), --operators [NAME,...] (the cases of
-perf/operators.py through the library), --profile-only [--cold]
+perf/operators.py and more_operators.py through the library), --profile-only [--cold]
 [--pattern ...] [--operators ...] (launches without timing, for rocprofv3).
 
 Usage: python bench.py [--gpus 1] [--steps K] [--warmup W] [--no-compact] [--no-sort]
@@ -231,8 +231,8 @@ def tile_lds_experiment(args):
 
 
 def operators_experiment(args):
-    """The language-model operators: the cases of perf/operators.py (all, or
-    those named) through the library. A case's time is the median of five runs
+    """The language-model operators: the cases of perf/operators.py and
+    perf/more_operators.py (all, or those named) through the library. A case's time is the median of five runs
     of --steps passes, on three prepared inputs in turn, one event pair around a
     run; bytes and operations are what the case cannot do without (its `work`).
     --profile-only: nine passes per case, an erfinv kernel before and after
@@ -242,18 +242,20 @@ def operators_experiment(args):
 
     import torch
 
-    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
-    ops = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(ops)
-    ops.own = True
-    cases = [c for c in ops.listed() if args.operators == "all" or c["name"] in args.operators.split(",")]
+    cases = []
+    for name in ("operators", "more_operators"):
+        spec = importlib.util.spec_from_file_location(name, os.path.join(ROOT, "perf", name + ".py"))
+        ops = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ops)
+        ops.own = True
+        cases += [(ops, c) for c in ops.listed() if args.operators == "all" or c["name"] in args.operators.split(",")]
     if not cases:
         print(f"--operators: no case is named {args.operators}", file=sys.stderr)
         sys.exit(2)
     torch.cuda.set_device(0)
     mark = torch.zeros(8, device="cuda")
     rows = []
-    for c in cases:
+    for ops, c in cases:
         states = [ops.prepare(c, seed) for seed in range(3)]
         for s in states * 3:
             ops.run(s)
