@@ -4,7 +4,7 @@
 //
 // The rows are cut into tiles whatever the sequences' lengths are. A workgroup
 // holds a tile of kSub * TQ rows by kLanes * V channels in registers, read once:
-// 16 lanes hold TQ successive rows of 16 V channels, V to a lane. A tile makes
+// 16 lanes hold TQ successive rows of 16 V channels, V (16 bytes) to a lane. A tile makes
 // its pair (A, B), publishes it, and finds the state that enters it from the
 // pairs of the tiles before it in its group and the state that entered the group,
 // which the group before published. Which pairs are joined is fixed by the
@@ -13,6 +13,13 @@
 // Tiles of one sequence alone are held in registers; of a tile in which sequences
 // meet, the rows are read a second time, two or four at a time, which costs few
 // registers (the same code for both needed more than there are and spilled).
+//
+// A scan has 3 elements' bytes a step (gate, x, h), its gradient 5 or, mixed, 6, and
+// some 10 to 20 operations: memory is the floor. What keeps it from that floor:
+// 2,036 vector instructions a wave, which fill half of its time, and the tiles'
+// waits for each other (65,536 x 2,048 of 32 sequences in bf16, sigmoid, mixed: 227
+// us, 3.5 TB/s; 186 with the waits left out, 129 at a copy's rate; the gradient of
+// 32,768 x 4,096, one sequence: 350 us, 4.6 TB/s; 258).
 //
 // Words between workgroups are 64 bits, a pair or a state and which of them it is
 // in one, so that a value needs no order with a flag; a launch before clears them
@@ -40,22 +47,23 @@ constexpr int kGroup = 8;                               // tiles to a group
 // is a row that all lanes have in common and a lane's bytes from it (32 bits:
 // kMostStride), so that a tile's many addresses take scalar registers.
 template <typename T, int V> struct Cells {
-    typename std::conditional<V == 1, T, u32x4>::type raw;
+    static constexpr int kBytes = V * (int)sizeof(T);  // 16, 4 or an element
+    typename std::conditional<kBytes == 16, u32x4, typename std::conditional<kBytes == 4, uint32_t, T>::type>::type raw;
     __device__ __forceinline__ void load(const T* row, uint32_t bytes)
     {
         const char* const p = reinterpret_cast<const char*>(row) + bytes;
-        if constexpr (V == 1)
-            raw = *reinterpret_cast<const T*>(p);
-        else
+        if constexpr (kBytes == 16)
             raw = *reinterpret_cast<const typename Vec16<T>::type*>(p);
+        else
+            __builtin_memcpy(&raw, reinterpret_cast<const T*>(p), kBytes);
     }
     __device__ __forceinline__ void store(T* row, uint32_t bytes) const
     {
         char* const p = reinterpret_cast<char*>(row) + bytes;
-        if constexpr (V == 1)
-            *reinterpret_cast<T*>(p) = raw;
-        else
+        if constexpr (kBytes == 16)
             *reinterpret_cast<typename Vec16<T>::type*>(p) = raw;
+        else
+            __builtin_memcpy(reinterpret_cast<T*>(p), &raw, kBytes);
     }
     __device__ __forceinline__ void fill(T x)
     {
@@ -89,7 +97,7 @@ template <typename T, int V> struct Cells {
     // for the rows themselves.
     __device__ __forceinline__ void pin()
     {
-        if constexpr (V != 1) asm volatile("" : "+v"(raw));
+        if constexpr (kBytes == 16) asm volatile("" : "+v"(raw));
     }
 };
 template <int V>
@@ -315,7 +323,10 @@ __device__ __forceinline__ void pass_empty(const GatedScan& a, const Place<V>& p
     }
 }
 
-// Rows of a part: what the registers hold at two workgroups to a CU.
+// Rows of a part, by what the registers hold: of the scan 8 at three workgroups to a
+// CU (65,536 x 2,048: 227 us; 4 rows 247, four workgroups of 6 rows 228); of the
+// gradient of mixed inputs in 16 bits, which holds four matrices, 4 at three
+// workgroups (32,768 x 4,096: 351 us, 8 rows at two 396), of other gradients 8 at two.
 template <typename T> constexpr int kScanRows = 8;
 template <typename T, bool MIX> constexpr int kGradRows = sizeof(T) == 2 && MIX ? 4 : 8;
 template <typename T, bool MIX> constexpr int kGradPerCu = sizeof(T) == 2 && MIX ? 3 : 2;
@@ -326,15 +337,25 @@ inline int vector_of(ElemKind kind, int64_t dim)
     return dim < v ? 1 : v;
 }
 
+// Workgroups of 16 bytes to a lane below which a lane has 4 instead: four times as
+// many, each of a quarter of the work (256 rows of four sequences by 2,048 channels
+// in bf16, 32 workgroups: 18.5 us, 14.6 so; the gradient of 1,003 x 1,000 in fp32,
+// 128 workgroups: 19.1 and 19.6).
+constexpr int64_t kNarrowBelow = 128;
+
 inline GatedPlan gated_plan_of(ElemKind kind, bool grad, bool mix, int64_t tokens, int64_t dim)
 {
     const int part = !grad              ? (kind == kF32 ? kScanRows<float> : kScanRows<bf16>)
                      : kind == kF32 ? (mix ? kGradRows<float, true> : kGradRows<float, false>)
                                     : (mix ? kGradRows<bf16, true> : kGradRows<bf16, false>);
-    const int64_t rows = kSub * part, span = (int64_t)kLanes * vector_of(kind, dim);
+    const int64_t rows = kSub * part;
     GatedPlan p;
     p.tiles = tokens > 0 ? (tokens + rows - 1) / rows : 1;
-    p.cblocks = (dim + span - 1) / span;
+    p.vector = vector_of(kind, dim);
+    const auto blocks = [&] { return (dim + kLanes * p.vector - 1) / (kLanes * p.vector); };
+    if (p.tiles * blocks() < kNarrowBelow) p.vector = kind == kF32 || dim < 2 ? 1 : 2;
+    p.cblocks = blocks();
+    const int64_t span = (int64_t)kLanes * p.vector;
     p.pair_words = p.tiles > 1 ? p.tiles * p.cblocks * span : 0;
     p.rows = rows;
     p.entry_words = p.tiles > 1 ? (p.tiles + kGroup - 1) / kGroup * p.cblocks * span : 0;
@@ -371,6 +392,16 @@ template <typename F> hipError_t with_type(ElemKind kind, int form, bool mix, F&
     return hipGetLastError();
 }
 
+// f(a lane's channels) of a plan: those of 16 bytes, of 4, or one
+template <typename T, typename F> void with_vector(int vector, F&& f)
+{
+    if (vector == Vec16<T>::kN)
+        f(std::integral_constant<int, Vec16<T>::kN>{});
+    else if (vector == 1)
+        f(std::integral_constant<int, 1>{});
+    else if constexpr (sizeof(T) == 2)
+        f(std::integral_constant<int, 2>{});
+}
 
 // The words of a call in its scratch, cleared, and its tiles' sequences.
 GatedWords begin_words(const GatedScan& a, const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit,

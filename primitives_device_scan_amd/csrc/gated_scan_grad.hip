@@ -10,7 +10,8 @@ namespace ds {
 
 // The gradient runs from the last row to the first. What passes from row t to
 // row t - 1 is S = a_t G_t, with G_t = dh_t + S of row t + 1 (or dfinal), so the
-// scan's pairs need no row but their own.
+// scan's pairs need no row but their own. h_{t-1} and x are loaded into the gates'
+// registers once the tile's pairs are made, and arrive while it waits.
 template <typename T, int V, GateForm FORM, bool MIX, int TQ>
 __global__ __launch_bounds__(kThreads, (kGradPerCu<T, MIX>)) void gated_scan_grad_kernel(GatedScanGrad a, GatedWords w)
 {
@@ -198,11 +199,11 @@ hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, const G
     const dim3 grid((unsigned)(plan.tiles * plan.cblocks)), block(kThreads);
     return with_type(kind, a.s.form, a.s.mix, [&](auto t, auto fm, auto mx) {
         using T = decltype(t);
-        if (vector_of(kind, a.s.dim) == 1)
-            gated_scan_grad_kernel<T, 1, decltype(fm)::value, decltype(mx)::value, kGradRows<T, decltype(mx)::value>><<<grid, block, 0, stream>>>(a, w);
-        else
-            gated_scan_grad_kernel<T, Vec16<T>::kN, decltype(fm)::value, decltype(mx)::value, kGradRows<T, decltype(mx)::value>>
+        with_vector<T>(plan.vector, [&](auto v) {
+            constexpr bool kMix = decltype(mx)::value;
+            gated_scan_grad_kernel<T, decltype(v)::value, decltype(fm)::value, kMix, kGradRows<T, kMix>>
                 <<<grid, block, 0, stream>>>(a, w);
+        });
     });
 }
 

@@ -180,6 +180,7 @@ struct GatedStep {
 struct GatedPlan {
     int64_t tiles, cblocks, rows;   // workgroups: tiles (of so many rows) x cblocks
     int64_t pair_words, entry_words, words;  // 64-bit words of scratch: tiles' pairs, groups' states, in all (0: one tile)
+    int vector;  // channels of a lane
 };
 struct GatedWords {
     uint64_t *pairs, *entries, *infos;

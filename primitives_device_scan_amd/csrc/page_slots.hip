@@ -8,7 +8,10 @@
 //
 // The bytes are few (8 a request, 12 a token), so a launch's latency and the
 // two prefix sums are the time. One launch does all: every workgroup scans all
-// requests itself (from the L2) and serves its share of the tokens and pages.
+// requests itself (from the L2) and serves its share of the tokens and pages (256
+// requests of one token each: 5.0 us; 512 of up to 512, 133,000 tokens: 9.8, where
+// the bytes take 0.3; a binary search of the requests in LDS for each token and
+// page is most of the rest).
 // Slots of pages that this call takes are worked out from the free list, not
 // read back from the tables, so that workgroups need not wait for each other.
 #include "launch.hpp"
