@@ -5,7 +5,7 @@
 The decoding step looks the tokens up, routes them and runs the experts. The training step trains the router and the
 table by a loss of the routing weights alone, as a router is distilled or balanced: its gradient goes back through the
 router to its matrix and to the token embeddings, whose rows are accumulated in 32 bits over micro-batches. (A loss of
-the experts' output has a path through the experts too, and there is no backward pass of theirs here.) Weights, tokens
+the experts' output has a path through the experts too, by grouped_matmul and its gradient; not here.) Weights, tokens
 and d loss / d weights are random; the router's own product is a plain matrix product and left to torch.
 """
 from __future__ import annotations

@@ -2,8 +2,9 @@
  * devscan.h -- device-wide prefix sums (scans), stream compaction, two users
  * of the scan built on one counting-sort pass (a radix-sort pass, MoE token
  * alignment) and the language-model operators around them (token embedding and
- * its gradient, an MoE router and its gradient, MoE experts) for AMD Instinct
- * MI355X (gfx950), as a plain C ABI.
+ * its gradient, an MoE router and its gradient, MoE experts; on ragged batches
+ * page tables, a gated recurrence and products grouped by expert) for AMD
+ * Instinct MI355X (gfx950), as a plain C ABI.
  *
  * Every entry point takes device pointers and an element count, enqueues its
  * work on `stream` and returns without waiting for it. The caller owns every
@@ -13,7 +14,8 @@
  * scratch buffer, for the counting-sort pass its digit-by-tile table, for
  * ds_embedding_grad its sorted ids and the parts of sums that cross chunks (two
  * fp32 rows per 8 to 64 ids), for ds_moe_experts h and the down products of
- * every assignment. It grows on demand and is freed by ds_release_workspace().
+ * every assignment, for ds_gated_scan and its gradient the words between tiles.
+ * It grows on demand and is freed by ds_release_workspace().
  *
  * Errors. Argument errors are found on the host before any HIP call and
  * returned at once (DS_ERR_*); launch failures return DS_ERR_HIP. A fault
@@ -25,6 +27,8 @@
  * kernel always finishes. A call in which any wait gave up has produced
  * invalid outputs (compact_if writes -1 as its count when its last tile saw
  * the give-up); ds_query_timeout reports it and restores the workspace.
+ * ds_gated_scan and its gradient keep no words from one call to the next: what
+ * a wait that gave up would have given is NaN there, and nothing is reported.
  *
  * Graph capture. A call records only kernel launches once the workspace of
  * its (device, stream) is large enough, so make one call of at least the
@@ -35,10 +39,11 @@
  * do, so graphs recorded on the same stream must not run at the same time, nor
  * beside an eager call on it, if their calls use a workspace (the scans,
  * compact_if, ds_radix_pass, ds_moe_align, ds_tile_pipeline, ds_embedding_grad,
- * ds_moe_experts). The last two also take scratch from the caller
- * (ds_embedding_grad_scratch, ds_moe_experts_scratch): a graph with scratch of
+ * ds_moe_experts, ds_gated_scan and ds_gated_scan_grad). The last four also
+ * take scratch from the caller (ds_embedding_grad_scratch,
+ * ds_moe_experts_scratch, d_scratch of the gated calls): a graph with scratch of
  * its own runs beside anything, and needs no call before the capture (the
- * Python binding records these two that way). Status words carry a
+ * Python binding records these four that way). Status words carry a
  * 30-bit launch number that the kernels advance themselves, and the host
  * clears them every 2^29 eager launches; a captured graph therefore may be
  * replayed at most 2^29 times before ds_release_workspace() (or one eager
@@ -530,8 +535,8 @@ int ds_grouped_matmul_grad(int dtype, const void* d_dy, int64_t m, int64_t dy_st
  *   d_positions  [tokens] its p
  *   d_left       [1] the free pages that are left; negative: so many were missing
  * Entries of d_slots and d_positions behind the last token are -1 and 0; tokens
- * past `tokens` are left out of them. *d_count counts as cut to [0, capacity]. Calls again with the same inputs give the same
- * results. requests, tokens, capacity < 2^31 (else DS_ERR_TOO_LARGE).
+ * past `tokens` are left out of them. *d_count counts as cut to [0, capacity].
+ * Calls again with the same inputs give the same results. requests, tokens, capacity < 2^31 (else DS_ERR_TOO_LARGE).
  */
 int ds_page_slots(const int32_t* d_context, const int32_t* d_new, int64_t requests, int32_t* d_tables, int64_t width,
                   int64_t table_stride, const int32_t* d_free, int64_t capacity, const int32_t* d_count, int page,
