@@ -422,6 +422,7 @@ typedef enum {
 } ds_gate;
 
 #define DS_GATED_MAX_STRIDE 1048576
+#define DS_GATED_MAX_SLOTS 65536
 
 /*
  * Gated linear recurrence over packed sequences, channel by channel:
@@ -478,7 +479,8 @@ int ds_gated_scan_grad(int dtype, const void* d_gate, int64_t gate_stride, const
  * state_stride apart, through ds_gated_scan's step, in place, and d_h[i] is the
  * new state in the matrices' type. A row whose slot lies outside [0, pool) is a
  * row of zeros and changes no state. Rows that name the same slot are its tokens
- * in the order of the rows.
+ * in the order of the rows; d_slots has at most DS_GATED_MAX_SLOTS of them (else
+ * DS_ERR_TOO_LARGE), since each is looked for among all.
  */
 int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride, int64_t rows,
                   int64_t dim, const int32_t* d_slots, float* d_state, int64_t pool, int64_t state_stride, int form,

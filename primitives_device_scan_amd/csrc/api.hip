@@ -1015,7 +1015,7 @@ int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void
         gate_stride < dim || x_stride < dim || h_stride < dim || state_stride < dim || (!d_slots && pool < rows))
         return DS_ERR_INVALID_VALUE;
     if (rows == 0 || dim == 0) return DS_OK;
-    if (rows > kMost31 || dim > kMost31 || pool > kMost31) return DS_ERR_TOO_LARGE;
+    if (rows > (d_slots ? DS_GATED_MAX_SLOTS : kMost31) || dim > kMost31 || pool > kMost31) return DS_ERR_TOO_LARGE;
     const Buf bufs[5] = {{d_gate, span_bytes(rows, dim, gate_stride, esz), esz, false},
                          {d_x, span_bytes(rows, dim, x_stride, esz), esz, false},
                          {d_slots, d_slots ? rows * 4 : 0, 4, false},

@@ -199,19 +199,28 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
                  if (j == k) h[j] = state[k];
          });
     __shared__ int s_first, s_next;  // the first row of this slot; the next one after i
-    const auto find_rows = [&](int64_t from) {
-        if (threadIdx.x == 0) s_first = s_next = INT32_MAX;
-        __syncthreads();
-        for (int64_t j = from + threadIdx.x; j < a.rows; j += blockDim.x)
-            if (a.slots[j] == slot && j != i) atomicMin(j < i ? &s_first : &s_next, (int)j);
-        __syncthreads();
-    };
     int next = INT32_MAX;
     if (a.slots) {
-        find_rows(0);
+        if (threadIdx.x == 0) s_first = s_next = INT32_MAX;
+        __syncthreads();
+        for (int64_t j = threadIdx.x; j < a.rows; j += blockDim.x)
+            if (a.slots[j] == slot && j != i) atomicMin(j < i ? &s_first : &s_next, (int)j);
+        __syncthreads();
         if (s_first != INT32_MAX) return;  // an earlier row's workgroups do this one
         next = s_next;
     }
+    // From the row behind `from` on, as far as there is none: all rows of a slot in one walk.
+    const auto find_next = [&](int64_t from) {
+        __syncthreads();  // all have read s_next
+        if (threadIdx.x == 0) s_next = INT32_MAX;
+        __syncthreads();
+        for (int64_t j = from + 1 + threadIdx.x; j - (int)threadIdx.x < a.rows; j += blockDim.x) {
+            const bool hit = j < a.rows && a.slots[j] == slot;
+            if (hit) atomicMin(&s_next, (int)j);
+            if (__syncthreads_or(hit)) break;
+        }
+        return s_next;
+    };
     for (;;) {
 #pragma unroll
         for (int k = 0; k < V; ++k) h[k] = step_of<FORM, MIX>(gate_of<T, FORM>(g[k]), h[k], x[k]);
@@ -222,9 +231,7 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
         if (next == INT32_MAX) break;
         i = next;
         load();
-        __syncthreads();  // all have read s_next
-        find_rows(i + 1);
-        next = s_next;
+        next = find_next(i);
     }
     each([&] { store_states(state, h); },
          [&](int k) {

@@ -367,3 +367,27 @@ def test_matrices_and_states_past_4_gib():
                         torch.tensor([len(pool) - 1, 0, len(pool) - 1], dtype=torch.int32, device="cuda"), form="decay")
     assert got[:, 0].tolist() == [4.0, 6.0, 5.0] and (got == got[:, :1]).all()
     assert (pool[-1] == 5).all() and (pool[0] == 6).all() and pool.sum().item() == 11 * 1030
+
+
+def test_step_of_many_rows():
+    """The most rows that name slots: 2,000 of them slot 5's, the last ones too; one row more is refused."""
+    n = 65536
+    slots = torch.arange(10, 10 + n, dtype=torch.int32)
+    slots[100:n:33] = 5
+    slots[-1] = 5
+    gate, x, _ = make(n, 24, torch.float32, "sigmoid", 3)
+    state = states([0] * (n + 21), 24, 4)
+    pool = state.cuda()
+    h = ds.gated_step(gate.cuda(), x.cuda(), pool, slots.cuda())
+    rows = (slots == 5).nonzero()[:, 0]
+    want, after, he, se = ro.step(gate[rows], x[rows], state, slots[rows], "sigmoid", False)
+    close(h[rows.cuda()], want, he, torch.float32, "rows of one slot")
+    close(pool[5:6], after[5:6], se[5:6], torch.float32, "its state")
+    a = torch.sigmoid(gate.double())
+    other = slots != 5
+    want = (a * state.double()[slots.long()] + x.double())[other]
+    size = (a * state.double()[slots.long()].abs() + x.double().abs())[other]
+    assert ((h.double().cpu()[other] - want).abs() <= (2 * float(gate.abs().max()) + 12) * ro.U * size).all()
+    with pytest.raises(ds.DevscanError):
+        ds.gated_step(torch.ones((n + 1, 8), device="cuda"), torch.ones((n + 1, 8), device="cuda"), pool[:, :8],
+                      torch.zeros(n + 1, dtype=torch.int32, device="cuda"))

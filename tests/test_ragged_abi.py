@@ -66,7 +66,7 @@ def test_gated_step_refusals(lib):
     assert f(n=0, gate=None, x=None, h=None) == OK and f(d=0, gs=0, xs=0, ss=0, hs=0) == OK
     assert f(gate=A + 1) == MIS and f(slots=C + 2) == MIS and f(state=D + 2) == MIS
     assert f(h=A) == OVL and f(h=D + 8) == OVL and f(state=B) == OVL and f(state=C - 64) == OVL
-    assert f(n=1 << 31) == BIG and f(pool=1 << 31) == BIG
+    assert f(n=1 << 31) == BIG and f(pool=1 << 31) == BIG and f(n=(1 << 16) + 1) == BIG
 
 
 def test_grouped_refusals(lib):
