@@ -501,9 +501,10 @@ int ds_gated_step(int dtype, const void* d_gate, int64_t gate_stride, const void
  *              d_sorted_ids: it is row d_index[r] / top_k of x, a row of zeros
  *              where that lies outside x (padding)
  *   d_y        [m, rows] (transposed: cols), rows y_stride apart
- * Sums in 32 bits. num_experts <= 2,048; m, x_rows < 2^31, rows and cols at most
- * DS_EXPERTS_MAX_WIDTH (else DS_ERR_TOO_LARGE).
+ * Sums in 32 bits. num_experts <= 2,048; m at most DS_GROUPED_MAX_ROWS, x_rows
+ * < 2^31, rows and cols at most DS_EXPERTS_MAX_WIDTH (else DS_ERR_TOO_LARGE).
  */
+#define DS_GROUPED_MAX_ROWS 2147483136 /* 2^31 - 512: a tile of rows past the last one is still counted in 32 bits */
 int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stride, const void* d_w, int num_experts,
                       int64_t rows, int64_t cols, int transposed, const int32_t* d_offsets, int64_t m,
                       const int32_t* d_index, int top_k, void* d_y, int64_t y_stride, hipStream_t stream);

@@ -1037,7 +1037,7 @@ static int check_grouped(int dtype, int64_t x_rows, int num_experts, int64_t row
     if (x_rows < 0 || m < 0 || rows < 0 || cols < 0 || num_experts < 0 || num_experts > ds::grouped_most_experts() ||
         (index ? top_k < 1 : x_rows < m))
         return DS_ERR_INVALID_VALUE;
-    return m > kMost31 || x_rows > kMost31 || rows > DS_EXPERTS_MAX_WIDTH || cols > DS_EXPERTS_MAX_WIDTH
+    return m > DS_GROUPED_MAX_ROWS || x_rows > kMost31 || rows > DS_EXPERTS_MAX_WIDTH || cols > DS_EXPERTS_MAX_WIDTH
                ? DS_ERR_TOO_LARGE
                : DS_OK;
 }

@@ -63,6 +63,8 @@ constexpr int kDepth = 32;           // k of a stage
 constexpr int kBlockBytes = 4096;    // of a stage, for 64 rows of an operand
 constexpr int kRing = 4;             // stages in LDS
 constexpr int kMostGroups = 2048;
+// Rows of a batch, tiles' rows past a group's end and stages past its depth (up to
+// kAhead + 1 of them) are counted in 32 bits: the host takes 2^31 - 512 rows at most.
 constexpr int kXcds = 8;
 
 // What lanes that have nothing to load read instead.
