@@ -513,7 +513,8 @@ int ds_grouped_matmul(int dtype, const void* d_x, int64_t x_rows, int64_t x_stri
  * Gradient of the matrices of ds_grouped_matmul: d_dw[e] = the sum over its
  * group's rows r of dy_r x_r^T (added to d_dw with accumulate 1; else an expert
  * without rows gets zeros), from d_dy [m, rows] and the x, index and offsets
- * that the product had.
+ * that the product had. Rows for which the index names no row of x (padding)
+ * are left out, whatever d_dy holds there.
  *   grad_dtype  of d_dw [num_experts, rows, cols]: dtype or DS_FP32
  * The same on every run. Other arguments as ds_grouped_matmul.
  */

@@ -815,7 +815,8 @@ def grouped_matmul_grad(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor
                         top_k: int = 1, dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
                         accumulate: bool = False, stream=None) -> torch.Tensor:
     """The gradient of grouped_matmul's w [experts, rows, cols]: for each expert dy.T @ x over its rows of the batch,
-    from the gradient dy [rows of the batch, rows] of the products and the x, offsets, index and top_k that they had.
+    from the gradient dy [rows of the batch, rows] of the products and the x, offsets, index and top_k that they had (rows
+    for which the index names none of x are left out, whatever dy holds there).
     `dtype` is x's (the default) or float32. accumulate: added to `out`; otherwise all of it is written, zeros for an
     expert without rows, into `out` if it is given."""
     _refuse_history(dy, x, out)

@@ -317,6 +317,13 @@ template <typename T, int R, bool ACROSS> struct Rows {
         load_to_lds(from, stage + (by.wave * R + i) * 1024);
         p[i] += step;
     }
+    // ... 0 in this lane unless `there`
+    __device__ __forceinline__ void issue_if(const Issuer& by, int i, lds_char* stage, bool there)
+    {
+        const char* const from = there ? p[i] : by.none;
+        load_to_lds(from, stage + (by.wave * R + i) * 1024);
+        p[i] += step;
+    }
 };
 
 // Lines across k that an index names: a wave's 8 lines of a stage are 8
@@ -361,14 +368,20 @@ template <typename T, int R> struct IndexedRows {
         find_one<0>(g, by), find_one<1>(g, by), find_one<2>(g, by), find_one<3>(g, by);
         find_one<4>(g, by), find_one<5>(g, by), find_one<6>(g, by), find_one<7>(g, by);
     }
-    template <int I> __device__ __forceinline__ void issue(const Issuer& by, lds_char* stage)
+    // this lane's line of the I-th load
+    template <int I> __device__ __forceinline__ const char* choose() const
     {
-        const int lane = lane_id(), part = lane / (8 * R), k = (by.wave * R + I) * W + part;
+        const int part = lane_id() / (8 * R);
         const auto pick = [](bool second, const char* a, const char* b) { return second ? b : a; };
         const char* e = pick(part & 1, line[I * W], line[I * W + 1]);
         if constexpr (W >= 4) e = pick(part & 2, e, pick(part & 1, line[I * W + 2], line[I * W + 3]));
         if constexpr (W == 8)
             e = pick(part & 4, e, pick(part & 2, pick(part & 1, line[4], line[5]), pick(part & 1, line[6], line[7])));
+        return e;
+    }
+    template <int I> __device__ __forceinline__ void issue(const Issuer& by, const char* e, lds_char* stage)
+    {
+        const int lane = lane_id(), k = (by.wave * R + I) * W + lane / (8 * R);
         load_to_lds(e + min((lane % (8 * R) ^ k % 4 * 2) * kVecBytes, most), stage + (by.wave * R + I) * 1024);
     }
 };
@@ -494,6 +507,7 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
     // The stream of stages: `ahead` and its k are three stages before what is multiplied.
     Rows<T, TM, OP == kGradient> ra;
     typename std::conditional<INDEXED, IndexedRows<T, TN>, Rows<T, TN, OP != kProduct>>::type rb;
+    static_assert(!INDEXED || (OP == kGradient && TM == TN), "the lines of A are those of B");
     int ahead_turn = 0, ahead_k = 0;
     const auto begin = [&] {
         const T* const w = static_cast<const T*>(a.w) + (int64_t)ahead.e * a.rows * a.cols;
@@ -515,14 +529,24 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
                 });
         }
     };
+    const char* chosen[TN];  // this lane's lines of x
+    const auto issue_a = [&](auto step, lds_char* stage, int left) {
+        constexpr int i = decltype(step)::value;
+        if constexpr (INDEXED) {  // a row of padding is left out, whatever dy has there
+            chosen[i] = rb.template choose<i>();
+            ra.issue_if(by, i, stage, chosen[i] != by.none);
+        } else {
+            ra.issue(by, i, stage, left);
+        }
+    };
     const auto issue = [&](auto step, int slot) {  // one of kLoads of a stage
         constexpr int i = decltype(step)::value;
         lds_char* const stage = (lds_char*)(ring + slot * kStage);
         const int left = ahead.depth - ahead_k;
         if constexpr (i < TM)
-            ra.issue(by, i, stage, left);
+            issue_a(step, stage, left);
         else if constexpr (INDEXED)
-            rb.template issue<i - TM>(by, stage + TM * kBlockBytes);
+            rb.template issue<i - TM>(by, chosen[i - TM], stage + TM * kBlockBytes);
         else
             rb.issue(by, i - TM, stage + TM * kBlockBytes, left);
     };
@@ -530,7 +554,10 @@ __global__ __launch_bounds__(kThreads, TM * TN > 4 ? 1 : 2) void grouped_kernel(
         if (ahead_k < ahead.depth || !ahead.there) return;
         ahead = tile_at(++ahead_turn);  // none left: depth 0, zeros
         ahead_k = 0;
-        if (ahead.there) begin();
+        if (ahead.there)
+            begin();
+        else if constexpr (INDEXED)
+            rb.depth = 0;  // no entry of the last group again
     };
     u32x4 fa[2][TM], fb[2][TN];
     const auto read = [&](auto step, int slot, auto half) {  // one of kLoads fragments
@@ -637,7 +664,7 @@ template <typename T, int R, bool ACROSS> struct RowsOdd {
     __device__ __forceinline__ int64_t element(int i, int k0) const { return (ACROSS ? from : k0) + segment(i) * 8; }
     // line_of(place, &there): a line that is there in any case. A piece that ends
     // past its line is loaded from the line's last 16 bytes, and moved down only
-    // as it is put into LDS, so that loading waits for nothing.
+    // as it is put into LDS (zeros unless `keep`), so that loading waits for nothing.
     template <typename F>
     __device__ __forceinline__ void load(int set, int k0, int depth, F&& line_of)
     {
@@ -655,7 +682,7 @@ template <typename T, int R, bool ACROSS> struct RowsOdd {
                 staged[set][i] = at < all ? load_end<T>(l, at, all) : u32x4{0, 0, 0, 0};
         }
     }
-    __device__ __forceinline__ void put(int set, int k0, int depth, lds_char* stage) const
+    __device__ __forceinline__ void put(int set, int k0, int depth, lds_char* stage, bool keep = true) const
     {
         const int64_t all = ACROSS ? length : depth;
 #pragma unroll
@@ -664,7 +691,7 @@ template <typename T, int R, bool ACROSS> struct RowsOdd {
             const int64_t at = element(i, k0);
             u32x4 v = staged[set][i];
             if (all >= 8 && at > all - 8) v = move_down<T>(v, at - (all - 8));
-            if (!(there[set] >> i & 1)) v = u32x4{0, 0, 0, 0};
+            if (!keep || !(there[set] >> i & 1)) v = u32x4{0, 0, 0, 0};
             lds_char* const to = ACROSS ? stage + p * (128 * R) + (s ^ p % 4 * 2) * 16 : stage + p * 64 + ((s ^ (p >> 1)) & 3) * 16;
             *reinterpret_cast<__attribute__((address_space(3))) u32x4*>(to) = v;
         }
@@ -697,11 +724,15 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_odd_kernel(Grouped a)
             for (int i = 0; i < TM; ++i) xrow[i] = RowsOdd<T, TM, false>::place(i);
             group_rows(a, t, xrow);
         }
+        static_assert(OP != kGradient || TM == 1, "one entry of the index for what a thread loads of dy");
+        int32_t entry[kAhead];  // of the row of dy
         const auto load = [&](int set, int k0) {
             if constexpr (OP == kGradient) {
                 ra.load(set, k0, t.depth, [&](int k, bool& is) {
+                    const int r = t.first + min(k0 + k, t.depth - 1);
                     is = k0 + k < t.depth;
-                    return static_cast<const T*>(a.y) + (t.first + min(k0 + k, t.depth - 1)) * a.y_stride;
+                    entry[set] = a.index ? a.index[r] : 0;
+                    return static_cast<const T*>(a.y) + r * a.y_stride;
                 });
                 rb.load(set, k0, t.depth, [&](int k, bool& is) {
                     const int64_t r = batch_row(a, t.first + min(k0 + k, t.depth - 1));
@@ -733,7 +764,9 @@ __global__ __launch_bounds__(kThreads, 2) void grouped_odd_kernel(Grouped a)
                 const int s = s0 + set;
                 if (s >= stages) return;  // uniform
                 lds_char* const stage = (lds_char*)(ring + set % 2 * kStage);
-                ra.put(set, s * kDepth, t.depth, stage);  // all are done with the slot: two stages ago it was read, one ago there was a barrier
+                bool keep = true;  // a row of padding is left out, whatever dy has there
+                if constexpr (OP == kGradient) keep = !a.index || row_of_entry(a, entry[set]) >= 0;
+                ra.put(set, s * kDepth, t.depth, stage, keep);  // all are done with the slot: two stages ago it was read, one ago there was a barrier
                 rb.put(set, s * kDepth, t.depth, stage + TM * kBlockBytes);
                 if (s + kAhead < stages) load(set, (s + kAhead) * kDepth);
                 __syncthreads();
