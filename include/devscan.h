@@ -28,7 +28,7 @@
  * invalid outputs (compact_if writes -1 as its count when its last tile saw
  * the give-up); ds_query_timeout reports it and restores the workspace.
  * ds_gated_scan and its gradient keep no words from one call to the next: what
- * a wait that gave up would have given is NaN there, and nothing is reported.
+ * a wait that gave up would have given is NaN there.
  *
  * Graph capture. A call records only kernel launches once the workspace of
  * its (device, stream) is large enough, so make one call of at least the
@@ -447,7 +447,8 @@ typedef enum {
  *
  * Rows are worked on in tiles, and a tile that continues a sequence waits for the
  * tiles before it, as the scans do ("Bounded waits"). Should such a wait give up,
- * the rest of the sequence is NaN.
+ * the tile's rows of that sequence are NaN, and so may later ones be;
+ * ds_query_timeout reports it, of these calls for all streams of the GPU.
  */
 int64_t ds_gated_scan_scratch_bytes(int dtype, int grad, int64_t tokens, int64_t dim);
 int ds_gated_scan(int dtype, const void* d_gate, int64_t gate_stride, const void* d_x, int64_t x_stride,
@@ -614,7 +615,9 @@ int ds_tile_pipeline(int dtype, int variant, const void* d_in, void* d_out, int6
  * Waits for `stream` and reports, in *timed_out, whether any look-back wait
  * on this (device, stream) gave up since the last query (1) or not (0), then
  * clears the record. A wait gives up only after the spin limit; the outputs of
- * such a call are not valid. After a give-up it also clears every status word
+ * such a call are not valid. A give-up of ds_gated_scan, its gradient or
+ * ds_scan_noalloc is reported to the first query on the GPU that comes after
+ * it, on whatever stream. After a give-up it also clears every status word
  * of the workspace (a tile that read the launch number late may have stamped
  * its word with the next one), so later calls start clean. Returns DS_OK or
  * DS_ERR_HIP.

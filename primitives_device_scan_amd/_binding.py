@@ -926,7 +926,8 @@ def tile_pipeline(x: torch.Tensor, variant: str, out: torch.Tensor | None = None
 
 
 def query_timeout(device=None, stream=None) -> bool:
-    """Waits for the stream; True if a look-back wait gave up since the last query."""
+    """Waits for the stream; True if a look-back wait gave up since the last query (of gated_scan and its gradient on any
+    stream of the device)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
         s = torch.cuda.current_stream(dev) if stream is None else stream

@@ -7,6 +7,7 @@
 #include <initializer_list>
 #include <map>
 #include <mutex>
+#include <set>
 #include <utility>
 #include <vector>
 
@@ -198,6 +199,9 @@ struct NoAllocDev {
     uint64_t launches = 0;         // launches since the last clear (epoch wrap guard)
 };
 std::map<int, NoAllocDev> g_noalloc;  // per device, guarded by g_mu
+
+// Devices on which a gated recurrence or its gradient has had tiles that wait.
+std::set<int> g_gated;
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb)
 {
@@ -527,8 +531,11 @@ int ds_query_timeout(hipStream_t stream, int* timed_out)
             from_scratch = 1;
         }
     }
-    auto it = g_ws.find({dev, stream});
     bool gave_up = false;
+    if (g_gated.count(dev) && (ds::take_gated_scan_give_up(&gave_up) != hipSuccess ||
+                               ds::take_gated_scan_grad_give_up(&gave_up) != hipSuccess))
+        return DS_ERR_HIP;
+    auto it = g_ws.find({dev, stream});
     if (it != g_ws.end()) {
         Workspace& w = it->second;
         if (w.base) {
@@ -933,6 +940,11 @@ static int gated_words(const ds::GatedPlan& plan, int64_t need, void* d_scratch,
     char* aux = static_cast<char*>(d_scratch);
     if (need && !aux) st = get_aux(stream, (size_t)need, &aux);
     *words = reinterpret_cast<uint64_t*>(aux);
+    if (plan.tiles > 1 && st == DS_OK) {
+        int dev = 0;
+        if (hipGetDevice(&dev) != hipSuccess) return DS_ERR_HIP;
+        g_gated.insert(dev);  // ds_query_timeout asks there
+    }
     return st;
 }
 

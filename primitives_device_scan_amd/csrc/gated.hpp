@@ -27,7 +27,7 @@
 // and reads all its channels' words once they are there (each channel polling its
 // own words kept the fabric busy: one sequence of 65,536 rows by 2,048 channels 243 us
 // instead of 203). Tile t waits for lower tiles only, which are dispatched before
-// it, and every wait ends after the spin limit (the state is NaN then).
+// it, and every wait ends after the spin limit (the state is NaN then, and `gave_up` set).
 #pragma once
 
 #include <type_traits>
@@ -175,12 +175,26 @@ __device__ __forceinline__ uint64_t state_word(float h) { return (uint64_t)kStat
 __device__ __forceinline__ float first_of(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)(w >> 32) ^ kTurn); }
 __device__ __forceinline__ float second_of(uint64_t w) { return __builtin_bit_cast(float, (uint32_t)w); }
 
+// Set where a wait gives up; of this file's kernels, on each GPU.
+static __device__ uint32_t gave_up;
+// On the host: whether a wait gave up on the current GPU since the last time (sets *flag if so).
+static hipError_t take_give_up(bool* flag)
+{
+    uint32_t set = 0;
+    hipError_t e = hipMemcpyFromSymbol(&set, HIP_SYMBOL(gave_up), sizeof(set));
+    if (e != hipSuccess || !set) return e;
+    *flag = true;
+    set = 0;
+    return hipMemcpyToSymbol(HIP_SYMBOL(gave_up), &set, sizeof(set));
+}
+
 // The state that enters tile `tile` in this thread's channel, from the words of
 // the tiles before it in its group and of the group; all lanes of a wave call
 // it. `pairs`, `entries`: this channel's words, `step` words to the next tile's.
+// polls: spin_limit after a wait that gave up, else less.
 template <GateForm FORM>
 __device__ __forceinline__ float entering_state(uint64_t* pairs, uint64_t* entries, int64_t step, int64_t tile,
-                                                uint32_t spin_limit)
+                                                uint32_t spin_limit, uint32_t& polls)
 {
     const int lane = lane_id();
     const int64_t group = tile / kGroup;
@@ -189,7 +203,6 @@ __device__ __forceinline__ float entering_state(uint64_t* pairs, uint64_t* entri
     uint64_t* const first = reinterpret_cast<uint64_t*>(readlane((uint64_t)(uintptr_t)pairs, 0));
     uint64_t* const entry = reinterpret_cast<uint64_t*>(readlane((uint64_t)(uintptr_t)entries, 0));
     uint64_t* const mine = lane < before ? first + (tile - 1 - lane) * step : entry + group * step;
-    uint32_t polls = 0;
     int need;  // words 0 .. need: up to the first state
     for (;;) {
         const uint32_t mark = lane <= before ? (uint32_t)(status_load(mine) >> 32) : kState;
@@ -250,10 +263,12 @@ __device__ __forceinline__ void join_parts(float (&s_a)[kSub][kLanes * V], float
         const bool known = anew || enter == kGiven;  // what leaves does not depend on the tiles before
         const float a = all.value(), leaving = anew ? b : keep_of<FORM>(a, h) + b;
         status_store(pairs + p.tile * step, known ? state_word(leaving) : pair_word(a, b));
-        if (enter == kBefore) h = entering_state<FORM>(pairs, entries, step, p.tile, w.spin_limit);
+        uint32_t polls = 0;
+        if (enter == kBefore) h = entering_state<FORM>(pairs, entries, step, p.tile, w.spin_limit, polls);
         if (p.tile % kGroup == kGroup - 1 && p.tile + 1 < tiles)
             status_store(entries + (p.tile / kGroup + 1) * step,
                          state_word(known ? leaving : keep_of<FORM>(a, h) + b));
+        if (polls >= w.spin_limit) __hip_atomic_store(&gave_up, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 #pragma unroll 4
     for (int q = 0; q < kSub; ++q) {

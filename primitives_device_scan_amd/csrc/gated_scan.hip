@@ -260,6 +260,8 @@ int64_t gated_step_blocks(ElemKind kind, const GatedStep& a)
     return (a.dim + wide - 1) / wide * a.rows;
 }
 
+hipError_t take_gated_scan_give_up(bool* flag) { return take_give_up(flag); }
+
 GatedWords begin_words(const GatedScan& a, const GatedPlan& plan, uint64_t* scratch, uint32_t spin_limit,
                        hipStream_t stream)
 {

@@ -192,6 +192,8 @@ __global__ __launch_bounds__(kThreads, (kGradPerCu<T, MIX>)) void gated_scan_gra
     pass_empty(a.s, p, a.dfinal, a.dinitial);
 }
 
+hipError_t take_gated_scan_grad_give_up(bool* flag) { return take_give_up(flag); }
+
 hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, const GatedPlan& plan, uint64_t* scratch,
                                   uint32_t spin_limit, hipStream_t stream)
 {

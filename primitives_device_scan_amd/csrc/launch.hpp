@@ -193,6 +193,9 @@ hipError_t launch_gated_scan(ElemKind kind, const GatedScan& a, const GatedPlan&
 hipError_t launch_gated_scan_grad(ElemKind kind, const GatedScanGrad& a, const GatedPlan& plan, uint64_t* scratch,
                                   uint32_t spin_limit, hipStream_t stream);
 hipError_t launch_gated_step(ElemKind kind, const GatedStep& a, hipStream_t stream);
+// Whether a wait of the scan, of its gradient has given up on the current GPU since the last time: *flag is set then.
+hipError_t take_gated_scan_give_up(bool* flag);
+hipError_t take_gated_scan_grad_give_up(bool* flag);
 
 // Products grouped by expert (16-bit kinds) and the gradient of their weights.
 struct Grouped {
