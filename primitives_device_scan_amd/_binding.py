@@ -766,8 +766,8 @@ def _check_batch(x: torch.Tensor, offsets: torch.Tensor, index: torch.Tensor | N
     if index is None:
         return offsets.numel() - 1, x.shape[0]
     _check_flat(index, "index", torch.int32, None, x)
-    if top_k < 1:
-        raise ValueError("top_k must be at least 1")
+    if not 1 <= top_k < 1 << 31:  # 32 bits in the library
+        raise ValueError("top_k must be at least 1 and below 2^31")
     return offsets.numel() - 1, index.numel()
 
 
@@ -866,8 +866,8 @@ def page_slots(context: torch.Tensor, new: torch.Tensor, tables: torch.Tensor, f
         raise TypeError("tables must be int32")
     _check_flat(free, "free", torch.int32, None, context)
     _check_flat(count, "count", torch.int32, (1,), context)
-    if page < 1 or tokens < 0:
-        raise ValueError("page must be at least 1 and tokens at least 0")
+    if not 1 <= page < 1 << 31 or tokens < 0:  # 32 bits in the library
+        raise ValueError("page must be at least 1 and below 2^31, and tokens at least 0")
     if _elsewhere(context, stream):
         return _call_elsewhere(lambda: page_slots(context, new, tables, free, count, page, tokens), context, stream,
                                (context, new, tables, free, count))
