@@ -74,12 +74,24 @@ __global__ __launch_bounds__(kPageThreads) void page_slots_kernel(PageSlots a)
         s_first[threadIdx.x] = {t0, p0};
         if (blockIdx.x == 0 && r < a.requests) a.offsets[r] = (int32_t)min(t0, (int64_t)INT32_MAX);
         __syncthreads();
-        // pages that the chunk's requests take
-        for (int64_t q = first_page + blockIdx.x * kPageThreads + threadIdx.x; q < pages;
-             q += (int64_t)gridDim.x * kPageThreads) {
-            const int i = owner(&Before::pages, here, q);
-            const int64_t col = pages_of(s_context[i]) + (q - s_first[i].pages);
-            if (col < a.width) a.tables[(base + i) * a.table_stride + col] = free_page(q);
+        // pages that the chunk's requests take, or where those are more than its tables have entries
+        // (lengths of 2^31 would take minutes) the entries that they go to
+        const int64_t entries = here * a.width;
+        if (pages - first_page <= entries) {
+            for (int64_t q = first_page + blockIdx.x * kPageThreads + threadIdx.x; q < pages;
+                 q += (int64_t)gridDim.x * kPageThreads) {
+                const int i = owner(&Before::pages, here, q);
+                const int64_t col = pages_of(s_context[i]) + (q - s_first[i].pages);
+                if (col < a.width) a.tables[(base + i) * a.table_stride + col] = free_page(q);
+            }
+        } else {
+            for (int64_t c = (int64_t)blockIdx.x * kPageThreads + threadIdx.x; c < entries;
+                 c += (int64_t)gridDim.x * kPageThreads) {
+                const int i = (int)(c / a.width);
+                const int64_t col = c % a.width, own = pages_of(s_context[i]), q = s_first[i].pages + (col - own);
+                if (col >= own && q < (i + 1 < here ? s_first[i + 1].pages : pages))
+                    a.tables[(base + i) * a.table_stride + col] = free_page(q);
+            }
         }
         // their tokens
         const int64_t end = min(tokens, a.tokens);
