@@ -650,7 +650,9 @@ def _check_sequences(offsets: torch.Tensor | None, like: torch.Tensor) -> int:
 def gated_scan(gate: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor | None = None, *, form: str = "sigmoid",
                mix: bool = False, initial: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
     """A gated linear recurrence over packed sequences: h_t = a_t h_{t-1} + x_t, with mix a_t h_{t-1} + (1 - a_t) x_t.
-    gate and x are [tokens, dim]; a_t is the gate ("decay"), its exponential ("log", gates at most 0) or its sigmoid.
+    gate and x are [tokens, dim]; a_t is the gate ("decay"), its exponential ("log", gates at most 0) or its sigmoid. (Gates
+    have x's dtype: between 1 - 2^-8 and 1 bfloat16 holds no number, float16 from 1 - 2^-11 on, so that memories of more
+    than some 256 or 2,048 steps need "log" or "sigmoid" there.)
     Sequence s holds the rows offsets[s] to offsets[s + 1] (int32 [sequences + 1]; None: all rows are one sequence) and
     starts from initial[s] (float32 [sequences, dim], or None for 0). Returns (h, final): h [tokens, dim] in x's dtype,
     into `out` if it is given (rows outside the sequences are not written), and final float32 [sequences, dim], the

@@ -66,6 +66,8 @@ __device__ __forceinline__ float gate_of(float g)
         p = __builtin_fmaf(p, g, 1.0f / 6.0f);
         p = __builtin_fmaf(p, g, 0.5f);
         p = __builtin_fmaf(p, g, 1.0f);
+        // Below -ln 2 the gate itself, from one rounded product: |g| 2^-24 of it off, but it
+        // is below a half, so that no state lives through steps enough to gather that.
         const float near = -__builtin_fabsf(p * g);
         return g <= 0.0f && g > -0.6931f ? near : __builtin_amdgcn_exp2f(g * 1.44269504f);
     }

@@ -16,10 +16,12 @@
 //
 // A scan has 3 elements' bytes a step (gate, x, h), its gradient 5 or, mixed, 6, and
 // some 10 to 20 operations: memory is the floor. What keeps it from that floor:
-// 2,036 vector instructions a wave, which fill half of its time, and the tiles'
+// 2,028 vector instructions a wave, which fill half of its time, and the tiles'
 // waits for each other (65,536 x 2,048 of 32 sequences in bf16, sigmoid, mixed: 227
 // us, 3.5 TB/s; 186 with the waits left out, 129 at a copy's rate; the gradient of
-// 32,768 x 4,096, one sequence: 350 us, 4.6 TB/s; 258).
+// 32,768 x 4,096, one sequence: 350 us, 4.6 TB/s; 258; in fp32 32,768 x 2,048 of 16
+// sequences 184 and 332 us, 4.4 and 4.9 TB/s). Of few channels the chain of groups is
+// the time (65,536 x 64, one sequence: 123 us, where the bytes take 4).
 //
 // Words between workgroups are 64 bits, a pair or a state and which of them it is
 // in one, so that a value needs no order with a flag; a launch before clears them

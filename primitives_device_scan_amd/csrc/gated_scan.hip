@@ -145,11 +145,13 @@ __global__ __launch_bounds__(kThreads) void gated_begin_kernel(GatedScan a, u32x
 
 // A workgroup takes one row's columns, V to a thread. Rows whose slot an earlier
 // row names are that slot's next tokens: the first such row's workgroups do them,
-// in order. All slots are looked through for that while the row's data is loaded
-// (n slots by each of n rows: nothing for the few thousand sequences of a step). A
-// step moves 3 elements and a state in and out for 8 operations: memory's time, a
-// launch's for few rows (1,024 x 4,096 bf16 in a pool of 4,096: 13.5 us, 4.3 TB/s;
-// 64 x 2,048: 3.2). 16 bytes to a thread; with a channel to a thread 26 us.
+// in order. All slots are looked through for that while the row's data is loaded:
+// n slots by each of n rows, which shows from some thousands of rows on (of 2,048
+// channels in bf16 with slots and without them: 1,024 rows 10.2 and 9.4 us, 4,096
+// 29 and 19, 16,384 199 and 82, 65,536 1,790 and 322). A step moves 3 elements and a
+// state in and out for 8 operations: memory's time, a launch's for few rows (1,024 x
+// 4,096 bf16 in a pool of 4,096: 13.6 us, 4.3 TB/s; 64 x 2,048: 3.1). 16 bytes to a
+// thread; with a channel to a thread 26 us.
 template <typename T, int V, GateForm FORM, bool MIX>
 __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStep a)
 {

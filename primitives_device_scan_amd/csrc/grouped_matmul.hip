@@ -25,11 +25,12 @@
 // orders the lanes that are served together lie in different banks.
 //
 // Bound by the matrix cores for many rows: 65,536 rows of 64 experts, 1,536 x 2,048
-// in bf16, run at 903 TFLOP/s (456 us; a large plain product 1,163), the gradient of
-// the matrices, indexed, at 775 (532 us): in both the matrix instructions are
-// busy for 0.51 and 0.33 of the cycles, what is left are the tiles' starts and ends
-// and the waits at a stage's barrier, and the gradient turns both its operands as it
-// reads them. For few rows it is the matrices' bytes.
+// in bf16, run at 880 to 917 TFLOP/s (449-467 us; a large plain product 1,163), the
+// gradient of the matrices, indexed, at 764 to 790 (522-540 us): the matrix
+// instructions are busy for 0.50 and 0.32 of the cycles, what is left are the tiles'
+// starts and ends and the waits at a stage's barrier, and the gradient turns both its
+// operands as it reads them. For few rows it is the matrices' bytes (256 experts of
+// that size with some 8, 32, 128 rows each: 348-361, 361-376, 417-419 us; the bytes 258).
 //
 // Workgroups stay and take one tile after another; each finds the experts' tiles
 // by a prefix sum of its own over the groups. Workgroup i runs on XCD i % 8: each
@@ -833,6 +834,8 @@ template <typename T, typename G, GroupedOp OP> static void launch_op(const Grou
     // tiles 74 and 58; 1,024 tiles of 128 rows 81 and 69). Tiles of 128 down to half
     // a tile for each CU in a product (192 tiles 14.2 us, with tiles of 64 16.9; 108
     // tiles 18.8 and 14.6), a tile in a gradient (512: 17.5 and 20.7; 64: 42 and 27).
+    // All of a product's were timed with hundreds of rows to a group; how many rows a
+    // group has is not asked, and short groups are padded to the tile.
     const auto sized = [&](auto indexed) {
         const int64_t large = most_tiles(OP, a, 256, 256), medium = most_tiles(OP, a, 128, 128);
         const bool deep = OP != kGradient || a.m / 512 >= a.experts;
